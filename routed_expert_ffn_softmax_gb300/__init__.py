@@ -1,8 +1,8 @@
-"""Routed-expert MoE FFN and decode GQA attention for the GB300 (sm_103a): Python binding of
-libmoe.so.
+"""Routed-expert MoE FFN, decode GQA attention and the serving path over a paged key/value cache
+for the GB300 (sm_103a): Python binding of libmoe.so.
 
 Every function here has the name of the C entry point it calls (include/moe.h,
-include/moe_gqa.h)
+include/moe_gqa.h, include/paged/moe_paged.h)
 and only marshals arguments: torch tensors in, device pointers and sizes out.
 All arithmetic runs in the library's CUDA kernels. There is no fallback: if
 libmoe.so is missing or cannot be loaded, importing the binding's functions
@@ -28,6 +28,8 @@ __all__ = [
     "moe_expert_ffn_noalloc", "moe_expert_ffn_noalloc_status", "moe_gqa_workspace_size", "moe_gqa_decode", "alloc_gqa_workspace",
     "moe_expert_ffn_residual", "moe_ffn_forward_residual", "moe_set_decode_step_policy", "moe_ffn_forward_launches",
     "moe_test_expire_grid_barrier", "moe_set_expert_pass_tokens", "moe_test_expert_wait_limit",
+    "moe_paged_workspace_size", "alloc_paged_workspace", "moe_paged_plan", "moe_qk_norm_rope", "moe_gqa_paged_decode",
+    "moe_gqa_paged_prefill", "moe_gqa_prefix_decode",
 ]
 
 MOE_W_BF16 = 0
@@ -76,6 +78,17 @@ def load() -> ctypes.CDLL:
         lib.moe_gqa_decode.argtypes = [P, P, P, P, i, i, i, i, i, ctypes.c_float, P, P, z, P]
         lib.moe_set_decode_step_policy.argtypes = [i]
         lib.moe_ffn_forward_launches.argtypes = [i, i, i, i, i, i]
+        f32, i64 = ctypes.c_float, ctypes.c_int64
+        lib.moe_paged_workspace_size.argtypes = [i] * 6
+        lib.moe_paged_workspace_size.restype = z
+        lib.moe_paged_plan.argtypes = [P, P, i, i, i, P, i, P, P, i, P, P, P, P, i, P, P, z, P]
+        lib.moe_qk_norm_rope.argtypes = [P, i64, i, i, i, i, P, P, f32, P, i, i, P, P, P, P, P, i, i, P]
+        lib.moe_gqa_paged_decode.argtypes = [P] * 5 + [i] * 7 + [f32, i, i, P, P, z, P]
+        lib.moe_gqa_paged_prefill.argtypes = [P] * 6 + [i] * 8 + [f32, i, i, P, P, z, P]
+        lib.moe_gqa_prefix_decode.argtypes = [P, P, i, P, P, P, P] + [i] * 7 + [f32, P, P, z, P]
+        for f in ("moe_paged_plan", "moe_qk_norm_rope", "moe_gqa_paged_decode", "moe_gqa_paged_prefill",
+                  "moe_gqa_prefix_decode"):
+            getattr(lib, f).restype = i
         for f in ("moe_set_decode_step_policy", "moe_ffn_forward_launches"):
             getattr(lib, f).restype = i
         for f in ("moe_route_topk", "moe_gather", "moe_expert_ffn", "moe_combine", "moe_ffn_forward",
@@ -281,3 +294,138 @@ def moe_ffn_forward_residual(x, logits, W_gate, W_up, W_down, s_gate, s_up, s_do
         _ptr(x), _ptr(logits), _ptr(W_gate), _ptr(W_up), _ptr(W_down), _ptr(s_gate), _ptr(s_up), _ptr(s_down),
         _ptr(Wr_gate), _ptr(Wr_up), _ptr(sr_gate), _ptr(sr_up), T, H, I, E, top_k, _ptr(out), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- paged key/value cache (include/paged/moe_paged.h)
+def _paged_ptr(fn: str, name: str, t: torch.Tensor, dtype: torch.dtype, device, shape) -> int:
+    """The device pointer of a contiguous tensor of this type, device and shape (None: any extent)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{fn}: {name} must be on the same CUDA device as the other tensors, got {t.device}")
+    if len(t.shape) != len(shape) or any(w is not None and w != h for w, h in zip(shape, t.shape)):
+        raise ValueError(f"{fn}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libmoe must be contiguous")
+    return t.data_ptr()
+
+
+def _paged_call(fn: str, device, stream, *args) -> None:
+    """The C call on `stream` (the tensors' device's current stream by default), with that device current."""
+    f = getattr(_lib or load(), fn)
+    if device.index == torch.cuda.current_device():
+        _check(fn, f(*args, _stream(stream)))
+        return
+    with torch.cuda.device(device):
+        _check(fn, f(*args, _stream(stream)))
+
+
+def _paged_workspace(fn: str, workspace: torch.Tensor, device) -> tuple:
+    return _paged_ptr(fn, "workspace", workspace, torch.uint8, device, (None,)), workspace.numel()
+
+
+def moe_paged_workspace_size(N: int = 1, B: int = 1, h_q: int = 1, h_kv: int = 1, d: int = 128,
+                             prefix_len: int = 0) -> int:
+    return int(load().moe_paged_workspace_size(N, B, h_q, h_kv, d, prefix_len))
+
+
+def alloc_paged_workspace(N: int = 1, B: int = 1, h_q: int = 1, h_kv: int = 1, d: int = 128, prefix_len: int = 0,
+                          device="cuda") -> torch.Tensor:
+    """A zero-filled workspace for the calls over the paged cache (it must start zeroed; calls leave it reusable).
+    N query tokens in all, B sequences (N = B for decode), prefix_len keys shared by the batch."""
+    n = moe_paged_workspace_size(N, B, h_q, h_kv, d, prefix_len)
+    if n == 0:
+        raise ValueError("invalid or unsupported sizes for moe_paged_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def moe_paged_plan(ctx_lens, new_lens, page_size: int, num_pages: int, free_pages, free_count, block_table, seq_lens,
+                   cu_new, positions, slots, free_left, workspace, stream=None) -> None:
+    """Block tables and slot maps of one step: ctx_lens, new_lens [B], free_pages [n], free_count [1],
+    block_table [B, max_pages] (gets the new pages); out: seq_lens [B], cu_new [B + 1], positions and slots
+    [n_rows], free_left [1]. All int32."""
+    fn, dev, i32 = "moe_paged_plan", ctx_lens.device, torch.int32
+    B, n_rows = ctx_lens.shape[0], positions.shape[0]
+    p = lambda name, t, shape: _paged_ptr(fn, name, t, i32, dev, shape)  # noqa: E731
+    _paged_call(fn, dev, stream, p("ctx_lens", ctx_lens, (None,)), p("new_lens", new_lens, (B,)), B, page_size,
+                num_pages, p("free_pages", free_pages, (None,)), free_pages.shape[0], p("free_count", free_count, (1,)),
+                p("block_table", block_table, (B, None)), block_table.shape[1], p("seq_lens", seq_lens, (B,)),
+                p("cu_new", cu_new, (B + 1,)), p("positions", positions, (None,)), p("slots", slots, (n_rows,)), n_rows,
+                p("free_left", free_left, (1,)), *_paged_workspace(fn, workspace, dev))
+
+
+def moe_qk_norm_rope(qkv, q_weight, k_weight, eps: float, inv_freq, positions, slots, q_out, k_cache, v_cache,
+                     interleaved: bool = False, stream=None) -> None:
+    """qkv [N, (h_q + 2 h_kv) * d] bf16 (rows may be strided); q_weight, k_weight [d] bf16 or None;
+    inv_freq [rot_dim / 2] f32 (or None: no rotation); positions, slots [N] int32; out: q_out [N, h_q, d],
+    the caches [num_pages, h_kv, page_size, d]."""
+    fn, dev, bf = "moe_qk_norm_rope", qkv.device, torch.bfloat16
+    N, h_q, d = q_out.shape
+    num_pages, h_kv, page_size, _ = k_cache.shape
+    if qkv.dtype is not bf or not qkv.is_cuda:
+        raise TypeError(f"{fn}: qkv must be a bf16 CUDA tensor")
+    if tuple(qkv.shape) != (N, (h_q + 2 * h_kv) * d) or qkv.stride(1) != 1:
+        raise ValueError(f"{fn}: qkv must have shape {(N, (h_q + 2 * h_kv) * d)} with contiguous rows, got {tuple(qkv.shape)}")
+    row_stride = qkv.stride(0) if N > 1 else qkv.shape[1]
+    p = lambda name, t, dtype, shape: None if t is None else _paged_ptr(fn, name, t, dtype, dev, shape)  # noqa: E731
+    rot_dim = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    _paged_call(fn, dev, stream, qkv.data_ptr(), row_stride, N, h_q, h_kv, d, p("q_weight", q_weight, bf, (d,)),
+                p("k_weight", k_weight, bf, (d,)), float(eps), p("inv_freq", inv_freq, torch.float32, (None,)), rot_dim,
+                1 if interleaved else 0, p("positions", positions, torch.int32, (N,)),
+                p("slots", slots, torch.int32, (N,)), p("q_out", q_out, bf, (N, h_q, d)),
+                p("k_cache", k_cache, bf, (num_pages, h_kv, page_size, d)),
+                p("v_cache", v_cache, bf, (num_pages, h_kv, page_size, d)), num_pages, page_size)
+
+
+def _paged_attention(fn, q, k_cache, v_cache, block_table, seq_lens, out):
+    """(the checked pointers q, k_cache, v_cache, block_table, seq_lens, out; the sizes the calls end with)."""
+    dev, bf, i32 = q.device, torch.bfloat16, torch.int32
+    N, h_q, d = q.shape
+    B = seq_lens.shape[0]
+    num_pages, h_kv, page_size, _ = k_cache.shape
+    cache = (num_pages, h_kv, page_size, d)
+    ptrs = (_paged_ptr(fn, "q", q, bf, dev, (N, h_q, d)), _paged_ptr(fn, "k_cache", k_cache, bf, dev, cache),
+            _paged_ptr(fn, "v_cache", v_cache, bf, dev, cache),
+            _paged_ptr(fn, "block_table", block_table, i32, dev, (B, None)),
+            _paged_ptr(fn, "seq_lens", seq_lens, i32, dev, (B,)), _paged_ptr(fn, "out", out, bf, dev, (N, h_q, d)))
+    return ptrs, (B, h_q, h_kv, d, num_pages, page_size, block_table.shape[1])
+
+
+def moe_gqa_paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float, out, workspace, window: int = 0,
+                         n_sink: int = 0, stream=None) -> None:
+    """One token per sequence: q [B, h_q, d] bf16, caches [num_pages, h_kv, page_size, d] bf16, block_table
+    [B, max_pages] and seq_lens [B] int32, out [B, h_q, d] bf16. window = 0: every key."""
+    fn = "moe_gqa_paged_decode"
+    (qp, kp, vp, tp, lp, op), sizes = _paged_attention(fn, q, k_cache, v_cache, block_table, seq_lens, out)
+    if q.shape[0] != sizes[0]:
+        raise ValueError(f"{fn}: q must have one row per sequence")
+    _paged_call(fn, q.device, stream, qp, kp, vp, tp, lp, *sizes, float(scale), window, n_sink, op,
+                *_paged_workspace(fn, workspace, q.device))
+
+
+def moe_gqa_paged_prefill(q, cu_q, k_cache, v_cache, block_table, seq_lens, scale: float, out, workspace,
+                          window: int = 0, n_sink: int = 0, stream=None) -> None:
+    """Many tokens per sequence: q [N, h_q, d] bf16 packed, cu_q [B + 1] int32, the rest as in
+    moe_gqa_paged_decode; out [N, h_q, d] bf16 (rows outside every sequence are left as they were)."""
+    fn = "moe_gqa_paged_prefill"
+    (qp, kp, vp, tp, lp, op), sizes = _paged_attention(fn, q, k_cache, v_cache, block_table, seq_lens, out)
+    cp = _paged_ptr(fn, "cu_q", cu_q, torch.int32, q.device, (sizes[0] + 1,))
+    _paged_call(fn, q.device, stream, qp, cp, kp, vp, tp, lp, q.shape[0], *sizes, float(scale), window, n_sink, op,
+                *_paged_workspace(fn, workspace, q.device))
+
+
+def moe_gqa_prefix_decode(q, prefix_table, prefix_len: int, k_cache, v_cache, block_table, seq_lens, scale: float, out,
+                          workspace, stream=None) -> None:
+    """moe_gqa_paged_decode (no window) behind the prefix_len keys in the pages prefix_table [n] int32 that every
+    sequence of the batch sees; seq_lens and block_table hold the sequences' own keys."""
+    fn = "moe_gqa_prefix_decode"
+    (qp, kp, vp, tp, lp, op), sizes = _paged_attention(fn, q, k_cache, v_cache, block_table, seq_lens, out)
+    if q.shape[0] != sizes[0]:
+        raise ValueError(f"{fn}: q must have one row per sequence")
+    pp = None
+    if prefix_len > 0:
+        pp = _paged_ptr(fn, "prefix_table", prefix_table, torch.int32, q.device, (None,))
+        if prefix_table.shape[0] < -(-prefix_len // k_cache.shape[2]):
+            raise ValueError(f"{fn}: prefix_table is shorter than prefix_len")
+    _paged_call(fn, q.device, stream, qp, pp, prefix_len, kp, vp, tp, lp, *sizes, float(scale), op,
+                *_paged_workspace(fn, workspace, q.device))

@@ -8,16 +8,16 @@
 
 #include <cmath>
 
+#include "api_util.h"
 #include "moe.h"
 #include "moe_gqa.h"
 #include "moe_launch.h"
 
 namespace {
 
-constexpr int kMaxCtas = moe::kPartialCtas;
+using namespace moe::api;
 
-constexpr size_t kAlign = 256;
-inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+constexpr int kMaxCtas = moe::kPartialCtas;
 
 // Workspace layout, in order (each section 256-byte aligned):
 //   ctrl      status word (byte 0), the fused decode step's grid barrier (bytes 8..15), stream-K
@@ -29,9 +29,7 @@ inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 //   ids, w, counts, offsets, sorted_token, inv_pos, active, num_active, xg [P,H] bf16, Y [P,H] f32,
 //   INT8 only: hrec: the fused decode step's token records of 400 bytes (digit planes), [P, H/128] for
 //   the token rows (T <= P of them used) then [P, I/128] for h
-constexpr size_t kCtrlBytes = 4096;
 constexpr size_t kGridBarrierOffset = 8;
-constexpr size_t kCountersOffset = 256;
 constexpr size_t kRowCountersOffset = 2048;
 constexpr int kMaxRowBlocks = static_cast<int>((kCtrlBytes - kRowCountersOffset) / 4);  // H <= 65536
 constexpr int kZeroWords = static_cast<int>((kCountersOffset + 4 * kMaxCtas) / 4);
@@ -97,8 +95,6 @@ Layout layout(int64_t P, int H, int I, int E, bool int8) {
   return L;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 // Size checks shared by the entry points. Returns MOE_OK or the error to report.
 moe_status_t check_sizes(int T, int H, int I, int E, int top_k, moe_wtype_t wtype) {
   if (T < 0 || H < 1 || I < 1 || E < 1 || top_k < 1) return MOE_ERR_INVALID_ARG;
@@ -110,23 +106,6 @@ moe_status_t check_sizes(int T, int H, int I, int E, int top_k, moe_wtype_t wtyp
   if (static_cast<int64_t>(T) * top_k > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
-
-int sm_count() {
-  constexpr int kMaxDev = 64;
-  static std::atomic<int> cache[kMaxDev];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
-  if (dev < kMaxDev) {
-    const int c = cache[dev].load(std::memory_order_relaxed);
-    if (c > 0) return c;
-  }
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return -1;
-  if (dev < kMaxDev) cache[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
-
-moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 // moe_set_decode_step_policy: 0 = by batch shape, 1 = never, 2 = whenever the sizes allow it.
 std::atomic<int> g_decode_policy{0};

@@ -42,6 +42,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cfloat>
 #include <cstdint>
 
 #include "moe_device.cuh"
@@ -95,6 +96,8 @@ struct Params {
   int32_t* status;
   int B, h_q, h_kv, G, L_cap;
   float scale_log2;         // softmax scale * log2(e)
+  PagedKv kv;               // paged kernels only
+  PrefixPartials prefix;    // paged kernels only; o == null: no shared prefix
 };
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -117,8 +120,62 @@ __device__ __forceinline__ int seq_tiles(int len, int L_cap) {
   return (len <= 0 || len > L_cap) ? 0 : (len + kKeys - 1) / kKeys;
 }
 
-// kGP: the group size rounded up to a power of two (1..16); p.G <= kGP is the real group size.
+// Paged cache: what the query of a sequence of `len` keys sees is the window [lo, len) and the sink keys
+// [0, sk), sk <= lo. Its tiles are the sink's (those before the window's first, w0), then the window's.
+struct Span {
+  int len, lo, sk, w0, ns, nt;
+  __device__ __forceinline__ int key_tile(int t) const { return t < ns ? t : w0 + t - ns; }
+  __device__ __forceinline__ bool sees(int key) const { return key < len && (key >= lo || key < sk); }
+  __device__ __forceinline__ bool sees_any(int key, int n) const { return key < len && (key + n > lo || key < sk); }
+};
+__device__ __forceinline__ Span span_of(int len, int L_cap, const PagedKv& kv) {
+  Span s;
+  s.len = (len <= 0 || len > L_cap) ? 0 : len;
+  s.lo = kv.window > 0 && s.len > kv.window ? s.len - kv.window : 0;
+  s.sk = min(kv.n_sink, s.lo);
+  s.w0 = s.lo / kKeys;
+  s.ns = min((s.sk + kKeys - 1) / kKeys, s.w0);
+  s.nt = s.len == 0 ? 0 : s.ns + (s.len + kKeys - 1) / kKeys - s.w0;
+  return s;
+}
+
+// Adds the shared prefix's pieces, in key order, to the running (M, L, O) of group j's heads for sequence b;
+// this thread holds dimension r.
 template <int kGP>
+__device__ __forceinline__ void add_prefix(const Params& p, int b, int j, int r, float (&M)[kGP], float (&L)[kGP],
+                                           float (&O)[kGP]) {
+  const PrefixPartials& x = p.prefix;
+  const int block = b / (2 * x.half_seqs);
+  const int i = b - block * 2 * x.half_seqs;
+  const int half = i >= x.half_seqs ? 1 : 0;
+  const int row = half * (kRowTile / 2) + (i - half * x.half_seqs) * p.G;
+  const int64_t piece0 = (static_cast<int64_t>(j) * x.blocks + block) * x.splits;
+  for (int s = 0; s < x.splits; ++s) {
+    const int64_t at = (piece0 + s) * kRowTile + row;
+    float mc[kGP], lc[kGP], oc[kGP];
+#pragma unroll
+    for (int h = 0; h < kGP; ++h) {
+      const bool in = h < p.G;
+      mc[h] = in ? __ldcg(x.m + at + h) : -FLT_MAX;
+      lc[h] = in ? __ldcg(x.l + at + h) : 0.0f;
+      oc[h] = in ? __ldcg(x.o + (at + h) * kD + r) : 0.0f;
+    }
+#pragma unroll
+    for (int h = 0; h < kGP; ++h) {
+      const float m_new = fmaxf(M[h], mc[h]);
+      const float a_old = exp2f(M[h] - m_new);
+      const float a_c = exp2f(mc[h] - m_new);
+      O[h] = O[h] * a_old + oc[h] * a_c;
+      L[h] = L[h] * a_old + lc[h] * a_c;
+      M[h] = m_new;
+    }
+  }
+}
+
+// kGP: the group size rounded up to a power of two (1..16); p.G <= kGP is the real group size.
+// kPaged: keys and values come through a block table, under a sliding window with sink tokens, and a shared
+// prefix computed beforehand may be added at the end.
+template <int kGP, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
     gqa_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmQ, const Params p) {
@@ -192,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i0 + k < i1) {
         const int len = p.seq_lens[i0 + k];
         bad |= (len < 0 || len > p.L_cap);
-        nt[k] = seq_tiles(len, p.L_cap);
+        nt[k] = kPaged ? span_of(len, p.L_cap, p.kv).nt : seq_tiles(len, p.L_cap);
         sum += nt[k];
       }
     }
@@ -256,7 +313,80 @@ __global__ void __launch_bounds__(kThreads, 1)
     return r;
   };
 
-  if (warp == 0) {
+  if (warp == 0 && kPaged) {
+    // =========================== TMA producer, paged ===========================
+    // A tile is 128 / page_size pages (one part of a page from 128 up); lane (page, K or V, half of the
+    // dimensions) issues that box, so the boxes of a tile go out together even at 16-token pages. The next
+    // tile's table entry is read while this one's slot is waited for. Pages no query sees are not loaded.
+    const uint64_t policy = l2_policy_evict_first();
+    const int page = 1 << p.kv.page_shift;
+    const int rows = page < kKeys ? page : kKeys;
+    const int lp = lane >> 2;         // page of the tile
+    const int box = lane & 3;         // K low, K high, V low, V high
+    const int row0 = lp * rows;
+    const bool mine = row0 < kKeys;
+    int it = 0;
+    int pi = 0;
+    bool ok = true;
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity));
+    };
+    for (int x = beg; x < end && ok; ++pi) {
+      const Piece pc = locate(x);
+      const Span sp = span_of(p.seq_lens[pc.b], p.L_cap, p.kv);
+      const int32_t* table = p.kv.block_table + static_cast<int64_t>(pc.b) * p.kv.max_pages;
+      auto entry = [&](int t) {  // this lane's page in tile t: -2 nothing to load, -1 a bad entry (reads as zeros)
+        const int key = sp.key_tile(t) * kKeys + row0;
+        if (!mine || !sp.sees_any(key, rows)) return -2;
+        const int id = table[key >> p.kv.page_shift];
+        return static_cast<uint32_t>(id) < static_cast<uint32_t>(p.kv.num_pages) ? id : -1;
+      };
+      int id = entry(pc.tl);
+      const int qb = pi & 1;
+      wait_all(&q_empty[qb], ((pi >> 1) & 1) ^ 1);
+      if (!ok) break;
+      if (lane == 0) {
+        uint8_t* qs = smem + kOffQ + qb * kQBytes;
+        const int qrow = pc.b * p.h_q + pc.j * p.G;
+        mbar_arrive_expect_tx(&q_full[qb], kQBytes);
+        tma_load_2d(qs, &tmQ, &q_full[qb], 0, qrow);
+        tma_load_2d(qs + 2048, &tmQ, &q_full[qb], 64, qrow);
+      }
+      for (int t = pc.tl; t < pc.tl + pc.n; ++t, ++it) {
+        const int next = t + 1 < pc.tl + pc.n ? entry(t + 1) : -2;
+        const int st = it % kStages;
+        wait_all(&empty[st], static_cast<uint32_t>(((it / kStages) & 1) ^ 1));
+        if (!ok) break;
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, id != -2));
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * static_cast<uint32_t>(rows) * 128u);
+        __syncwarp();
+        if (id != -2) {
+          const int key = sp.key_tile(t) * kKeys + row0;
+          uint8_t* dst = smem + st * kStageBytes + box * kBox + row0 * 128;
+          const int z = id < 0 ? -1 : id * p.h_kv + pc.j;
+          tma_load_3d(dst, box < 2 ? &tmK : &tmV, &full[st], (box & 1) * 64, key & (page - 1), z, policy);
+          if (id < 0) atomicExch(p.status, kStatusBadPage);
+        }
+        id = next;
+      }
+      x += pc.n;
+    }
+    if (lane == 0) {
+      if (!ok) atomicExch(p.status, kStatusWaitEmptyTimeout);
+      const int n = it < kStages ? it : kStages;
+      for (int i = it - n; i < it; ++i)
+        if (!mbar_wait(&full[i % kStages], static_cast<uint32_t>((i / kStages) & 1))) {
+          atomicExch(p.status, kStatusDrainTimeout);
+          break;
+        }
+      for (int q = pi - 2 < 0 ? 0 : pi - 2; q < pi; ++q)
+        if (!mbar_wait(&q_full[q & 1], (q >> 1) & 1)) {
+          atomicExch(p.status, kStatusDrainTimeout);
+          break;
+        }
+    }
+    __syncwarp();
+  } else if (warp == 0) {
     // =========================== TMA producer ===========================
     if (lane == 0) {
       const uint64_t policy = l2_policy_evict_first();
@@ -404,11 +534,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = beg; x < end; ++pi) {
         const Piece pc = locate(x);
         const int len = p.seq_lens[pc.b];
+        Span sp{};
+        if constexpr (kPaged) sp = span_of(len, p.L_cap, p.kv);
         // a1, a2: the rescale factors of the previous tile and of the one before it
         float m_run[kGP], l_thr[kGP], o_acc[kGP], a1[kGP], a2[kGP];
 #pragma unroll
         for (int h = 0; h < kGP; ++h) {
-          m_run[h] = -INFINITY;
+          m_run[h] = kPaged ? -FLT_MAX : -INFINITY;  // finite: a first tile of -inf scores alone counts nothing
           l_thr[h] = 0.0f;
           o_acc[h] = 0.0f;
           a1[h] = a2[h] = 0.0f;
@@ -437,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int h = 0; h < kGP; ++h) o_acc[h] = fmaf(o_acc[h], a2[h], so[16 + h]);
           }
 
-          const bool valid = t * kKeys + r < len;
+          const bool valid = kPaged ? sp.sees(sp.key_tile(t) * kKeys + r) : t * kKeys + r < len;
           float sv[kGP], alpha[kGP];
 #pragma unroll
           for (int h = 0; h < kGP; ++h) {
@@ -572,6 +704,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool whole = pc.tl == 0 && pc.n == pc.nt;
         uint16_t* outp = p.out + (static_cast<int64_t>(pc.b) * p.h_q + static_cast<int64_t>(pc.j) * p.G) * kD + r;
         if (whole) {
+          if constexpr (kPaged)
+            if (p.prefix.o) add_prefix<kGP>(p, pc.b, pc.j, r, m_run, l_tot, o_acc);
 #pragma unroll
           for (int h = 0; h < kGP; ++h)
             if (h < p.G) {
@@ -627,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float M[kGP], O[kGP], L[kGP];
 #pragma unroll
             for (int h = 0; h < kGP; ++h) {
-              M[h] = -INFINITY;
+              M[h] = kPaged ? -FLT_MAX : -INFINITY;
               O[h] = 0.0f;
               L[h] = 0.0f;
             }
@@ -669,6 +803,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
+            if constexpr (kPaged)
+              if (p.prefix.o) add_prefix<kGP>(p, pc.b, pc.j, r, M, L, O);
 #pragma unroll
             for (int h = 0; h < kGP; ++h)
               if (h < p.G) {
@@ -684,6 +820,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- sequences with no keys (or a length outside [0, L_cap]) attend to nothing: output 0
       for (int b = cta; b < p.B; b += grid) {
         if (pre[b + 1] != pre[b]) continue;
+        if constexpr (kPaged)
+          if (p.prefix.o) {  // no keys of its own: the prefix alone
+            for (int j = 0; j < p.h_kv; ++j) {
+              float M[kGP], L[kGP], O[kGP];
+#pragma unroll
+              for (int h = 0; h < kGP; ++h) {
+                M[h] = -FLT_MAX;
+                L[h] = O[h] = 0.0f;
+              }
+              add_prefix<kGP>(p, b, j, r, M, L, O);
+              uint16_t* o = p.out + (static_cast<int64_t>(b) * p.h_q + static_cast<int64_t>(j) * p.G) * kD + r;
+#pragma unroll
+              for (int h = 0; h < kGP; ++h)
+                if (h < p.G) {
+                  const __nv_bfloat16 v = __float2bfloat16_rn(O[h] / L[h]);
+                  o[h * kD] = *reinterpret_cast<const uint16_t*>(&v);
+                }
+            }
+            continue;
+          }
         uint16_t* o = p.out + static_cast<int64_t>(b) * p.h_q * kD;
         for (int i = gt; i < p.h_q * kD; i += kSoft) o[i] = 0;
       }
@@ -697,11 +853,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
 }
 
-bool encode_kv(CUtensorMap* map, const uint16_t* base, int B, int h_kv, int L_cap) {
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(L_cap),
-                              static_cast<cuuint64_t>(B) * h_kv};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD) * 2, static_cast<cuuint64_t>(L_cap) * kD * 2};
-  const cuuint32_t box[3] = {64, kKeys, 1};
+// A cache of `blocks` blocks (sequences or pages) x h_kv x `rows` rows.
+bool encode_kv(CUtensorMap* map, const uint16_t* base, int blocks, int h_kv, int rows, int box_rows) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(blocks) * h_kv};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD) * 2, static_cast<cuuint64_t>(rows) * kD * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   TensorMapEncodeFn enc = tensor_map_encoder();
   return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), dims, strides, box, estr,
@@ -720,7 +877,7 @@ bool encode_q(CUtensorMap* map, const uint16_t* q, int rows) {
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kGP>
+template <int kGP, bool kPaged>
 cudaError_t launch_g(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const Params& p, int grid,
                      cudaStream_t stream) {
   constexpr int kMaxDev = 64;  // the shared-memory opt-in is per device: done once on each
@@ -729,20 +886,34 @@ cudaError_t launch_g(const CUtensorMap& k, const CUtensorMap& v, const CUtensorM
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= kMaxDev || !done[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(gqa_decode_kernel<kGP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(gqa_decode_kernel<kGP, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     if (dev < kMaxDev) done[dev].store(true, std::memory_order_release);
   }
-  return launch_pdl(gqa_decode_kernel<kGP>, dim3(grid), dim3(kThreads), kSmem, stream, k, v, q, p);
+  return launch_pdl(gqa_decode_kernel<kGP, kPaged>, dim3(grid), dim3(kThreads), kSmem, stream, k, v, q, p);
+}
+
+template <bool kPaged>
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq, const Params& p, int grid,
+                   cudaStream_t stream) {
+  if (p.G <= 1) return launch_g<1, kPaged>(tk, tv, tq, p, grid, stream);
+  if (p.G <= 2) return launch_g<2, kPaged>(tk, tv, tq, p, grid, stream);
+  if (p.G <= 4) return launch_g<4, kPaged>(tk, tv, tq, p, grid, stream);
+  if (p.G <= 8) return launch_g<8, kPaged>(tk, tv, tq, p, grid, stream);
+  return launch_g<16, kPaged>(tk, tv, tq, p, grid, stream);
 }
 
 }  // namespace gqa
 
 cudaError_t launch_gqa_decode(const GqaPlan& plan, cudaStream_t stream) {
   using namespace gqa;
+  const bool paged = plan.paged.block_table != nullptr;
+  const int blocks = paged ? plan.paged.num_pages : plan.B;
+  const int rows = paged ? 1 << plan.paged.page_shift : plan.L_cap;
+  const int box_rows = paged && rows < kKeys ? rows : kKeys;
   CUtensorMap tk, tv, tq;
-  if (!encode_kv(&tk, plan.k_cache, plan.B, plan.h_kv, plan.L_cap) ||
-      !encode_kv(&tv, plan.v_cache, plan.B, plan.h_kv, plan.L_cap) ||
+  if (!encode_kv(&tk, plan.k_cache, blocks, plan.h_kv, rows, box_rows) ||
+      !encode_kv(&tv, plan.v_cache, blocks, plan.h_kv, rows, box_rows) ||
       !encode_q(&tq, plan.q, plan.B * plan.h_q))
     return cudaErrorInvalidValue;
   Params p{};
@@ -757,12 +928,10 @@ cudaError_t launch_gqa_decode(const GqaPlan& plan, cudaStream_t stream) {
   p.G = plan.h_q / plan.h_kv;
   p.L_cap = plan.L_cap;
   p.scale_log2 = plan.scale_log2;
-  const int grid = plan.num_ctas;
-  if (p.G <= 1) return launch_g<1>(tk, tv, tq, p, grid, stream);
-  if (p.G <= 2) return launch_g<2>(tk, tv, tq, p, grid, stream);
-  if (p.G <= 4) return launch_g<4>(tk, tv, tq, p, grid, stream);
-  if (p.G <= 8) return launch_g<8>(tk, tv, tq, p, grid, stream);
-  return launch_g<16>(tk, tv, tq, p, grid, stream);
+  p.kv = plan.paged;
+  p.prefix = plan.prefix;
+  return paged ? launch<true>(tk, tv, tq, p, plan.num_ctas, stream)
+               : launch<false>(tk, tv, tq, p, plan.num_ctas, stream);
 }
 
 }  // namespace moe

@@ -16,6 +16,8 @@ enum : int32_t {
   kStatusWaitEmptyTimeout = 2,  // the producer gave up waiting for a stage to drain
   kStatusDrainTimeout = 3,      // copies still in flight when the kernel gave up
   kStatusBadSeqLen = 4,         // attention: a sequence length outside [0, L_cap] (treated as 0)
+  kStatusBadPage = 6,           // paged cache: a visible page's table entry outside the cache
+  kStatusPlanNoRoom = 7,        // paged plan: a sequence was left out
 };
 
 // Upper bound on any single wait inside a kernel (ns of %globaltimer). A wait

@@ -105,7 +105,24 @@ cudaError_t launch_expert_ffn(const ExpertFfnPlan& plan, cudaStream_t stream);
 // Decode-phase GQA attention (gqa_decode.cu) over a key/value cache [B, h_kv, L_cap, 128].
 constexpr int kGqaMaxSeqs = 2048;  // sequences per call (the tile prefix lives in shared memory)
 constexpr int kGqaSlotFloats = 16 * 128 + 2 * 16;  // one stream-K partial: o[16][128], m[16], l[16]
+struct PagedKv {
+  const int32_t* block_table;  // [B, max_pages]; null: the contiguous cache
+  int num_pages, page_shift, max_pages;
+  int window, n_sink;          // 0 = every key
+};
+// Partials of a shared prefix: pieces of every (key/value head, block of 2 * (128 / G) queries), in key order.
+constexpr int kRowTile = 256;  // query rows of a block: two 128-row halves
+struct PrefixPartials {
+  const float* o;           // [pieces][kRowTile][128], unnormalised; null: no prefix
+  const float* m;           // [pieces][kRowTile] running maximum (base-2 units)
+  const float* l;           // [pieces][kRowTile] softmax sum
+  int splits;               // pieces per (head, block)
+  int blocks;               // blocks of queries
+  int half_seqs;            // queries per 128-row half, 128 / G
+};
 struct GqaPlan {
+  PagedKv paged;
+  PrefixPartials prefix;
   const uint16_t* q;        // [B, h_q, 128] bf16
   const uint16_t* k_cache;  // [B, h_kv, L_cap, 128] bf16
   const uint16_t* v_cache;  // [B, h_kv, L_cap, 128] bf16
@@ -119,6 +136,64 @@ struct GqaPlan {
   int num_ctas;
 };
 cudaError_t launch_gqa_decode(const GqaPlan& plan, cudaStream_t stream);
+
+// Paged key/value cache (include/paged/moe_paged.h): [num_pages, h_kv, page_size, 128] bf16, page_size = 1 << page_shift.
+struct PagedPlanArgs {
+  const int32_t* ctx_lens;     // [B]
+  const int32_t* new_lens;     // [B]
+  const int32_t* free_pages;   // [n_free], the first *free_count valid
+  const int32_t* free_count;
+  int32_t* block_table;        // [B, max_pages]
+  int32_t* seq_lens;           // [B] (may be ctx_lens)
+  int32_t* cu_new;             // [B + 1]
+  int32_t* positions;          // [n_rows]
+  int32_t* slots;              // [n_rows]
+  int32_t* free_left;          // (may be free_count)
+  int32_t* ticket;             // zero on entry, left zero
+  int32_t* status;
+  int B, n_rows, n_free, max_pages, num_pages, page_size, page_shift;
+};
+cudaError_t launch_paged_plan(const PagedPlanArgs& args, int num_sms, cudaStream_t stream);
+
+struct QkNormRopeArgs {
+  const uint16_t* qkv;         // [N] rows of (h_q + 2 h_kv) * 128, row_stride apart
+  const uint16_t* q_weight;    // [128] or null
+  const uint16_t* k_weight;    // [128] or null
+  const float* inv_freq;       // [rot / 2]
+  const int32_t* positions;    // [N]
+  const int32_t* slots;        // [N]
+  uint16_t* q_out;             // [N, h_q, 128]
+  uint16_t* k_cache;
+  uint16_t* v_cache;
+  int64_t row_stride;
+  float eps;
+  int N, h_q, h_kv, rot, interleaved, num_pages, page_shift;
+};
+cudaError_t launch_qk_norm_rope(const QkNormRopeArgs& args, int num_sms, cudaStream_t stream);
+
+// Attention of blocks of query rows (gqa_rows.cu): many tokens per sequence, or a shared prefix for a batch.
+constexpr int kRowsCtas = 152;                                 // CTAs a launch may use: one per SM of the GB300
+constexpr int kRowsPieceFloats = kRowTile * 128 + 2 * kRowTile;  // one partial: o, m, l
+struct GqaRowsPlan {
+  const uint16_t* q;        // [N, h_q, 128]
+  const int32_t* cu_q;      // [B + 1]
+  const uint16_t* k_cache;
+  const uint16_t* v_cache;
+  const int32_t* seq_lens;  // [B]
+  PagedKv paged;
+  uint16_t* out;            // [N, h_q, 128]
+  int32_t* status;
+  float* pieces;            // partials
+  int32_t* tables;          // the launch's tables
+  // shared prefix (then cu_q, seq_lens and out are not used): table, length
+  const int32_t* prefix_table;
+  int prefix_len, prefix_splits, prefix_blocks;
+  const int32_t* own_lens;  // [B] (simple form)
+  int N, B, h_q, h_kv;
+  float scale_log2;
+  int num_sms;
+};
+cudaError_t launch_gqa_rows(const GqaRowsPlan& plan, cudaStream_t stream);
 
 // The whole decode step (routing, gate+up, down, combine) in one cooperative persistent launch
 // (decode_step.cu), for small batches: at most kDecodeMaxT tokens and kDecodeMaxP assignments.
