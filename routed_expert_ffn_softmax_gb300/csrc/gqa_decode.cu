@@ -45,6 +45,7 @@
 #include <cfloat>
 #include <cstdint>
 
+#include "gqa_paged.cuh"
 #include "moe_device.cuh"
 #include "moe_launch.h"
 
@@ -52,7 +53,6 @@ namespace moe {
 namespace gqa {
 
 constexpr int kD = 128;                       // head dimension
-constexpr int kKeys = 128;                    // keys per tile
 constexpr int kN = 16;                        // MMA N: query heads of a group, padded
 constexpr int kStages = 3;
 constexpr int kBox = kKeys * 64 * 2;          // one TMA box: 128 rows x 64 dims x 2 B = 16 KB
@@ -120,25 +120,6 @@ __device__ __forceinline__ int seq_tiles(int len, int L_cap) {
   return (len <= 0 || len > L_cap) ? 0 : (len + kKeys - 1) / kKeys;
 }
 
-// Paged cache: what the query of a sequence of `len` keys sees is the window [lo, len) and the sink keys
-// [0, sk), sk <= lo. Its tiles are the sink's (those before the window's first, w0), then the window's.
-struct Span {
-  int len, lo, sk, w0, ns, nt;
-  __device__ __forceinline__ int key_tile(int t) const { return t < ns ? t : w0 + t - ns; }
-  __device__ __forceinline__ bool sees(int key) const { return key < len && (key >= lo || key < sk); }
-  __device__ __forceinline__ bool sees_any(int key, int n) const { return key < len && (key + n > lo || key < sk); }
-};
-__device__ __forceinline__ Span span_of(int len, int L_cap, const PagedKv& kv) {
-  Span s;
-  s.len = (len <= 0 || len > L_cap) ? 0 : len;
-  s.lo = kv.window > 0 && s.len > kv.window ? s.len - kv.window : 0;
-  s.sk = min(kv.n_sink, s.lo);
-  s.w0 = s.lo / kKeys;
-  s.ns = min((s.sk + kKeys - 1) / kKeys, s.w0);
-  s.nt = s.len == 0 ? 0 : s.ns + (s.len + kKeys - 1) / kKeys - s.w0;
-  return s;
-}
-
 // Adds the shared prefix's pieces, in key order, to the running (M, L, O) of group j's heads for sequence b;
 // this thread holds dimension r.
 template <int kGP>
@@ -151,14 +132,15 @@ __device__ __forceinline__ void add_prefix(const Params& p, int b, int j, int r,
   const int row = half * (kRowTile / 2) + (i - half * x.half_seqs) * p.G;
   const int64_t piece0 = (static_cast<int64_t>(j) * x.blocks + block) * x.splits;
   for (int s = 0; s < x.splits; ++s) {
-    const int64_t at = (piece0 + s) * kRowTile + row;
+    const int64_t piece = piece0 + s;
+    const int64_t at = piece * kRowTile + row;
     float mc[kGP], lc[kGP], oc[kGP];
 #pragma unroll
     for (int h = 0; h < kGP; ++h) {
       const bool in = h < p.G;
       mc[h] = in ? __ldcg(x.m + at + h) : -FLT_MAX;
       lc[h] = in ? __ldcg(x.l + at + h) : 0.0f;
-      oc[h] = in ? __ldcg(x.o + (at + h) * kD + r) : 0.0f;
+      oc[h] = in ? __ldcg(x.o + piece_at(piece, row + h, r)) : 0.0f;
     }
 #pragma unroll
     for (int h = 0; h < kGP; ++h) {

@@ -1,0 +1,50 @@
+// What a query sees of a paged cache, as key tiles, and the layout of row-block partials: shared by the decode and
+// the row-block attention kernels.
+#pragma once
+
+#include <cstdint>
+
+#include "moe_launch.h"
+
+namespace moe {
+namespace gqa {
+
+constexpr int kKeys = 128;  // keys per tile
+
+// The visible keys of a run of queries: the window [lo, len) and the sink keys [0, sk), sk <= lo. Its tiles are
+// the sink's (those before the window's first, w0), then the window's.
+struct Span {
+  int len, lo, sk, w0, ns, nt;
+  __device__ __forceinline__ int key_tile(int t) const { return t < ns ? t : w0 + t - ns; }
+  __device__ __forceinline__ bool sees(int key) const { return key < len && (key >= lo || key < sk); }
+  __device__ __forceinline__ bool sees_any(int key, int n) const { return key < len && (key + n > lo || key < sk); }
+};
+// Keys below `len` (0: none), from `lo` on or below n_sink.
+__device__ __forceinline__ Span span_of_range(int len, int lo, int n_sink) {
+  Span s;
+  s.len = len;
+  s.lo = lo;
+  s.sk = min(n_sink, lo);
+  s.w0 = lo / kKeys;
+  s.ns = min((s.sk + kKeys - 1) / kKeys, s.w0);
+  s.nt = len == 0 ? 0 : s.ns + (len + kKeys - 1) / kKeys - s.w0;
+  return s;
+}
+// The first key of the window of a query at position pos.
+__device__ __forceinline__ int window_start(int pos, int window) {
+  return window > 0 && pos >= window ? pos - window + 1 : 0;
+}
+// One query at the end of a sequence of len keys; a length outside [0, L_cap] counts as empty.
+__device__ __forceinline__ Span span_of(int len, int L_cap, const PagedKv& kv) {
+  if (len < 0 || len > L_cap) len = 0;
+  return span_of_range(len, window_start(len - 1, kv.window), kv.n_sink);
+}
+
+// Row-block partials: per piece the unnormalised output as [16 groups of 8 dimensions][kRowTile rows][8], so that the
+// writer (a thread per row) and the readers (a thread per dimension) both move whole 32-byte sectors.
+__device__ __forceinline__ int64_t piece_at(int64_t piece, int row, int dim) {
+  return ((piece * 16 + (dim >> 3)) * kRowTile + row) * 8 + (dim & 7);
+}
+
+}  // namespace gqa
+}  // namespace moe

@@ -1,130 +1,849 @@
-// Attention of many query rows per key/value head over the paged cache (include/paged/moe_paged.h): prompts and
-// chunks (causal, sliding window, sink tokens) and the shared prefix of a decode batch.
+// Attention of many query rows per key/value head over the paged cache (include/paged/moe_paged.h): prompts, chunks
+// and drafted tokens (causal, sliding window, sink tokens), and the prefix a decode batch shares.
 //
-// First form: one warp per (query token, query head), 4 dimensions per lane, the online softmax over the visible
-// keys one at a time. For a shared prefix each warp takes one split of the keys and leaves its (o, m, l).
+// A row is one (query token, query head); the G heads of a group read the same keys, so a block of 2 x (128 / G)
+// consecutive tokens of one sequence makes 2 x 128 rows (token major) against one key/value head, two halves that
+// share every key and value tile. Per tile of 128 keys and half, on tcgen05.mma:
+//     S [128 rows x 128 keys] = Q . K^T        (Q and the K tile from shared memory, as TMA lands them)
+//     O [128 rows x 128 dims] += P . V         (P from TMEM, the V tile read MN-major: the cache is never rearranged)
+// 4 * 128 * 128 * 128 flops per half and tile: long prompts are bound by the tensor pipe, few rows behind long
+// contexts by HBM. The halves alternate, so the softmax of one runs under the products of the other.
+//
+// Softmax: a thread owns a row (TMEM lane), so its maximum and sum need no exchange. O stays in TMEM; it is rescaled
+// only when a row's maximum has grown by more than 2^8 since the reference in use (probabilities are then at most
+// 2^8, exact to the same relative bf16 step, and sums stay far inside fp32), which after the first tiles is rare.
+//
+// Work split: the key tiles of all (sequence, head, block) segments form one list (causal blocks have different
+// lengths, windows bound them) and each CTA takes a contiguous range of it, so any mix of prompts balances to within
+// a tile. Which range holds what comes from a small table kernel, since lengths are only known on the device. A
+// segment cut between CTAs leaves (o, m, l) pieces that a third kernel joins in CTA order, one warp per row. For a
+// shared prefix the host knows the sizes: equal splits per segment, whose pieces the decode kernel joins with the
+// sequences' own keys.
+//
+// Per CTA, 12 warps: 0 TMA producer (Q per piece; K and V tiles alternate in a ring of 5 x 32 KB), 1 issues the
+// MMAs, 2 and 3 write zeros for blocks that see nothing, 4-7 and 8-11 the softmax and output of the two halves.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cfloat>
 #include <cstdint>
 
+#include "gqa_paged.cuh"
 #include "moe_device.cuh"
 #include "moe_launch.h"
 
 namespace moe {
 namespace rows {
 
-constexpr int kThreads = 256;
+using namespace gqa;
 
-__device__ __forceinline__ void load4(const uint16_t* p, float (&x)[4]) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  x[0] = __uint_as_float(v.x << 16);
-  x[1] = __uint_as_float(v.x & 0xffff0000u);
-  x[2] = __uint_as_float(v.y << 16);
-  x[3] = __uint_as_float(v.y & 0xffff0000u);
+constexpr int kD = 128;
+constexpr int kHalf = 128;                  // rows of a half
+constexpr int kStages = 5;
+constexpr int kBox = kKeys * 64 * 2;        // 128 rows x 64 dims
+constexpr int kTile = 2 * kBox;             // one K or V tile, or the queries of a half: 32 KB
+constexpr int kThreads = 384;
+constexpr int kOffQ = 0;
+constexpr int kOffRing = 2 * kTile;
+constexpr int kOffBar = kOffRing + kStages * kTile;
+constexpr int kNumBars = 2 * kStages + 2 + 2 * 4 + 1;
+constexpr int kSmem = kOffBar + 256;
+static_assert(kNumBars * 8 + 8 <= 256, "barrier area");
+static_assert(kSmem <= 232448, "dynamic shared memory per CTA");
+static_assert(kRowTile == 2 * kHalf, "partials hold both halves");
+
+// TMEM columns: scores of half h at 128 h (the probabilities, two a column, over their first 64), outputs behind.
+constexpr int kTmemCols = 512;
+__device__ constexpr uint32_t col_s(int h) { return 128u * h; }
+__device__ constexpr uint32_t col_o(int h) { return 256u + 128u * h; }
+
+constexpr float kGrowth = 8.0f;  // log2 of how far a row's maximum may outgrow its reference
+
+struct Params {
+  const int32_t* cu_q;       // [B + 1]
+  const int32_t* seq_lens;   // [B]
+  PagedKv kv;
+  uint16_t* out;
+  float* pieces_o;           // see piece_at
+  float* pieces_m;           // [pieces][kRowTile]
+  float* pieces_l;
+  int32_t* status;
+  int32_t* pre;              // [B + 1] tiles of the sequences before, for one key/value head
+  int32_t* base;             // [B + 1] row blocks of the sequences before
+  int32_t* cum;              // [blocks + 1] tiles of the blocks before
+  const int32_t* prefix_table;
+  int prefix_len, prefix_splits, prefix_blocks;
+  int N, B, h_q, h_kv, G, half_tokens, max_blocks, L_cap;
+  float scale_log2;
+};
+
+// Rows cu_q[b] .. of sequence b, 0 unless they lie within [0, N] in order.
+__device__ __forceinline__ int tokens_of(const Params& p, int b, bool* bad) {
+  const int x0 = p.cu_q[b], x1 = p.cu_q[b + 1];
+  *bad = x0 < 0 || x1 < x0 || x1 > p.N;
+  return *bad ? 0 : x1 - x0;
 }
 
-__global__ void __launch_bounds__(kThreads) gqa_rows_kernel(const GqaRowsPlan p) {
+// One block of query rows against one key/value head.
+struct Block {
+  int seq;
+  int tok0, ntok;  // packed tokens
+  int pos0;        // position of the first
+  Span sp;         // keys some row sees
+};
+__device__ __forceinline__ Block block_of(const Params& p, int b, int r) {
+  Block k;
+  k.seq = b;
+  bool bad;
+  const int n = tokens_of(p, b, &bad);
+  int len = p.seq_lens[b];
+  if (len < 0 || len > p.L_cap) len = 0;
+  const int per = 2 * p.half_tokens;
+  k.tok0 = p.cu_q[b] + r * per;
+  k.ntok = min(per, n - r * per);
+  k.pos0 = len - n + r * per;
+  // a sequence without keys has queries at negative positions only
+  k.sp = span_of_range(max(0, k.pos0 + k.ntok), window_start(k.pos0, p.kv.window), p.kv.n_sink);
+  return k;
+}
+
+// ---------------------------------------------------------------- tables
+constexpr int kTableThreads = 1024;
+
+__device__ __forceinline__ int scan_block(int v, int* sums) {  // inclusive over the block's threads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += n;
+  }
+  if (lane == 31) sums[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int s = sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += n;
+    }
+    sums[lane] = s;
+  }
+  __syncthreads();
+  const int out = v + (warp ? sums[warp - 1] : 0);
+  __syncthreads();
+  return out;
+}
+
+__device__ __forceinline__ int last_at_most(const int32_t* a, int n, int x) {  // last i < n with a[i] <= x
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Row blocks and key tiles before each sequence and each block.
+__global__ void __launch_bounds__(kTableThreads) rows_tables_kernel(const Params p) {
+  __shared__ int sums[32];
+  __shared__ int base[kGqaMaxSeqs + 1];
+  const int tid = threadIdx.x;
   pdl_wait_predecessor();
   pdl_allow_successor();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-  const bool prefix = p.prefix_table != nullptr;
-  const int splits = prefix ? p.prefix_splits : 1;
-  const int64_t row = w / splits;
-  const int s = static_cast<int>(w - row * splits);
-  const int n = static_cast<int>(row / p.h_q);
-  const int hq = static_cast<int>(row - static_cast<int64_t>(n) * p.h_q);
-  if (n >= p.N) return;
-  const int G = p.h_q / p.h_kv;
-  const int j = hq / G;
-  const int page = 1 << p.paged.page_shift;
-  int beg = 0, end = 0, lo = 0, sk = 0;
-  const int32_t* table = p.prefix_table;
-  if (prefix) {
-    const int tiles = (p.prefix_len + 127) / 128;
-    beg = 128 * static_cast<int>(static_cast<int64_t>(s) * tiles / splits);
-    end = min(p.prefix_len, 128 * static_cast<int>(static_cast<int64_t>(s + 1) * tiles / splits));
-    lo = beg;
+  const int per = 2 * p.half_tokens;
+  int nb[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int b = 2 * tid + k;
+    nb[k] = 0;
+    if (b < p.B) {
+      bool bad;
+      nb[k] = (tokens_of(p, b, &bad) + per - 1) / per;
+      const int len = p.seq_lens[b];
+      if (bad || len < 0 || len > p.L_cap) atomicExch(p.status, kStatusBadSeqLen);
+    }
+  }
+  // offsets that run over each other could ask for more blocks than N tokens make: the tables end there
+  const int incl = scan_block(nb[0] + nb[1], sums);
+  int run = incl - nb[0] - nb[1];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int b = 2 * tid + k;
+    if (b < p.B) {
+      base[b] = min(run, p.max_blocks);
+      if (run + nb[k] > p.max_blocks) atomicExch(p.status, kStatusBadSeqLen);
+    }
+    run += nb[k];
+    if (b + 1 == p.B) base[p.B] = min(run, p.max_blocks);
+  }
+  __syncthreads();
+  const int blocks = base[p.B];
+  for (int b = tid; b <= p.B; b += kTableThreads) p.base[b] = base[b];
+  int carry = 0;
+  for (int i0 = 0; i0 < blocks; i0 += kTableThreads) {
+    const int i = i0 + tid;
+    int nt = 0, b = 0;
+    if (i < blocks) {
+      b = last_at_most(base, p.B, i);
+      nt = block_of(p, b, i - base[b]).sp.nt;
+    }
+    const int t = carry + scan_block(nt, sums);
+    if (i < blocks) {
+      p.cum[i + 1] = t;
+      // the sequences that end with this block's one (empty ones behind it too)
+      for (int e = b + 1; e <= p.B && base[e] == i + 1; ++e) p.pre[e] = t;
+    }
+    if (tid == kTableThreads - 1) sums[0] = t;
+    __syncthreads();
+    carry = sums[0];
+    __syncthreads();
+  }
+  if (tid == 0) p.cum[0] = 0;
+  for (int b = tid; b <= p.B && base[b] == 0; b += kTableThreads) p.pre[b] = 0;
+}
+
+// ---------------------------------------------------------------- the list of tiles, and a CTA's pieces of it
+struct Share {  // CTA c's tiles: the first rm CTAs take q + 1, the others q; CTAs past nc take none
+  int total, nc, q, rm;
+  __device__ __forceinline__ explicit Share(int t, int ctas) {
+    total = t;
+    nc = min(t, ctas);
+    q = nc > 0 ? t / nc : 0;
+    rm = nc > 0 ? t - q * nc : 0;
+  }
+  __device__ __forceinline__ int start(int c) const { return c < nc ? c * q + min(c, rm) : total; }
+  __device__ __forceinline__ int cta_of(int i) const {
+    const int big = rm * (q + 1);
+    return i < big ? i / (q + 1) : rm + (i - big) / q;
+  }
+};
+
+struct Piece {
+  int j;            // key/value head
+  int t0, n;        // tiles t0 .. t0 + n - 1 of the block's
+  int64_t slot;     // where a partial goes, -1: the piece is the whole segment
+  Block k;
+};
+
+// Walks a CTA's pieces in order; every role walks alike.
+class Walk {
+ public:
+  __device__ __forceinline__ Walk(const Params& p) : p_(p) {
+    if (p.prefix_table) {
+      x_ = blockIdx.x;
+      end_ = p.h_kv * p.prefix_blocks * p.prefix_splits;
+      return;
+    }
+    const Share s(p.h_kv * p.pre[p.B], gridDim.x);
+    x_ = s.start(blockIdx.x);
+    end_ = s.start(blockIdx.x + 1);
+    if (x_ >= end_) return;
+    // the last sequence whose first tile is at most x (empty ones before it are skipped by the search)
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.h_kv * p.pre[mid] <= x_) lo = mid; else hi = mid - 1;
+    }
+    b_ = lo;
+    const int first = p.pre[b_];
+    const int tiles = p.pre[b_ + 1] - first;
+    const int off = x_ - p.h_kv * first;
+    j_ = off / tiles;
+    const int rem = off - j_ * tiles;
+    const int base = p.base[b_];
+    i_ = base + last_at_most(p.cum + base, p.base[b_ + 1] - base, first + rem);
+    t_ = first + rem - p.cum[i_];
+  }
+  __device__ __forceinline__ bool next(Piece& c) {
+    if (x_ >= end_) return false;
+    if (p_.prefix_table) {
+      const int s = x_ % p_.prefix_splits;
+      const int seg = x_ / p_.prefix_splits;
+      const int per = 2 * p_.half_tokens;
+      c.j = seg / p_.prefix_blocks;
+      c.k.tok0 = (seg - c.j * p_.prefix_blocks) * per;
+      c.k.ntok = min(per, p_.B - c.k.tok0);
+      c.k.seq = 0;
+      c.k.pos0 = 0;
+      c.k.sp = span_of_range(p_.prefix_len, 0, 0);
+      c.t0 = static_cast<int>(static_cast<int64_t>(s) * c.k.sp.nt / p_.prefix_splits);
+      c.n = static_cast<int>(static_cast<int64_t>(s + 1) * c.k.sp.nt / p_.prefix_splits) - c.t0;
+      c.slot = x_;
+      x_ += gridDim.x;
+      return true;
+    }
+    c.j = j_;
+    c.k = block_of(p_, b_, i_ - p_.base[b_]);
+    c.t0 = t_;
+    c.n = min(end_ - x_, c.k.sp.nt - t_);
+    const bool whole = c.n == c.k.sp.nt;
+    c.slot = whole ? -1 : 2 * static_cast<int64_t>(blockIdx.x) + (first_ ? 0 : 1);
+    first_ = false;
+    x_ += c.n;
+    t_ = 0;
+    if (x_ < end_) {  // the next block with tiles: of this head, of the next head, of the next sequence
+      ++i_;
+      for (;;) {
+        const int stop = p_.base[b_ + 1];
+        while (i_ < stop && p_.cum[i_ + 1] == p_.cum[i_]) ++i_;
+        if (i_ < stop) break;
+        if (++j_ >= p_.h_kv) {
+          j_ = 0;
+          do ++b_;
+          while (p_.pre[b_ + 1] == p_.pre[b_]);
+        }
+        i_ = p_.base[b_];
+      }
+    }
+    return true;
+  }
+
+ private:
+  const Params& p_;
+  int x_ = 0, end_ = 0, b_ = 0, j_ = 0, i_ = 0, t_ = 0;
+  bool first_ = true;
+};
+
+// ---------------------------------------------------------------- the attention kernel
+// Bits c of keys cb + c (c = 0 .. 31) that are below `n`.
+__device__ __forceinline__ uint32_t bits_below(int n, int cb) {
+  const int k = n - cb;
+  return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    gqa_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ Params p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint64_t* empty = full + kStages;
+  uint64_t* q_full = empty + kStages;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_empty + 1;   // [2]
+  uint64_t* p_full = s_full + 2;    // [2]
+  uint64_t* o_full = p_full + 2;    // [2]
+  uint64_t* o_free = o_full + 2;    // [2]
+  uint64_t* mma_done = o_free + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&s_full[h], 1);
+      mbar_init(&p_full[h], kHalf);
+      mbar_init(&o_full[h], 1);
+      mbar_init(&o_free[h], kHalf);
+    }
+    mbar_init(mma_done, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmQ);
+  }
+  pdl_wait_predecessor();
+  pdl_allow_successor();
+  if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);  // after the wait: a predecessor may still hold columns
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  Walk walk(p);
+  Piece c;
+
+  if (warp == 0) {
+    // =========================== TMA producer ===========================
+    // A tile is 128 / page_size pages (one part of a page from 128 up): lane (page, dimension half) of the lower half
+    // warp issues K boxes, of the upper half warp V boxes. Pages no row sees are not loaded.
+    const uint64_t policy_q = l2_policy_evict_first();
+    const int page = 1 << p.kv.page_shift;
+    const int rows = page < kKeys ? page : kKeys;
+    const int row0 = ((lane & 15) >> 1) * rows;
+    const bool is_v = lane >= 16;
+    const bool mine = row0 < kKeys;
+    int it = 0, pi = 0;
+    int issued = 0;  // K and V tiles whose copies are under way or done
+    bool ok = true;
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity));
+    };
+    while (ok && walk.next(c)) {
+      const Span sp = c.k.sp;
+      const int32_t* table =
+          p.prefix_table ? p.prefix_table : p.kv.block_table + static_cast<int64_t>(c.k.seq) * p.kv.max_pages;
+      auto entry = [&](int t) {  // this lane's page in tile t: -2 nothing to load, -1 a bad entry (reads as zeros)
+        const int key = sp.key_tile(t) * kKeys + row0;
+        if (!mine || !sp.sees_any(key, rows)) return -2;
+        const int id = table[key >> p.kv.page_shift];
+        return static_cast<uint32_t>(id) < static_cast<uint32_t>(p.kv.num_pages) ? id : -1;
+      };
+      int id = entry(c.t0);
+      for (int t = c.t0; t < c.t0 + c.n; ++t, ++it) {
+        const int next = t + 1 < c.t0 + c.n ? entry(t + 1) : -2;
+        const int key = sp.key_tile(t) * kKeys + row0;
+        const int z = id < 0 ? -1 : id * p.h_kv + c.j;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id != -2 && !is_v)) * static_cast<uint32_t>(rows) * 128u;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int idx = 2 * it + kv;
+          const int st = idx % kStages;
+          wait_all(&empty[st], static_cast<uint32_t>(((idx / kStages) & 1) ^ 1));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
+          __syncwarp();
+          issued = idx + 1;
+          if (id != -2 && is_v == (kv == 1))
+            tma_load_3d(smem + kOffRing + st * kTile + (lane & 1) * kBox + row0 * 128, kv ? &tmV : &tmK, &full[st],
+                        (lane & 1) * 64, key & (page - 1), z, policy_q);
+          if (kv == 0 && t == c.t0) {  // the queries go between the first K and V tiles
+            wait_all(q_empty, static_cast<uint32_t>((pi & 1) ^ 1));
+            if (!ok) break;
+            if (lane == 0) {
+              const int nh = c.k.ntok > p.half_tokens ? 2 : 1;
+              mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(nh * p.half_tokens * p.G * 256));
+              for (int h = 0; h < nh; ++h)
+                for (int d = 0; d < 2; ++d)
+                  tma_load_3d(smem + kOffQ + h * kTile + d * kBox, &tmQ, q_full, 64 * d, c.j * p.G,
+                              c.k.tok0 + h * p.half_tokens, policy_q);
+              ++pi;
+            }
+            pi = __shfl_sync(0xffffffffu, pi, 0);
+          }
+        }
+        if (!ok) break;
+        if (id == -1) atomicExch(p.status, kStatusBadPage);
+        id = next;
+      }
+    }
+    if (!ok && lane == 0) atomicExch(p.status, kStatusWaitEmptyTimeout);
+    // never leave copies in flight: the last stages and queries issued
+    if (lane == 0) {
+      for (int i = issued < kStages ? 0 : issued - kStages; i < issued; ++i)
+        if (!mbar_wait(&full[i % kStages], static_cast<uint32_t>((i / kStages) & 1))) {
+          atomicExch(p.status, kStatusDrainTimeout);
+          break;
+        }
+      if (pi > 0 && !mbar_wait(q_full, static_cast<uint32_t>((pi - 1) & 1))) atomicExch(p.status, kStatusDrainTimeout);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // =========================== MMA issuer ===========================
+    if (lane == 0) {
+      const uint32_t sbase = smem_addr(smem);
+      const uint32_t idesc_s = umma_idesc_bf16_m128(kKeys);
+      const uint32_t idesc_o = umma_idesc_bf16_m128(kD) | kIdescBMajorMN;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && !mbar_wait(bar, parity)) {
+          ok = false;
+          atomicExch(p.status, kStatusWaitFullTimeout);
+        }
+      };
+      uint32_t pv[2] = {0, 0};     // products P . V issued for each half
+      uint32_t seg[2] = {0, 0};    // pieces begun for each half
+      auto issue_o = [&](int h, int i, bool first) {
+        const int idx = 2 * i + 1;
+        const int st = idx % kStages;
+        if (h == 0) wait(&full[st], static_cast<uint32_t>((idx / kStages) & 1));
+        wait(&p_full[h], pv[h] & 1);
+        if (first) wait(&o_free[h], (seg[h]++ & 1) ^ 1);
+        if (ok) {
+          tc_fence_after_sync();
+          const uint32_t v = sbase + kOffRing + st * kTile;
+#pragma unroll
+          for (int s = 0; s < kKeys / 16; ++s)
+            umma_bf16_tmem_a(tmem + col_o(h), tmem + col_s(h) + 8 * s, umma_desc_sw128_mn(v + s * 2048, kBox), idesc_o,
+                             !(first && s == 0));
+        }
+        umma_commit(&o_full[h]);
+        ++pv[h];
+      };
+      int it = 0, pi = 0;
+      for (; walk.next(c); ++pi) {
+        const int nh = c.k.ntok > p.half_tokens ? 2 : 1;
+        wait(q_full, static_cast<uint32_t>(pi & 1));
+        for (int t = 0; t < c.n; ++t, ++it) {
+          const int idx = 2 * it;
+          const int st = idx % kStages;
+          wait(&full[st], static_cast<uint32_t>((idx / kStages) & 1));
+          for (int h = 0; h < nh; ++h) {
+            // the scores overwrite the probabilities of the tile before, whose product was issued just now: MMAs of
+            // one thread run in order
+            if (t > 0) issue_o(h, it - 1, t == 1);
+            if (ok) {
+              tc_fence_after_sync();
+              const uint32_t k = sbase + kOffRing + st * kTile;
+              const uint32_t q = sbase + kOffQ + h * kTile;
+#pragma unroll
+              for (int s = 0; s < kD / 16; ++s)
+                umma_bf16(tmem + col_s(h), umma_desc_sw128(q + (s >> 2) * kBox + (s & 3) * 32),
+                          umma_desc_sw128(k + (s >> 2) * kBox + (s & 3) * 32), idesc_s, s > 0);
+            }
+            umma_commit(&s_full[h]);
+          }
+          if (t > 0) umma_commit(&empty[(idx - 1) % kStages]);
+          umma_commit(&empty[st]);
+          if (t == c.n - 1) umma_commit(q_empty);
+        }
+        for (int h = 0; h < nh; ++h) issue_o(h, it - 1, c.n == 1);
+        umma_commit(&empty[(2 * it - 1) % kStages]);
+      }
+      // every MMA has completed before TMEM is released
+      umma_commit(mma_done);
+      if (!mbar_wait(mma_done, 0)) atomicExch(p.status, kStatusDrainTimeout);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // =========================== blocks that see nothing ===========================
+    if (!p.prefix_table) {
+      const int blocks = p.base[p.B];
+      for (int i = blockIdx.x; i < blocks; i += gridDim.x) {
+        if (p.cum[i + 1] != p.cum[i]) continue;
+        const int b = last_at_most(p.base, p.B, i);
+        const Block k = block_of(p, b, i - p.base[b]);
+        uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(k.tok0) * p.h_q * kD);
+        const int64_t n = static_cast<int64_t>(k.ntok) * p.h_q * (kD / 8);
+        for (int64_t e = tid - 64; e < n; e += 64) o[e] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
   } else {
-    int b = -1;
-    for (int i = 0; i < p.B; ++i) {
-      const int x0 = p.cu_q[i], x1 = p.cu_q[i + 1];
-      if (x0 < 0 || x1 < x0 || x1 > p.N) {
-        if (lane == 0) atomicExch(p.status, kStatusBadSeqLen);
+    // =========================== softmax and output of half h ===========================
+    const int h = (warp - 4) >> 2;
+    const int r = (warp & 3) * 32 + lane;  // row of the half
+    const uint32_t tbase = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const int i = r / p.G;                  // token of the half
+    const int g = r - i * p.G;
+    const bool neg = p.scale_log2 < 0.0f;
+    const float hidden = neg ? INFINITY : -INFINITY;
+    bool ok = true;
+    auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+      const bool w = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity));
+      if (!w && ok) {
+        ok = false;
+        atomicExch(p.status, kStatusWaitFullTimeout);
+      }
+    };
+    uint32_t cnt = 0;  // tiles of this half so far
+    int it = 0;        // tiles of the CTA so far
+    while (walk.next(c)) {
+      const int nh = c.k.ntok > p.half_tokens ? 2 : 1;
+      if (h >= nh) {
+        it += c.n;
         continue;
       }
-      if (x0 <= n && n < x1) b = i;
-    }
-    if (b < 0) return;
-    int len = p.seq_lens[b];
-    if (len < 0 || len > p.paged.max_pages * page) {
-      if (lane == 0) atomicExch(p.status, kStatusBadSeqLen);
-      len = 0;
-    }
-    const int pos = len - (p.cu_q[b + 1] - n);
-    end = len == 0 ? 0 : max(pos + 1, 0);
-    lo = p.paged.window > 0 ? max(0, end - p.paged.window) : 0;
-    sk = min(p.paged.n_sink, lo);
-    table = p.paged.block_table + static_cast<int64_t>(b) * p.paged.max_pages;
-  }
-  float q[4], o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  load4(p.q + (static_cast<int64_t>(n) * p.h_q + hq) * 128 + 4 * lane, q);
-  float m = -FLT_MAX, l = 0.0f;
-  for (int key = sk > 0 ? 0 : max(beg, lo); key < end; key = key + 1 == sk ? max(sk, lo) : key + 1) {
-    const int id = table[key >> p.paged.page_shift];
-    const bool ok = static_cast<uint32_t>(id) < static_cast<uint32_t>(p.paged.num_pages);
-    float k[4] = {0.0f, 0.0f, 0.0f, 0.0f}, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (ok) {
-      const int64_t at =
-          (((static_cast<int64_t>(id) * p.h_kv + j) << p.paged.page_shift) + (key & (page - 1))) * 128 + 4 * lane;
-      load4(p.k_cache + at, k);
-      load4(p.v_cache + at, v);
-    } else if (lane == 0) {
-      atomicExch(p.status, kStatusBadPage);
-    }
-    float d = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
+      const int tok = h * p.half_tokens + i;  // within the block
+      const bool live = i < p.half_tokens && tok < c.k.ntok;
+      const int pos = p.prefix_table ? p.prefix_len - 1 : c.k.pos0 + tok;
+      const int end = live ? min(pos + 1, c.k.sp.len) : 0;   // keys below it are seen ...
+      const int lo = window_start(pos, p.kv.window);         // ... from here on, or below n_sink
+      // a tile needs no mask when the half's first token sees its end and its last token's window begins before it
+      const int last = min(c.k.ntok, (h + 1) * p.half_tokens) - 1;
+      const int end_min = p.prefix_table ? p.prefix_len : c.k.pos0 + h * p.half_tokens + 1;
+      const int lo_max = p.prefix_table ? 0 : window_start(c.k.pos0 + last, p.kv.window);
+      float m = -FLT_MAX, l = 0.0f;
+      for (int t = c.t0; t < c.t0 + c.n; ++t, ++it, ++cnt) {
+        const int kb = c.k.sp.key_tile(t) * kKeys;
+        wait_warp(&s_full[h], cnt & 1);
+        tc_fence_after_sync();
+        uint32_t s[128];
+        if (ok) {
+          tmem_ld128(tbase + col_s(h), s);
+        } else {
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
-    d *= p.scale_log2;
-    const float m_new = fmaxf(m, d);
-    const float a = exp2f(m - m_new), e = exp2f(d - m_new);
-    l = l * a + e;
+          for (int x = 0; x < 128; ++x) s[x] = 0u;
+        }
+        const bool plain = kb + kKeys <= end_min && (kb >= lo_max || kb + kKeys <= p.kv.n_sink);
+        if (!plain) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x) o[x] = o[x] * a + e * v[x];
-    m = m_new;
-  }
-  if (prefix) {
-    const int half = 128 / G;
-    const int block = n / (2 * half);
-    const int i = n - block * 2 * half;
-    const int hf = i >= half ? 1 : 0;
-    const int r = hf * 128 + (i - hf * half) * G + hq - j * G;
-    const int64_t pieces = static_cast<int64_t>(p.h_kv) * p.prefix_blocks * splits;
-    const int64_t at = ((static_cast<int64_t>(j) * p.prefix_blocks + block) * splits + s) * kRowTile + r;
-    float* po = p.pieces + at * 128 + 4 * lane;
-    for (int x = 0; x < 4; ++x) po[x] = o[x];
-    if (lane == 0) {
-      p.pieces[pieces * kRowTile * 128 + at] = m;
-      p.pieces[pieces * kRowTile * 128 + pieces * kRowTile + at] = l;
+          for (int w = 0; w < 4; ++w) {
+            const int cb = kb + 32 * w;
+            const uint32_t see = bits_below(end, cb) & (~bits_below(lo, cb) | bits_below(p.kv.n_sink, cb));
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (!((see >> x) & 1u)) s[32 * w + x] = __float_as_uint(hidden);
+          }
+          if (h == 0 && !c.k.sp.sees(kb + r)) {
+            // a key no row sees: its cache row is arbitrary (even NaN) and a zero probability times NaN is NaN, so
+            // this row of the V tile is cleared (the wait orders the overwrite behind the tile's landing)
+            const int idx = 2 * it + 1;
+            const int st = idx % kStages;
+            if (mbar_wait(&full[st], static_cast<uint32_t>((idx / kStages) & 1))) {
+              uint4* v0 = reinterpret_cast<uint4*>(smem + kOffRing + st * kTile + r * 128);
+              uint4* v1 = reinterpret_cast<uint4*>(smem + kOffRing + st * kTile + kBox + r * 128);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) v0[x] = v1[x] = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+              atomicExch(p.status, kStatusWaitFullTimeout);
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        float mx = hidden;
+        if (neg) {
+#pragma unroll
+          for (int x = 0; x < 128; ++x) mx = fminf(mx, __uint_as_float(s[x]));
+        } else {
+#pragma unroll
+          for (int x = 0; x < 128; ++x) mx = fmaxf(mx, __uint_as_float(s[x]));
+        }
+        const float m_new = fmaxf(m, mx * p.scale_log2);
+        // O holds nothing until the row has seen a key
+        const bool grow = live && l > 0.0f && m_new > m + kGrowth;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float a = grow ? ex2_approx(m - m_new) : 1.0f;
+          wait_warp(&o_full[h], (cnt - 1) & 1);
+          tc_fence_after_sync();
+#pragma unroll 1
+          for (int x = 0; x < 4; ++x) {
+            if (!ok) break;
+            float o[32];
+            uint32_t u[32];
+            tmem_ld32(tbase + col_o(h) + 32 * x, o);
+#pragma unroll
+            for (int y = 0; y < 32; ++y) u[y] = __float_as_uint(o[y] * a);
+            tmem_st32(tbase + col_o(h) + 32 * x, u);
+          }
+          l *= a;
+          if (grow) m = m_new;
+        }
+        if (!(l > 0.0f)) m = m_new;
+        uint32_t u[64];
+#pragma unroll
+        for (int x = 0; x < 64; ++x) {
+          const float p0 = ex2_approx(fmaf(__uint_as_float(s[2 * x]), p.scale_log2, -m));
+          const float p1 = ex2_approx(fmaf(__uint_as_float(s[2 * x + 1]), p.scale_log2, -m));
+          l += p0 + p1;
+          const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+          u[x] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        if (ok) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t w[32];
+#pragma unroll
+            for (int y = 0; y < 32; ++y) w[y] = u[32 * x + y];
+            tmem_st32(tbase + col_s(h) + 32 * x, w);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before_sync();
+        mbar_arrive(&p_full[h]);
+      }
+      // the piece's output
+      wait_warp(&o_full[h], (cnt - 1) & 1);
+      tc_fence_after_sync();
+      const bool some = l > 0.0f;
+      if (c.slot < 0) {
+        const float inv = some ? 1.0f / l : 0.0f;
+        uint4* o = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(c.k.tok0 + tok) * p.h_q + c.j * p.G + g) * kD);
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {
+          float v[32];
+          if (ok) {
+            tmem_ld32(tbase + col_o(h) + 32 * x, v);
+          } else {
+#pragma unroll
+            for (int y = 0; y < 32; ++y) v[y] = 0.0f;
+          }
+          if (live) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float a = some ? v[8 * y + 2 * e] * inv : 0.0f;
+                const float b = some ? v[8 * y + 2 * e + 1] * inv : 0.0f;
+                const __nv_bfloat162 ab = __floats2bfloat162_rn(a, b);
+                w[e] = *reinterpret_cast<const uint32_t*>(&ab);
+              }
+              o[4 * x + y] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      } else {
+        const int row = h * kHalf + r;
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {
+          float v[32];
+          if (ok) {
+            tmem_ld32(tbase + col_o(h) + 32 * x, v);
+          } else {
+#pragma unroll
+            for (int y = 0; y < 32; ++y) v[y] = 0.0f;
+          }
+          if (live) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              float4 f = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+              if (!some) f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              *reinterpret_cast<float4*>(p.pieces_o + piece_at(c.slot, row, 32 * x + 4 * y)) = f;
+            }
+          }
+        }
+        if (live) {
+          p.pieces_m[c.slot * kRowTile + row] = some ? m : -FLT_MAX;
+          p.pieces_l[c.slot * kRowTile + row] = l;
+        }
+      }
+      tc_fence_before_sync();
+      mbar_arrive(&o_free[h]);
     }
-  } else {
-    uint16_t* out = p.out + (static_cast<int64_t>(n) * p.h_q + hq) * 128 + 4 * lane;
-    for (int x = 0; x < 4; ++x) {
-      const __nv_bfloat16 b = __float2bfloat16_rn(l > 0.0f ? o[x] / l : 0.0f);
-      out[x] = *reinterpret_cast<const uint16_t*>(&b);
-    }
   }
+
+  // ---- teardown: every role has finished; warp 1 releases TMEM
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+// ---------------------------------------------------------------- joining cut segments
+constexpr int kMergeThreads = 256;
+constexpr int kMergeParts = 16;  // CTAs per segment
+
+// CTA (c, part) joins rows part * 16 .. + 15 of the segment that begins in CTA c's range and ends past it.
+__global__ void __launch_bounds__(kMergeThreads) rows_merge_kernel(const Params p, int ctas) {
+  pdl_wait_predecessor();
+  pdl_allow_successor();
+  const Share s(p.h_kv * p.pre[p.B], ctas);
+  const int c = blockIdx.x;
+  if (c >= s.nc - 1) return;
+  const int x = s.start(c + 1) - 1;  // the range's last tile
+  int lo = 0, hi = p.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.h_kv * p.pre[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  const int first = p.pre[lo];
+  const int tiles = p.pre[lo + 1] - first;
+  const int off = x - p.h_kv * first;
+  const int j = off / tiles;
+  const int rem = off - j * tiles;
+  const int base = p.base[lo];
+  const int i = base + last_at_most(p.cum + base, p.base[lo + 1] - base, first + rem);
+  const int seg0 = x - (first + rem - p.cum[i]);
+  const int seg1 = seg0 + p.cum[i + 1] - p.cum[i];
+  if (seg1 <= x + 1 || seg0 < s.start(c)) return;
+  const Block k = block_of(p, lo, i - base);
+  const int c_last = s.cta_of(seg1 - 1);
+  const int lane = threadIdx.x & 31;
+  for (int row = blockIdx.y * (kRowTile / kMergeParts) + (threadIdx.x >> 5); row < static_cast<int>(blockIdx.y + 1) * (kRowTile / kMergeParts);
+       row += kMergeThreads / 32) {
+    const int hf = row / kHalf;
+    const int r = row - hf * kHalf;
+    const int ti = r / p.G;
+    const int tok = hf * p.half_tokens + ti;
+    if (ti >= p.half_tokens || tok >= k.ntok) continue;
+    float M = -FLT_MAX, L = 0.0f;
+    float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int cc = c; cc <= c_last; ++cc) {
+      const int64_t slot = 2 * static_cast<int64_t>(cc) + (s.start(cc) >= seg0 ? 0 : 1);
+      const float mc = p.pieces_m[slot * kRowTile + row];
+      const float lc = p.pieces_l[slot * kRowTile + row];
+      const float4 oc = *reinterpret_cast<const float4*>(p.pieces_o + piece_at(slot, row, 4 * lane));
+      const float mn = fmaxf(M, mc);
+      const float a = exp2f(M - mn), b = exp2f(mc - mn);
+      O.x = O.x * a + oc.x * b;
+      O.y = O.y * a + oc.y * b;
+      O.z = O.z * a + oc.z * b;
+      O.w = O.w * a + oc.w * b;
+      L = L * a + lc * b;
+      M = mn;
+    }
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const __nv_bfloat162 x0 = __floats2bfloat162_rn(O.x * inv, O.y * inv);
+    const __nv_bfloat162 x1 = __floats2bfloat162_rn(O.z * inv, O.w * inv);
+    uint16_t* o = p.out + (static_cast<int64_t>(k.tok0 + tok) * p.h_q + j * p.G + (r - ti * p.G)) * kD + 4 * lane;
+    *reinterpret_cast<uint2*>(o) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&x0), *reinterpret_cast<const uint32_t*>(&x1));
+  }
+}
+
+// ---------------------------------------------------------------- host
+bool encode(CUtensorMap* map, const uint16_t* base, uint64_t d1, uint64_t d2, uint32_t b1, uint32_t b2) {
+  const cuuint64_t dims[3] = {kD, d1, d2};
+  const cuuint64_t strides[2] = {kD * 2, d1 * kD * 2};
+  const cuuint32_t box[3] = {64, b1, b2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  TensorMapEncodeFn enc = tensor_map_encoder();
+  return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace rows
 
 cudaError_t launch_gqa_rows(const GqaRowsPlan& plan, cudaStream_t stream) {
-  const int64_t warps =
-      static_cast<int64_t>(plan.N) * plan.h_q * (plan.prefix_table ? plan.prefix_splits : 1);
-  const int64_t grid = (warps * 32 + rows::kThreads - 1) / rows::kThreads;
-  return launch_pdl(rows::gqa_rows_kernel, dim3(static_cast<unsigned>(grid)), dim3(rows::kThreads), 0, stream, plan);
+  using namespace rows;
+  const int G = plan.h_q / plan.h_kv;
+  const int page = 1 << plan.paged.page_shift;
+  const int box_rows = page < kKeys ? page : kKeys;
+  const bool prefix = plan.prefix_table != nullptr;
+  Params p{};
+  p.half_tokens = kHalf / G;
+  CUtensorMap tk, tv, tq;
+  if (!encode(&tk, plan.k_cache, page, static_cast<uint64_t>(plan.paged.num_pages) * plan.h_kv, box_rows, 1) ||
+      !encode(&tv, plan.v_cache, page, static_cast<uint64_t>(plan.paged.num_pages) * plan.h_kv, box_rows, 1) ||
+      !encode(&tq, plan.q, plan.h_q, plan.N, G, p.half_tokens))
+    return cudaErrorInvalidValue;
+  const int64_t pieces = prefix ? static_cast<int64_t>(plan.h_kv) * plan.prefix_blocks * plan.prefix_splits
+                                : 2 * static_cast<int64_t>(kRowsCtas);
+  p.cu_q = plan.cu_q;
+  p.seq_lens = plan.seq_lens;
+  p.kv = plan.paged;
+  p.out = plan.out;
+  p.pieces_o = plan.pieces;
+  p.pieces_m = plan.pieces + pieces * kRowTile * kD;
+  p.pieces_l = p.pieces_m + pieces * kRowTile;
+  p.status = plan.status;
+  p.pre = plan.tables;
+  p.base = p.pre + plan.B + 1;
+  p.cum = p.base + plan.B + 1;
+  p.prefix_table = plan.prefix_table;
+  p.prefix_len = plan.prefix_len;
+  p.prefix_splits = plan.prefix_splits;
+  p.prefix_blocks = plan.prefix_blocks;
+  p.N = plan.N;
+  p.B = plan.B;
+  p.h_q = plan.h_q;
+  p.h_kv = plan.h_kv;
+  p.G = G;
+  p.max_blocks = plan.N / (2 * p.half_tokens) + plan.B;
+  p.L_cap = plan.paged.max_pages * page;
+  // a scale of 0 makes all scores equal; the mask's infinities need a factor other than 0
+  p.scale_log2 = plan.scale_log2 == 0.0f ? 1e-30f : plan.scale_log2;
+
+  constexpr int kMaxDev = 64;  // the shared-memory opt-in is per device: done once on each
+  static std::atomic<bool> done[kMaxDev];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kMaxDev || !done[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(gqa_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDev) done[dev].store(true, std::memory_order_release);
+  }
+  const int ctas = plan.num_sms;
+  if (prefix) {
+    p.kv.window = 0;
+    p.kv.n_sink = 0;
+    const int grid = pieces < ctas ? static_cast<int>(pieces) : ctas;
+    return launch_pdl(gqa_rows_kernel, dim3(grid), dim3(kThreads), kSmem, stream, tk, tv, tq, p);
+  }
+  e = launch_pdl(rows_tables_kernel, dim3(1), dim3(kTableThreads), 0, stream, p);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(gqa_rows_kernel, dim3(ctas), dim3(kThreads), kSmem, stream, tk, tv, tq, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(rows_merge_kernel, dim3(ctas, kMergeParts), dim3(kMergeThreads), 0, stream, p, ctas);
 }
 
 }  // namespace moe
