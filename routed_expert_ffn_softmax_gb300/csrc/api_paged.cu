@@ -92,7 +92,7 @@ moe_status_t check_attention(const Attention& a) {
   if (!std::isfinite(a.scale) || a.window < 0 || a.n_sink < 0) return MOE_ERR_INVALID_ARG;
   // key tiles are counted in 32 bits, over all key/value heads and row blocks
   const int per_block = 2 * half_tokens(a.h_q / a.h_kv);
-  const int64_t tiles = (static_cast<int64_t>(a.max_pages) * a.page_size + 127) / 128;
+  const int64_t tiles = (static_cast<int64_t>(a.max_pages) * a.page_size + 127) / 128 + 8;
   const int64_t blocks = a.N / per_block + a.B;
   if (static_cast<double>(tiles) * a.h_kv * blocks > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (a.B == 0 || a.N == 0) return MOE_OK;
@@ -316,7 +316,7 @@ moe_status_t moe_gqa_prefix_decode(const uint16_t* q, const int32_t* prefix_tabl
     own.prefix.o = plan.pieces;
     own.prefix.m = plan.pieces + pieces * moe::kRowTile * 128;
     own.prefix.l = own.prefix.m + pieces * moe::kRowTile;
-    own.prefix.splits = L.prefix_splits;
+    own.prefix.stride = L.prefix_splits;
     own.prefix.blocks = L.prefix_blocks;
     own.prefix.half_seqs = half_tokens(h_q / h_kv);
   }

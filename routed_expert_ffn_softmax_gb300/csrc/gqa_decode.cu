@@ -120,8 +120,8 @@ __device__ __forceinline__ int seq_tiles(int len, int L_cap) {
   return (len <= 0 || len > L_cap) ? 0 : (len + kKeys - 1) / kKeys;
 }
 
-// Adds the shared prefix's pieces, in key order, to the running (M, L, O) of group j's heads for sequence b;
-// this thread holds dimension r.
+// Adds the shared prefix's part to the running (M, L, O) of group j's heads for sequence b; this thread holds
+// dimension r.
 template <int kGP>
 __device__ __forceinline__ void add_prefix(const Params& p, int b, int j, int r, float (&M)[kGP], float (&L)[kGP],
                                            float (&O)[kGP]) {
@@ -130,27 +130,23 @@ __device__ __forceinline__ void add_prefix(const Params& p, int b, int j, int r,
   const int i = b - block * 2 * x.half_seqs;
   const int half = i >= x.half_seqs ? 1 : 0;
   const int row = half * (kRowTile / 2) + (i - half * x.half_seqs) * p.G;
-  const int64_t piece0 = (static_cast<int64_t>(j) * x.blocks + block) * x.splits;
-  for (int s = 0; s < x.splits; ++s) {
-    const int64_t piece = piece0 + s;
-    const int64_t at = piece * kRowTile + row;
-    float mc[kGP], lc[kGP], oc[kGP];
+  const int64_t piece = (static_cast<int64_t>(j) * x.blocks + block) * x.stride;
+  float mc[kGP], lc[kGP], oc[kGP];
 #pragma unroll
-    for (int h = 0; h < kGP; ++h) {
-      const bool in = h < p.G;
-      mc[h] = in ? __ldcg(x.m + at + h) : -FLT_MAX;
-      lc[h] = in ? __ldcg(x.l + at + h) : 0.0f;
-      oc[h] = in ? __ldcg(x.o + piece_at(piece, row + h, r)) : 0.0f;
-    }
+  for (int h = 0; h < kGP; ++h) {
+    const bool in = h < p.G;
+    mc[h] = in ? __ldcg(x.m + piece * kRowTile + row + h) : -FLT_MAX;
+    lc[h] = in ? __ldcg(x.l + piece * kRowTile + row + h) : 0.0f;
+    oc[h] = in ? __ldcg(x.o + piece_at(piece, row + h, r)) : 0.0f;
+  }
 #pragma unroll
-    for (int h = 0; h < kGP; ++h) {
-      const float m_new = fmaxf(M[h], mc[h]);
-      const float a_old = exp2f(M[h] - m_new);
-      const float a_c = exp2f(mc[h] - m_new);
-      O[h] = O[h] * a_old + oc[h] * a_c;
-      L[h] = L[h] * a_old + lc[h] * a_c;
-      M[h] = m_new;
-    }
+  for (int h = 0; h < kGP; ++h) {
+    const float m_new = fmaxf(M[h], mc[h]);
+    const float a_old = exp2f(M[h] - m_new);
+    const float a_c = exp2f(mc[h] - m_new);
+    O[h] = O[h] * a_old + oc[h] * a_c;
+    L[h] = L[h] * a_old + lc[h] * a_c;
+    M[h] = m_new;
   }
 }
 

@@ -9,7 +9,9 @@
 // 4 * 128 * 128 * 128 flops per half and tile: long prompts are bound by the tensor pipe, few rows behind long
 // contexts by HBM. The halves alternate, so the softmax of one runs under the products of the other.
 //
-// Softmax: a thread owns a row (TMEM lane), so its maximum and sum need no exchange. O stays in TMEM; it is rescaled
+// Softmax: two threads share a row (TMEM lane), 64 keys each, and exchange its maximum through shared memory. (One
+// thread per row holds 128 scores, and its chain of loads, maxima, exponentials and stores took 2000 cycles a tile, twice
+// what the other half's products cover.) O stays in TMEM; it is rescaled
 // only when a row's maximum has grown by more than 2^8 since the reference in use (probabilities are then at most
 // 2^8, exact to the same relative bf16 step, and sums stay far inside fp32), which after the first tiles is rare.
 //
@@ -17,11 +19,11 @@
 // lengths, windows bound them) and each CTA takes a contiguous range of it, so any mix of prompts balances to within
 // a tile. Which range holds what comes from a small table kernel, since lengths are only known on the device. A
 // segment cut between CTAs leaves (o, m, l) pieces that a third kernel joins in CTA order, one warp per row. For a
-// shared prefix the host knows the sizes: equal splits per segment, whose pieces the decode kernel joins with the
-// sequences' own keys.
+// shared prefix the host knows the sizes: equal splits per segment, joined the same way; the decode kernel adds the
+// result to the sequences' own keys.
 //
-// Per CTA, 12 warps: 0 TMA producer (Q per piece; K and V tiles alternate in a ring of 5 x 32 KB), 1 issues the
-// MMAs, 2 and 3 write zeros for blocks that see nothing, 4-7 and 8-11 the softmax and output of the two halves.
+// Per CTA, 20 warps: 0 TMA producer (Q per piece; K and V tiles alternate in a ring of 5 x 32 KB), 1 issues the
+// MMAs, 2 and 3 write zeros for blocks that see nothing, 4-11 and 12-19 the softmax and output of the two halves.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -44,12 +46,20 @@ constexpr int kHalf = 128;                  // rows of a half
 constexpr int kStages = 5;
 constexpr int kBox = kKeys * 64 * 2;        // 128 rows x 64 dims
 constexpr int kTile = 2 * kBox;             // one K or V tile, or the queries of a half: 32 KB
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
+constexpr int kSoft = 256;                  // softmax threads of a half: two per row, 64 columns each
 constexpr int kOffQ = 0;
 constexpr int kOffRing = 2 * kTile;
 constexpr int kOffBar = kOffRing + kStages * kTile;
 constexpr int kNumBars = 2 * kStages + 2 + 2 * 4 + 1;
-constexpr int kSmem = kOffBar + 256;
+constexpr int kOffRed = kOffBar + 256;      // row maxima and sums, [2 halves][2 parts][128 rows]
+constexpr int kSmem = kOffRed + 2 * 2 * kHalf * 4;
+// Registers per thread: at launch, and after the warpgroups have shared them out (128 threads that load and issue,
+// 512 softmax threads that hold half a row of scores each).
+constexpr int kRegsLaunch = 96;
+constexpr int kRegsIo = 64;
+constexpr int kRegsSoftmax = 104;
+static_assert(128 * kRegsIo + 512 * kRegsSoftmax <= kThreads * kRegsLaunch, "a larger share would wait forever");
 static_assert(kNumBars * 8 + 8 <= 256, "barrier area");
 static_assert(kSmem <= 232448, "dynamic shared memory per CTA");
 static_assert(kRowTile == 2 * kHalf, "partials hold both halves");
@@ -58,6 +68,10 @@ static_assert(kRowTile == 2 * kHalf, "partials hold both halves");
 constexpr int kTmemCols = 512;
 __device__ constexpr uint32_t col_s(int h) { return 128u * h; }
 __device__ constexpr uint32_t col_o(int h) { return 256u + 128u * h; }
+
+// What a segment costs beside its tiles (its queries' load, the first scores and the output, which no product
+// overlaps), in tiles: the CTAs' shares are cut so that those with many short segments get fewer tiles.
+constexpr int kSegCost = 2;
 
 constexpr float kGrowth = 8.0f;  // log2 of how far a row's maximum may outgrow its reference
 
@@ -70,9 +84,10 @@ struct Params {
   float* pieces_m;           // [pieces][kRowTile]
   float* pieces_l;
   int32_t* status;
-  int32_t* pre;              // [B + 1] tiles of the sequences before, for one key/value head
+  // work is counted in units: a block's tiles and kSegCost more (none for a block that sees nothing)
+  int32_t* pre;              // [B + 1] units of the sequences before, for one key/value head
   int32_t* base;             // [B + 1] row blocks of the sequences before
-  int32_t* cum;              // [blocks + 1] tiles of the blocks before
+  int32_t* cum;              // [blocks + 1] units of the blocks before
   const int32_t* prefix_table;
   int prefix_len, prefix_splits, prefix_blocks;
   int N, B, h_q, h_kv, G, half_tokens, max_blocks, L_cap;
@@ -145,7 +160,7 @@ __device__ __forceinline__ int last_at_most(const int32_t* a, int n, int x) {  /
   return lo;
 }
 
-// Row blocks and key tiles before each sequence and each block.
+// Row blocks and work units before each sequence and each block.
 __global__ void __launch_bounds__(kTableThreads) rows_tables_kernel(const Params p) {
   __shared__ int sums[32];
   __shared__ int base[kGqaMaxSeqs + 1];
@@ -188,6 +203,7 @@ __global__ void __launch_bounds__(kTableThreads) rows_tables_kernel(const Params
     if (i < blocks) {
       b = last_at_most(base, p.B, i);
       nt = block_of(p, b, i - base[b]).sp.nt;
+      if (nt > 0) nt += kSegCost;
     }
     const int t = carry + scan_block(nt, sums);
     if (i < blocks) {
@@ -204,8 +220,8 @@ __global__ void __launch_bounds__(kTableThreads) rows_tables_kernel(const Params
   for (int b = tid; b <= p.B && base[b] == 0; b += kTableThreads) p.pre[b] = 0;
 }
 
-// ---------------------------------------------------------------- the list of tiles, and a CTA's pieces of it
-struct Share {  // CTA c's tiles: the first rm CTAs take q + 1, the others q; CTAs past nc take none
+// ---------------------------------------------------------------- the list of units, and a CTA's pieces of it
+struct Share {  // CTA c's units: the first rm CTAs take q + 1, the others q; CTAs past nc take none
   int total, nc, q, rm;
   __device__ __forceinline__ explicit Share(int t, int ctas) {
     total = t;
@@ -240,7 +256,7 @@ class Walk {
     x_ = s.start(blockIdx.x);
     end_ = s.start(blockIdx.x + 1);
     if (x_ >= end_) return;
-    // the last sequence whose first tile is at most x (empty ones before it are skipped by the search)
+    // the last sequence whose first unit is at most x (empty ones before it are skipped by the search)
     int lo = 0, hi = p.B - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -257,16 +273,16 @@ class Walk {
     t_ = first + rem - p.cum[i_];
   }
   __device__ __forceinline__ bool next(Piece& c) {
-    if (x_ >= end_) return false;
     if (p_.prefix_table) {
+      if (x_ >= end_) return false;
       const int s = x_ % p_.prefix_splits;
       const int seg = x_ / p_.prefix_splits;
       const int per = 2 * p_.half_tokens;
       c.j = seg / p_.prefix_blocks;
-      c.k.tok0 = (seg - c.j * p_.prefix_blocks) * per;
-      c.k.ntok = min(per, p_.B - c.k.tok0);
       c.k.seq = 0;
       c.k.pos0 = 0;
+      c.k.tok0 = (seg - c.j * p_.prefix_blocks) * per;
+      c.k.ntok = min(per, p_.B - c.k.tok0);
       c.k.sp = span_of_range(p_.prefix_len, 0, 0);
       c.t0 = static_cast<int>(static_cast<int64_t>(s) * c.k.sp.nt / p_.prefix_splits);
       c.n = static_cast<int>(static_cast<int64_t>(s + 1) * c.k.sp.nt / p_.prefix_splits) - c.t0;
@@ -274,36 +290,40 @@ class Walk {
       x_ += gridDim.x;
       return true;
     }
-    c.j = j_;
-    c.k = block_of(p_, b_, i_ - p_.base[b_]);
-    c.t0 = t_;
-    c.n = min(end_ - x_, c.k.sp.nt - t_);
-    const bool whole = c.n == c.k.sp.nt;
-    c.slot = whole ? -1 : 2 * static_cast<int64_t>(blockIdx.x) + (first_ ? 0 : 1);
-    first_ = false;
-    x_ += c.n;
-    t_ = 0;
-    if (x_ < end_) {  // the next block with tiles: of this head, of the next head, of the next sequence
-      ++i_;
-      for (;;) {
-        const int stop = p_.base[b_ + 1];
-        while (i_ < stop && p_.cum[i_ + 1] == p_.cum[i_]) ++i_;
-        if (i_ < stop) break;
-        if (++j_ >= p_.h_kv) {
-          j_ = 0;
-          do ++b_;
-          while (p_.pre[b_ + 1] == p_.pre[b_]);
+    while (x_ < end_) {
+      c.j = j_;
+      c.k = block_of(p_, b_, i_ - p_.base[b_]);
+      const int units = min(end_ - x_, c.k.sp.nt + kSegCost - t_);
+      c.t0 = max(0, t_ - kSegCost);
+      c.n = t_ + units - kSegCost - c.t0;
+      // a cut piece that goes on from an earlier CTA's (at most one per CTA), and one that others go on from
+      c.slot = c.n == c.k.sp.nt ? -1 : 2 * static_cast<int64_t>(blockIdx.x) + (c.t0 > 0 ? 0 : 1);
+      x_ += units;
+      t_ = 0;
+      if (x_ < end_) {  // the next block with tiles: of this head, of the next head, of the next sequence
+        ++i_;
+        for (;;) {
+          const int stop = p_.base[b_ + 1];
+          while (i_ < stop && p_.cum[i_ + 1] == p_.cum[i_]) ++i_;
+          if (i_ < stop) break;
+          if (++j_ >= p_.h_kv) {
+            j_ = 0;
+            do ++b_;
+            while (p_.pre[b_ + 1] == p_.pre[b_]);
+          }
+          i_ = p_.base[b_];
         }
-        i_ = p_.base[b_];
       }
+      if (c.n > 0) return true;
     }
-    return true;
+    return false;
   }
 
  private:
   const Params& p_;
-  int x_ = 0, end_ = 0, b_ = 0, j_ = 0, i_ = 0, t_ = 0;
-  bool first_ = true;
+  int x_ = 0, end_ = 0;           // units done before, and where the CTA's share ends
+  int b_ = 0, j_ = 0, i_ = 0;     // sequence, head, row block
+  int t_ = 0;                     // unit within the block
 };
 
 // ---------------------------------------------------------------- the attention kernel
@@ -340,9 +360,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_empty, 1);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&s_full[h], 1);
-      mbar_init(&p_full[h], kHalf);
+      mbar_init(&p_full[h], kSoft);
       mbar_init(&o_full[h], 1);
-      mbar_init(&o_free[h], kHalf);
+      mbar_init(&o_free[h], kSoft);
     }
     mbar_init(mma_done, 1);
     fence_mbar_init();
@@ -360,6 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk walk(p);
   Piece c;
 
+  if (warp < 4) {
+  reg_dealloc<kRegsIo>();
   if (warp == 0) {
     // =========================== TMA producer ===========================
     // A tile is 128 / page_size pages (one part of a page from 128 up): lane (page, dimension half) of the lower half
@@ -458,11 +480,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (first) wait(&o_free[h], (seg[h]++ & 1) ^ 1);
         if (ok) {
           tc_fence_after_sync();
-          const uint32_t v = sbase + kOffRing + st * kTile;
+          const uint64_t v = umma_desc_sw128_mn(sbase + kOffRing + st * kTile, kBox);
 #pragma unroll
-          for (int s = 0; s < kKeys / 16; ++s)
-            umma_bf16_tmem_a(tmem + col_o(h), tmem + col_s(h) + 8 * s, umma_desc_sw128_mn(v + s * 2048, kBox), idesc_o,
-                             !(first && s == 0));
+          for (int s = 0; s < kKeys / 16; ++s)  // a descriptor's address field counts 16 bytes
+            umma_bf16_tmem_a(tmem + col_o(h), tmem + col_s(h) + 8 * s, v + s * (2048 >> 4), idesc_o, !(first && s == 0));
         }
         umma_commit(&o_full[h]);
         ++pv[h];
@@ -481,12 +502,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t > 0) issue_o(h, it - 1, t == 1);
             if (ok) {
               tc_fence_after_sync();
-              const uint32_t k = sbase + kOffRing + st * kTile;
-              const uint32_t q = sbase + kOffQ + h * kTile;
+              const uint64_t k = umma_desc_sw128(sbase + kOffRing + st * kTile);
+              const uint64_t q = umma_desc_sw128(sbase + kOffQ + h * kTile);
 #pragma unroll
-              for (int s = 0; s < kD / 16; ++s)
-                umma_bf16(tmem + col_s(h), umma_desc_sw128(q + (s >> 2) * kBox + (s & 3) * 32),
-                          umma_desc_sw128(k + (s >> 2) * kBox + (s & 3) * 32), idesc_s, s > 0);
+              for (int s = 0; s < kD / 16; ++s) {
+                const uint64_t off = static_cast<uint64_t>(((s >> 2) * kBox + (s & 3) * 32) >> 4);
+                umma_bf16(tmem + col_s(h), q + off, k + off, idesc_s, s > 0);
+              }
             }
             umma_commit(&s_full[h]);
           }
@@ -502,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait(mma_done, 0)) atomicExch(p.status, kStatusDrainTimeout);
     }
     __syncwarp();
-  } else if (warp < 4) {
+  } else {
     // =========================== blocks that see nothing ===========================
     if (!p.prefix_table) {
       const int blocks = p.base[p.B];
@@ -515,15 +537,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int64_t e = tid - 64; e < n; e += 64) o[e] = make_uint4(0u, 0u, 0u, 0u);
       }
     }
+  }
   } else {
-    // =========================== softmax and output of half h ===========================
-    const int h = (warp - 4) >> 2;
+    reg_alloc<kRegsSoftmax>();
+    // =========================== softmax and output of half h, columns 64 part .. + 63 ===========================
+    const int h = (warp - 4) >> 3;
+    const int part = ((warp - 4) >> 2) & 1;
     const int r = (warp & 3) * 32 + lane;  // row of the half
     const uint32_t tbase = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    float* red = reinterpret_cast<float*>(smem + kOffRed) + h * 2 * kHalf;
+    const int pair_bar = 1 + h * 4 + (warp & 3);  // the two warps that share these rows
+    auto exchange = [&](float mine) {             // the other thread's value of this row
+      red[part * kHalf + r] = mine;
+      tc_fence_before_sync();
+      named_bar_sync(pair_bar, 64);
+      tc_fence_after_sync();
+      return red[(part ^ 1) * kHalf + r];
+    };
     const int i = r / p.G;                  // token of the half
     const int g = r - i * p.G;
     const bool neg = p.scale_log2 < 0.0f;
     const float hidden = neg ? INFINITY : -INFINITY;
+    const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
     bool ok = true;
     auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
       const bool w = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity));
@@ -549,23 +584,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int last = min(c.k.ntok, (h + 1) * p.half_tokens) - 1;
       const int end_min = p.prefix_table ? p.prefix_len : c.k.pos0 + h * p.half_tokens + 1;
       const int lo_max = p.prefix_table ? 0 : window_start(c.k.pos0 + last, p.kv.window);
-      float m = -FLT_MAX, l = 0.0f;
+      float m = -FLT_MAX, l = 0.0f;  // the row's reference, this thread's share of its sum
       for (int t = c.t0; t < c.t0 + c.n; ++t, ++it, ++cnt) {
         const int kb = c.k.sp.key_tile(t) * kKeys;
         wait_warp(&s_full[h], cnt & 1);
         tc_fence_after_sync();
-        uint32_t s[128];
+        uint32_t s[64];
         if (ok) {
-          tmem_ld128(tbase + col_s(h), s);
+          tmem_ld64(tbase + col_s(h) + 64 * part, s);
         } else {
 #pragma unroll
-          for (int x = 0; x < 128; ++x) s[x] = 0u;
+          for (int x = 0; x < 64; ++x) s[x] = 0u;
         }
         const bool plain = kb + kKeys <= end_min && (kb >= lo_max || kb + kKeys <= p.kv.n_sink);
         if (!plain) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int cb = kb + 32 * w;
+          for (int w = 0; w < 2; ++w) {
+            const int cb = kb + 64 * part + 32 * w;
             const uint32_t see = bits_below(end, cb) & (~bits_below(lo, cb) | bits_below(p.kv.n_sink, cb));
 #pragma unroll
             for (int x = 0; x < 32; ++x)
@@ -577,125 +612,126 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int idx = 2 * it + 1;
             const int st = idx % kStages;
             if (mbar_wait(&full[st], static_cast<uint32_t>((idx / kStages) & 1))) {
-              uint4* v0 = reinterpret_cast<uint4*>(smem + kOffRing + st * kTile + r * 128);
-              uint4* v1 = reinterpret_cast<uint4*>(smem + kOffRing + st * kTile + kBox + r * 128);
+              uint4* v = reinterpret_cast<uint4*>(smem + kOffRing + st * kTile + part * kBox + r * 128);
 #pragma unroll
-              for (int x = 0; x < 8; ++x) v0[x] = v1[x] = make_uint4(0u, 0u, 0u, 0u);
+              for (int x = 0; x < 8; ++x) v[x] = make_uint4(0u, 0u, 0u, 0u);
             } else {
               atomicExch(p.status, kStatusWaitFullTimeout);
             }
             fence_proxy_async_smem();
           }
         }
-        float mx = hidden;
+        // four chains, so that their latency overlaps
+        float mx[4] = {hidden, hidden, hidden, hidden};
         if (neg) {
 #pragma unroll
-          for (int x = 0; x < 128; ++x) mx = fminf(mx, __uint_as_float(s[x]));
+          for (int x = 0; x < 64; x += 2)
+            mx[(x >> 1) & 3] = min3_f32(mx[(x >> 1) & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+          mx[0] = fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3]));
         } else {
 #pragma unroll
-          for (int x = 0; x < 128; ++x) mx = fmaxf(mx, __uint_as_float(s[x]));
+          for (int x = 0; x < 64; x += 2)
+            mx[(x >> 1) & 3] = max3_f32(mx[(x >> 1) & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+          mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         }
-        const float m_new = fmaxf(m, mx * p.scale_log2);
+        const float mine = mx[0] * p.scale_log2;
+        const float m_new = max3_f32(m, mine, exchange(mine));
         // O holds nothing until the row has seen a key
-        const bool grow = live && l > 0.0f && m_new > m + kGrowth;
+        const bool seen = m > -FLT_MAX;
+        const bool grow = live && seen && m_new > m + kGrowth;
         if (__any_sync(0xffffffffu, grow)) {
           const float a = grow ? ex2_approx(m - m_new) : 1.0f;
           wait_warp(&o_full[h], (cnt - 1) & 1);
           tc_fence_after_sync();
 #pragma unroll 1
-          for (int x = 0; x < 4; ++x) {
+          for (int x = 0; x < 4; ++x) {  // this part's dimensions of O
             if (!ok) break;
-            float o[32];
-            uint32_t u[32];
-            tmem_ld32(tbase + col_o(h) + 32 * x, o);
+            float o[16];
+            uint32_t u[16];
+            tmem_ld16(tbase + col_o(h) + 64 * part + 16 * x, o);
 #pragma unroll
-            for (int y = 0; y < 32; ++y) u[y] = __float_as_uint(o[y] * a);
-            tmem_st32(tbase + col_o(h) + 32 * x, u);
+            for (int y = 0; y < 16; ++y) u[y] = __float_as_uint(o[y] * a);
+            tmem_st16(tbase + col_o(h) + 64 * part + 16 * x, u);
           }
           l *= a;
           if (grow) m = m_new;
         }
-        if (!(l > 0.0f)) m = m_new;
-        uint32_t u[64];
+        if (!seen) m = m_new;
+        const uint64_t minus_m = pack_f32x2(-m, -m);
+        uint64_t sum2[2] = {0u, 0u};
 #pragma unroll
-        for (int x = 0; x < 64; ++x) {
-          const float p0 = ex2_approx(fmaf(__uint_as_float(s[2 * x]), p.scale_log2, -m));
-          const float p1 = ex2_approx(fmaf(__uint_as_float(s[2 * x + 1]), p.scale_log2, -m));
-          l += p0 + p1;
-          const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
-          u[x] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        if (ok) {
+        for (int w = 0; w < 2; ++w) {
+          uint32_t u[16];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t w[32];
-#pragma unroll
-            for (int y = 0; y < 32; ++y) w[y] = u[32 * x + y];
-            tmem_st32(tbase + col_s(h) + 32 * x, w);
+          for (int x = 0; x < 16; ++x) {
+            const int y = 32 * w + 2 * x;
+            float p0, p1;
+            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[y]), __uint_as_float(s[y + 1])), scale2, minus_m), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            sum2[x & 1] = add_f32x2(sum2[x & 1], pack_f32x2(p0, p1));
+            const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+            u[x] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          tmem_wait_st();
+          // the probabilities overwrite the first 64 score columns: both parts have read theirs (the exchange)
+          if (ok) tmem_st16(tbase + col_s(h) + 32 * part + 16 * w, u);
         }
+        float s0, s1;
+        unpack_f32x2(add_f32x2(sum2[0], sum2[1]), s0, s1);
+        l += s0 + s1;
+        if (ok) tmem_wait_st();
         tc_fence_before_sync();
         mbar_arrive(&p_full[h]);
       }
-      // the piece's output
+      // the piece's output: this part's dimensions
+      named_bar_sync(pair_bar, 64);  // the maxima exchanged last have been read
+      l += exchange(l);
       wait_warp(&o_full[h], (cnt - 1) & 1);
       tc_fence_after_sync();
       const bool some = l > 0.0f;
-      if (c.slot < 0) {
-        const float inv = some ? 1.0f / l : 0.0f;
-        uint4* o = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(c.k.tok0 + tok) * p.h_q + c.j * p.G + g) * kD);
+      const int row = h * kHalf + r;
+      const float inv = some ? 1.0f / l : 0.0f;
+      uint4* out = reinterpret_cast<uint4*>(
+          p.out + (static_cast<int64_t>(c.k.tok0 + tok) * p.h_q + c.j * p.G + g) * kD + 64 * part);
 #pragma unroll 1
-        for (int x = 0; x < 4; ++x) {
-          float v[32];
-          if (ok) {
-            tmem_ld32(tbase + col_o(h) + 32 * x, v);
-          } else {
+      for (int x = 0; x < 4; ++x) {
+        float v[16];
+        if (ok) {
+          tmem_ld16(tbase + col_o(h) + 64 * part + 16 * x, v);
+        } else {
 #pragma unroll
-            for (int y = 0; y < 32; ++y) v[y] = 0.0f;
-          }
-          if (live) {
+          for (int y = 0; y < 16; ++y) v[y] = 0.0f;
+        }
+        if (!some) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              uint32_t w[4];
+          for (int y = 0; y < 16; ++y) v[y] = 0.0f;
+        }
+        if (!live) continue;
+        if (c.slot < 0) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float a = some ? v[8 * y + 2 * e] * inv : 0.0f;
-                const float b = some ? v[8 * y + 2 * e + 1] * inv : 0.0f;
-                const __nv_bfloat162 ab = __floats2bfloat162_rn(a, b);
-                w[e] = *reinterpret_cast<const uint32_t*>(&ab);
-              }
-              o[4 * x + y] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int y = 0; y < 2; ++y) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 ab = __floats2bfloat162_rn(v[8 * y + 2 * e] * inv, v[8 * y + 2 * e + 1] * inv);
+              w[e] = *reinterpret_cast<const uint32_t*>(&ab);
             }
+            out[2 * x + y] = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        }
-      } else {
-        const int row = h * kHalf + r;
-#pragma unroll 1
-        for (int x = 0; x < 4; ++x) {
-          float v[32];
-          if (ok) {
-            tmem_ld32(tbase + col_o(h) + 32 * x, v);
-          } else {
+        } else {
 #pragma unroll
-            for (int y = 0; y < 32; ++y) v[y] = 0.0f;
-          }
-          if (live) {
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              float4 f = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
-              if (!some) f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              *reinterpret_cast<float4*>(p.pieces_o + piece_at(c.slot, row, 32 * x + 4 * y)) = f;
-            }
-          }
+          for (int y = 0; y < 4; ++y)
+            *reinterpret_cast<float4*>(p.pieces_o + piece_at(c.slot, row, 64 * part + 16 * x + 4 * y)) =
+                make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
         }
-        if (live) {
-          p.pieces_m[c.slot * kRowTile + row] = some ? m : -FLT_MAX;
-          p.pieces_l[c.slot * kRowTile + row] = l;
-        }
+      }
+      if (live && c.slot >= 0 && part == 0) {
+        p.pieces_m[c.slot * kRowTile + row] = m;
+        p.pieces_l[c.slot * kRowTile + row] = l;
       }
       tc_fence_before_sync();
       mbar_arrive(&o_free[h]);
+      named_bar_sync(pair_bar, 64);  // the sums exchanged have been read
     }
   }
 
@@ -706,65 +742,105 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-// ---------------------------------------------------------------- joining cut segments
+// ---------------------------------------------------------------- joining pieces
 constexpr int kMergeThreads = 256;
-constexpr int kMergeParts = 16;  // CTAs per segment
+constexpr int kMergeParts = 16;  // CTAs per segment, 16 rows each
 
-// CTA (c, part) joins rows part * 16 .. + 15 of the segment that begins in CTA c's range and ends past it.
+// Joins a row's pieces in key order: the first, then n - 1 more from `next` on, `stride` apart. Lane: 4 dimensions.
+__device__ __forceinline__ void join_row(const Params& p, int row, int64_t first, int64_t next, int stride, int n,
+                                         float& M, float& L, float4& O) {
+  const int lane = threadIdx.x & 31;
+  M = -FLT_MAX;
+  L = 0.0f;
+  O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  constexpr int kChunk = 4;  // pieces whose loads are in flight together
+  for (int s0 = 0; s0 < n; s0 += kChunk) {
+    float mc[kChunk], lc[kChunk];
+    float4 oc[kChunk];
+#pragma unroll
+    for (int u = 0; u < kChunk; ++u) {
+      if (s0 + u >= n) continue;
+      const int64_t slot = s0 + u == 0 ? first : next + static_cast<int64_t>(s0 + u - 1) * stride;
+      mc[u] = p.pieces_m[slot * kRowTile + row];
+      lc[u] = p.pieces_l[slot * kRowTile + row];
+      oc[u] = *reinterpret_cast<const float4*>(p.pieces_o + piece_at(slot, row, 4 * lane));
+    }
+#pragma unroll
+    for (int u = 0; u < kChunk; ++u) {
+      if (s0 + u >= n) continue;
+      const float mn = fmaxf(M, mc[u]);
+      const float a = exp2f(M - mn), b = exp2f(mc[u] - mn);
+      O.x = O.x * a + oc[u].x * b;
+      O.y = O.y * a + oc[u].y * b;
+      O.z = O.z * a + oc[u].z * b;
+      O.w = O.w * a + oc[u].w * b;
+      L = L * a + lc[u] * b;
+      M = mn;
+    }
+  }
+}
+
+// CTA (c, part) joins its rows of the segment whose first tile is in CTA c's share and whose last is not.
 __global__ void __launch_bounds__(kMergeThreads) rows_merge_kernel(const Params p, int ctas) {
   pdl_wait_predecessor();
   pdl_allow_successor();
   const Share s(p.h_kv * p.pre[p.B], ctas);
   const int c = blockIdx.x;
   if (c >= s.nc - 1) return;
-  const int x = s.start(c + 1) - 1;  // the range's last tile
-  int lo = 0, hi = p.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.h_kv * p.pre[mid] <= x) lo = mid; else hi = mid - 1;
+  const int x = s.start(c + 1) - 1;  // the share's last unit
+  int b = 0, hi = p.B - 1;
+  while (b < hi) {
+    const int mid = (b + hi + 1) >> 1;
+    if (p.h_kv * p.pre[mid] <= x) b = mid; else hi = mid - 1;
   }
-  const int first = p.pre[lo];
-  const int tiles = p.pre[lo + 1] - first;
-  const int off = x - p.h_kv * first;
-  const int j = off / tiles;
-  const int rem = off - j * tiles;
-  const int base = p.base[lo];
-  const int i = base + last_at_most(p.cum + base, p.base[lo + 1] - base, first + rem);
-  const int seg0 = x - (first + rem - p.cum[i]);
-  const int seg1 = seg0 + p.cum[i + 1] - p.cum[i];
-  if (seg1 <= x + 1 || seg0 < s.start(c)) return;
-  const Block k = block_of(p, lo, i - base);
-  const int c_last = s.cta_of(seg1 - 1);
-  const int lane = threadIdx.x & 31;
-  for (int row = blockIdx.y * (kRowTile / kMergeParts) + (threadIdx.x >> 5); row < static_cast<int>(blockIdx.y + 1) * (kRowTile / kMergeParts);
-       row += kMergeThreads / 32) {
+  const int first = p.pre[b];
+  const int units = p.pre[b + 1] - first;
+  const int j = (x - p.h_kv * first) / units;
+  const int rem = x - p.h_kv * first - j * units;
+  const int base = p.base[b];
+  const int i = base + last_at_most(p.cum + base, p.base[b + 1] - base, first + rem);
+  const int tile0 = x - (first + rem - p.cum[i]) + kSegCost;  // the segment's first tile, as a unit of the list
+  const int tile1 = tile0 - kSegCost + p.cum[i + 1] - p.cum[i];
+  if (tile1 <= x + 1 || tile0 > x || tile0 < s.start(c)) return;
+  const int pieces = s.cta_of(tile1 - 1) - c + 1;
+  const Block k = block_of(p, b, i - base);
+  const int row0 = blockIdx.y * (kRowTile / kMergeParts);
+  for (int row = row0 + (threadIdx.x >> 5); row < row0 + kRowTile / kMergeParts; row += kMergeThreads / 32) {
     const int hf = row / kHalf;
-    const int r = row - hf * kHalf;
-    const int ti = r / p.G;
+    const int ti = (row - hf * kHalf) / p.G;
     const int tok = hf * p.half_tokens + ti;
     if (ti >= p.half_tokens || tok >= k.ntok) continue;
-    float M = -FLT_MAX, L = 0.0f;
-    float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int cc = c; cc <= c_last; ++cc) {
-      const int64_t slot = 2 * static_cast<int64_t>(cc) + (s.start(cc) >= seg0 ? 0 : 1);
-      const float mc = p.pieces_m[slot * kRowTile + row];
-      const float lc = p.pieces_l[slot * kRowTile + row];
-      const float4 oc = *reinterpret_cast<const float4*>(p.pieces_o + piece_at(slot, row, 4 * lane));
-      const float mn = fmaxf(M, mc);
-      const float a = exp2f(M - mn), b = exp2f(mc - mn);
-      O.x = O.x * a + oc.x * b;
-      O.y = O.y * a + oc.y * b;
-      O.z = O.z * a + oc.z * b;
-      O.w = O.w * a + oc.w * b;
-      L = L * a + lc * b;
-      M = mn;
-    }
+    float M, L;
+    float4 O;
+    join_row(p, row, 2 * static_cast<int64_t>(c) + 1, 2 * static_cast<int64_t>(c + 1), 2, pieces, M, L, O);
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
     const __nv_bfloat162 x0 = __floats2bfloat162_rn(O.x * inv, O.y * inv);
     const __nv_bfloat162 x1 = __floats2bfloat162_rn(O.z * inv, O.w * inv);
-    uint16_t* o = p.out + (static_cast<int64_t>(k.tok0 + tok) * p.h_q + j * p.G + (r - ti * p.G)) * kD + 4 * lane;
-    *reinterpret_cast<uint2*>(o) =
+    uint16_t* o = p.out + (static_cast<int64_t>(k.tok0 + tok) * p.h_q + j * p.G + (row - hf * kHalf - ti * p.G)) * kD;
+    reinterpret_cast<uint2*>(o)[threadIdx.x & 31] =
         make_uint2(*reinterpret_cast<const uint32_t*>(&x0), *reinterpret_cast<const uint32_t*>(&x1));
+  }
+}
+
+// Joins the splits of each segment of a shared prefix into its first piece.
+__global__ void __launch_bounds__(kMergeThreads) prefix_join_kernel(const Params p) {
+  pdl_wait_predecessor();
+  pdl_allow_successor();
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * p.prefix_splits;
+  const int tok0 = (blockIdx.x % p.prefix_blocks) * 2 * p.half_tokens;
+  const int row0 = blockIdx.y * (kRowTile / kMergeParts);
+  for (int row = row0 + (threadIdx.x >> 5); row < row0 + kRowTile / kMergeParts; row += kMergeThreads / 32) {
+    const int hf = row / kHalf;
+    const int ti = (row - hf * kHalf) / p.G;
+    if (ti >= p.half_tokens || tok0 + hf * p.half_tokens + ti >= p.B) continue;
+    float M, L;
+    float4 O;
+    join_row(p, row, first, first + 1, 1, p.prefix_splits, M, L, O);
+    *reinterpret_cast<float4*>(p.pieces_o + piece_at(first, row, 4 * (threadIdx.x & 31))) = O;
+    if ((threadIdx.x & 31) == 0) {
+      p.pieces_m[first * kRowTile + row] = M;
+      p.pieces_l[first * kRowTile + row] = L;
+    }
   }
 }
 
@@ -828,6 +904,10 @@ cudaError_t launch_gqa_rows(const GqaRowsPlan& plan, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= kMaxDev || !done[dev].load(std::memory_order_acquire)) {
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, gqa_rows_kernel);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the shares are counted from it
     e = cudaFuncSetAttribute(gqa_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     if (dev < kMaxDev) done[dev].store(true, std::memory_order_release);
@@ -837,7 +917,10 @@ cudaError_t launch_gqa_rows(const GqaRowsPlan& plan, cudaStream_t stream) {
     p.kv.window = 0;
     p.kv.n_sink = 0;
     const int grid = pieces < ctas ? static_cast<int>(pieces) : ctas;
-    return launch_pdl(gqa_rows_kernel, dim3(grid), dim3(kThreads), kSmem, stream, tk, tv, tq, p);
+    e = launch_pdl(gqa_rows_kernel, dim3(grid), dim3(kThreads), kSmem, stream, tk, tv, tq, p);
+    if (e != cudaSuccess || plan.prefix_splits == 1) return e;
+    return launch_pdl(prefix_join_kernel, dim3(static_cast<unsigned>(pieces / plan.prefix_splits), kMergeParts),
+                      dim3(kMergeThreads), 0, stream, p);
   }
   e = launch_pdl(rows_tables_kernel, dim3(1), dim3(kTableThreads), 0, stream, p);
   if (e != cudaSuccess) return e;

@@ -110,13 +110,13 @@ struct PagedKv {
   int num_pages, page_shift, max_pages;
   int window, n_sink;          // 0 = every key
 };
-// Partials of a shared prefix: pieces of every (key/value head, block of 2 * (128 / G) queries), in key order.
+// A shared prefix's part of the attention of every (key/value head, block of 2 * (128 / G) queries).
 constexpr int kRowTile = 256;  // query rows of a block: two 128-row halves
 struct PrefixPartials {
-  const float* o;           // [pieces][kRowTile][128], unnormalised; null: no prefix
+  const float* o;           // pieces (see piece_at), unnormalised; null: no prefix
   const float* m;           // [pieces][kRowTile] running maximum (base-2 units)
   const float* l;           // [pieces][kRowTile] softmax sum
-  int splits;               // pieces per (head, block)
+  int stride;               // pieces from one (head, block) to the next
   int blocks;               // blocks of queries
   int half_seqs;            // queries per 128-row half, 128 / G
 };
