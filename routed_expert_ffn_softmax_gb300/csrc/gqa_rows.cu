@@ -22,8 +22,8 @@
 // shared prefix the host knows the sizes: equal splits per segment, joined the same way; the decode kernel adds the
 // result to the sequences' own keys.
 //
-// Per CTA, 20 warps: 0 TMA producer (Q per piece; K and V tiles alternate in a ring of 5 x 32 KB), 1 issues the
-// MMAs, 2 and 3 write zeros for blocks that see nothing, 4-11 and 12-19 the softmax and output of the two halves.
+// Per CTA, 20 warps: 0 TMA producer (Q per piece; K and V tiles alternate in a ring of 5 x 32 KB), 1 and 2 issue
+// the MMAs of the two halves in turn, 3 announces the pieces and writes zeros for blocks that see nothing, 4-11 and 12-19 the softmax and output of the two halves.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -51,9 +51,11 @@ constexpr int kSoft = 256;                  // softmax threads of a half: two pe
 constexpr int kOffQ = 0;
 constexpr int kOffRing = 2 * kTile;
 constexpr int kOffBar = kOffRing + kStages * kTile;
-constexpr int kNumBars = 2 * kStages + 2 + 2 * 4 + 1;
+constexpr int kItems = 4;                   // pieces announced ahead
+constexpr int kNumBars = 2 * kStages + 2 + 2 * 4 + 1 + 2 * kItems;
 constexpr int kOffRed = kOffBar + 256;      // row maxima and sums, [2 halves][2 parts][128 rows]
-constexpr int kSmem = kOffRed + 2 * 2 * kHalf * 4;
+constexpr int kOffItem = kOffRed + 2 * 2 * kHalf * 4;
+constexpr int kSmem = kOffItem + kItems * 64;
 // Registers per thread: at launch, and after the warpgroups have shared them out (128 threads that load and issue,
 // 512 softmax threads that hold half a row of scores each).
 constexpr int kRegsLaunch = 96;
@@ -72,6 +74,10 @@ __device__ constexpr uint32_t col_o(int h) { return 256u + 128u * h; }
 // What a segment costs beside its tiles (its queries' load, the first scores and the output, which no product
 // overlaps), in tiles: the CTAs' shares are cut so that those with many short segments get fewer tiles.
 constexpr int kSegCost = 2;
+
+constexpr int kReaders = 3 + 2 * kSoft / 32;  // warps that read the announced pieces
+
+constexpr int kTurnBar = 10;  // named barriers: 1..8 the softmax warps' pairs, these two the issuers' turns
 
 constexpr float kGrowth = 8.0f;  // log2 of how far a row's maximum may outgrow its reference
 
@@ -236,14 +242,15 @@ struct Share {  // CTA c's units: the first rm CTAs take q + 1, the others q; CT
   }
 };
 
-struct Piece {
+struct alignas(64) Piece {
   int j;            // key/value head
-  int t0, n;        // tiles t0 .. t0 + n - 1 of the block's
-  int64_t slot;     // where a partial goes, -1: the piece is the whole segment
+  int t0, n;        // tiles t0 .. t0 + n - 1 of the block's; n = 0: no more pieces
+  int slot;         // where a partial goes, -1: the piece is the whole segment
   Block k;
 };
+static_assert(sizeof(Piece) == 64, "a piece's place in shared memory");
 
-// Walks a CTA's pieces in order; every role walks alike.
+// Walks a CTA's pieces in order.
 class Walk {
  public:
   __device__ __forceinline__ Walk(const Params& p) : p_(p) {
@@ -274,6 +281,7 @@ class Walk {
   }
   __device__ __forceinline__ bool next(Piece& c) {
     if (p_.prefix_table) {
+      c.n = 0;
       if (x_ >= end_) return false;
       const int s = x_ % p_.prefix_splits;
       const int seg = x_ / p_.prefix_splits;
@@ -297,7 +305,7 @@ class Walk {
       c.t0 = max(0, t_ - kSegCost);
       c.n = t_ + units - kSegCost - c.t0;
       // a cut piece that goes on from an earlier CTA's (at most one per CTA), and one that others go on from
-      c.slot = c.n == c.k.sp.nt ? -1 : 2 * static_cast<int64_t>(blockIdx.x) + (c.t0 > 0 ? 0 : 1);
+      c.slot = c.n == c.k.sp.nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (c.t0 > 0 ? 0 : 1);
       x_ += units;
       t_ = 0;
       if (x_ < end_) {  // the next block with tiles: of this head, of the next head, of the next sequence
@@ -316,6 +324,7 @@ class Walk {
       }
       if (c.n > 0) return true;
     }
+    c.n = 0;
     return false;
   }
 
@@ -346,7 +355,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* o_full = p_full + 2;    // [2]
   uint64_t* o_free = o_full + 2;    // [2]
   uint64_t* mma_done = o_free + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  uint64_t* d_full = mma_done + 1;      // [kItems]
+  uint64_t* d_empty = d_full + kItems;  // [kItems]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(d_empty + kItems);
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -354,17 +365,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);  // both issuers
     }
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, 2);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&s_full[h], 1);
-      mbar_init(&p_full[h], kSoft);
+      mbar_init(&p_full[h], kSoft / 32);  // one arrival per warp
       mbar_init(&o_full[h], 1);
-      mbar_init(&o_free[h], kSoft);
+      mbar_init(&o_free[h], kSoft / 32);
     }
-    mbar_init(mma_done, 1);
+    mbar_init(mma_done, 2);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_empty[i], kReaders);
+    }
     fence_mbar_init();
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
@@ -377,8 +392,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  Walk walk(p);
-  Piece c;
+  // The pieces come announced in shared memory by warp 3, a few ahead, so that no other role keeps the walk's state in
+  // registers or waits for its table look-ups.
+  Piece* items = reinterpret_cast<Piece*>(smem + kOffItem);
+  int di = 0;
+  // The next piece's place, kItems when there is none; its reader copies what it needs and hands the place back.
+  auto next_piece = [&]() -> int {
+    const int s = di % kItems;
+    const bool got = __all_sync(0xffffffffu, mbar_wait_soon(&d_full[s], static_cast<uint32_t>((di / kItems) & 1)));
+    if (!got && lane == 0) atomicExch(p.status, kStatusWaitFullTimeout);
+    ++di;
+    return got && items[s].n > 0 ? s : kItems;
+  };
+  auto hand_back = [&](int s) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&d_empty[s]);
+  };
 
   if (warp < 4) {
   reg_dealloc<kRegsIo>();
@@ -398,21 +427,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
       ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity));
     };
-    while (ok && walk.next(c)) {
-      const Span sp = c.k.sp;
+    for (int s; ok && (s = next_piece()) < kItems;) {
+      const Span sp = items[s].k.sp;
       const int32_t* table =
-          p.prefix_table ? p.prefix_table : p.kv.block_table + static_cast<int64_t>(c.k.seq) * p.kv.max_pages;
+          p.prefix_table ? p.prefix_table : p.kv.block_table + static_cast<int64_t>(items[s].k.seq) * p.kv.max_pages;
+      const int t0 = items[s].t0, t1 = t0 + items[s].n, j = items[s].j;
+      const int tok0 = items[s].k.tok0, ntok = items[s].k.ntok;
+      hand_back(s);
       auto entry = [&](int t) {  // this lane's page in tile t: -2 nothing to load, -1 a bad entry (reads as zeros)
         const int key = sp.key_tile(t) * kKeys + row0;
         if (!mine || !sp.sees_any(key, rows)) return -2;
         const int id = table[key >> p.kv.page_shift];
         return static_cast<uint32_t>(id) < static_cast<uint32_t>(p.kv.num_pages) ? id : -1;
       };
-      int id = entry(c.t0);
-      for (int t = c.t0; t < c.t0 + c.n; ++t, ++it) {
-        const int next = t + 1 < c.t0 + c.n ? entry(t + 1) : -2;
+      int id = entry(t0);
+      for (int t = t0; t < t1; ++t, ++it) {
+        const int next = t + 1 < t1 ? entry(t + 1) : -2;
         const int key = sp.key_tile(t) * kKeys + row0;
-        const int z = id < 0 ? -1 : id * p.h_kv + c.j;
+        const int z = id < 0 ? -1 : id * p.h_kv + j;
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id != -2 && !is_v)) * static_cast<uint32_t>(rows) * 128u;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
@@ -426,16 +458,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (id != -2 && is_v == (kv == 1))
             tma_load_3d(smem + kOffRing + st * kTile + (lane & 1) * kBox + row0 * 128, kv ? &tmV : &tmK, &full[st],
                         (lane & 1) * 64, key & (page - 1), z, policy_q);
-          if (kv == 0 && t == c.t0) {  // the queries go between the first K and V tiles
+          if (kv == 0 && t == t0) {  // the queries go between the first K and V tiles
             wait_all(q_empty, static_cast<uint32_t>((pi & 1) ^ 1));
             if (!ok) break;
             if (lane == 0) {
-              const int nh = c.k.ntok > p.half_tokens ? 2 : 1;
+              const int nh = ntok > p.half_tokens ? 2 : 1;
               mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(nh * p.half_tokens * p.G * 256));
               for (int h = 0; h < nh; ++h)
                 for (int d = 0; d < 2; ++d)
-                  tma_load_3d(smem + kOffQ + h * kTile + d * kBox, &tmQ, q_full, 64 * d, c.j * p.G,
-                              c.k.tok0 + h * p.half_tokens, policy_q);
+                  tma_load_3d(smem + kOffQ + h * kTile + d * kBox, &tmQ, q_full, 64 * d, j * p.G,
+                              tok0 + h * p.half_tokens, policy_q);
               ++pi;
             }
             pi = __shfl_sync(0xffffffffu, pi, 0);
@@ -457,75 +489,110 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (pi > 0 && !mbar_wait(q_full, static_cast<uint32_t>((pi - 1) & 1))) atomicExch(p.status, kStatusDrainTimeout);
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // =========================== MMA issuer ===========================
-    if (lane == 0) {
-      const uint32_t sbase = smem_addr(smem);
-      const uint32_t idesc_s = umma_idesc_bf16_m128(kKeys);
-      const uint32_t idesc_o = umma_idesc_bf16_m128(kD) | kIdescBMajorMN;
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok && !mbar_wait(bar, parity)) {
-          ok = false;
-          atomicExch(p.status, kStatusWaitFullTimeout);
+  } else if (warp < 3) {
+    // =========================== MMA issuer of half h ===========================
+    // The tensor pipe holds few MMAs ahead, so whatever their issuer does in between (waits, commits: 300 to 400 cycles
+    // in one warp for both halves) leaves it idle. So each half has an issuer, and a pair of named barriers passes the
+    // turn: one waits for its operands while the other's MMAs run, and the halves stay half a period apart. (Without
+    // turns their MMAs interleave, and both softmaxes wait for both products.) The whole warp runs the loop, so that
+    // descriptors are warp-uniform values, as the instruction takes them; one elected lane issues.
+    const int h = warp - 1;
+    const uint32_t ring = uniform((smem_addr(smem) + kOffRing) >> 4);  // descriptors count 16 bytes
+    const uint64_t q = umma_desc_sw128(0) + uniform((smem_addr(smem) + kOffQ + h * kTile) >> 4);
+    const uint32_t d_s = uniform(tmem + col_s(h));
+    const uint32_t d_o = uniform(tmem + col_o(h));
+    const uint32_t idesc_s = umma_idesc_bf16_m128(kKeys);
+    const uint32_t idesc_o = umma_idesc_bf16_m128(kD) | kIdescBMajorMN;
+    const int my_turn = kTurnBar + h, other_turn = kTurnBar + 1 - h;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!mbar_wait_soon(bar, parity)) ok = false;
+    };
+    uint32_t pv = 0, seg = 0;    // products P . V issued, pieces begun
+    uint32_t st_k = 0, ph = 0;   // ring place and phase of the next K tile; the V tile due is the one before
+    if (h == 1) named_bar_arrive(other_turn, 64);
+    for (int pi = 0;; ++pi) {
+      const uint32_t s = uniform(next_piece());
+      if (s >= kItems) break;
+      const bool active = uniform(h == 0 || items[s].k.ntok > p.half_tokens) != 0;
+      const int n = static_cast<int>(uniform(items[s].n));
+      hand_back(s);
+      if (active) wait(q_full, static_cast<uint32_t>(pi & 1));
+      for (int t = 0; t <= n; ++t) {
+        const uint32_t st_v = st_k == 0 ? kStages - 1 : st_k - 1;
+        if (t > 0) wait(&full[st_v], st_k == 0 ? ph ^ 1 : ph);
+        if (t < n) wait(&full[st_k], ph);
+        if (active) {
+          if (t == 1) wait(&o_free[h], (seg++ & 1) ^ 1);
+          if (t > 0) wait(&p_full[h], pv++ & 1);
         }
-      };
-      uint32_t pv[2] = {0, 0};     // products P . V issued for each half
-      uint32_t seg[2] = {0, 0};    // pieces begun for each half
-      auto issue_o = [&](int h, int i, bool first) {
-        const int idx = 2 * i + 1;
-        const int st = idx % kStages;
-        if (h == 0) wait(&full[st], static_cast<uint32_t>((idx / kStages) & 1));
-        wait(&p_full[h], pv[h] & 1);
-        if (first) wait(&o_free[h], (seg[h]++ & 1) ^ 1);
-        if (ok) {
-          tc_fence_after_sync();
-          const uint64_t v = umma_desc_sw128_mn(sbase + kOffRing + st * kTile, kBox);
+        tc_fence_after_sync();
+        named_bar_sync(my_turn, 64);
+        if (elect_one()) {
+          if (active) {
+            if (ok && t > 0) {
+              const uint64_t v = umma_desc_sw128_mn(0, kBox) + (ring + st_v * (kTile >> 4));
+              umma_bf16_tmem_a(d_o, d_s, v, idesc_o, t > 1);
 #pragma unroll
-          for (int s = 0; s < kKeys / 16; ++s)  // a descriptor's address field counts 16 bytes
-            umma_bf16_tmem_a(tmem + col_o(h), tmem + col_s(h) + 8 * s, v + s * (2048 >> 4), idesc_o, !(first && s == 0));
-        }
-        umma_commit(&o_full[h]);
-        ++pv[h];
-      };
-      int it = 0, pi = 0;
-      for (; walk.next(c); ++pi) {
-        const int nh = c.k.ntok > p.half_tokens ? 2 : 1;
-        wait(q_full, static_cast<uint32_t>(pi & 1));
-        for (int t = 0; t < c.n; ++t, ++it) {
-          const int idx = 2 * it;
-          const int st = idx % kStages;
-          wait(&full[st], static_cast<uint32_t>((idx / kStages) & 1));
-          for (int h = 0; h < nh; ++h) {
-            // the scores overwrite the probabilities of the tile before, whose product was issued just now: MMAs of
-            // one thread run in order
-            if (t > 0) issue_o(h, it - 1, t == 1);
-            if (ok) {
-              tc_fence_after_sync();
-              const uint64_t k = umma_desc_sw128(sbase + kOffRing + st * kTile);
-              const uint64_t q = umma_desc_sw128(sbase + kOffQ + h * kTile);
+              for (int x = 1; x < kKeys / 16; ++x)
+                umma_bf16_tmem_a(d_o, d_s + 8 * x, v + x * (2048 >> 4), idesc_o, true);
+            }
+            // the scores overwrite the probabilities of the tile before, whose product was issued just now: MMAs of one
+            // thread run in order
+            if (ok && t < n) {
+              const uint64_t k = umma_desc_sw128(0) + (ring + st_k * (kTile >> 4));
 #pragma unroll
-              for (int s = 0; s < kD / 16; ++s) {
-                const uint64_t off = static_cast<uint64_t>(((s >> 2) * kBox + (s & 3) * 32) >> 4);
-                umma_bf16(tmem + col_s(h), q + off, k + off, idesc_s, s > 0);
+              for (int x = 0; x < kD / 16; ++x) {
+                const uint32_t off = ((x >> 2) * kBox + (x & 3) * 32) >> 4;
+                umma_bf16(d_s, q + off, k + off, idesc_s, x > 0);
               }
             }
-            umma_commit(&s_full[h]);
+            // one commit tells of both: the output is read only after the last product or, to rescale it, with scores
+            umma_commit(t < n ? &s_full[h] : &o_full[h]);
+            if (t > 0) umma_commit(&empty[st_v]);
+            if (t < n) umma_commit(&empty[st_k]);
+            if (t == n - 1) umma_commit(q_empty);
+          } else {
+            if (t > 0) mbar_arrive(&empty[st_v]);
+            if (t < n) mbar_arrive(&empty[st_k]);
+            if (t == n - 1) mbar_arrive(q_empty);
           }
-          if (t > 0) umma_commit(&empty[(idx - 1) % kStages]);
-          umma_commit(&empty[st]);
-          if (t == c.n - 1) umma_commit(q_empty);
         }
-        for (int h = 0; h < nh; ++h) issue_o(h, it - 1, c.n == 1);
-        umma_commit(&empty[(2 * it - 1) % kStages]);
+        __syncwarp();
+        named_bar_arrive(other_turn, 64);
+        if (t < n) {
+          st_k += 2;
+          if (st_k >= kStages) {
+            st_k -= kStages;
+            ph ^= 1;
+          }
+        }
       }
-      // every MMA has completed before TMEM is released
-      umma_commit(mma_done);
-      if (!mbar_wait(mma_done, 0)) atomicExch(p.status, kStatusDrainTimeout);
+    }
+    if (h == 0) named_bar_sync(my_turn, 64);  // the turn that half 1 passed last
+    if (!ok && lane == 0) atomicExch(p.status, kStatusWaitFullTimeout);
+    // every MMA has completed before TMEM is released
+    if (elect_one()) umma_commit(mma_done);
+    if (!mbar_wait(mma_done, 0) && lane == 0) atomicExch(p.status, kStatusDrainTimeout);
+    __syncwarp();
+  } else if (warp == 3) {
+    // =========================== announces the pieces ===========================
+    if (lane == 0) {
+      Walk walk(p);
+      for (bool more = true; more; ++di) {
+        Piece c{};
+        more = walk.next(c);
+        const int s = di % kItems;
+        if (!mbar_wait(&d_empty[s], static_cast<uint32_t>(((di / kItems) & 1) ^ 1))) {
+          atomicExch(p.status, kStatusWaitEmptyTimeout);
+          break;
+        }
+        items[s] = c;
+        mbar_arrive(&d_full[s]);  // releases the write
+      }
     }
     __syncwarp();
-  } else {
-    // =========================== blocks that see nothing ===========================
+    // =========================== and writes zeros for blocks that see nothing ===========================
     if (!p.prefix_table) {
       const int blocks = p.base[p.B];
       for (int i = blockIdx.x; i < blocks; i += gridDim.x) {
@@ -534,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Block k = block_of(p, b, i - p.base[b]);
         uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(k.tok0) * p.h_q * kD);
         const int64_t n = static_cast<int64_t>(k.ntok) * p.h_q * (kD / 8);
-        for (int64_t e = tid - 64; e < n; e += 64) o[e] = make_uint4(0u, 0u, 0u, 0u);
+        for (int64_t e = lane; e < n; e += 32) o[e] = make_uint4(0u, 0u, 0u, 0u);
       }
     }
   }
@@ -557,44 +624,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = r / p.G;                  // token of the half
     const int g = r - i * p.G;
     const bool neg = p.scale_log2 < 0.0f;
-    const float hidden = neg ? INFINITY : -INFINITY;
-    const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
+    const float scale = fabsf(p.scale_log2);
     bool ok = true;
     auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
-      const bool w = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity));
+      const bool w = __all_sync(0xffffffffu, ok && mbar_wait_soon(bar, parity));
       if (!w && ok) {
         ok = false;
         atomicExch(p.status, kStatusWaitFullTimeout);
       }
     };
-    uint32_t cnt = 0;  // tiles of this half so far
-    int it = 0;        // tiles of the CTA so far
-    while (walk.next(c)) {
-      const int nh = c.k.ntok > p.half_tokens ? 2 : 1;
-      if (h >= nh) {
-        it += c.n;
+    uint32_t cnt = 0;     // tiles of this half so far
+    uint32_t pieces = 0;  // and pieces
+    int it = 0;           // tiles of the CTA so far
+    for (int s; (s = next_piece()) < kItems;) {
+      const int t0 = items[s].t0, t1 = t0 + items[s].n;
+      if (h == 1 && items[s].k.ntok <= p.half_tokens) {
+        hand_back(s);
+        it += t1 - t0;
         continue;
       }
+      // what only some tiles or the output need stays in shared memory until then
+      const Span& sp = items[s].k.sp;
+      const int ntok = items[s].k.ntok, pos0 = items[s].k.pos0;
       const int tok = h * p.half_tokens + i;  // within the block
-      const bool live = i < p.half_tokens && tok < c.k.ntok;
-      const int pos = p.prefix_table ? p.prefix_len - 1 : c.k.pos0 + tok;
-      const int end = live ? min(pos + 1, c.k.sp.len) : 0;   // keys below it are seen ...
+      const bool live = i < p.half_tokens && tok < ntok;
+      const int pos = p.prefix_table ? p.prefix_len - 1 : pos0 + tok;
+      const int end = live ? min(pos + 1, sp.len) : 0;   // keys below it are seen ...
       const int lo = window_start(pos, p.kv.window);         // ... from here on, or below n_sink
       // a tile needs no mask when the half's first token sees its end and its last token's window begins before it
-      const int last = min(c.k.ntok, (h + 1) * p.half_tokens) - 1;
-      const int end_min = p.prefix_table ? p.prefix_len : c.k.pos0 + h * p.half_tokens + 1;
-      const int lo_max = p.prefix_table ? 0 : window_start(c.k.pos0 + last, p.kv.window);
+      const int last = min(ntok, (h + 1) * p.half_tokens) - 1;
+      const int end_min = p.prefix_table ? p.prefix_len : pos0 + h * p.half_tokens + 1;
+      const int lo_max = p.prefix_table ? 0 : window_start(pos0 + last, p.kv.window);
       float m = -FLT_MAX, l = 0.0f;  // the row's reference, this thread's share of its sum
-      for (int t = c.t0; t < c.t0 + c.n; ++t, ++it, ++cnt) {
-        const int kb = c.k.sp.key_tile(t) * kKeys;
+      for (int t = t0; t < t1; ++t, ++it, ++cnt) {
+        const int kb = sp.key_tile(t) * kKeys;
         wait_warp(&s_full[h], cnt & 1);
         tc_fence_after_sync();
-        uint32_t s[64];
+        uint32_t sc[64];
         if (ok) {
-          tmem_ld64(tbase + col_s(h) + 64 * part, s);
+          tmem_ld64(tbase + col_s(h) + 64 * part, sc);
         } else {
 #pragma unroll
-          for (int x = 0; x < 64; ++x) s[x] = 0u;
+          for (int x = 0; x < 64; ++x) sc[x] = 0u;
+        }
+        if (neg) {
+#pragma unroll
+          for (int x = 0; x < 64; ++x) sc[x] ^= 0x80000000u;
         }
         const bool plain = kb + kKeys <= end_min && (kb >= lo_max || kb + kKeys <= p.kv.n_sink);
         if (!plain) {
@@ -604,9 +679,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t see = bits_below(end, cb) & (~bits_below(lo, cb) | bits_below(p.kv.n_sink, cb));
 #pragma unroll
             for (int x = 0; x < 32; ++x)
-              if (!((see >> x) & 1u)) s[32 * w + x] = __float_as_uint(hidden);
+              if (!((see >> x) & 1u)) sc[32 * w + x] = __float_as_uint(-INFINITY);
           }
-          if (h == 0 && !c.k.sp.sees(kb + r)) {
+          if (h == 0 && !sp.sees(kb + r)) {
             // a key no row sees: its cache row is arbitrary (even NaN) and a zero probability times NaN is NaN, so
             // this row of the V tile is cleared (the wait orders the overwrite behind the tile's landing)
             const int idx = 2 * it + 1;
@@ -622,27 +697,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // four chains, so that their latency overlaps
-        float mx[4] = {hidden, hidden, hidden, hidden};
-        if (neg) {
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int x = 0; x < 64; x += 2)
-            mx[(x >> 1) & 3] = min3_f32(mx[(x >> 1) & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
-          mx[0] = fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3]));
-        } else {
-#pragma unroll
-          for (int x = 0; x < 64; x += 2)
-            mx[(x >> 1) & 3] = max3_f32(mx[(x >> 1) & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
-          mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        }
-        const float mine = mx[0] * p.scale_log2;
+        for (int x = 0; x < 64; x += 2)
+          mx[(x >> 1) & 3] = max3_f32(mx[(x >> 1) & 3], __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
+        mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float mine = mx[0] * scale;
         const float m_new = max3_f32(m, mine, exchange(mine));
         // O holds nothing until the row has seen a key
         const bool seen = m > -FLT_MAX;
         const bool grow = live && seen && m_new > m + kGrowth;
         if (__any_sync(0xffffffffu, grow)) {
           const float a = grow ? ex2_approx(m - m_new) : 1.0f;
-          wait_warp(&o_full[h], (cnt - 1) & 1);
-          tc_fence_after_sync();
+          // the scores' commit covered the product before them
 #pragma unroll 1
           for (int x = 0; x < 4; ++x) {  // this part's dimensions of O
             if (!ok) break;
@@ -658,6 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!seen) m = m_new;
         const uint64_t minus_m = pack_f32x2(-m, -m);
+        const uint64_t scale2 = pack_f32x2(scale, scale);
         uint64_t sum2[2] = {0u, 0u};
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
@@ -666,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 16; ++x) {
             const int y = 32 * w + 2 * x;
             float p0, p1;
-            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[y]), __uint_as_float(s[y + 1])), scale2, minus_m), p0, p1);
+            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(sc[y]), __uint_as_float(sc[y + 1])), scale2, minus_m), p0, p1);
             p0 = ex2_approx(p0);
             p1 = ex2_approx(p1);
             sum2[x & 1] = add_f32x2(sum2[x & 1], pack_f32x2(p0, p1));
@@ -681,18 +749,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += s0 + s1;
         if (ok) tmem_wait_st();
         tc_fence_before_sync();
-        mbar_arrive(&p_full[h]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[h]);
       }
       // the piece's output: this part's dimensions
       named_bar_sync(pair_bar, 64);  // the maxima exchanged last have been read
       l += exchange(l);
-      wait_warp(&o_full[h], (cnt - 1) & 1);
+      wait_warp(&o_full[h], pieces++ & 1);
       tc_fence_after_sync();
       const bool some = l > 0.0f;
       const int row = h * kHalf + r;
+      const int j = items[s].j, slot = items[s].slot, tok0 = items[s].k.tok0;
+      hand_back(s);
       const float inv = some ? 1.0f / l : 0.0f;
       uint4* out = reinterpret_cast<uint4*>(
-          p.out + (static_cast<int64_t>(c.k.tok0 + tok) * p.h_q + c.j * p.G + g) * kD + 64 * part);
+          p.out + (static_cast<int64_t>(tok0 + tok) * p.h_q + j * p.G + g) * kD + 64 * part);
 #pragma unroll 1
       for (int x = 0; x < 4; ++x) {
         float v[16];
@@ -707,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int y = 0; y < 16; ++y) v[y] = 0.0f;
         }
         if (!live) continue;
-        if (c.slot < 0) {
+        if (slot < 0) {
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             uint32_t w[4];
@@ -721,16 +792,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll
           for (int y = 0; y < 4; ++y)
-            *reinterpret_cast<float4*>(p.pieces_o + piece_at(c.slot, row, 64 * part + 16 * x + 4 * y)) =
+            *reinterpret_cast<float4*>(p.pieces_o + piece_at(slot, row, 64 * part + 16 * x + 4 * y)) =
                 make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
         }
       }
-      if (live && c.slot >= 0 && part == 0) {
-        p.pieces_m[c.slot * kRowTile + row] = m;
-        p.pieces_l[c.slot * kRowTile + row] = l;
+      if (live && slot >= 0 && part == 0) {
+        p.pieces_m[slot * kRowTile + row] = m;
+        p.pieces_l[slot * kRowTile + row] = l;
       }
       tc_fence_before_sync();
-      mbar_arrive(&o_free[h]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_free[h]);
       named_bar_sync(pair_bar, 64);  // the sums exchanged have been read
     }
   }
