@@ -18,6 +18,23 @@ using namespace moe::api;
 constexpr size_t kTicketOffset = 8;
 constexpr size_t kDecodePartialBytes = sizeof(float) * static_cast<size_t>(moe::kPartialCtas) * 2 * moe::kGqaSlotFloats;
 
+// Splits of each of `segs` segments of a shared prefix of `tiles` key tiles over the CTAs: whole waves of pieces, each
+// its tiles and about 3 tiles' time of start and output, and for joining about 1/50 of a tile's time per piece.
+constexpr int kMaxPrefixPieces = 4 * moe::kRowsCtas;
+int prefix_splits(int64_t segs, int tiles) {
+  int best = 1;
+  double least = 0.0;
+  for (int s = 1; s <= tiles && (s == 1 || segs * s <= kMaxPrefixPieces); ++s) {
+    const int64_t waves = (segs * s + moe::kRowsCtas - 1) / moe::kRowsCtas;
+    const double cost = static_cast<double>(waves) * ((tiles + s - 1) / s + 3) + 0.02 * static_cast<double>(segs * s);
+    if (s == 1 || cost < least) {
+      best = s;
+      least = cost;
+    }
+  }
+  return best;
+}
+
 struct Layout {
   size_t partials, tables, pieces, total;
   int prefix_blocks, prefix_splits;
@@ -33,18 +50,17 @@ Layout layout(int64_t N, int64_t B, int h_q, int h_kv, int prefix_len) {
   L.partials = o;
   o = align_up(o + kDecodePartialBytes);
   L.tables = o;
-  // per sequence: tile prefix, row-block base; per row block: its tile prefix within the sequence
+  // per CTA the segment it cuts; per sequence and per row block the work before
   const int64_t blocks = N / per_block + B;
-  o = align_up(o + sizeof(int32_t) * static_cast<size_t>(3 * (B + 1) + blocks + B));
+  o = align_up(o + sizeof(int32_t) * static_cast<size_t>(4 * moe::kRowsCtas + 2 * (B + 1) + blocks + 1));
   L.pieces = o;
   int64_t pieces = 2 * moe::kRowsCtas;
   if (prefix_len > 0) {
     L.prefix_blocks = static_cast<int>((B + per_block - 1) / per_block);
     const int64_t segs = static_cast<int64_t>(L.prefix_blocks) * h_kv;
-    const int tiles = (prefix_len + 127) / 128;
-    int splits = segs > 0 && segs < moe::kRowsCtas ? static_cast<int>(moe::kRowsCtas / segs) : 1;
-    L.prefix_splits = splits < tiles ? splits : tiles;
-    if (segs * L.prefix_splits > pieces) pieces = segs * L.prefix_splits;
+    L.prefix_splits = prefix_splits(segs, (prefix_len + 127) / 128);
+    // (the bound does not depend on the split, so that a workspace for larger sizes serves smaller ones)
+    pieces = segs > kMaxPrefixPieces ? segs : kMaxPrefixPieces;
   }
   o = align_up(o + sizeof(float) * static_cast<size_t>(pieces) * moe::kRowsPieceFloats);
   L.total = o;

@@ -22,7 +22,7 @@
 // shared prefix the host knows the sizes: equal splits per segment, joined the same way; the decode kernel adds the
 // result to the sequences' own keys.
 //
-// Per CTA, 20 warps: 0 TMA producer (Q per piece; K and V tiles alternate in a ring of 5 x 32 KB), 1 and 2 issue
+// Per CTA, 20 warps: 0 TMA producer (Q per piece; K and V tiles alternate in a ring of 4 x 32 KB), 1 and 2 issue
 // the MMAs of the two halves in turn, 3 announces the pieces and writes zeros for blocks that see nothing, 4-11 and 12-19 the softmax and output of the two halves.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -43,7 +43,7 @@ using namespace gqa;
 
 constexpr int kD = 128;
 constexpr int kHalf = 128;                  // rows of a half
-constexpr int kStages = 5;
+constexpr int kStages = 4;
 constexpr int kBox = kKeys * 64 * 2;        // 128 rows x 64 dims
 constexpr int kTile = 2 * kBox;             // one K or V tile, or the queries of a half: 32 KB
 constexpr int kThreads = 640;
@@ -55,7 +55,8 @@ constexpr int kItems = 4;                   // pieces announced ahead
 constexpr int kNumBars = 2 * kStages + 2 + 2 * 4 + 1 + 2 * kItems;
 constexpr int kOffRed = kOffBar + 256;      // row maxima and sums, [2 halves][2 parts][128 rows]
 constexpr int kOffItem = kOffRed + 2 * 2 * kHalf * 4;
-constexpr int kSmem = kOffItem + kItems * 64;
+constexpr int kOffOut = kOffItem + kItems * 64;  // per softmax warp 32 rows x 32 dimensions of bf16 output
+constexpr int kSmem = kOffOut + 16 * 2048;
 // Registers per thread: at launch, and after the warpgroups have shared them out (128 threads that load and issue,
 // 512 softmax threads that hold half a row of scores each).
 constexpr int kRegsLaunch = 96;
@@ -94,6 +95,7 @@ struct Params {
   int32_t* pre;              // [B + 1] units of the sequences before, for one key/value head
   int32_t* base;             // [B + 1] row blocks of the sequences before
   int32_t* cum;              // [blocks + 1] units of the blocks before
+  int4* join;                // [CTAs] the segment that begins in a CTA's share and ends past it: tok0, ntok, head, pieces
   const int32_t* prefix_table;
   int prefix_len, prefix_splits, prefix_blocks;
   int N, B, h_q, h_kv, G, half_tokens, max_blocks, L_cap;
@@ -322,10 +324,20 @@ class Walk {
           i_ = p_.base[b_];
         }
       }
-      if (c.n > 0) return true;
+      if (c.n > 0) {
+        last_ = c;
+        return true;
+      }
     }
     c.n = 0;
     return false;
+  }
+  // The segment that the share's last piece begins and later CTAs go on with, pieces = 0 when there is none.
+  __device__ __forceinline__ int4 cut() const {
+    if (p_.prefix_table || last_.n == 0 || last_.slot != 2 * static_cast<int>(blockIdx.x) + 1) return make_int4(0, 0, 0, 0);
+    const Share s(p_.h_kv * p_.pre[p_.B], gridDim.x);
+    const int past = last_.k.sp.nt - last_.t0 - last_.n;  // its tiles in later shares
+    return make_int4(last_.k.tok0, last_.k.ntok, last_.j, s.cta_of(end_ - 1 + past) - static_cast<int>(blockIdx.x) + 1);
   }
 
  private:
@@ -333,6 +345,7 @@ class Walk {
   int x_ = 0, end_ = 0;           // units done before, and where the CTA's share ends
   int b_ = 0, j_ = 0, i_ = 0;     // sequence, head, row block
   int t_ = 0;                     // unit within the block
+  Piece last_{};
 };
 
 // ---------------------------------------------------------------- the attention kernel
@@ -590,6 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         items[s] = c;
         mbar_arrive(&d_full[s]);  // releases the write
       }
+      if (!p.prefix_table) p.join[blockIdx.x] = walk.cut();
     }
     __syncwarp();
     // =========================== and writes zeros for blocks that see nothing ===========================
@@ -703,27 +717,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           mx[(x >> 1) & 3] = max3_f32(mx[(x >> 1) & 3], __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
         mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         const float mine = mx[0] * scale;
-        const float m_new = max3_f32(m, mine, exchange(mine));
-        // O holds nothing until the row has seen a key
+        // The reference both threads of the row use changes only when one of them sees a value far above it (or the
+        // row's first key); otherwise this barrier, which also tells that both have read their scores, is all they
+        // exchange.
         const bool seen = m > -FLT_MAX;
-        const bool grow = live && seen && m_new > m + kGrowth;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float a = grow ? ex2_approx(m - m_new) : 1.0f;
-          // the scores' commit covered the product before them
+        const bool far = live && (seen ? mine > m + kGrowth : mine > -FLT_MAX);
+        tc_fence_before_sync();
+        const bool any = named_bar_any(pair_bar, 64, far);
+        tc_fence_after_sync();
+        if (any) {
+          const float m_new = fmaxf(mine, exchange(mine));
+          const bool grow = live && (seen ? m_new > m + kGrowth : m_new > -FLT_MAX);
+          // O holds nothing until the row has seen a key
+          if (__any_sync(0xffffffffu, grow && seen)) {
+            const float a = grow && seen ? ex2_approx(m - m_new) : 1.0f;
+            // the scores' commit covered the product before them
 #pragma unroll 1
-          for (int x = 0; x < 4; ++x) {  // this part's dimensions of O
-            if (!ok) break;
-            float o[16];
-            uint32_t u[16];
-            tmem_ld16(tbase + col_o(h) + 64 * part + 16 * x, o);
+            for (int x = 0; x < 4; ++x) {  // this part's dimensions of O
+              if (!ok) break;
+              float o[16];
+              uint32_t u[16];
+              tmem_ld16(tbase + col_o(h) + 64 * part + 16 * x, o);
 #pragma unroll
-            for (int y = 0; y < 16; ++y) u[y] = __float_as_uint(o[y] * a);
-            tmem_st16(tbase + col_o(h) + 64 * part + 16 * x, u);
+              for (int y = 0; y < 16; ++y) u[y] = __float_as_uint(o[y] * a);
+              tmem_st16(tbase + col_o(h) + 64 * part + 16 * x, u);
+            }
+            l *= a;
           }
-          l *= a;
           if (grow) m = m_new;
+          named_bar_sync(pair_bar, 64);  // the maxima exchanged have been read
         }
-        if (!seen) m = m_new;
         const uint64_t minus_m = pack_f32x2(-m, -m);
         const uint64_t scale2 = pack_f32x2(scale, scale);
         uint64_t sum2[2] = {0u, 0u};
@@ -753,7 +776,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[h]);
       }
       // the piece's output: this part's dimensions
-      named_bar_sync(pair_bar, 64);  // the maxima exchanged last have been read
       l += exchange(l);
       wait_warp(&o_full[h], pieces++ & 1);
       tc_fence_after_sync();
@@ -762,38 +784,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int j = items[s].j, slot = items[s].slot, tok0 = items[s].k.tok0;
       hand_back(s);
       const float inv = some ? 1.0f / l : 0.0f;
-      uint4* out = reinterpret_cast<uint4*>(
-          p.out + (static_cast<int64_t>(tok0 + tok) * p.h_q + j * p.G + g) * kD + 64 * part);
+      if (slot < 0) {
+        // a thread's row is 256 bytes from its neighbour's: through shared memory, so that four lanes write 64 bytes of
+        // a row together (a store instruction then touches 8 lines instead of 32)
+        uint8_t* stage = smem + kOffOut + (warp - 4) * 2048;
+        const int64_t mine = live ? static_cast<int64_t>(tok0 + tok) * p.h_q + j * p.G + g : -1;
 #pragma unroll 1
-      for (int x = 0; x < 4; ++x) {
-        float v[16];
-        if (ok) {
-          tmem_ld16(tbase + col_o(h) + 64 * part + 16 * x, v);
-        } else {
+        for (int x = 0; x < 2; ++x) {
+          float v[32];
+          if (ok) {
+            tmem_ld32(tbase + col_o(h) + 64 * part + 32 * x, v);
+          } else {
 #pragma unroll
-          for (int y = 0; y < 16; ++y) v[y] = 0.0f;
-        }
-        if (!some) {
+            for (int y = 0; y < 32; ++y) v[y] = 0.0f;
+          }
 #pragma unroll
-          for (int y = 0; y < 16; ++y) v[y] = 0.0f;
-        }
-        if (!live) continue;
-        if (slot < 0) {
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
+          for (int y = 0; y < 4; ++y) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 ab = __floats2bfloat162_rn(v[8 * y + 2 * e] * inv, v[8 * y + 2 * e + 1] * inv);
+              const float a = some ? v[8 * y + 2 * e] * inv : 0.0f, b = some ? v[8 * y + 2 * e + 1] * inv : 0.0f;
+              const __nv_bfloat162 ab = __floats2bfloat162_rn(a, b);
               w[e] = *reinterpret_cast<const uint32_t*>(&ab);
             }
-            out[2 * x + y] = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((y ^ (lane >> 1)) & 3) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        } else {
+          __syncwarp();
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            *reinterpret_cast<float4*>(p.pieces_o + piece_at(slot, row, 64 * part + 16 * x + 4 * y)) =
-                make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+          for (int y = 0; y < 4; ++y) {
+            const int rr = 8 * y + (lane >> 2);
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((lane ^ (rr >> 1)) & 3) * 16);
+            const int64_t to = __shfl_sync(0xffffffffu, mine, rr);
+            if (to >= 0) *reinterpret_cast<uint4*>(p.out + to * kD + 64 * part + 32 * x + 8 * (lane & 3)) = w;
+          }
+          __syncwarp();
+        }
+      } else {
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {
+          float v[16];
+          if (ok) {
+            tmem_ld16(tbase + col_o(h) + 64 * part + 16 * x, v);
+          } else {
+#pragma unroll
+            for (int y = 0; y < 16; ++y) v[y] = 0.0f;
+          }
+          if (!live) continue;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            float4 f = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+            if (!some) f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            *reinterpret_cast<float4*>(p.pieces_o + piece_at(slot, row, 64 * part + 16 * x + 4 * y)) = f;
+          }
         }
       }
       if (live && slot >= 0 && part == 0) {
@@ -853,42 +895,25 @@ __device__ __forceinline__ void join_row(const Params& p, int row, int64_t first
 }
 
 // CTA (c, part) joins its rows of the segment whose first tile is in CTA c's share and whose last is not.
-__global__ void __launch_bounds__(kMergeThreads) rows_merge_kernel(const Params p, int ctas) {
+__global__ void __launch_bounds__(kMergeThreads) rows_merge_kernel(const Params p) {
   pdl_wait_predecessor();
   pdl_allow_successor();
-  const Share s(p.h_kv * p.pre[p.B], ctas);
   const int c = blockIdx.x;
-  if (c >= s.nc - 1) return;
-  const int x = s.start(c + 1) - 1;  // the share's last unit
-  int b = 0, hi = p.B - 1;
-  while (b < hi) {
-    const int mid = (b + hi + 1) >> 1;
-    if (p.h_kv * p.pre[mid] <= x) b = mid; else hi = mid - 1;
-  }
-  const int first = p.pre[b];
-  const int units = p.pre[b + 1] - first;
-  const int j = (x - p.h_kv * first) / units;
-  const int rem = x - p.h_kv * first - j * units;
-  const int base = p.base[b];
-  const int i = base + last_at_most(p.cum + base, p.base[b + 1] - base, first + rem);
-  const int tile0 = x - (first + rem - p.cum[i]) + kSegCost;  // the segment's first tile, as a unit of the list
-  const int tile1 = tile0 - kSegCost + p.cum[i + 1] - p.cum[i];
-  if (tile1 <= x + 1 || tile0 > x || tile0 < s.start(c)) return;
-  const int pieces = s.cta_of(tile1 - 1) - c + 1;
-  const Block k = block_of(p, b, i - base);
+  const int4 seg = p.join[c];  // tok0, ntok, head, pieces
   const int row0 = blockIdx.y * (kRowTile / kMergeParts);
+  if (seg.w == 0) return;
   for (int row = row0 + (threadIdx.x >> 5); row < row0 + kRowTile / kMergeParts; row += kMergeThreads / 32) {
     const int hf = row / kHalf;
     const int ti = (row - hf * kHalf) / p.G;
     const int tok = hf * p.half_tokens + ti;
-    if (ti >= p.half_tokens || tok >= k.ntok) continue;
+    if (ti >= p.half_tokens || tok >= seg.y) continue;
     float M, L;
     float4 O;
-    join_row(p, row, 2 * static_cast<int64_t>(c) + 1, 2 * static_cast<int64_t>(c + 1), 2, pieces, M, L, O);
+    join_row(p, row, 2 * static_cast<int64_t>(c) + 1, 2 * static_cast<int64_t>(c + 1), 2, seg.w, M, L, O);
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
     const __nv_bfloat162 x0 = __floats2bfloat162_rn(O.x * inv, O.y * inv);
     const __nv_bfloat162 x1 = __floats2bfloat162_rn(O.z * inv, O.w * inv);
-    uint16_t* o = p.out + (static_cast<int64_t>(k.tok0 + tok) * p.h_q + j * p.G + (row - hf * kHalf - ti * p.G)) * kD;
+    uint16_t* o = p.out + (static_cast<int64_t>(seg.x + tok) * p.h_q + seg.z * p.G + (row - hf * kHalf - ti * p.G)) * kD;
     reinterpret_cast<uint2*>(o)[threadIdx.x & 31] =
         make_uint2(*reinterpret_cast<const uint32_t*>(&x0), *reinterpret_cast<const uint32_t*>(&x1));
   }
@@ -953,7 +978,8 @@ cudaError_t launch_gqa_rows(const GqaRowsPlan& plan, cudaStream_t stream) {
   p.pieces_m = plan.pieces + pieces * kRowTile * kD;
   p.pieces_l = p.pieces_m + pieces * kRowTile;
   p.status = plan.status;
-  p.pre = plan.tables;
+  p.join = reinterpret_cast<int4*>(plan.tables);
+  p.pre = plan.tables + 4 * kRowsCtas;
   p.base = p.pre + plan.B + 1;
   p.cum = p.base + plan.B + 1;
   p.prefix_table = plan.prefix_table;
@@ -998,7 +1024,7 @@ cudaError_t launch_gqa_rows(const GqaRowsPlan& plan, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(gqa_rows_kernel, dim3(ctas), dim3(kThreads), kSmem, stream, tk, tv, tq, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(rows_merge_kernel, dim3(ctas, kMergeParts), dim3(kMergeThreads), 0, stream, p, ctas);
+  return launch_pdl(rows_merge_kernel, dim3(ctas, kMergeParts), dim3(kMergeThreads), 0, stream, p);
 }
 
 }  // namespace moe
