@@ -74,6 +74,8 @@ __host__ __device__ constexpr uint32_t col_s(int k) { return 32u * k; }
 __host__ __device__ constexpr uint32_t col_o(int k) { return 32u * k + 16u; }
 __host__ __device__ constexpr uint32_t col_h(int k) { return 64u + 32u * k; }
 
+constexpr float kGrowth = 8.0f;  // paged: log2 of how far a score may outgrow its head's reference
+
 constexpr int kOffQ = kStages * kStageBytes;
 constexpr int kOffP = kOffQ + 2 * kQBytes;
 constexpr int kOffBar = kOffP + 2 * kPBytes;
@@ -82,9 +84,11 @@ constexpr int kOffHand = kOffRed + (2 * 4 * kN + 4 * kN) * 4;  // hand-off scala
 constexpr int kOffMisc = kOffHand + 2 * 3 * kN * 4;
 constexpr int kOffPre = kOffMisc + 64;         // tile prefix over sequences, kMaxSeqs + 1 ints
 constexpr int kSmem = kOffPre + (kGqaMaxSeqs + 1) * 4;
+constexpr int kOffLens = (kSmem + 15) / 16 * 16;  // paged: the lengths
+constexpr int kSmemPaged = kOffLens + kGqaMaxSeqs * 4;
 static_assert(kNumBars * 8 <= 256, "barrier area");
 static_assert(kSlotFloats == kN * kD + 2 * kN, "partial slot layout");
-static_assert(kSmem <= 232448, "dynamic shared memory per CTA");
+static_assert(kSmemPaged <= 232448, "dynamic shared memory per CTA");
 static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0, "operand tiles keep the 1024-byte swizzle alignment");
 static_assert(kGqaMaxSeqs <= 8 * kScan, "each prefix thread keeps at most 8 lengths in registers");
 
@@ -104,6 +108,34 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// Sums kVals values over the warp at once, halving the values a lane keeps at each step; returns the index of the
+// one whose sum the lane ends with.
+template <int kVals>
+__device__ __forceinline__ int warp_sums(const float (&vals)[kVals], int lane, float& sum) {
+  float v[kVals];
+#pragma unroll
+  for (int i = 0; i < kVals; ++i) v[i] = vals[i];
+  int at = 0;
+#pragma unroll
+  for (int o = 16, n = kVals; o > 0; o >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = (lane & o) != 0;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float send = up ? v[i] : v[i + n];
+        const float keep = up ? v[i + n] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      }
+      at += up ? n : 0;
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    }
+  }
+  sum = v[0];
+  return at;
 }
 
 // Byte offset of element (row, col) of a 16-row operand tile stored K-major with the 128-byte
@@ -142,13 +174,21 @@ __device__ __forceinline__ void add_prefix(const Params& p, int b, int j, int r,
 #pragma unroll
   for (int h = 0; h < kGP; ++h) {
     const float m_new = fmaxf(M[h], mc[h]);
-    const float a_old = exp2f(M[h] - m_new);
-    const float a_c = exp2f(mc[h] - m_new);
+    const float a_old = ex2_approx(M[h] - m_new);
+    const float a_c = ex2_approx(mc[h] - m_new);
     O[h] = O[h] * a_old + oc[h] * a_c;
     L[h] = L[h] * a_old + lc[h] * a_c;
     M[h] = m_new;
   }
 }
+
+// Paged: the caches in boxes of kFold rows, for sink keys folded into a window's first tile.
+template <bool kPaged>
+struct FoldMaps {};
+template <>
+struct FoldMaps<true> {
+  CUtensorMap k, v;
+};
 
 // kGP: the group size rounded up to a power of two (1..16); p.G <= kGP is the real group size.
 // kPaged: keys and values come through a block table, under a sliding window with sink tokens, and a shared
@@ -156,7 +196,8 @@ __device__ __forceinline__ void add_prefix(const Params& p, int b, int j, int r,
 template <int kGP, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
     gqa_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                      const __grid_constant__ CUtensorMap tmQ, const Params p) {
+                      const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ FoldMaps<kPaged> tm16,
+                      const Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint64_t* empty = full + kStages;
@@ -176,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* misc = reinterpret_cast<int*>(smem + kOffMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 12);
   int* pre = reinterpret_cast<int*>(smem + kOffPre);
+  int* lens = reinterpret_cast<int*>(smem + kOffLens);  // paged only
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -227,6 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i0 + k < i1) {
         const int len = p.seq_lens[i0 + k];
         bad |= (len < 0 || len > p.L_cap);
+        if (kPaged) lens[i0 + k] = len;
         nt[k] = kPaged ? span_of(len, p.L_cap, p.kv).nt : seq_tiles(len, p.L_cap);
         sum += nt[k];
       }
@@ -292,78 +335,83 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp == 0 && kPaged) {
-    // =========================== TMA producer, paged ===========================
-    // A tile is 128 / page_size pages (one part of a page from 128 up); lane (page, K or V, half of the
-    // dimensions) issues that box, so the boxes of a tile go out together even at 16-token pages. The next
-    // tile's table entry is read while this one's slot is waited for. Pages no query sees are not loaded.
-    const uint64_t policy = l2_policy_evict_first();
-    const int page = 1 << p.kv.page_shift;
-    const int rows = page < kKeys ? page : kKeys;
-    const int lp = lane >> 2;         // page of the tile
-    const int box = lane & 3;         // K low, K high, V low, V high
-    const int row0 = lp * rows;
-    const bool mine = row0 < kKeys;
-    int it = 0;
-    int pi = 0;
-    bool ok = true;
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity));
-    };
-    for (int x = beg; x < end && ok; ++pi) {
-      const Piece pc = locate(x);
-      const Span sp = span_of(p.seq_lens[pc.b], p.L_cap, p.kv);
-      const int32_t* table = p.kv.block_table + static_cast<int64_t>(pc.b) * p.kv.max_pages;
-      auto entry = [&](int t) {  // this lane's page in tile t: -2 nothing to load, -1 a bad entry (reads as zeros)
-        const int key = sp.key_tile(t) * kKeys + row0;
-        if (!mine || !sp.sees_any(key, rows)) return -2;
-        const int id = table[key >> p.kv.page_shift];
-        return static_cast<uint32_t>(id) < static_cast<uint32_t>(p.kv.num_pages) ? id : -1;
+    if constexpr (kPaged) {
+      // =========================== TMA producer, paged ===========================
+      // A tile is 128 / page_size pages (one part of a page from 128 up); lane (page, K or V, half of the
+      // dimensions) issues that box, so the boxes of a tile go out together even at 16-token pages. The next
+      // tile's table entry is read while this one's slot is waited for. Pages no query sees are not loaded.
+      const uint64_t policy = l2_policy_evict_first();
+      const int page = 1 << p.kv.page_shift;
+      const int rows = page < kKeys ? page : kKeys;
+      const int lp = lane >> 2;         // page of the tile
+      const int box = lane & 3;         // K low, K high, V low, V high
+      int it = 0;
+      int pi = 0;
+      bool ok = true;
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity));
       };
-      int id = entry(pc.tl);
-      const int qb = pi & 1;
-      wait_all(&q_empty[qb], ((pi >> 1) & 1) ^ 1);
-      if (!ok) break;
-      if (lane == 0) {
-        uint8_t* qs = smem + kOffQ + qb * kQBytes;
-        const int qrow = pc.b * p.h_q + pc.j * p.G;
-        mbar_arrive_expect_tx(&q_full[qb], kQBytes);
-        tma_load_2d(qs, &tmQ, &q_full[qb], 0, qrow);
-        tma_load_2d(qs + 2048, &tmQ, &q_full[qb], 64, qrow);
-      }
-      for (int t = pc.tl; t < pc.tl + pc.n; ++t, ++it) {
-        const int next = t + 1 < pc.tl + pc.n ? entry(t + 1) : -2;
-        const int st = it % kStages;
-        wait_all(&empty[st], static_cast<uint32_t>(((it / kStages) & 1) ^ 1));
+      for (int x = beg; x < end && ok; ++pi) {
+        const Piece pc = locate(x);
+        const DecodeSpan sp = span_of(lens[pc.b], p.L_cap, p.kv);
+        const int32_t* table = p.kv.block_table + static_cast<int64_t>(pc.b) * p.kv.max_pages;
+        auto entry = [&](int t) {  // this lane's page in tile t: -2 nothing to load, -1 a bad entry (reads as zeros)
+          const bool folded = t == 0 && sp.fold > 0;  // boxes of kFold rows
+          const int n = folded ? kFold : rows;
+          const int key = sp.key_of(t, lp * n);
+          if (lp * n >= kKeys || !sp.sees_any(key, n)) return -2;
+          const int id = table[key >> p.kv.page_shift];
+          return static_cast<uint32_t>(id) < static_cast<uint32_t>(p.kv.num_pages) ? id : -1;
+        };
+        int id = entry(pc.tl);
+        const int qb = pi & 1;
+        wait_all(&q_empty[qb], ((pi >> 1) & 1) ^ 1);
         if (!ok) break;
-        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, id != -2));
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * static_cast<uint32_t>(rows) * 128u);
-        __syncwarp();
-        if (id != -2) {
-          const int key = sp.key_tile(t) * kKeys + row0;
-          uint8_t* dst = smem + st * kStageBytes + box * kBox + row0 * 128;
-          const int z = id < 0 ? -1 : id * p.h_kv + pc.j;
-          tma_load_3d(dst, box < 2 ? &tmK : &tmV, &full[st], (box & 1) * 64, key & (page - 1), z, policy);
-          if (id < 0) atomicExch(p.status, kStatusBadPage);
+        if (lane == 0) {
+          uint8_t* qs = smem + kOffQ + qb * kQBytes;
+          const int qrow = pc.b * p.h_q + pc.j * p.G;
+          mbar_arrive_expect_tx(&q_full[qb], kQBytes);
+          tma_load_2d(qs, &tmQ, &q_full[qb], 0, qrow);
+          tma_load_2d(qs + 2048, &tmQ, &q_full[qb], 64, qrow);
         }
-        id = next;
+        for (int t = pc.tl; t < pc.tl + pc.n; ++t, ++it) {
+          const int next = t + 1 < pc.tl + pc.n ? entry(t + 1) : -2;
+          const int st = it % kStages;
+          wait_all(&empty[st], static_cast<uint32_t>(((it / kStages) & 1) ^ 1));
+          if (!ok) break;
+          const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, id != -2));
+          const bool folded = t == 0 && sp.fold > 0;
+          const int n = folded ? kFold : rows;
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * static_cast<uint32_t>(n) * 128u);
+          __syncwarp();
+          if (id != -2) {
+            const int key = sp.key_of(t, lp * n);
+            uint8_t* dst = smem + st * kStageBytes + box * kBox + lp * n * 128;
+            const int z = id < 0 ? -1 : id * p.h_kv + pc.j;
+            const CUtensorMap* map = folded ? (box < 2 ? &tm16.k : &tm16.v) : (box < 2 ? &tmK : &tmV);
+            tma_load_3d(dst, map, &full[st], (box & 1) * 64, key & (page - 1), z, policy);
+            if (id < 0) atomicExch(p.status, kStatusBadPage);
+          }
+          id = next;
+        }
+        x += pc.n;
       }
-      x += pc.n;
+      if (lane == 0) {
+        if (!ok) atomicExch(p.status, kStatusWaitEmptyTimeout);
+        const int n = it < kStages ? it : kStages;
+        for (int i = it - n; i < it; ++i)
+          if (!mbar_wait(&full[i % kStages], static_cast<uint32_t>((i / kStages) & 1))) {
+            atomicExch(p.status, kStatusDrainTimeout);
+            break;
+          }
+        for (int q = pi - 2 < 0 ? 0 : pi - 2; q < pi; ++q)
+          if (!mbar_wait(&q_full[q & 1], (q >> 1) & 1)) {
+            atomicExch(p.status, kStatusDrainTimeout);
+            break;
+          }
+      }
+      __syncwarp();
     }
-    if (lane == 0) {
-      if (!ok) atomicExch(p.status, kStatusWaitEmptyTimeout);
-      const int n = it < kStages ? it : kStages;
-      for (int i = it - n; i < it; ++i)
-        if (!mbar_wait(&full[i % kStages], static_cast<uint32_t>((i / kStages) & 1))) {
-          atomicExch(p.status, kStatusDrainTimeout);
-          break;
-        }
-      for (int q = pi - 2 < 0 ? 0 : pi - 2; q < pi; ++q)
-        if (!mbar_wait(&q_full[q & 1], (q >> 1) & 1)) {
-          atomicExch(p.status, kStatusDrainTimeout);
-          break;
-        }
-    }
-    __syncwarp();
   } else if (warp == 0) {
     // =========================== TMA producer ===========================
     if (lane == 0) {
@@ -511,14 +559,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       int pi = 0;
       for (int x = beg; x < end; ++pi) {
         const Piece pc = locate(x);
-        const int len = p.seq_lens[pc.b];
-        Span sp{};
+        const int len = kPaged ? lens[pc.b] : p.seq_lens[pc.b];
+        DecodeSpan sp{};
         if constexpr (kPaged) sp = span_of(len, p.L_cap, p.kv);
         // a1, a2: the rescale factors of the previous tile and of the one before it
         float m_run[kGP], l_thr[kGP], o_acc[kGP], a1[kGP], a2[kGP];
 #pragma unroll
         for (int h = 0; h < kGP; ++h) {
-          m_run[h] = kPaged ? -FLT_MAX : -INFINITY;  // finite: a first tile of -inf scores alone counts nothing
+          // paged: finite, as a first tile of -inf scores alone counts nothing; padding heads never outgrow theirs
+          m_run[h] = kPaged ? (h < p.G ? -FLT_MAX : FLT_MAX) : -INFINITY;
           l_thr[h] = 0.0f;
           o_acc[h] = 0.0f;
           a1[h] = a2[h] = 0.0f;
@@ -547,28 +596,66 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int h = 0; h < kGP; ++h) o_acc[h] = fmaf(o_acc[h], a2[h], so[16 + h]);
           }
 
-          const bool valid = kPaged ? sp.sees(sp.key_tile(t) * kKeys + r) : t * kKeys + r < len;
+          const bool valid = kPaged ? sp.sees(sp.key_of(t, r)) : t * kKeys + r < len;
           float sv[kGP], alpha[kGP];
+          if constexpr (kPaged) {
+            // The maxima in use stay until some score is more than 2^kGrowth times above one (probabilities are then at
+            // most 2^kGrowth, exact to the same relative bf16 step), so most tiles need one barrier that tells of such a
+            // score instead of kGP maxima over 128 threads (at 16 heads a tile took 2200 cycles that way, more than its
+            // share of the memory's time).
+            bool far = false;
 #pragma unroll
-          for (int h = 0; h < kGP; ++h) {
-            sv[h] = valid ? so[h] * p.scale_log2 : -INFINITY;
-            const float mx = warp_max_f32(sv[h]);
-            if (lane == 0) red_max[(sb * 4 + q4) * kN + h] = mx;
-          }
-          named_bar_sync(1, kSoft);
-          uint8_t* pt = smem + kOffP + sb * kPBytes;
+            for (int h = 0; h < kGP; ++h) {
+              sv[h] = valid ? so[h] * p.scale_log2 : -INFINITY;
+              far |= sv[h] > m_run[h] + kGrowth;
+              alpha[h] = 1.0f;
+            }
+            if (named_bar_any(1, kSoft, far)) {
 #pragma unroll
-          for (int h = 0; h < kGP; ++h) {
-            const float* rm = red_max + sb * 4 * kN + h;
-            const float mt = fmaxf(fmaxf(rm[0], rm[kN]), fmaxf(rm[2 * kN], rm[3 * kN]));
-            const float m_new = fmaxf(m_run[h], mt);  // finite: every tile holds a valid key
-            alpha[h] = ex2_approx(m_run[h] - m_new);
-            const float pr = ex2_approx(sv[h] - m_new);
-            l_thr[h] = fmaf(l_thr[h], alpha[h], pr);
-            m_run[h] = m_new;
-            if (h < p.G) {
-              const __nv_bfloat16 pb = __float2bfloat16_rn(pr);
-              *reinterpret_cast<__nv_bfloat16*>(pt + sw128_offset(h, r)) = pb;
+              for (int h = 0; h < kGP; ++h) {
+                const float mx = warp_max_f32(sv[h]);
+                if (lane == 0) red_max[(sb * 4 + q4) * kN + h] = mx;
+              }
+              named_bar_sync(1, kSoft);
+#pragma unroll
+              for (int h = 0; h < kGP; ++h) {
+                const float* rm = red_max + sb * 4 * kN + h;
+                const float mt = fmaxf(fmaxf(rm[0], rm[kN]), fmaxf(rm[2 * kN], rm[3 * kN]));
+                if (mt > m_run[h] + kGrowth) {
+                  alpha[h] = ex2_approx(m_run[h] - mt);
+                  m_run[h] = mt;
+                }
+              }
+            }
+            uint8_t* pt = smem + kOffP + sb * kPBytes;
+#pragma unroll
+            for (int h = 0; h < kGP; ++h) {
+              const float pr = ex2_approx(sv[h] - m_run[h]);
+              l_thr[h] = fmaf(l_thr[h], alpha[h], pr);
+              if (h < p.G) *reinterpret_cast<__nv_bfloat16*>(pt + sw128_offset(h, r)) = __float2bfloat16_rn(pr);
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < kGP; ++h) {
+              sv[h] = valid ? so[h] * p.scale_log2 : -INFINITY;
+              const float mx = warp_max_f32(sv[h]);
+              if (lane == 0) red_max[(sb * 4 + q4) * kN + h] = mx;
+            }
+            named_bar_sync(1, kSoft);
+            uint8_t* pt = smem + kOffP + sb * kPBytes;
+#pragma unroll
+            for (int h = 0; h < kGP; ++h) {
+              const float* rm = red_max + sb * 4 * kN + h;
+              const float mt = fmaxf(fmaxf(rm[0], rm[kN]), fmaxf(rm[2 * kN], rm[3 * kN]));
+              const float m_new = fmaxf(m_run[h], mt);  // finite: every tile holds a valid key
+              alpha[h] = ex2_approx(m_run[h] - m_new);
+              const float pr = ex2_approx(sv[h] - m_new);
+              l_thr[h] = fmaf(l_thr[h], alpha[h], pr);
+              m_run[h] = m_new;
+              if (h < p.G) {
+                const __nv_bfloat16 pb = __float2bfloat16_rn(pr);
+                *reinterpret_cast<__nv_bfloat16*>(pt + sw128_offset(h, r)) = pb;
+              }
             }
           }
           if (!valid) {
@@ -579,7 +666,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint4* v0 = reinterpret_cast<uint4*>(smem + st * kStageBytes + 2 * kBox + r * 128);
               uint4* v1 = reinterpret_cast<uint4*>(smem + st * kStageBytes + 3 * kBox + r * 128);
 #pragma unroll
-              for (int c = 0; c < 8; ++c) v0[c] = v1[c] = make_uint4(0u, 0u, 0u, 0u);
+              for (int c = 0; c < 8; ++c) {  // the order keeps neighbouring rows in different banks
+                const int x = c ^ (r & 7);
+                v0[x] = v1[x] = make_uint4(0u, 0u, 0u, 0u);
+              }
             } else {
               atomicExch(p.status, kStatusWaitFullTimeout);
             }
@@ -670,9 +760,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- the piece's softmax denominators: sum of the 128 key threads' partial sums
         float l_tot[kGP];
 #pragma unroll
-        for (int h = 0; h < kGP; ++h) {
+        for (int h = 0; h < (kPaged ? 0 : kGP); ++h) {
           const float sm = warp_sum(l_thr[h]);
           if (lane == 0) red_sum[q4 * kN + h] = sm;
+        }
+        if constexpr (kPaged) {
+          float sum;
+          const int h = warp_sums(l_thr, lane, sum);
+          red_sum[q4 * kN + h] = sum;
         }
         named_bar_sync(2, kSoft);
 #pragma unroll
@@ -687,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < kGP; ++h)
             if (h < p.G) {
-              const __nv_bfloat16 v = __float2bfloat16_rn(o_acc[h] / l_tot[h]);
+              const __nv_bfloat16 v = __float2bfloat16_rn(kPaged ? __fdividef(o_acc[h], l_tot[h]) : o_acc[h] / l_tot[h]);
               outp[h * kD] = *reinterpret_cast<const uint16_t*>(&v);
             }
           named_bar_sync(2, kSoft);  // red_sum is reused by the next piece
@@ -786,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int h = 0; h < kGP; ++h)
               if (h < p.G) {
-                const __nv_bfloat16 v = __float2bfloat16_rn(O[h] / L[h]);
+                const __nv_bfloat16 v = __float2bfloat16_rn(kPaged ? __fdividef(O[h], L[h]) : O[h] / L[h]);
                 outp[h * kD] = *reinterpret_cast<const uint16_t*>(&v);
               }
           }
@@ -812,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int h = 0; h < kGP; ++h)
                 if (h < p.G) {
-                  const __nv_bfloat16 v = __float2bfloat16_rn(O[h] / L[h]);
+                  const __nv_bfloat16 v = __float2bfloat16_rn(kPaged ? __fdividef(O[h], L[h]) : O[h] / L[h]);
                   o[h * kD] = *reinterpret_cast<const uint16_t*>(&v);
                 }
             }
@@ -856,29 +951,30 @@ bool encode_q(CUtensorMap* map, const uint16_t* q, int rows) {
 }
 
 template <int kGP, bool kPaged>
-cudaError_t launch_g(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, const Params& p, int grid,
-                     cudaStream_t stream) {
+cudaError_t launch_g(const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q,
+                     const FoldMaps<kPaged>& fold, const Params& p, int grid, cudaStream_t stream) {
+  constexpr int kBytes = kPaged ? kSmemPaged : kSmem;
   constexpr int kMaxDev = 64;  // the shared-memory opt-in is per device: done once on each
   static std::atomic<bool> done[kMaxDev];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= kMaxDev || !done[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(gqa_decode_kernel<kGP, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(gqa_decode_kernel<kGP, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
     if (dev < kMaxDev) done[dev].store(true, std::memory_order_release);
   }
-  return launch_pdl(gqa_decode_kernel<kGP, kPaged>, dim3(grid), dim3(kThreads), kSmem, stream, k, v, q, p);
+  return launch_pdl(gqa_decode_kernel<kGP, kPaged>, dim3(grid), dim3(kThreads), kBytes, stream, k, v, q, fold, p);
 }
 
 template <bool kPaged>
-cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq, const Params& p, int grid,
-                   cudaStream_t stream) {
-  if (p.G <= 1) return launch_g<1, kPaged>(tk, tv, tq, p, grid, stream);
-  if (p.G <= 2) return launch_g<2, kPaged>(tk, tv, tq, p, grid, stream);
-  if (p.G <= 4) return launch_g<4, kPaged>(tk, tv, tq, p, grid, stream);
-  if (p.G <= 8) return launch_g<8, kPaged>(tk, tv, tq, p, grid, stream);
-  return launch_g<16, kPaged>(tk, tv, tq, p, grid, stream);
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq, const FoldMaps<kPaged>& fold,
+                   const Params& p, int grid, cudaStream_t stream) {
+  if (p.G <= 1) return launch_g<1, kPaged>(tk, tv, tq, fold, p, grid, stream);
+  if (p.G <= 2) return launch_g<2, kPaged>(tk, tv, tq, fold, p, grid, stream);
+  if (p.G <= 4) return launch_g<4, kPaged>(tk, tv, tq, fold, p, grid, stream);
+  if (p.G <= 8) return launch_g<8, kPaged>(tk, tv, tq, fold, p, grid, stream);
+  return launch_g<16, kPaged>(tk, tv, tq, fold, p, grid, stream);
 }
 
 }  // namespace gqa
@@ -894,6 +990,11 @@ cudaError_t launch_gqa_decode(const GqaPlan& plan, cudaStream_t stream) {
       !encode_kv(&tv, plan.v_cache, blocks, plan.h_kv, rows, box_rows) ||
       !encode_q(&tq, plan.q, plan.B * plan.h_q))
     return cudaErrorInvalidValue;
+  FoldMaps<true> fold{tk, tv};
+  if (paged && plan.paged.window > 0 && plan.paged.n_sink > 0 && box_rows != kFold &&
+      (!encode_kv(&fold.k, plan.k_cache, blocks, plan.h_kv, rows, kFold) ||
+       !encode_kv(&fold.v, plan.v_cache, blocks, plan.h_kv, rows, kFold)))
+    return cudaErrorInvalidValue;
   Params p{};
   p.seq_lens = plan.seq_lens;
   p.out = plan.out;
@@ -908,8 +1009,8 @@ cudaError_t launch_gqa_decode(const GqaPlan& plan, cudaStream_t stream) {
   p.scale_log2 = plan.scale_log2;
   p.kv = plan.paged;
   p.prefix = plan.prefix;
-  return paged ? launch<true>(tk, tv, tq, p, plan.num_ctas, stream)
-               : launch<false>(tk, tv, tq, p, plan.num_ctas, stream);
+  return paged ? launch<true>(tk, tv, tq, fold, p, plan.num_ctas, stream)
+               : launch<false>(tk, tv, tq, FoldMaps<false>{}, p, plan.num_ctas, stream);
 }
 
 }  // namespace moe

@@ -34,10 +34,26 @@ __device__ __forceinline__ Span span_of_range(int len, int lo, int n_sink) {
 __device__ __forceinline__ int window_start(int pos, int window) {
   return window > 0 && pos >= window ? pos - window + 1 : 0;
 }
-// One query at the end of a sequence of len keys; a length outside [0, L_cap] counts as empty.
-__device__ __forceinline__ Span span_of(int len, int L_cap, const PagedKv& kv) {
+// One query at the end of a sequence of len keys; a length outside [0, L_cap] counts as empty. When the rows of the
+// window's first tile that lie before the window have room for the sink keys (in runs of kFold rows), those are
+// folded into them and need no tile of their own.
+constexpr int kFold = 16;
+struct DecodeSpan : Span {
+  int fold;  // rows of the first tile that hold keys 0 .. fold - 1 instead
+  __device__ __forceinline__ int key_of(int t, int row) const { return t == 0 && row < fold ? row : key_tile(t) * kKeys + row; }
+};
+__device__ __forceinline__ DecodeSpan span_of(int len, int L_cap, const PagedKv& kv) {
   if (len < 0 || len > L_cap) len = 0;
-  return span_of_range(len, window_start(len - 1, kv.window), kv.n_sink);
+  DecodeSpan s;
+  static_cast<Span&>(s) = span_of_range(len, window_start(len - 1, kv.window), kv.n_sink);
+  const int before = s.lo - s.w0 * kKeys;
+  s.fold = 0;
+  if (s.ns > 0 && s.sk <= kKeys && (s.sk + kFold - 1) / kFold <= before / kFold) {
+    s.fold = (s.sk + kFold - 1) / kFold * kFold;
+    s.nt -= s.ns;
+    s.ns = 0;
+  }
+  return s;
 }
 
 // Row-block partials: per piece the unnormalised output as [16 groups of 8 dimensions][kRowTile rows][8], so that the

@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (mbar_wait(&full[st], static_cast<uint32_t>((idx / kStages) & 1))) {
               uint4* v = reinterpret_cast<uint4*>(smem + kOffRing + st * kTile + part * kBox + r * 128);
 #pragma unroll
-              for (int x = 0; x < 8; ++x) v[x] = make_uint4(0u, 0u, 0u, 0u);
+              for (int x = 0; x < 8; ++x) v[x ^ (r & 7)] = make_uint4(0u, 0u, 0u, 0u);  // neighbours in other banks
             } else {
               atomicExch(p.status, kStatusWaitFullTimeout);
             }
