@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int issued = 0;  // K and V tiles whose copies are under way or done
     bool ok = true;
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity));
+      ok = __all_sync(0xffffffffu, ok && mbar_wait_soon(bar, parity));
     };
     for (int s; ok && (s = next_piece()) < kItems;) {
       const Span sp = items[s].k.sp;
@@ -495,11 +495,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // never leave copies in flight: the last stages and queries issued
     if (lane == 0) {
       for (int i = issued < kStages ? 0 : issued - kStages; i < issued; ++i)
-        if (!mbar_wait(&full[i % kStages], static_cast<uint32_t>((i / kStages) & 1))) {
+        if (!mbar_wait_soon(&full[i % kStages], static_cast<uint32_t>((i / kStages) & 1))) {
           atomicExch(p.status, kStatusDrainTimeout);
           break;
         }
-      if (pi > 0 && !mbar_wait(q_full, static_cast<uint32_t>((pi - 1) & 1))) atomicExch(p.status, kStatusDrainTimeout);
+      if (pi > 0 && !mbar_wait_soon(q_full, static_cast<uint32_t>((pi - 1) & 1))) atomicExch(p.status, kStatusDrainTimeout);
     }
     __syncwarp();
   } else if (warp < 3) {
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) atomicExch(p.status, kStatusWaitFullTimeout);
     // every MMA has completed before TMEM is released
     if (elect_one()) umma_commit(mma_done);
-    if (!mbar_wait(mma_done, 0) && lane == 0) atomicExch(p.status, kStatusDrainTimeout);
+    if (!mbar_wait_soon(mma_done, 0) && lane == 0) atomicExch(p.status, kStatusDrainTimeout);
     __syncwarp();
   } else if (warp == 3) {
     // =========================== announces the pieces ===========================
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Piece c{};
         more = walk.next(c);
         const int s = di % kItems;
-        if (!mbar_wait(&d_empty[s], static_cast<uint32_t>(((di / kItems) & 1) ^ 1))) {
+        if (!mbar_wait_soon(&d_empty[s], static_cast<uint32_t>(((di / kItems) & 1) ^ 1))) {
           atomicExch(p.status, kStatusWaitEmptyTimeout);
           break;
         }
@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // this row of the V tile is cleared (the wait orders the overwrite behind the tile's landing)
             const int idx = 2 * it + 1;
             const int st = idx % kStages;
-            if (mbar_wait(&full[st], static_cast<uint32_t>((idx / kStages) & 1))) {
+            if (mbar_wait_soon(&full[st], static_cast<uint32_t>((idx / kStages) & 1))) {
               uint4* v = reinterpret_cast<uint4*>(smem + kOffRing + st * kTile + part * kBox + r * 128);
 #pragma unroll
               for (int x = 0; x < 8; ++x) v[x ^ (r & 7)] = make_uint4(0u, 0u, 0u, 0u);  // neighbours in other banks

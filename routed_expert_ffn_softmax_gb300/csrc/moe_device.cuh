@@ -77,12 +77,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
-// The same wait for hand-offs that are due within a few hundred cycles: the timer is read only after a run of tries.
+// The same wait in few instructions, for kernels whose many waits would crowd the instruction cache: limited by a count
+// of tries (each suspends the thread for some tens of nanoseconds, so about the same two seconds).
 __device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
-  for (int i = 0; i < 64; ++i)
+  for (int i = 0; i < (1 << 25); ++i)
     if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity);
+  return false;
 }
 
 // ---------------------------------------------------------------- TMA
@@ -332,6 +333,11 @@ __device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
