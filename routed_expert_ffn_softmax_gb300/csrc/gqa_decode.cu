@@ -182,6 +182,13 @@ __device__ __forceinline__ void add_prefix(const Params& p, int b, int j, int r,
   }
 }
 
+// The paged kernels' waits are compact: with the others' loops at every wait their code (120 KB at 16 heads) outgrew the
+// instruction cache.
+template <bool kPaged>
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
+  return kPaged ? mbar_wait_soon(bar, parity) : mbar_wait(bar, parity);
+}
+
 // Paged: the caches in boxes of kFold rows, for sink keys folded into a window's first tile.
 template <bool kPaged>
 struct FoldMaps {};
@@ -337,19 +344,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && kPaged) {
     if constexpr (kPaged) {
       // =========================== TMA producer, paged ===========================
-      // A tile is 128 / page_size pages (one part of a page from 128 up); lane (page, K or V, half of the
-      // dimensions) issues that box, so the boxes of a tile go out together even at 16-token pages. The next
+      // A tile is 128 / page_size pages (one part of a page from 128 up); lane (page, K or V) issues that box. The next
       // tile's table entry is read while this one's slot is waited for. Pages no query sees are not loaded.
       const uint64_t policy = l2_policy_evict_first();
       const int page = 1 << p.kv.page_shift;
       const int rows = page < kKeys ? page : kKeys;
-      const int lp = lane >> 2;         // page of the tile
-      const int box = lane & 3;         // K low, K high, V low, V high
+      const int lp = lane >> 1;         // page of the tile
+      const int is_v = lane & 1;
       int it = 0;
       int pi = 0;
       bool ok = true;
       auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity));
+        ok = __all_sync(0xffffffffu, ok && bar_wait<kPaged>(bar, parity));
       };
       for (int x = beg; x < end && ok; ++pi) {
         const Piece pc = locate(x);
@@ -382,14 +388,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, id != -2));
           const bool folded = t == 0 && sp.fold > 0;
           const int n = folded ? kFold : rows;
-          if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * static_cast<uint32_t>(n) * 128u);
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * static_cast<uint32_t>(n) * 256u);
           __syncwarp();
           if (id != -2) {
             const int key = sp.key_of(t, lp * n);
-            uint8_t* dst = smem + st * kStageBytes + box * kBox + lp * n * 128;
+            uint8_t* dst = smem + st * kStageBytes + is_v * 2 * kBox + tile_row(lp * n);
             const int z = id < 0 ? -1 : id * p.h_kv + pc.j;
-            const CUtensorMap* map = folded ? (box < 2 ? &tm16.k : &tm16.v) : (box < 2 ? &tmK : &tmV);
-            tma_load_3d(dst, map, &full[st], (box & 1) * 64, key & (page - 1), z, policy);
+            const CUtensorMap* map = folded ? (is_v ? &tm16.v : &tm16.k) : (is_v ? &tmV : &tmK);
+            tma_load_5d(dst, map, &full[st], 0, 0, 0, (key & (page - 1)) >> 3, z, policy);
             if (id < 0) atomicExch(p.status, kStatusBadPage);
           }
           id = next;
@@ -400,12 +406,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) atomicExch(p.status, kStatusWaitEmptyTimeout);
         const int n = it < kStages ? it : kStages;
         for (int i = it - n; i < it; ++i)
-          if (!mbar_wait(&full[i % kStages], static_cast<uint32_t>((i / kStages) & 1))) {
+          if (!bar_wait<kPaged>(&full[i % kStages], static_cast<uint32_t>((i / kStages) & 1))) {
             atomicExch(p.status, kStatusDrainTimeout);
             break;
           }
         for (int q = pi - 2 < 0 ? 0 : pi - 2; q < pi; ++q)
-          if (!mbar_wait(&q_full[q & 1], (q >> 1) & 1)) {
+          if (!bar_wait<kPaged>(&q_full[q & 1], (q >> 1) & 1)) {
             atomicExch(p.status, kStatusDrainTimeout);
             break;
           }
@@ -422,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = beg; x < end && ok; ++pi) {
         const Piece pc = locate(x);
         const int qb = pi & 1;
-        if (!mbar_wait(&q_empty[qb], ((pi >> 1) & 1) ^ 1)) {
+        if (!bar_wait<kPaged>(&q_empty[qb], ((pi >> 1) & 1) ^ 1)) {
           ok = false;
           break;
         }
@@ -434,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int z = pc.b * p.h_kv + pc.j;
         for (int t = pc.tl; t < pc.tl + pc.n; ++t, ++it) {
           const int st = it % kStages;
-          if (!mbar_wait(&empty[st], static_cast<uint32_t>(((it / kStages) & 1) ^ 1))) {
+          if (!bar_wait<kPaged>(&empty[st], static_cast<uint32_t>(((it / kStages) & 1) ^ 1))) {
             ok = false;
             break;
           }
@@ -451,12 +457,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // never leave copies in flight: the last stages and query blocks issued
       const int n = it < kStages ? it : kStages;
       for (int i = it - n; i < it; ++i)
-        if (!mbar_wait(&full[i % kStages], static_cast<uint32_t>((i / kStages) & 1))) {
+        if (!bar_wait<kPaged>(&full[i % kStages], static_cast<uint32_t>((i / kStages) & 1))) {
           atomicExch(p.status, kStatusDrainTimeout);
           break;
         }
       for (int q = pi - 2 < 0 ? 0 : pi - 2; q < pi; ++q)
-        if (!mbar_wait(&q_full[q & 1], (q >> 1) & 1)) {
+        if (!bar_wait<kPaged>(&q_full[q & 1], (q >> 1) & 1)) {
           atomicExch(p.status, kStatusDrainTimeout);
           break;
         }
@@ -478,15 +484,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int sb = i & 1;
         const uint32_t ph = static_cast<uint32_t>((i >> 1) & 1);
         const int st = i % kStages;
-        if (ok && !mbar_wait(&p_full[sb], ph)) fail(kStatusWaitFullTimeout);
-        if (ok && !mbar_wait(&o_free[sb], ph ^ 1)) fail(kStatusWaitEmptyTimeout);
+        if (ok && !bar_wait<kPaged>(&p_full[sb], ph)) fail(kStatusWaitFullTimeout);
+        if (ok && !bar_wait<kPaged>(&o_free[sb], ph ^ 1)) fail(kStatusWaitEmptyTimeout);
         if (ok) {
           tc_fence_after_sync();
           const uint32_t v = sbase + st * kStageBytes + 2 * kBox;
           const uint32_t pt = sbase + kOffP + sb * kPBytes;
 #pragma unroll
           for (int s = 0; s < kKeys / 16; ++s)
-            umma_bf16(tmem_base + col_o(sb), umma_desc_sw128_mn(v + s * 2048, kBox),
+            umma_bf16(tmem_base + col_o(sb),
+                      kPaged ? umma_desc_sw128_mn_sbo(v + s * 2 * kGroupBytes, kUpper, kGroupBytes)
+                             : umma_desc_sw128_mn(v + s * 2048, kBox),
                       umma_desc_sw128(pt + (s >> 2) * 2048 + (s & 3) * 32), idesc_o, s > 0);
         }
         umma_commit(&o_full[sb]);
@@ -497,20 +505,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = beg; x < end; ++pi) {
         const Piece pc = locate(x);
         const int qb = pi & 1;
-        if (ok && !mbar_wait(&q_full[qb], (pi >> 1) & 1)) fail(kStatusWaitFullTimeout);
+        if (ok && !bar_wait<kPaged>(&q_full[qb], (pi >> 1) & 1)) fail(kStatusWaitFullTimeout);
         const uint32_t qs = sbase + kOffQ + qb * kQBytes;
         for (int t = 0; t < pc.n; ++t, ++it) {
           const int st = it % kStages;
           const int sb = it & 1;
-          if (ok && !mbar_wait(&full[st], static_cast<uint32_t>((it / kStages) & 1))) fail(kStatusWaitFullTimeout);
-          if (ok && !mbar_wait(&s_free[sb], static_cast<uint32_t>(((it >> 1) & 1) ^ 1)))
+          if (ok && !bar_wait<kPaged>(&full[st], static_cast<uint32_t>((it / kStages) & 1))) fail(kStatusWaitFullTimeout);
+          if (ok && !bar_wait<kPaged>(&s_free[sb], static_cast<uint32_t>(((it >> 1) & 1) ^ 1)))
             fail(kStatusWaitEmptyTimeout);
           if (ok) {
             tc_fence_after_sync();
             const uint32_t k = sbase + st * kStageBytes;
 #pragma unroll
             for (int s = 0; s < kD / 16; ++s)
-              umma_bf16(tmem_base + col_s(sb), umma_desc_sw128(k + (s >> 2) * kBox + (s & 3) * 32),
+              umma_bf16(tmem_base + col_s(sb),
+                        kPaged ? umma_desc_sw128_sbo(k + (s >> 2) * kUpper + (s & 3) * 32, kGroupBytes)
+                               : umma_desc_sw128(k + (s >> 2) * kBox + (s & 3) * 32),
                         umma_desc_sw128(qs + (s >> 2) * 2048 + (s & 3) * 32), idesc_s, s > 0);
           }
           umma_commit(&s_full[sb]);
@@ -524,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it > 0) issue_o(it - 1);
       // every MMA has completed before TMEM is released
       umma_commit(mma_done);
-      if (!mbar_wait(mma_done, 0)) atomicExch(p.status, kStatusDrainTimeout);
+      if (!bar_wait<kPaged>(mma_done, 0)) atomicExch(p.status, kStatusDrainTimeout);
     }
     __syncwarp();
   } else {
@@ -537,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // executed by all 32 lanes together
     bool ok = true;
     auto wait_warp = [&](uint64_t* bar, uint32_t parity, int code) {
-      const bool w = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity));
+      const bool w = __all_sync(0xffffffffu, ok && bar_wait<kPaged>(bar, parity));
       if (!w && ok) {
         ok = false;
         atomicExch(p.status, code);
@@ -662,9 +672,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // keys past the sequence: the cache rows there are arbitrary (even NaN) and a zero
             // probability times NaN is NaN, so clear this key's row of the V tile
             // (the wait makes the tile's landing visible to this thread before it overwrites)
-            if (mbar_wait(&full[st], static_cast<uint32_t>((it / kStages) & 1))) {
-              uint4* v0 = reinterpret_cast<uint4*>(smem + st * kStageBytes + 2 * kBox + r * 128);
-              uint4* v1 = reinterpret_cast<uint4*>(smem + st * kStageBytes + 3 * kBox + r * 128);
+            if (bar_wait<kPaged>(&full[st], static_cast<uint32_t>((it / kStages) & 1))) {
+              uint8_t* v = smem + st * kStageBytes + 2 * kBox + (kPaged ? tile_row(r) : r * 128);
+              uint4* v0 = reinterpret_cast<uint4*>(v);
+              uint4* v1 = reinterpret_cast<uint4*>(v + (kPaged ? kUpper : kBox));
 #pragma unroll
               for (int c = 0; c < 8; ++c) {  // the order keeps neighbouring rows in different banks
                 const int x = c ^ (r & 7);
@@ -926,12 +937,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
 }
 
-// A cache of `blocks` blocks (sequences or pages) x h_kv x `rows` rows.
-bool encode_kv(CUtensorMap* map, const uint16_t* base, int blocks, int h_kv, int rows, int box_rows) {
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(rows),
-                              static_cast<cuuint64_t>(blocks) * h_kv};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD) * 2, static_cast<cuuint64_t>(rows) * kD * 2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+bool encode_kv(CUtensorMap* map, const uint16_t* base, int B, int h_kv, int L_cap) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(L_cap),
+                              static_cast<cuuint64_t>(B) * h_kv};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD) * 2, static_cast<cuuint64_t>(L_cap) * kD * 2};
+  const cuuint32_t box[3] = {64, kKeys, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   TensorMapEncodeFn enc = tensor_map_encoder();
   return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), dims, strides, box, estr,
@@ -986,15 +996,21 @@ cudaError_t launch_gqa_decode(const GqaPlan& plan, cudaStream_t stream) {
   const int rows = paged ? 1 << plan.paged.page_shift : plan.L_cap;
   const int box_rows = paged && rows < kKeys ? rows : kKeys;
   CUtensorMap tk, tv, tq;
-  if (!encode_kv(&tk, plan.k_cache, blocks, plan.h_kv, rows, box_rows) ||
-      !encode_kv(&tv, plan.v_cache, blocks, plan.h_kv, rows, box_rows) ||
-      !encode_q(&tq, plan.q, plan.B * plan.h_q))
-    return cudaErrorInvalidValue;
-  FoldMaps<true> fold{tk, tv};
-  if (paged && plan.paged.window > 0 && plan.paged.n_sink > 0 && box_rows != kFold &&
-      (!encode_kv(&fold.k, plan.k_cache, blocks, plan.h_kv, rows, kFold) ||
-       !encode_kv(&fold.v, plan.v_cache, blocks, plan.h_kv, rows, kFold)))
-    return cudaErrorInvalidValue;
+  FoldMaps<true> fold;
+  bool ok = encode_q(&tq, plan.q, plan.B * plan.h_q);
+  if (paged) {
+    const bool folds = plan.paged.window > 0 && plan.paged.n_sink > 0 && box_rows != kFold;
+    ok = ok && encode_paged(&tk, plan.k_cache, blocks, plan.h_kv, rows, box_rows) &&
+         encode_paged(&tv, plan.v_cache, blocks, plan.h_kv, rows, box_rows);
+    fold = {tk, tv};
+    if (folds)
+      ok = ok && encode_paged(&fold.k, plan.k_cache, blocks, plan.h_kv, rows, kFold) &&
+           encode_paged(&fold.v, plan.v_cache, blocks, plan.h_kv, rows, kFold);
+  } else {
+    ok = ok && encode_kv(&tk, plan.k_cache, plan.B, plan.h_kv, plan.L_cap) &&
+         encode_kv(&tv, plan.v_cache, plan.B, plan.h_kv, plan.L_cap);
+  }
+  if (!ok) return cudaErrorInvalidValue;
   Params p{};
   p.seq_lens = plan.seq_lens;
   p.out = plan.out;

@@ -11,6 +11,25 @@ namespace gqa {
 
 constexpr int kKeys = 128;  // keys per tile
 
+// A K or V tile of a paged cache in shared memory: groups of 8 keys, in each the lower 64 dimensions of its keys (a
+// 1024-byte swizzle atom of 8 x 128 bytes), then the upper 64. One copy then brings a whole page (with the halves
+// apart, as one copy per half wants them, a tile of 16-token pages took 32 copies of some 70 cycles each, more than its
+// share of the memory's time).
+constexpr int kGroupBytes = 2048;  // 8 keys
+constexpr int kUpper = 1024;       // the upper dimensions within a group
+__device__ __forceinline__ uint32_t tile_row(int key) { return (key >> 3) * kGroupBytes + (key & 7) * 128; }
+// The cache as {64 dimensions, 8 keys, 2 halves, groups of a page, pages x heads}; a copy moves box_rows keys.
+inline bool encode_paged(CUtensorMap* map, const uint16_t* base, int num_pages, int h_kv, int page, int box_rows) {
+  const cuuint64_t dims[5] = {64, 8, 2, static_cast<cuuint64_t>(page / 8), static_cast<cuuint64_t>(num_pages) * h_kv};
+  const cuuint64_t strides[4] = {256, 128, 2048, static_cast<cuuint64_t>(page) * 256};
+  const cuuint32_t box[5] = {64, 8, 2, static_cast<cuuint32_t>(box_rows / 8), 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  TensorMapEncodeFn enc = tensor_map_encoder();
+  return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<uint16_t*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The visible keys of a run of queries: the window [lo, len) and the sink keys [0, sk), sk <= lo. Its tiles are
 // the sink's (those before the window's first, w0), then the window's.
 struct Span {

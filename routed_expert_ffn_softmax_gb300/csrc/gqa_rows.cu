@@ -44,7 +44,7 @@ using namespace gqa;
 constexpr int kD = 128;
 constexpr int kHalf = 128;                  // rows of a half
 constexpr int kStages = 4;
-constexpr int kBox = kKeys * 64 * 2;        // 128 rows x 64 dims
+constexpr int kBox = kKeys * 64 * 2;        // queries: 128 rows x 64 dims
 constexpr int kTile = 2 * kBox;             // one K or V tile, or the queries of a half: 32 KB
 constexpr int kThreads = 640;
 constexpr int kSoft = 256;                  // softmax threads of a half: two per row, 64 columns each
@@ -426,12 +426,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   reg_dealloc<kRegsIo>();
   if (warp == 0) {
     // =========================== TMA producer ===========================
-    // A tile is 128 / page_size pages (one part of a page from 128 up): lane (page, dimension half) of the lower half
-    // warp issues K boxes, of the upper half warp V boxes. Pages no row sees are not loaded.
+    // A tile is 128 / page_size pages (one part of a page from 128 up): a lane of the lower half warp issues a K box, of
+    // the upper half warp a V box. Pages no row sees are not loaded.
     const uint64_t policy_q = l2_policy_evict_first();
     const int page = 1 << p.kv.page_shift;
     const int rows = page < kKeys ? page : kKeys;
-    const int row0 = ((lane & 15) >> 1) * rows;
+    const int row0 = (lane & 15) * rows;
     const bool is_v = lane >= 16;
     const bool mine = row0 < kKeys;
     int it = 0, pi = 0;
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int next = t + 1 < t1 ? entry(t + 1) : -2;
         const int key = sp.key_tile(t) * kKeys + row0;
         const int z = id < 0 ? -1 : id * p.h_kv + j;
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id != -2 && !is_v)) * static_cast<uint32_t>(rows) * 128u;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id != -2 && !is_v)) * static_cast<uint32_t>(rows) * 256u;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           const int idx = 2 * it + kv;
@@ -469,8 +469,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           issued = idx + 1;
           if (id != -2 && is_v == (kv == 1))
-            tma_load_3d(smem + kOffRing + st * kTile + (lane & 1) * kBox + row0 * 128, kv ? &tmV : &tmK, &full[st],
-                        (lane & 1) * 64, key & (page - 1), z, policy_q);
+            tma_load_5d(smem + kOffRing + st * kTile + tile_row(row0), kv ? &tmV : &tmK, &full[st], 0, 0, 0,
+                        (key & (page - 1)) >> 3, z, policy_q);
           if (kv == 0 && t == t0) {  // the queries go between the first K and V tiles
             wait_all(q_empty, static_cast<uint32_t>((pi & 1) ^ 1));
             if (!ok) break;
@@ -544,21 +544,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
           if (active) {
             if (ok && t > 0) {
-              const uint64_t v = umma_desc_sw128_mn(0, kBox) + (ring + st_v * (kTile >> 4));
+              const uint64_t v = umma_desc_sw128_mn_sbo(0, kUpper, kGroupBytes) + (ring + st_v * (kTile >> 4));
               umma_bf16_tmem_a(d_o, d_s, v, idesc_o, t > 1);
 #pragma unroll
               for (int x = 1; x < kKeys / 16; ++x)
-                umma_bf16_tmem_a(d_o, d_s + 8 * x, v + x * (2048 >> 4), idesc_o, true);
+                umma_bf16_tmem_a(d_o, d_s + 8 * x, v + x * (2 * kGroupBytes >> 4), idesc_o, true);
             }
             // the scores overwrite the probabilities of the tile before, whose product was issued just now: MMAs of one
             // thread run in order
             if (ok && t < n) {
-              const uint64_t k = umma_desc_sw128(0) + (ring + st_k * (kTile >> 4));
+              const uint64_t k = umma_desc_sw128_sbo(0, kGroupBytes) + (ring + st_k * (kTile >> 4));
 #pragma unroll
-              for (int x = 0; x < kD / 16; ++x) {
-                const uint32_t off = ((x >> 2) * kBox + (x & 3) * 32) >> 4;
-                umma_bf16(d_s, q + off, k + off, idesc_s, x > 0);
-              }
+              for (int x = 0; x < kD / 16; ++x)
+                umma_bf16(d_s, q + (((x >> 2) * kBox + (x & 3) * 32) >> 4), k + (((x >> 2) * kUpper + (x & 3) * 32) >> 4),
+                          idesc_s, x > 0);
             }
             // one commit tells of both: the output is read only after the last product or, to rescale it, with scores
             umma_commit(t < n ? &s_full[h] : &o_full[h]);
@@ -701,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int idx = 2 * it + 1;
             const int st = idx % kStages;
             if (mbar_wait_soon(&full[st], static_cast<uint32_t>((idx / kStages) & 1))) {
-              uint4* v = reinterpret_cast<uint4*>(smem + kOffRing + st * kTile + part * kBox + r * 128);
+              uint4* v = reinterpret_cast<uint4*>(smem + kOffRing + st * kTile + part * kUpper + tile_row(r));
 #pragma unroll
               for (int x = 0; x < 8; ++x) v[x ^ (r & 7)] = make_uint4(0u, 0u, 0u, 0u);  // neighbours in other banks
             } else {
@@ -942,7 +941,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_join_kernel(const Params
 }
 
 // ---------------------------------------------------------------- host
-bool encode(CUtensorMap* map, const uint16_t* base, uint64_t d1, uint64_t d2, uint32_t b1, uint32_t b2) {
+bool encode_q(CUtensorMap* map, const uint16_t* base, uint64_t d1, uint64_t d2, uint32_t b1, uint32_t b2) {
   const cuuint64_t dims[3] = {kD, d1, d2};
   const cuuint64_t strides[2] = {kD * 2, d1 * kD * 2};
   const cuuint32_t box[3] = {64, b1, b2};
@@ -964,9 +963,9 @@ cudaError_t launch_gqa_rows(const GqaRowsPlan& plan, cudaStream_t stream) {
   Params p{};
   p.half_tokens = kHalf / G;
   CUtensorMap tk, tv, tq;
-  if (!encode(&tk, plan.k_cache, page, static_cast<uint64_t>(plan.paged.num_pages) * plan.h_kv, box_rows, 1) ||
-      !encode(&tv, plan.v_cache, page, static_cast<uint64_t>(plan.paged.num_pages) * plan.h_kv, box_rows, 1) ||
-      !encode(&tq, plan.q, plan.h_q, plan.N, G, p.half_tokens))
+  if (!encode_paged(&tk, plan.k_cache, plan.paged.num_pages, plan.h_kv, page, box_rows) ||
+      !encode_paged(&tv, plan.v_cache, plan.paged.num_pages, plan.h_kv, page, box_rows) ||
+      !encode_q(&tq, plan.q, plan.h_q, plan.N, G, p.half_tokens))
     return cudaErrorInvalidValue;
   const int64_t pieces = prefix ? static_cast<int64_t>(plan.h_kv) * plan.prefix_blocks * plan.prefix_splits
                                 : 2 * static_cast<int64_t>(kRowsCtas);

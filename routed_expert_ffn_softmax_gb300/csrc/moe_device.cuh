@@ -118,6 +118,16 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// 5-D tiled tensor load into shared memory, completion signalled on `bar`.
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2, int c3,
+                                            int c4, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "l"(policy)
+      : "memory");
+}
+
 // 2-D tiled tensor load into shared memory, completion signalled on `bar`.
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
                                             int c1) {
@@ -209,6 +219,15 @@ __device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t smem_byte_addr, 
   return static_cast<uint64_t>((smem_byte_addr >> 4) & 0x3FFFu) |
          (static_cast<uint64_t>((mn_block_bytes >> 4) & 0x3FFFu) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
          (1ull << 46) | (2ull << 61);
+}
+
+// The same two with the distance between 8-row groups (stride byte offset) given.
+__device__ __forceinline__ uint64_t umma_desc_sw128_sbo(uint32_t smem_byte_addr, uint32_t sbo) {
+  return static_cast<uint64_t>((smem_byte_addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+__device__ __forceinline__ uint64_t umma_desc_sw128_mn_sbo(uint32_t smem_byte_addr, uint32_t mn_block_bytes, uint32_t sbo) {
+  return umma_desc_sw128_sbo(smem_byte_addr, sbo) | (static_cast<uint64_t>((mn_block_bytes >> 4) & 0x3FFFu) << 16);
 }
 
 // Instruction descriptor of tcgen05.mma kind::f16: bf16 A and B (both K-major), fp32 D,
