@@ -857,16 +857,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- joining pieces
 constexpr int kMergeThreads = 256;
-constexpr int kMergeParts = 16;  // CTAs per segment, 16 rows each
+constexpr int kMergeParts = 16;  // CTAs per cut segment, which mostly has two or three pieces
+constexpr int kJoinParts = 32;   // CTAs per segment of a prefix, which may have tens: a row for each warp
 
 // Joins a row's pieces in key order: the first, then n - 1 more from `next` on, `stride` apart. Lane: 4 dimensions.
+template <int kChunk>  // pieces whose loads are in flight together
 __device__ __forceinline__ void join_row(const Params& p, int row, int64_t first, int64_t next, int stride, int n,
                                          float& M, float& L, float4& O) {
   const int lane = threadIdx.x & 31;
   M = -FLT_MAX;
   L = 0.0f;
   O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  constexpr int kChunk = 4;  // pieces whose loads are in flight together
   for (int s0 = 0; s0 < n; s0 += kChunk) {
     float mc[kChunk], lc[kChunk];
     float4 oc[kChunk];
@@ -908,7 +909,7 @@ __global__ void __launch_bounds__(kMergeThreads) rows_merge_kernel(const Params 
     if (ti >= p.half_tokens || tok >= seg.y) continue;
     float M, L;
     float4 O;
-    join_row(p, row, 2 * static_cast<int64_t>(c) + 1, 2 * static_cast<int64_t>(c + 1), 2, seg.w, M, L, O);
+    join_row<4>(p, row, 2 * static_cast<int64_t>(c) + 1, 2 * static_cast<int64_t>(c + 1), 2, seg.w, M, L, O);
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
     const __nv_bfloat162 x0 = __floats2bfloat162_rn(O.x * inv, O.y * inv);
     const __nv_bfloat162 x1 = __floats2bfloat162_rn(O.z * inv, O.w * inv);
@@ -924,14 +925,14 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_join_kernel(const Params
   pdl_allow_successor();
   const int64_t first = static_cast<int64_t>(blockIdx.x) * p.prefix_splits;
   const int tok0 = (blockIdx.x % p.prefix_blocks) * 2 * p.half_tokens;
-  const int row0 = blockIdx.y * (kRowTile / kMergeParts);
-  for (int row = row0 + (threadIdx.x >> 5); row < row0 + kRowTile / kMergeParts; row += kMergeThreads / 32) {
+  const int row0 = blockIdx.y * (kRowTile / kJoinParts);
+  for (int row = row0 + (threadIdx.x >> 5); row < row0 + kRowTile / kJoinParts; row += kMergeThreads / 32) {
     const int hf = row / kHalf;
     const int ti = (row - hf * kHalf) / p.G;
     if (ti >= p.half_tokens || tok0 + hf * p.half_tokens + ti >= p.B) continue;
     float M, L;
     float4 O;
-    join_row(p, row, first, first + 1, 1, p.prefix_splits, M, L, O);
+    join_row<10>(p, row, first, first + 1, 1, p.prefix_splits, M, L, O);
     *reinterpret_cast<float4*>(p.pieces_o + piece_at(first, row, 4 * (threadIdx.x & 31))) = O;
     if ((threadIdx.x & 31) == 0) {
       p.pieces_m[first * kRowTile + row] = M;
@@ -1016,7 +1017,7 @@ cudaError_t launch_gqa_rows(const GqaRowsPlan& plan, cudaStream_t stream) {
     const int grid = pieces < ctas ? static_cast<int>(pieces) : ctas;
     e = launch_pdl(gqa_rows_kernel, dim3(grid), dim3(kThreads), kSmem, stream, tk, tv, tq, p);
     if (e != cudaSuccess || plan.prefix_splits == 1) return e;
-    return launch_pdl(prefix_join_kernel, dim3(static_cast<unsigned>(pieces / plan.prefix_splits), kMergeParts),
+    return launch_pdl(prefix_join_kernel, dim3(static_cast<unsigned>(pieces / plan.prefix_splits), kJoinParts),
                       dim3(kMergeThreads), 0, stream, p);
   }
   e = launch_pdl(rows_tables_kernel, dim3(1), dim3(kTableThreads), 0, stream, p);
