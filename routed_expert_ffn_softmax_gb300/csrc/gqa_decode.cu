@@ -152,35 +152,70 @@ __device__ __forceinline__ int seq_tiles(int len, int L_cap) {
   return (len <= 0 || len > L_cap) ? 0 : (len + kKeys - 1) / kKeys;
 }
 
-// Adds the shared prefix's part to the running (M, L, O) of group j's heads for sequence b; this thread holds
-// dimension r.
-template <int kGP>
-__device__ __forceinline__ void add_prefix(const Params& p, int b, int j, int r, float (&M)[kGP], float (&L)[kGP],
-                                           float (&O)[kGP]) {
-  const PrefixPartials& x = p.prefix;
-  const int block = b / (2 * x.half_seqs);
-  const int i = b - block * 2 * x.half_seqs;
-  const int half = i >= x.half_seqs ? 1 : 0;
-  const int row = half * (kRowTile / 2) + (i - half * x.half_seqs) * p.G;
-  const int64_t piece = (static_cast<int64_t>(j) * x.blocks + block) * x.stride;
-  float mc[kGP], lc[kGP], oc[kGP];
+// kVals values of a row of kN floats in shared memory.
+template <int kVals>
+__device__ __forceinline__ void load_row(const float* row, float (&v)[kVals]) {
+  if constexpr (kVals >= 4) {
 #pragma unroll
-  for (int h = 0; h < kGP; ++h) {
-    const bool in = h < p.G;
-    mc[h] = in ? __ldcg(x.m + piece * kRowTile + row + h) : -FLT_MAX;
-    lc[h] = in ? __ldcg(x.l + piece * kRowTile + row + h) : 0.0f;
-    oc[h] = in ? __ldcg(x.o + piece_at(piece, row + h, r)) : 0.0f;
-  }
+    for (int h = 0; h < kVals; h += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(row + h);
+      v[h] = f.x;
+      v[h + 1] = f.y;
+      v[h + 2] = f.z;
+      v[h + 3] = f.w;
+    }
+  } else {
 #pragma unroll
-  for (int h = 0; h < kGP; ++h) {
-    const float m_new = fmaxf(M[h], mc[h]);
-    const float a_old = ex2_approx(M[h] - m_new);
-    const float a_c = ex2_approx(mc[h] - m_new);
-    O[h] = O[h] * a_old + oc[h] * a_c;
-    L[h] = L[h] * a_old + lc[h] * a_c;
-    M[h] = m_new;
+    for (int h = 0; h < kVals; ++h) v[h] = row[h];
   }
 }
+
+// The shared prefix's part of group j's heads for sequence b, and adding it to the running (M, L, O); this thread
+// holds dimension r.
+template <int kGP>
+struct PrefixRow {
+  float m[kGP], l[kGP], o[kGP];
+  __device__ __forceinline__ void load(const Params& p, int b, int j, int r) {
+    const PrefixPartials& x = p.prefix;
+    const int block = b / (2 * x.half_seqs);
+    const int i = b - block * 2 * x.half_seqs;
+    const int half = i >= x.half_seqs ? 1 : 0;
+    const int row = half * (kRowTile / 2) + (i - half * x.half_seqs) * p.G;
+    const int64_t piece = (static_cast<int64_t>(j) * x.blocks + block) * x.stride;
+    const float* pm = x.m + piece * kRowTile + row;
+    const float* pl = x.l + piece * kRowTile + row;
+    const float* po = x.o + piece_at(piece, row, r);
+#pragma unroll
+    for (int h = 0; h < kGP; ++h) o[h] = __ldcg(po + min(h, p.G - 1) * 8);  // (padding heads load the last one's)
+    if (kGP >= 4 && p.G == kGP) {
+#pragma unroll
+      for (int h = 0; h < kGP; h += 4) {
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(pm + h)), b = __ldcg(reinterpret_cast<const float4*>(pl + h));
+        m[h] = a.x, m[h + 1] = a.y, m[h + 2] = a.z, m[h + 3] = a.w;
+        l[h] = b.x, l[h + 1] = b.y, l[h + 2] = b.z, l[h + 3] = b.w;
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < kGP; ++h) {
+        m[h] = __ldcg(pm + min(h, p.G - 1));
+        l[h] = __ldcg(pl + min(h, p.G - 1));
+      }
+    }
+  }
+  __device__ __forceinline__ void add_to(float (&M)[kGP], float (&L)[kGP], float (&O)[kGP]) const {
+#pragma unroll
+    for (int h = 0; h < kGP; ++h) {
+      const float m_new = fmaxf(M[h], m[h]);
+      const float a_old = ex2_approx(M[h] - m_new);
+      const float a_c = ex2_approx(m[h] - m_new);
+      O[h] = O[h] * a_old + o[h] * a_c;
+      L[h] = L[h] * a_old + l[h] * a_c;
+      M[h] = m_new;
+    }
+  }
+};
+template <>
+struct PrefixRow<0> {};
 
 // The paged kernels' waits are compact: with the others' loops at every wait their code (120 KB at 16 heads) outgrew the
 // instruction cache.
@@ -627,13 +662,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) red_max[(sb * 4 + q4) * kN + h] = mx;
               }
               named_bar_sync(1, kSoft);
+              float mt[kGP], other[kGP];
+              load_row(red_max + sb * 4 * kN, mt);
+#pragma unroll
+              for (int w = 1; w < 4; ++w) {
+                load_row(red_max + (sb * 4 + w) * kN, other);
+#pragma unroll
+                for (int h = 0; h < kGP; ++h) mt[h] = fmaxf(mt[h], other[h]);
+              }
 #pragma unroll
               for (int h = 0; h < kGP; ++h) {
-                const float* rm = red_max + sb * 4 * kN + h;
-                const float mt = fmaxf(fmaxf(rm[0], rm[kN]), fmaxf(rm[2 * kN], rm[3 * kN]));
-                if (mt > m_run[h] + kGrowth) {
-                  alpha[h] = ex2_approx(m_run[h] - mt);
-                  m_run[h] = mt;
+                if (mt[h] > m_run[h] + kGrowth) {
+                  alpha[h] = ex2_approx(m_run[h] - mt[h]);
+                  m_run[h] = mt[h];
                 }
               }
             }
@@ -727,6 +768,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Piece pc = locate(x);
         it += pc.n;  // tiles through the end of this piece
         const int hb = pi & 1;
+        PrefixRow<kPaged ? kGP : 0> prefix;
+        if constexpr (kPaged)
+          if (kGP <= 8 && p.prefix.o) prefix.load(p, pc.b, pc.j, r);  // under way while the piece is worked on
         wait_warp(&h_full[hb], (pi >> 1) & 1, kStatusWaitFullTimeout);
         tc_fence_after_sync();
         float hv[32];
@@ -781,15 +825,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           red_sum[q4 * kN + h] = sum;
         }
         named_bar_sync(2, kSoft);
+        if constexpr (kPaged) {
+          float other[kGP];
+          load_row(red_sum, l_tot);
 #pragma unroll
-        for (int h = 0; h < kGP; ++h)
-          l_tot[h] = (red_sum[h] + red_sum[kN + h]) + (red_sum[2 * kN + h] + red_sum[3 * kN + h]);
+          for (int w = 1; w < 4; ++w) {
+            load_row(red_sum + w * kN, other);
+#pragma unroll
+            for (int h = 0; h < kGP; ++h) l_tot[h] += other[h];
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < kGP; ++h)
+            l_tot[h] = (red_sum[h] + red_sum[kN + h]) + (red_sum[2 * kN + h] + red_sum[3 * kN + h]);
+        }
 
         const bool whole = pc.tl == 0 && pc.n == pc.nt;
         uint16_t* outp = p.out + (static_cast<int64_t>(pc.b) * p.h_q + static_cast<int64_t>(pc.j) * p.G) * kD + r;
         if (whole) {
           if constexpr (kPaged)
-            if (p.prefix.o) add_prefix<kGP>(p, pc.b, pc.j, r, m_run, l_tot, o_acc);
+            if (p.prefix.o) {
+              if (kGP > 8) prefix.load(p, pc.b, pc.j, r);  // (early, its registers would spill)
+              prefix.add_to(m_run, l_tot, o_acc);
+            }
 #pragma unroll
           for (int h = 0; h < kGP; ++h)
             if (h < p.G) {
@@ -888,7 +946,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             if constexpr (kPaged)
-              if (p.prefix.o) add_prefix<kGP>(p, pc.b, pc.j, r, M, L, O);
+              if (p.prefix.o) {
+                if (kGP > 8) prefix.load(p, pc.b, pc.j, r);
+                prefix.add_to(M, L, O);
+              }
 #pragma unroll
             for (int h = 0; h < kGP; ++h)
               if (h < p.G) {
@@ -913,7 +974,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 M[h] = -FLT_MAX;
                 L[h] = O[h] = 0.0f;
               }
-              add_prefix<kGP>(p, b, j, r, M, L, O);
+              PrefixRow<kGP> prefix;
+              prefix.load(p, b, j, r);
+              prefix.add_to(M, L, O);
               uint16_t* o = p.out + (static_cast<int64_t>(b) * p.h_q + static_cast<int64_t>(j) * p.G) * kD + r;
 #pragma unroll
               for (int h = 0; h < kGP; ++h)
