@@ -297,33 +297,23 @@ def moe_ffn_forward_residual(x, logits, W_gate, W_up, W_down, s_gate, s_up, s_do
 
 
 # ---------------------------------------------------------------- paged key/value cache (include/paged/moe_paged.h)
-def _paged_ptr(fn: str, name: str, t: torch.Tensor, dtype: torch.dtype, device: int, shape) -> int:
-    """The device pointer of a contiguous tensor of this type, device and shape."""
-    if t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous() and device >= 0:
-        return t.data_ptr()
-    if t.dtype is not dtype:
-        raise TypeError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != device or device < 0:
-        raise ValueError(f"{fn}: {name} must be on the same CUDA device as the other tensors, got {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{fn}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError("tensors passed to libmoe must be contiguous")
+# Arguments are checked and the calls made in csrc/py_paged.cpp; every check raises before anything is launched.
+_native = None
 
 
-def _paged_call(f, device: int, stream, *args) -> None:
-    """The C call on `stream` (the device's current stream by default), with that device current."""
-    if stream is None:
-        # what torch.cuda.current_stream() wraps, without building a Stream object (3 us of a 7 us call)
-        raw = torch._C._cuda_getCurrentRawStream(device)
-    else:
-        raw = _stream(stream)
-    if device == torch._C._cuda_getDevice():
-        status = f(*args, raw)
-    else:
-        with torch.cuda.device(device):
-            status = f(*args, raw)
-    if status != 0:
-        raise MoeError(f.__name__, status)
+def _load_native():
+    """The compiled Python side; raises if it has not been built."""
+    global _native
+    if _native is None:
+        if not os.path.exists(_build.PY_LIB):
+            raise ImportError(f"{_build.PY_LIB} not found: build it with routed_expert_ffn_softmax_gb300.build.build()")
+        from . import _paged as native
+        _native = native
+    return _native
+
+
+def _raw(stream):
+    return None if stream is None else _stream(stream)
 
 
 def moe_paged_workspace_size(N: int = 1, B: int = 1, h_q: int = 1, h_kv: int = 1, d: int = 128,
@@ -346,19 +336,10 @@ def moe_paged_plan(ctx_lens, new_lens, page_size: int, num_pages: int, free_page
     """Block tables and slot maps of one step: ctx_lens, new_lens [B], free_pages [n], free_count [1],
     block_table [B, max_pages] (gets the new pages); out: seq_lens [B], cu_new [B + 1], positions and slots
     [n_rows], free_left [1]. All int32."""
-    fn, dev, i32 = "moe_paged_plan", ctx_lens.get_device(), torch.int32
-    B, n_rows, n_free, n_ws = ctx_lens.shape[0], positions.shape[0], free_pages.shape[0], workspace.shape[0]
-    width = block_table.shape[1]
-    one, per_seq, per_row, p = (1,), (B,), (n_rows,), _paged_ptr
-    _paged_call((_lib or load()).moe_paged_plan, dev, stream, p(fn, "ctx_lens", ctx_lens, i32, dev, per_seq),
-                p(fn, "new_lens", new_lens, i32, dev, per_seq), B, page_size, num_pages,
-                p(fn, "free_pages", free_pages, i32, dev, (n_free,)), n_free,
-                p(fn, "free_count", free_count, i32, dev, one),
-                p(fn, "block_table", block_table, i32, dev, (B, width)), width,
-                p(fn, "seq_lens", seq_lens, i32, dev, per_seq), p(fn, "cu_new", cu_new, i32, dev, (B + 1,)),
-                p(fn, "positions", positions, i32, dev, per_row), p(fn, "slots", slots, i32, dev, per_row), n_rows,
-                p(fn, "free_left", free_left, i32, dev, one),
-                p(fn, "workspace", workspace, torch.uint8, dev, (n_ws,)), n_ws)
+    st = (_native or _load_native()).moe_paged_plan(ctx_lens, new_lens, page_size, num_pages, free_pages, free_count, block_table,
+                                                    seq_lens, cu_new, positions, slots, free_left, workspace, _raw(stream))
+    if st:
+        raise MoeError("moe_paged_plan", st)
 
 
 def moe_qk_norm_rope(qkv, q_weight, k_weight, eps: float, inv_freq, positions, slots, q_out, k_cache, v_cache,
@@ -366,76 +347,37 @@ def moe_qk_norm_rope(qkv, q_weight, k_weight, eps: float, inv_freq, positions, s
     """qkv [N, (h_q + 2 h_kv) * d] bf16 (rows may be strided); q_weight, k_weight [d] bf16 or None;
     inv_freq [rot_dim / 2] f32 (or None: no rotation); positions, slots [N] int32; out: q_out [N, h_q, d],
     the caches [num_pages, h_kv, page_size, d]."""
-    fn, dev, bf, f32, i32, p = "moe_qk_norm_rope", qkv.get_device(), torch.bfloat16, torch.float32, torch.int32, _paged_ptr
-    N, h_q, d = q_out.shape
-    cache = k_cache.shape
-    num_pages, h_kv, page_size, _ = cache
-    width = (h_q + 2 * h_kv) * d
-    if qkv.dtype is not bf or dev < 0:
-        raise TypeError(f"{fn}: qkv must be a bf16 CUDA tensor")
-    if qkv.shape != (N, width) or qkv.stride(1) != 1:
-        raise ValueError(f"{fn}: qkv must have shape {(N, width)} with contiguous rows, got {tuple(qkv.shape)}")
-    rot = 0 if inv_freq is None else inv_freq.shape[0]
-    _paged_call((_lib or load()).moe_qk_norm_rope, dev, stream, qkv.data_ptr(), qkv.stride(0) if N > 1 else width, N,
-                h_q, h_kv, d, None if q_weight is None else p(fn, "q_weight", q_weight, bf, dev, (d,)),
-                None if k_weight is None else p(fn, "k_weight", k_weight, bf, dev, (d,)), eps,
-                None if inv_freq is None else p(fn, "inv_freq", inv_freq, f32, dev, (rot,)), 2 * rot,
-                1 if interleaved else 0, p(fn, "positions", positions, i32, dev, (N,)),
-                p(fn, "slots", slots, i32, dev, (N,)), p(fn, "q_out", q_out, bf, dev, (N, h_q, d)),
-                p(fn, "k_cache", k_cache, bf, dev, (num_pages, h_kv, page_size, d)),
-                p(fn, "v_cache", v_cache, bf, dev, (num_pages, h_kv, page_size, d)), num_pages, page_size)
-
-
-def _paged_attention(fn, q, k_cache, v_cache, block_table, seq_lens, out, workspace):
-    """(the checked pointers q, k_cache, v_cache, block_table, seq_lens, out, workspace; the sizes B .. max_pages)."""
-    dev, bf, i32, p = q.get_device(), torch.bfloat16, torch.int32, _paged_ptr
-    N, h_q, d = q.shape
-    B, width = block_table.shape
-    num_pages, h_kv, page_size, _ = k_cache.shape
-    rows, cache = (N, h_q, d), (num_pages, h_kv, page_size, d)
-    return (p(fn, "q", q, bf, dev, rows), p(fn, "k_cache", k_cache, bf, dev, cache),
-            p(fn, "v_cache", v_cache, bf, dev, cache), p(fn, "block_table", block_table, i32, dev, (B, width)),
-            p(fn, "seq_lens", seq_lens, i32, dev, (B,)), p(fn, "out", out, bf, dev, rows),
-            p(fn, "workspace", workspace, torch.uint8, dev, (workspace.shape[0],))), \
-        (B, h_q, h_kv, d, num_pages, page_size, width)
+    st = (_native or _load_native()).moe_qk_norm_rope(qkv, q_weight, k_weight, eps, inv_freq, positions, slots, q_out, k_cache,
+                                                      v_cache, interleaved, _raw(stream))
+    if st:
+        raise MoeError("moe_qk_norm_rope", st)
 
 
 def moe_gqa_paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float, out, workspace, window: int = 0,
                          n_sink: int = 0, stream=None) -> None:
     """One token per sequence: q [B, h_q, d] bf16, caches [num_pages, h_kv, page_size, d] bf16, block_table
     [B, max_pages] and seq_lens [B] int32, out [B, h_q, d] bf16. window = 0: every key."""
-    fn = "moe_gqa_paged_decode"
-    (qp, kp, vp, tp, lp, op, wp), sizes = _paged_attention(fn, q, k_cache, v_cache, block_table, seq_lens, out, workspace)
-    if q.shape[0] != sizes[0]:
-        raise ValueError(f"{fn}: q must have one row per sequence")
-    _paged_call((_lib or load()).moe_gqa_paged_decode, q.get_device(), stream, qp, kp, vp, tp, lp, *sizes, scale,
-                window, n_sink, op, wp, workspace.shape[0])
+    st = (_native or _load_native()).moe_gqa_paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, out, workspace,
+                                                          window, n_sink, _raw(stream))
+    if st:
+        raise MoeError("moe_gqa_paged_decode", st)
 
 
 def moe_gqa_paged_prefill(q, cu_q, k_cache, v_cache, block_table, seq_lens, scale: float, out, workspace,
                           window: int = 0, n_sink: int = 0, stream=None) -> None:
     """Many tokens per sequence: q [N, h_q, d] bf16 packed, cu_q [B + 1] int32, the rest as in
     moe_gqa_paged_decode; out [N, h_q, d] bf16 (rows outside every sequence are left as they were)."""
-    fn = "moe_gqa_paged_prefill"
-    (qp, kp, vp, tp, lp, op, wp), sizes = _paged_attention(fn, q, k_cache, v_cache, block_table, seq_lens, out, workspace)
-    cp = _paged_ptr(fn, "cu_q", cu_q, torch.int32, q.get_device(), (sizes[0] + 1,))
-    _paged_call((_lib or load()).moe_gqa_paged_prefill, q.get_device(), stream, qp, cp, kp, vp, tp, lp, q.shape[0],
-                *sizes, scale, window, n_sink, op, wp, workspace.shape[0])
+    st = (_native or _load_native()).moe_gqa_paged_prefill(q, cu_q, k_cache, v_cache, block_table, seq_lens, scale, out, workspace,
+                                                           window, n_sink, _raw(stream))
+    if st:
+        raise MoeError("moe_gqa_paged_prefill", st)
 
 
 def moe_gqa_prefix_decode(q, prefix_table, prefix_len: int, k_cache, v_cache, block_table, seq_lens, scale: float, out,
                           workspace, stream=None) -> None:
     """moe_gqa_paged_decode (no window) behind the prefix_len keys in the pages prefix_table [n] int32 that every
     sequence of the batch sees; seq_lens and block_table hold the sequences' own keys."""
-    fn = "moe_gqa_prefix_decode"
-    (qp, kp, vp, tp, lp, op, wp), sizes = _paged_attention(fn, q, k_cache, v_cache, block_table, seq_lens, out, workspace)
-    if q.shape[0] != sizes[0]:
-        raise ValueError(f"{fn}: q must have one row per sequence")
-    pp = None
-    if prefix_len > 0:
-        n = prefix_table.shape[0]
-        pp = _paged_ptr(fn, "prefix_table", prefix_table, torch.int32, q.get_device(), (n,))
-        if n * k_cache.shape[2] < prefix_len:
-            raise ValueError(f"{fn}: prefix_table is shorter than prefix_len")
-    _paged_call((_lib or load()).moe_gqa_prefix_decode, q.get_device(), stream, qp, pp, prefix_len, kp, vp, tp, lp,
-                *sizes, scale, op, wp, workspace.shape[0])
+    st = (_native or _load_native()).moe_gqa_prefix_decode(q, prefix_table, prefix_len, k_cache, v_cache, block_table, seq_lens,
+                                                           scale, out, workspace, _raw(stream))
+    if st:
+        raise MoeError("moe_gqa_prefix_decode", st)
