@@ -298,8 +298,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int i1 = warp >= 2 ? min(p.B, i0 + per) : 0;
   // warming L2 with the lengths is safe before the wait (L2 is where later writes land too)
   if (warp >= 2 && i0 < i1) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.seq_lens + i0));
-  // The lengths (and the cache rows of the newest token) may come from the preceding kernel.
-  pdl_wait_predecessor();
+  // The lengths (and the cache rows of the newest token) may come from the preceding kernel. Behind a shared prefix the
+  // preceding kernels are that prefix's, which waited for all before them and write only what the finisher reads: the
+  // sequences' own keys are worked on meanwhile.
+  const bool behind_prefix = kPaged && p.prefix.o != nullptr;
+  if (!behind_prefix) pdl_wait_predecessor();
   pdl_allow_successor();
   if (warp >= 2) {
     int nt[8];
@@ -762,6 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // =========================== finisher (warps 6..9) ===========================
+      if (behind_prefix) pdl_wait_predecessor();
       int it = 0;
       int pi = 0;
       for (int x = beg; x < end; ++pi) {

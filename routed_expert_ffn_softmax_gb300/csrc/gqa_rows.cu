@@ -922,8 +922,8 @@ __global__ void __launch_bounds__(kMergeThreads) rows_merge_kernel(const Params 
 
 // Joins the splits of each segment of a shared prefix into its first piece.
 __global__ void __launch_bounds__(kMergeThreads) prefix_join_kernel(const Params p) {
+  pdl_allow_successor();  // the decode kernel's own keys need nothing of the prefix
   pdl_wait_predecessor();
-  pdl_allow_successor();
   const int64_t first = static_cast<int64_t>(blockIdx.x) * p.prefix_splits;
   const int tok0 = (blockIdx.x % p.prefix_blocks) * 2 * p.half_tokens;
   const int row0 = blockIdx.y * (kRowTile / kJoinParts);
