@@ -750,23 +750,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t minus_m = pack_f32x2(-m, -m);
         const uint64_t scale2 = pack_f32x2(scale, scale);
         uint64_t sum2[2] = {0u, 0u};
+        uint32_t u[32];
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          uint32_t u[16];
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const int y = 32 * w + 2 * x;
-            float p0, p1;
-            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(sc[y]), __uint_as_float(sc[y + 1])), scale2, minus_m), p0, p1);
-            p0 = ex2_approx(p0);
-            p1 = ex2_approx(p1);
-            sum2[x & 1] = add_f32x2(sum2[x & 1], pack_f32x2(p0, p1));
-            const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
-            u[x] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-          // the probabilities overwrite the first 64 score columns: both parts have read theirs (the exchange)
-          if (ok) tmem_st16(tbase + col_s(h) + 32 * part + 16 * w, u);
+        for (int x = 0; x < 32; ++x) {
+          float p0, p1;
+          unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(sc[2 * x]), __uint_as_float(sc[2 * x + 1])), scale2, minus_m), p0, p1);
+          p0 = ex2_approx(p0);
+          p1 = ex2_approx(p1);
+          sum2[x & 1] = add_f32x2(sum2[x & 1], pack_f32x2(p0, p1));
+          const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+          u[x] = *reinterpret_cast<const uint32_t*>(&b);
         }
+        if (ok) tmem_st32(tbase + col_s(h) + 32 * part, u);
         float s0, s1;
         unpack_f32x2(add_f32x2(sum2[0], sum2[1]), s0, s1);
         l += s0 + s1;
