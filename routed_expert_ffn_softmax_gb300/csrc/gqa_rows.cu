@@ -9,11 +9,11 @@
 // 4 * 128 * 128 * 128 flops per half and tile: long prompts are bound by the tensor pipe, few rows behind long
 // contexts by HBM. The halves alternate, so the softmax of one runs under the products of the other.
 //
-// Softmax: two threads share a row (TMEM lane), 64 keys each, and exchange its maximum through shared memory. (One
-// thread per row holds 128 scores, and its chain of loads, maxima, exponentials and stores took 2000 cycles a tile, twice
-// what the other half's products cover.) O stays in TMEM; it is rescaled
-// only when a row's maximum has grown by more than 2^8 since the reference in use (probabilities are then at most
-// 2^8, exact to the same relative bf16 step, and sums stay far inside fp32), which after the first tiles is rare.
+// Softmax: a thread owns a row (TMEM lane): its 128 scores come with one TMEM load and its probabilities leave with one
+// store, so the row's maximum and sum need no exchange. (TMEM instructions that meet the running products stall: with
+// two threads per row and four times the instructions, 16K prompts took 391 us instead of 357.) O stays in TMEM; it is
+// rescaled only when a row's maximum has grown by more than 2^8 since the reference in use (probabilities are then at
+// most 2^8, exact to the same relative bf16 step, and sums stay far inside fp32), which after the first tiles is rare.
 //
 // Work split: the key tiles of all (sequence, head, block) segments form one list (causal blocks have different
 // lengths, windows bound them) and each CTA takes a contiguous range of it, so any mix of prompts balances to within
@@ -22,8 +22,9 @@
 // shared prefix the host knows the sizes: equal splits per segment, joined the same way; the decode kernel adds the
 // result to the sequences' own keys.
 //
-// Per CTA, 20 warps: 0 TMA producer (Q per piece; K and V tiles alternate in a ring of 4 x 32 KB), 1 and 2 issue
-// the MMAs of the two halves in turn, 3 announces the pieces and writes zeros for blocks that see nothing, 4-11 and 12-19 the softmax and output of the two halves.
+// Per CTA, 12 warps: 0 TMA producer (Q per piece; K and V tiles alternate in a ring of 4 x 32 KB), 1 and 2 issue the
+// MMAs of the two halves in turn, 3 announces the pieces and writes zeros for blocks that see nothing, 4-7 and 8-11 the
+// softmax and output of the two halves.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -46,23 +47,22 @@ constexpr int kHalf = 128;                  // rows of a half
 constexpr int kStages = 4;
 constexpr int kBox = kKeys * 64 * 2;        // queries: 128 rows x 64 dims
 constexpr int kTile = 2 * kBox;             // one K or V tile, or the queries of a half: 32 KB
-constexpr int kThreads = 640;
-constexpr int kSoft = 256;                  // softmax threads of a half: two per row, 64 columns each
+constexpr int kThreads = 384;
+constexpr int kSoft = kHalf;                // softmax threads of a half, one per row
 constexpr int kOffQ = 0;
 constexpr int kOffRing = 2 * kTile;
 constexpr int kOffBar = kOffRing + kStages * kTile;
 constexpr int kItems = 4;                   // pieces announced ahead
 constexpr int kNumBars = 2 * kStages + 2 + 2 * 4 + 1 + 2 * kItems;
-constexpr int kOffRed = kOffBar + 256;      // row maxima and sums, [2 halves][2 parts][128 rows]
-constexpr int kOffItem = kOffRed + 2 * 2 * kHalf * 4;
+constexpr int kOffItem = kOffBar + 256;
 constexpr int kOffOut = kOffItem + kItems * 64;  // per softmax warp 32 rows x 32 dimensions of bf16 output
-constexpr int kSmem = kOffOut + 16 * 2048;
+constexpr int kSmem = kOffOut + 8 * 2048;
 // Registers per thread: at launch, and after the warpgroups have shared them out (128 threads that load and issue,
-// 512 softmax threads that hold half a row of scores each).
-constexpr int kRegsLaunch = 96;
-constexpr int kRegsIo = 64;
-constexpr int kRegsSoftmax = 104;
-static_assert(128 * kRegsIo + 512 * kRegsSoftmax <= kThreads * kRegsLaunch, "a larger share would wait forever");
+// 256 softmax threads that hold a row of scores each).
+constexpr int kRegsLaunch = 168;
+constexpr int kRegsIo = 88;
+constexpr int kRegsSoftmax = 208;
+static_assert(128 * kRegsIo + 2 * kSoft * kRegsSoftmax <= kThreads * kRegsLaunch, "a larger share would wait forever");
 static_assert(kNumBars * 8 + 8 <= 256, "barrier area");
 static_assert(kSmem <= 232448, "dynamic shared memory per CTA");
 static_assert(kRowTile == 2 * kHalf, "partials hold both halves");
@@ -79,7 +79,7 @@ constexpr int kSegCost = 2;
 
 constexpr int kReaders = 3 + 2 * kSoft / 32;  // warps that read the announced pieces
 
-constexpr int kTurnBar = 10;  // named barriers: 1..8 the softmax warps' pairs, these two the issuers' turns
+constexpr int kTurnBar = 1;  // named barriers 1 and 2: the issuers' turns
 
 constexpr float kGrowth = 8.0f;  // log2 of how far a row's maximum may outgrow its reference
 
@@ -621,20 +621,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   } else {
     reg_alloc<kRegsSoftmax>();
-    // =========================== softmax and output of half h, columns 64 part .. + 63 ===========================
-    const int h = (warp - 4) >> 3;
-    const int part = ((warp - 4) >> 2) & 1;
+    // =========================== softmax and output of half h ===========================
+    const int h = (warp - 4) >> 2;
     const int r = (warp & 3) * 32 + lane;  // row of the half
     const uint32_t tbase = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    float* red = reinterpret_cast<float*>(smem + kOffRed) + h * 2 * kHalf;
-    const int pair_bar = 1 + h * 4 + (warp & 3);  // the two warps that share these rows
-    auto exchange = [&](float mine) {             // the other thread's value of this row
-      red[part * kHalf + r] = mine;
-      tc_fence_before_sync();
-      named_bar_sync(pair_bar, 64);
-      tc_fence_after_sync();
-      return red[(part ^ 1) * kHalf + r];
-    };
     const int i = r / p.G;                  // token of the half
     const int g = r - i * p.G;
     const bool neg = p.scale_log2 < 0.0f;
@@ -664,32 +654,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = i < p.half_tokens && tok < ntok;
       const int pos = p.prefix_table ? p.prefix_len - 1 : pos0 + tok;
       const int end = live ? min(pos + 1, sp.len) : 0;   // keys below it are seen ...
-      const int lo = window_start(pos, p.kv.window);         // ... from here on, or below n_sink
+      const int lo = window_start(pos, p.kv.window);     // ... from here on, or below n_sink
       // a tile needs no mask when the half's first token sees its end and its last token's window begins before it
       const int last = min(ntok, (h + 1) * p.half_tokens) - 1;
       const int end_min = p.prefix_table ? p.prefix_len : pos0 + h * p.half_tokens + 1;
       const int lo_max = p.prefix_table ? 0 : window_start(pos0 + last, p.kv.window);
-      float m = -FLT_MAX, l = 0.0f;  // the row's reference, this thread's share of its sum
+      float m = -FLT_MAX, l = 0.0f;  // the row's reference and sum
       for (int t = t0; t < t1; ++t, ++it, ++cnt) {
         const int kb = sp.key_tile(t) * kKeys;
         wait_warp(&s_full[h], cnt & 1);
         tc_fence_after_sync();
-        uint32_t sc[64];
+        uint32_t sc[128];
         if (ok) {
-          tmem_ld64(tbase + col_s(h) + 64 * part, sc);
+          tmem_ld128(tbase + col_s(h), sc);
         } else {
 #pragma unroll
-          for (int x = 0; x < 64; ++x) sc[x] = 0u;
+          for (int x = 0; x < 128; ++x) sc[x] = 0u;
         }
         if (neg) {
 #pragma unroll
-          for (int x = 0; x < 64; ++x) sc[x] ^= 0x80000000u;
+          for (int x = 0; x < 128; ++x) sc[x] ^= 0x80000000u;
         }
         const bool plain = kb + kKeys <= end_min && (kb >= lo_max || kb + kKeys <= p.kv.n_sink);
         if (!plain) {
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const int cb = kb + 64 * part + 32 * w;
+          for (int w = 0; w < 4; ++w) {
+            const int cb = kb + 32 * w;
             const uint32_t see = bits_below(end, cb) & (~bits_below(lo, cb) | bits_below(p.kv.n_sink, cb));
 #pragma unroll
             for (int x = 0; x < 32; ++x)
@@ -701,9 +691,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int idx = 2 * it + 1;
             const int st = idx % kStages;
             if (mbar_wait_soon(&full[st], static_cast<uint32_t>((idx / kStages) & 1))) {
-              uint4* v = reinterpret_cast<uint4*>(smem + kOffRing + st * kTile + part * kUpper + tile_row(r));
+              uint4* v0 = reinterpret_cast<uint4*>(smem + kOffRing + st * kTile + tile_row(r));
+              uint4* v1 = v0 + kUpper / 16;
 #pragma unroll
-              for (int x = 0; x < 8; ++x) v[x ^ (r & 7)] = make_uint4(0u, 0u, 0u, 0u);  // neighbours in other banks
+              for (int x = 0; x < 8; ++x)  // neighbours in other banks
+                v0[x ^ (r & 7)] = v1[x ^ (r & 7)] = make_uint4(0u, 0u, 0u, 0u);
             } else {
               atomicExch(p.status, kStatusWaitFullTimeout);
             }
@@ -713,65 +705,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         // four chains, so that their latency overlaps
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int x = 0; x < 64; x += 2)
+        for (int x = 0; x < 128; x += 2)
           mx[(x >> 1) & 3] = max3_f32(mx[(x >> 1) & 3], __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
-        mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const float mine = mx[0] * scale;
-        // The reference both threads of the row use changes only when one of them sees a value far above it (or the
-        // row's first key); otherwise this barrier, which also tells that both have read their scores, is all they
-        // exchange.
+        const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+        // O holds nothing until the row has seen a key
         const bool seen = m > -FLT_MAX;
-        const bool far = live && (seen ? mine > m + kGrowth : mine > -FLT_MAX);
-        tc_fence_before_sync();
-        const bool any = named_bar_any(pair_bar, 64, far);
-        tc_fence_after_sync();
-        if (any) {
-          const float m_new = fmaxf(mine, exchange(mine));
-          const bool grow = live && (seen ? m_new > m + kGrowth : m_new > -FLT_MAX);
-          // O holds nothing until the row has seen a key
-          if (__any_sync(0xffffffffu, grow && seen)) {
-            const float a = grow && seen ? ex2_approx(m - m_new) : 1.0f;
-            // the scores' commit covered the product before them
+        const bool grow = live && seen && m_new > m + kGrowth;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float a = grow ? ex2_approx(m - m_new) : 1.0f;
+          // the scores' commit covered the product before them
 #pragma unroll 1
-            for (int x = 0; x < 4; ++x) {  // this part's dimensions of O
-              if (!ok) break;
-              float o[16];
-              uint32_t u[16];
-              tmem_ld16(tbase + col_o(h) + 64 * part + 16 * x, o);
+          for (int x = 0; x < 8; ++x) {
+            if (!ok) break;
+            float o[16];
+            uint32_t u[16];
+            tmem_ld16(tbase + col_o(h) + 16 * x, o);
 #pragma unroll
-              for (int y = 0; y < 16; ++y) u[y] = __float_as_uint(o[y] * a);
-              tmem_st16(tbase + col_o(h) + 64 * part + 16 * x, u);
-            }
-            l *= a;
+            for (int y = 0; y < 16; ++y) u[y] = __float_as_uint(o[y] * a);
+            tmem_st16(tbase + col_o(h) + 16 * x, u);
           }
+          l *= a;
           if (grow) m = m_new;
-          named_bar_sync(pair_bar, 64);  // the maxima exchanged have been read
         }
+        if (!seen) m = fmaxf(m, m_new);
         const uint64_t minus_m = pack_f32x2(-m, -m);
         const uint64_t scale2 = pack_f32x2(scale, scale);
-        uint64_t sum2[2] = {0u, 0u};
-        uint32_t u[32];
+        uint64_t sum2[4] = {0u, 0u, 0u, 0u};
+        uint32_t u[64];
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
+        for (int x = 0; x < 64; ++x) {
           float p0, p1;
           unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(sc[2 * x]), __uint_as_float(sc[2 * x + 1])), scale2, minus_m), p0, p1);
           p0 = ex2_approx(p0);
           p1 = ex2_approx(p1);
-          sum2[x & 1] = add_f32x2(sum2[x & 1], pack_f32x2(p0, p1));
+          sum2[x & 3] = add_f32x2(sum2[x & 3], pack_f32x2(p0, p1));
           const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
           u[x] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        if (ok) tmem_st32(tbase + col_s(h) + 32 * part, u);
+        if (ok) tmem_st64(tbase + col_s(h), u);
         float s0, s1;
-        unpack_f32x2(add_f32x2(sum2[0], sum2[1]), s0, s1);
+        unpack_f32x2(add_f32x2(add_f32x2(sum2[0], sum2[1]), add_f32x2(sum2[2], sum2[3])), s0, s1);
         l += s0 + s1;
         if (ok) tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[h]);
       }
-      // the piece's output: this part's dimensions
-      l += exchange(l);
+      // the piece's output
       wait_warp(&o_full[h], pieces++ & 1);
       tc_fence_after_sync();
       const bool some = l > 0.0f;
@@ -785,10 +765,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* stage = smem + kOffOut + (warp - 4) * 2048;
         const int64_t mine = live ? static_cast<int64_t>(tok0 + tok) * p.h_q + j * p.G + g : -1;
 #pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < 4; ++x) {
           float v[32];
           if (ok) {
-            tmem_ld32(tbase + col_o(h) + 64 * part + 32 * x, v);
+            tmem_ld32(tbase + col_o(h) + 32 * x, v);
           } else {
 #pragma unroll
             for (int y = 0; y < 32; ++y) v[y] = 0.0f;
@@ -810,37 +790,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int rr = 8 * y + (lane >> 2);
             const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((lane ^ (rr >> 1)) & 3) * 16);
             const int64_t to = __shfl_sync(0xffffffffu, mine, rr);
-            if (to >= 0) *reinterpret_cast<uint4*>(p.out + to * kD + 64 * part + 32 * x + 8 * (lane & 3)) = w;
+            if (to >= 0) *reinterpret_cast<uint4*>(p.out + to * kD + 32 * x + 8 * (lane & 3)) = w;
           }
           __syncwarp();
         }
       } else {
 #pragma unroll 1
         for (int x = 0; x < 4; ++x) {
-          float v[16];
+          float v[32];
           if (ok) {
-            tmem_ld16(tbase + col_o(h) + 64 * part + 16 * x, v);
+            tmem_ld32(tbase + col_o(h) + 32 * x, v);
           } else {
 #pragma unroll
-            for (int y = 0; y < 16; ++y) v[y] = 0.0f;
+            for (int y = 0; y < 32; ++y) v[y] = 0.0f;
           }
           if (!live) continue;
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
+          for (int y = 0; y < 8; ++y) {
             float4 f = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
             if (!some) f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            *reinterpret_cast<float4*>(p.pieces_o + piece_at(slot, row, 64 * part + 16 * x + 4 * y)) = f;
+            *reinterpret_cast<float4*>(p.pieces_o + piece_at(slot, row, 32 * x + 4 * y)) = f;
           }
         }
-      }
-      if (live && slot >= 0 && part == 0) {
-        p.pieces_m[slot * kRowTile + row] = m;
-        p.pieces_l[slot * kRowTile + row] = l;
+        if (live) {
+          p.pieces_m[static_cast<int64_t>(slot) * kRowTile + row] = m;
+          p.pieces_l[static_cast<int64_t>(slot) * kRowTile + row] = l;
+        }
       }
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[h]);
-      named_bar_sync(pair_bar, 64);  // the sums exchanged have been read
     }
   }
 
