@@ -74,7 +74,7 @@ __device__ constexpr uint32_t col_o(int h) { return 256u + 128u * h; }
 
 // What a segment costs beside its tiles (its queries' load, the first scores and the output, which no product
 // overlaps), in tiles: the CTAs' shares are cut so that those with many short segments get fewer tiles (ragged and
-// 16K prompts take 227 and 429 us at 1, 193 and 393 at 2, 197 and 393 at 3).
+// 16K prompts take 175 and 355 us at 2, 181 and 355 at 3).
 constexpr int kSegCost = 2;
 
 constexpr int kReaders = 3 + 2 * kSoft / 32;  // warps that read the announced pieces
