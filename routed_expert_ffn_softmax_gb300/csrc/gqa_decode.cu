@@ -217,13 +217,6 @@ struct PrefixRow {
 template <>
 struct PrefixRow<0> {};
 
-// The paged kernels' waits are compact: with the others' loops at every wait their code (120 KB at 16 heads) outgrew the
-// instruction cache.
-template <bool kPaged>
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
-  return kPaged ? mbar_wait_soon(bar, parity) : mbar_wait(bar, parity);
-}
-
 // Paged: the caches in boxes of kFold rows, for sink keys folded into a window's first tile.
 template <bool kPaged>
 struct FoldMaps {};
@@ -393,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int pi = 0;
       bool ok = true;
       auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-        ok = __all_sync(0xffffffffu, ok && bar_wait<kPaged>(bar, parity));
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity));
       };
       for (int x = beg; x < end && ok; ++pi) {
         const Piece pc = locate(x);
@@ -444,12 +437,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) atomicExch(p.status, kStatusWaitEmptyTimeout);
         const int n = it < kStages ? it : kStages;
         for (int i = it - n; i < it; ++i)
-          if (!bar_wait<kPaged>(&full[i % kStages], static_cast<uint32_t>((i / kStages) & 1))) {
+          if (!mbar_wait(&full[i % kStages], static_cast<uint32_t>((i / kStages) & 1))) {
             atomicExch(p.status, kStatusDrainTimeout);
             break;
           }
         for (int q = pi - 2 < 0 ? 0 : pi - 2; q < pi; ++q)
-          if (!bar_wait<kPaged>(&q_full[q & 1], (q >> 1) & 1)) {
+          if (!mbar_wait(&q_full[q & 1], (q >> 1) & 1)) {
             atomicExch(p.status, kStatusDrainTimeout);
             break;
           }
@@ -466,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = beg; x < end && ok; ++pi) {
         const Piece pc = locate(x);
         const int qb = pi & 1;
-        if (!bar_wait<kPaged>(&q_empty[qb], ((pi >> 1) & 1) ^ 1)) {
+        if (!mbar_wait(&q_empty[qb], ((pi >> 1) & 1) ^ 1)) {
           ok = false;
           break;
         }
@@ -478,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int z = pc.b * p.h_kv + pc.j;
         for (int t = pc.tl; t < pc.tl + pc.n; ++t, ++it) {
           const int st = it % kStages;
-          if (!bar_wait<kPaged>(&empty[st], static_cast<uint32_t>(((it / kStages) & 1) ^ 1))) {
+          if (!mbar_wait(&empty[st], static_cast<uint32_t>(((it / kStages) & 1) ^ 1))) {
             ok = false;
             break;
           }
@@ -495,12 +488,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // never leave copies in flight: the last stages and query blocks issued
       const int n = it < kStages ? it : kStages;
       for (int i = it - n; i < it; ++i)
-        if (!bar_wait<kPaged>(&full[i % kStages], static_cast<uint32_t>((i / kStages) & 1))) {
+        if (!mbar_wait(&full[i % kStages], static_cast<uint32_t>((i / kStages) & 1))) {
           atomicExch(p.status, kStatusDrainTimeout);
           break;
         }
       for (int q = pi - 2 < 0 ? 0 : pi - 2; q < pi; ++q)
-        if (!bar_wait<kPaged>(&q_full[q & 1], (q >> 1) & 1)) {
+        if (!mbar_wait(&q_full[q & 1], (q >> 1) & 1)) {
           atomicExch(p.status, kStatusDrainTimeout);
           break;
         }
@@ -522,8 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int sb = i & 1;
         const uint32_t ph = static_cast<uint32_t>((i >> 1) & 1);
         const int st = i % kStages;
-        if (ok && !bar_wait<kPaged>(&p_full[sb], ph)) fail(kStatusWaitFullTimeout);
-        if (ok && !bar_wait<kPaged>(&o_free[sb], ph ^ 1)) fail(kStatusWaitEmptyTimeout);
+        if (ok && !mbar_wait(&p_full[sb], ph)) fail(kStatusWaitFullTimeout);
+        if (ok && !mbar_wait(&o_free[sb], ph ^ 1)) fail(kStatusWaitEmptyTimeout);
         if (ok) {
           tc_fence_after_sync();
           const uint32_t v = sbase + st * kStageBytes + 2 * kBox;
@@ -543,13 +536,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = beg; x < end; ++pi) {
         const Piece pc = locate(x);
         const int qb = pi & 1;
-        if (ok && !bar_wait<kPaged>(&q_full[qb], (pi >> 1) & 1)) fail(kStatusWaitFullTimeout);
+        if (ok && !mbar_wait(&q_full[qb], (pi >> 1) & 1)) fail(kStatusWaitFullTimeout);
         const uint32_t qs = sbase + kOffQ + qb * kQBytes;
         for (int t = 0; t < pc.n; ++t, ++it) {
           const int st = it % kStages;
           const int sb = it & 1;
-          if (ok && !bar_wait<kPaged>(&full[st], static_cast<uint32_t>((it / kStages) & 1))) fail(kStatusWaitFullTimeout);
-          if (ok && !bar_wait<kPaged>(&s_free[sb], static_cast<uint32_t>(((it >> 1) & 1) ^ 1)))
+          if (ok && !mbar_wait(&full[st], static_cast<uint32_t>((it / kStages) & 1))) fail(kStatusWaitFullTimeout);
+          if (ok && !mbar_wait(&s_free[sb], static_cast<uint32_t>(((it >> 1) & 1) ^ 1)))
             fail(kStatusWaitEmptyTimeout);
           if (ok) {
             tc_fence_after_sync();
@@ -572,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it > 0) issue_o(it - 1);
       // every MMA has completed before TMEM is released
       umma_commit(mma_done);
-      if (!bar_wait<kPaged>(mma_done, 0)) atomicExch(p.status, kStatusDrainTimeout);
+      if (!mbar_wait(mma_done, 0)) atomicExch(p.status, kStatusDrainTimeout);
     }
     __syncwarp();
   } else {
@@ -585,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // executed by all 32 lanes together
     bool ok = true;
     auto wait_warp = [&](uint64_t* bar, uint32_t parity, int code) {
-      const bool w = __all_sync(0xffffffffu, ok && bar_wait<kPaged>(bar, parity));
+      const bool w = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity));
       if (!w && ok) {
         ok = false;
         atomicExch(p.status, code);
@@ -716,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // keys past the sequence: the cache rows there are arbitrary (even NaN) and a zero
             // probability times NaN is NaN, so clear this key's row of the V tile
             // (the wait makes the tile's landing visible to this thread before it overwrites)
-            if (bar_wait<kPaged>(&full[st], static_cast<uint32_t>((it / kStages) & 1))) {
+            if (mbar_wait(&full[st], static_cast<uint32_t>((it / kStages) & 1))) {
               uint8_t* v = smem + st * kStageBytes + 2 * kBox + (kPaged ? tile_row(r) : r * 128);
               uint4* v0 = reinterpret_cast<uint4*>(v);
               uint4* v1 = reinterpret_cast<uint4*>(v + (kPaged ? kUpper : kBox));

@@ -12,9 +12,10 @@ namespace gqa {
 constexpr int kKeys = 128;  // keys per tile
 
 // A K or V tile of a paged cache in shared memory: groups of 8 keys, in each the lower 64 dimensions of its keys (a
-// 1024-byte swizzle atom of 8 x 128 bytes), then the upper 64. One copy then brings a whole page (with the halves
-// apart, as one copy per half wants them, a tile of 16-token pages took 32 copies of some 70 cycles each, more than its
-// share of the memory's time).
+// 1024-byte swizzle atom of 8 x 128 bytes), then the upper 64. One copy then brings a whole page: a copy costs its warp
+// some 70 cycles, and with one for each half a tile of 16-token pages took 32, more than its share of the memory's time.
+// Decode over 16 sequences of up to 32K keys, us by layout (halves apart, together): 173, 159 with pages of 16 tokens;
+// 159, 157 of 32; 157, 157 of 64; 158, 158 of 128.
 constexpr int kGroupBytes = 2048;  // 8 keys
 constexpr int kUpper = 1024;       // the upper dimensions within a group
 __device__ __forceinline__ uint32_t tile_row(int key) { return (key >> 3) * kGroupBytes + (key & 7) * 128; }
