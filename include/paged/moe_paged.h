@@ -58,8 +58,8 @@ extern "C" {
 
 /*
  * Bytes of workspace the calls of this header need for B sequences with N query tokens in all (N = B for
- * decode) and a shared prefix of prefix_len keys (0 without one). A workspace for larger sizes also serves
- * smaller ones. moe_paged_plan needs only the figure for (1, 1, 1, 1, 128, 0). Returns 0 when the
+ * decode) and a shared prefix of prefix_len keys (0 without one). A workspace for larger N, B and prefix_len
+ * also serves smaller ones with the same heads. moe_paged_plan needs only the figure for (1, 1, 1, 1, 128, 0). Returns 0 when the
  * sizes are invalid or unsupported. Pure host computation.
  */
 size_t moe_paged_workspace_size(int N, int B, int h_q, int h_kv, int d, int prefix_len);
@@ -77,8 +77,8 @@ size_t moe_paged_workspace_size(int N, int B, int h_q, int h_kv, int d, int pref
  *   slots        [n_rows] int32 out: its slot in the cache; -1 behind the last one and for sequences left out
  *   free_left    [1] int32 out: entries of free_pages still valid; may be free_count itself
  * New pages are taken from the end of the valid part of free_pages, in order of (sequence, page): the k-th
- * is free_pages[free_count - 1 - k]. A sequence is left out (status 7) when its tokens do not fit n_rows or
- * its pages the table, or when it needs pages and the pages needed up to and including it (by the sequences
+ * is free_pages[free_count - 1 - k]. A sequence is left out (status 7) when the tokens up to and
+ * including its own exceed n_rows or its pages the table, or when it needs pages and the pages needed up to and including it (by the sequences
  * in order that fit otherwise) exceed free_count; with a negative length it is left out with status 4 and its
  * new tokens count as 0 when that is the negative one. Sequences left out keep their row of block_table.
  * seq_lens may be ctx_lens itself. A page id outside [0, num_pages) gives slot -1 and status 6.
@@ -116,7 +116,7 @@ moe_status_t moe_qk_norm_rope(const uint16_t* qkv, int64_t row_stride, int N, in
  *   q [B, h_q, d] bf16, seq_lens [B] int32 (the new token included), out [B, h_q, d] bf16
  * Heads are grouped as in moe_gqa_decode (query head hq reads key/value head hq / (h_q / h_kv)). Supported:
  * d = 128, h_q a multiple of h_kv, h_q / h_kv <= 16, 0 <= B <= 2048 (B = 0 is a no-op), scale finite. q, the
- * caches and out 16-byte aligned. Each visible row is read once per call.
+ * caches and out 16-byte aligned, out apart from all inputs. Each visible row is read once per call.
  */
 moe_status_t moe_gqa_paged_decode(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache,
                                   const int32_t* block_table, const int32_t* seq_lens, int B, int h_q, int h_kv,

@@ -136,26 +136,27 @@ __device__ __forceinline__ Block block_of(const Params& p, int b, int r) {
 // ---------------------------------------------------------------- tables
 constexpr int kTableThreads = 1024;
 
-__device__ __forceinline__ int scan_block(int v, int* sums) {  // inclusive over the block's threads
+template <typename T>
+__device__ __forceinline__ T scan_block(T v, T* sums) {  // inclusive over the block's threads
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int n = __shfl_up_sync(0xffffffffu, v, o);
+    const T n = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += n;
   }
   if (lane == 31) sums[warp] = v;
   __syncthreads();
   if (warp == 0) {
-    int s = sums[lane];
+    T s = sums[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, s, o);
+      const T n = __shfl_up_sync(0xffffffffu, s, o);
       if (lane >= o) s += n;
     }
     sums[lane] = s;
   }
   __syncthreads();
-  const int out = v + (warp ? sums[warp - 1] : 0);
+  const T out = v + (warp ? sums[warp - 1] : 0);
   __syncthreads();
   return out;
 }
@@ -171,6 +172,7 @@ __device__ __forceinline__ int last_at_most(const int32_t* a, int n, int x) {  /
 
 // Row blocks and work units before each sequence and each block.
 __global__ void __launch_bounds__(kTableThreads) rows_tables_kernel(const Params p) {
+  __shared__ int64_t wide_sums[32];
   __shared__ int sums[32];
   __shared__ int base[kGqaMaxSeqs + 1];
   const int tid = threadIdx.x;
@@ -189,18 +191,18 @@ __global__ void __launch_bounds__(kTableThreads) rows_tables_kernel(const Params
       if (bad || len < 0 || len > p.L_cap) atomicExch(p.status, kStatusBadSeqLen);
     }
   }
-  // offsets that run over each other could ask for more blocks than N tokens make: the tables end there
-  const int incl = scan_block(nb[0] + nb[1], sums);
-  int run = incl - nb[0] - nb[1];
+  // offsets that run over each other could ask for more blocks than N tokens make, and than 32 bits count: the tables
+  // end there
+  int64_t run = scan_block(static_cast<int64_t>(nb[0]) + nb[1], wide_sums) - nb[0] - nb[1];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int b = 2 * tid + k;
     if (b < p.B) {
-      base[b] = min(run, p.max_blocks);
+      base[b] = static_cast<int>(min(run, static_cast<int64_t>(p.max_blocks)));
       if (run + nb[k] > p.max_blocks) atomicExch(p.status, kStatusBadSeqLen);
     }
     run += nb[k];
-    if (b + 1 == p.B) base[p.B] = min(run, p.max_blocks);
+    if (b + 1 == p.B) base[p.B] = static_cast<int>(min(run, static_cast<int64_t>(p.max_blocks)));
   }
   __syncthreads();
   const int blocks = base[p.B];
@@ -754,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the piece's output
       wait_warp(&o_full[h], pieces++ & 1);
       tc_fence_after_sync();
-      const bool some = l > 0.0f;
+      const bool some = l != 0.0f;  // (a query of NaN has a sum of NaN, and its output)
       const int row = h * kHalf + r;
       const int j = items[s].j, slot = items[s].slot, tok0 = items[s].k.tok0;
       hand_back(s);
@@ -885,7 +887,7 @@ __global__ void __launch_bounds__(kMergeThreads) rows_merge_kernel(const Params 
     float M, L;
     float4 O;
     join_row<4>(p, row, 2 * static_cast<int64_t>(c) + 1, 2 * static_cast<int64_t>(c + 1), 2, seg.w, M, L, O);
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const float inv = L != 0.0f ? 1.0f / L : 0.0f;
     const __nv_bfloat162 x0 = __floats2bfloat162_rn(O.x * inv, O.y * inv);
     const __nv_bfloat162 x1 = __floats2bfloat162_rn(O.z * inv, O.w * inv);
     uint16_t* o = p.out + (static_cast<int64_t>(seg.x + tok) * p.h_q + seg.z * p.G + (row - hf * kHalf - ti * p.G)) * kD;

@@ -628,3 +628,177 @@ def test_one_workspace_serves_smaller_calls():
         run_prefix(4097, EDGES, 32, 4, 16, ws=ws)
         run_prefill(LENS, NEW, 32, 4, 16, ws=ws)
         run_decode(EDGES, 32, 4, 16, ws=ws)
+
+
+def test_nothing_to_do():
+    """No sequences, or no tokens: calls that do nothing, and calls whose sequences are all empty."""
+    k = torch.full((4, 2, 16, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+    ws = moe.alloc_paged_workspace(8, 4, 16, 2, D, 64, device=DEV)
+    e = torch.empty(0, 16, D, dtype=torch.bfloat16, device=DEV)
+    none, no_rows = i32([]).view(0, 3), i32([])
+    moe.moe_paged_plan(no_rows, no_rows, 16, 4, i32([1]), i32([1]), none, no_rows, i32([0]), no_rows, no_rows, i32([9]), ws)
+    moe.moe_qk_norm_rope(torch.empty(0, 20 * D, dtype=torch.bfloat16, device=DEV), None, None, 0.0, None, no_rows, no_rows,
+                         e, k, k)
+    moe.moe_gqa_paged_decode(e, k, k, none, no_rows, SCALE, e, ws)
+    moe.moe_gqa_paged_prefill(e, i32([0]), k, k, none, no_rows, SCALE, e, ws)
+    moe.moe_gqa_paged_prefill(e, i32([0, 0]), k, k, i32([[0]]), i32([5]), SCALE, e, ws)
+    moe.moe_gqa_prefix_decode(e, i32([0]), 16, k, k, none, no_rows, SCALE, e, ws)
+    # sequences without keys, their queries NaN; and packed rows that belong to no sequence
+    q = torch.full((4, 16, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+    table = i32([[-1, -1]] * 4)
+    out = torch.full_like(q, 7.0)
+    moe.moe_gqa_paged_prefill(q, i32([2] * 5), k, k, table, i32([0] * 4), SCALE, out, ws)
+    torch.cuda.synchronize()
+    assert (out == 7.0).all()
+    moe.moe_gqa_paged_prefill(q, i32([0, 1, 2, 3, 4]), k, k, table, i32([0] * 4), SCALE, out, ws)
+    torch.cuda.synchronize()
+    assert not out.any()
+    out.fill_(7.0)
+    moe.moe_gqa_paged_decode(q, k, k, table, i32([0] * 4), SCALE, out, ws)
+    torch.cuda.synchronize()
+    assert not out.any() and moe.workspace_status(ws) == 0
+
+
+def test_a_query_of_nan_stays_in_its_row():
+    lens, new = (300, 70), (60, 70)
+    c = ref.Cache(lens, 2, 16, DEV)
+    clean = randn(130, 16, D, seed=2)
+    bad = clean.clone()
+    bad[33] = float("nan")
+    ws = moe.alloc_paged_workspace(130, 130, 16, 2, D, 300, device=DEV)
+
+    def prefill(q):
+        out = torch.empty_like(q)
+        moe.moe_gqa_paged_prefill(q, i32([0, 60, 130]), c.k, c.v, c.table, i32(lens), SCALE, out, ws)
+        return out
+
+    def behind(q):
+        out = torch.empty_like(q)
+        own = c.table[1:].expand(130, -1).contiguous()
+        moe.moe_gqa_prefix_decode(q, c.table[0].contiguous(), 300, c.k, c.v, own, i32([70] * 130), SCALE, out, ws)
+        return out
+
+    for f in (prefill, behind):
+        a, b = f(clean), f(bad)
+        rest = torch.arange(130, device=DEV) != 33
+        assert torch.equal(a[rest], b[rest]) and b[33].isnan().all()
+
+
+def test_prefix_bad_page():
+    c = ref.Cache((300, 40, 17), 2, 16, DEV)
+    q = randn(2, 16, D)
+    out, ws = torch.empty_like(q), moe.alloc_paged_workspace(2, 2, 16, 2, D, 300, device=DEV)
+    for page in (-1, c.k.shape[0], 2 ** 31 - 1):
+        ws[:4] = 0
+        shared = c.table[0].clone()
+        shared[7] = page
+        moe.moe_gqa_prefix_decode(q, shared, 300, c.k, c.v, c.table[1:].contiguous(), i32([40, 17]), SCALE, out, ws)
+        assert moe.workspace_status(ws) == 6
+        # the page's keys and values read as zeros
+        for b, n in enumerate((40, 17)):
+            k, v = (torch.cat([c.rows[0][i], c.rows[b + 1][i]]) for i in (0, 1))
+            k[7 * 16:8 * 16] = 0
+            v[7 * 16:8 * 16] = 0
+            see = torch.ones(1, 300 + n, dtype=torch.bool, device=DEV)
+            ref.check(out[b:b + 1], *ref.attend(q[b:b + 1], k, v, see, SCALE), "a page of zeros")
+
+
+def test_prefill_offsets_over_each_other():
+    """Offsets that descend and start again would make more row blocks than the tokens do: the status word tells, and the
+    workspace serves the next call."""
+    lens = [100] * 9
+    c = ref.Cache(lens, 2, 16, DEV)
+    q, ws = randn(100, 16, D), moe.alloc_paged_workspace(100, 9, 16, 2, D, device=DEV)
+    out = torch.empty_like(q)
+    moe.moe_gqa_paged_prefill(q, i32([0, 100] * 5), c.k, c.v, c.table, i32(lens), SCALE, out, ws)
+    torch.cuda.synchronize()
+    assert moe.workspace_status(ws) == 4
+    ws[:4] = 0
+    run_prefill((300, 17), (83, 17), 16, 2, 16, tail=0, ws=ws)
+
+
+def test_prefix_captured_between_writes_of_its_inputs():
+    """The sequences' own keys are started before the prefix's kernels have finished: what runs in front of the call must
+    have, in a stream and in a graph."""
+    lens = (40, 0, 900, 17, 300) * 8
+    c = ref.Cache((2500,) + lens, 2, 16, DEV)
+    shared, own = c.table[0].contiguous(), c.table[1:].contiguous()
+    qs = [randn(40, 16, D, seed=i) for i in range(3)]
+    tables = [own, own.roll(5, 0), own.roll(10, 0)]
+    ls = [i32(lens), i32(lens).roll(5, 0), i32(lens).roll(10, 0)]
+    ws = moe.alloc_paged_workspace(40, 40, 16, 2, D, 2500, device=DEV)
+    want = []
+    for q, t, n in zip(qs, tables, ls):
+        want.append(torch.empty_like(q))
+        moe.moe_gqa_prefix_decode(q, shared, 2500, c.k, c.v, t, n, SCALE, want[-1], ws)
+        torch.cuda.synchronize()
+    q, t, n = qs[0].clone(), own.clone(), ls[0].clone()
+    outs = [torch.empty_like(q) for _ in range(9)]
+
+    def run():
+        for i, o in enumerate(outs):
+            q.copy_(qs[i % 3])
+            t.copy_(tables[i % 3])
+            n.copy_(ls[i % 3])
+            moe.moe_gqa_prefix_decode(q, shared, 2500, c.k, c.v, t, n, SCALE, o, ws)
+
+    run()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i % 3]) for i, o in enumerate(outs))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want[i % 3]) for i, o in enumerate(outs))
+    assert moe.workspace_status(ws) == 0
+
+
+def test_binding_refuses_shapes_and_types():
+    c = ref.Cache((40, 300), 2, 16, DEV)
+    q = randn(2, 16, D)
+    ws = moe.alloc_paged_workspace(2, 2, 16, 2, D, 300, device=DEV)
+    good = dict(q=q, k_cache=c.k, v_cache=c.v, block_table=c.table, seq_lens=i32([40, 300]), scale=SCALE,
+                out=torch.empty_like(q), workspace=ws)
+    moe.moe_gqa_paged_decode(**good)
+    bad = [("q", q[:1], ValueError), ("q", q.view(32, D), ValueError), ("q", q.half(), TypeError), ("q", None, TypeError),
+           ("q", randn(2, D, 16).transpose(1, 2), ValueError), ("v_cache", c.v[:-1], ValueError),
+           ("k_cache", c.k[:, :, ::2], ValueError), ("block_table", c.table.long(), TypeError),
+           ("block_table", c.table[0], ValueError), ("block_table", c.table[:, ::2], ValueError),
+           ("seq_lens", i32([40]), ValueError), ("seq_lens", [40, 300], TypeError), ("out", torch.empty_like(q[:1]), ValueError),
+           ("out", torch.empty_like(q, device="cpu"), ValueError), ("scale", "x", TypeError), ("scale", float("nan"), moe.MoeError),
+           ("workspace", ws[:256], moe.MoeError), ("workspace", ws.int(), TypeError), ("workspace", ws[1:], moe.MoeError)]
+    for name, value, kind in bad:
+        with pytest.raises(kind):
+            moe.moe_gqa_paged_decode(**{**good, name: value})
+    for more in (dict(window=-1), dict(n_sink=-1)):
+        with pytest.raises(moe.MoeError):
+            moe.moe_gqa_paged_decode(**good, **more)
+    for more in (dict(window=2 ** 31), dict(window=1 << 80)):
+        with pytest.raises(OverflowError):
+            moe.moe_gqa_paged_decode(**good, **more)
+    for cu in (i32([0, 1]), i32([0, 1, 2, 2])):
+        with pytest.raises(ValueError):
+            moe.moe_gqa_paged_prefill(cu_q=cu, **good)
+    shared = c.table[1].contiguous()
+    moe.moe_gqa_prefix_decode(prefix_table=shared, prefix_len=300, **good)
+    for table, n, kind in ((shared[:18], 300, ValueError), (None, 300, ValueError), (shared, -1, moe.MoeError),
+                           (shared.view(1, -1), 300, ValueError), (shared.long(), 300, TypeError)):
+        with pytest.raises(kind):
+            moe.moe_gqa_prefix_decode(prefix_table=table, prefix_len=n, **good)
+    qkv, pos = randn(2, 20 * D), i32([0, 1])
+    qk = dict(qkv=qkv, q_weight=None, k_weight=None, eps=0.0, inv_freq=None, positions=pos, slots=i32([-1, -1]), q_out=q.clone(),
+              k_cache=c.k, v_cache=c.v)
+    moe.moe_qk_norm_rope(**qk)
+    f = lambda n: torch.ones(n, device=DEV)  # noqa: E731
+    for name, value, kind in [("qkv", qkv[:1], ValueError), ("qkv", qkv[:, :-1], ValueError), ("qkv", qkv[:1].expand(2, -1), moe.MoeError),
+                              ("q_weight", f(D), TypeError), ("k_weight", qkv[0, :64], ValueError), ("inv_freq", f(65), moe.MoeError),
+                              ("inv_freq", f(4), moe.MoeError), ("inv_freq", f((2, 32)), ValueError), ("eps", -1.0, moe.MoeError),
+                              ("positions", pos[:1], ValueError), ("slots", pos.long(), TypeError), ("interleaved", 2, moe.MoeError)]:
+        with pytest.raises(kind):
+            moe.moe_qk_norm_rope(**{**qk, name: value})
+    torch.cuda.synchronize()
+    assert moe.workspace_status(ws) == 0
