@@ -53,7 +53,7 @@ constexpr int kOffQ = 0;
 constexpr int kOffRing = 2 * kTile;
 constexpr int kOffBar = kOffRing + kStages * kTile;
 constexpr int kItems = 4;                   // pieces announced ahead
-constexpr int kNumBars = 2 * kStages + 2 + 2 * 4 + 1 + 2 * kItems;
+constexpr int kNumBars = 2 * kStages + 2 + 2 * 5 + 1 + 2 * kItems;
 constexpr int kOffItem = kOffBar + 256;
 constexpr int kOffOut = kOffItem + kItems * 64;  // per softmax warp 32 rows x 32 dimensions of bf16 output
 constexpr int kSmem = kOffOut + 8 * 2048;
@@ -80,6 +80,11 @@ constexpr int kSegCost = 2;
 constexpr int kReaders = 3 + 2 * kSoft / 32;  // warps that read the announced pieces
 
 constexpr int kTurnBar = 1;  // named barriers 1 and 2: the issuers' turns
+
+// Keys of a tile whose probabilities are handed over first: their part of P . V runs under the exponentials of the rest,
+// which take a warp 4 cycles each (16K and ragged prompts take 356 and 175 us with the tile as one, 341 and 173 with 64
+// keys first, 340 and 171 with 96).
+constexpr int kFirst = 96;
 
 constexpr float kGrowth = 8.0f;  // log2 of how far a row's maximum may outgrow its reference
 
@@ -352,6 +357,16 @@ class Walk {
 };
 
 // ---------------------------------------------------------------- the attention kernel
+template <int kN>
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t* v) {  // kN columns, a multiple of 16
+  if constexpr (kN >= 32) {
+    tmem_st32(taddr, reinterpret_cast<const uint32_t(&)[32]>(*v));
+    tmem_store<kN - 32>(taddr + 32, v + 32);
+  } else if constexpr (kN >= 16) {
+    tmem_st16(taddr, reinterpret_cast<const uint32_t(&)[16]>(*v));
+  }
+}
+
 // Bits c of keys cb + c (c = 0 .. 31) that are below `n`.
 __device__ __forceinline__ uint32_t bits_below(int n, int cb) {
   const int k = n - cb;
@@ -367,7 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_full = empty + kStages;
   uint64_t* q_empty = q_full + 1;
   uint64_t* s_full = q_empty + 1;   // [2]
-  uint64_t* p_full = s_full + 2;    // [2]
+  uint64_t* p_half = s_full + 2;    // [2]
+  uint64_t* p_full = p_half + 2;    // [2]
   uint64_t* o_full = p_full + 2;    // [2]
   uint64_t* o_free = o_full + 2;    // [2]
   uint64_t* mma_done = o_free + 2;
@@ -387,7 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_empty, 2);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&s_full[h], 1);
-      mbar_init(&p_full[h], kSoft / 32);  // one arrival per warp
+      mbar_init(&p_half[h], kSoft / 32);  // one arrival per warp (likewise below)
+      mbar_init(&p_full[h], kSoft / 32);
       mbar_init(&o_full[h], 1);
       mbar_init(&o_free[h], kSoft / 32);
     }
@@ -519,6 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t d_o = uniform(tmem + col_o(h));
     const uint32_t idesc_s = umma_idesc_bf16_m128(kKeys);
     const uint32_t idesc_o = umma_idesc_bf16_m128(kD) | kIdescBMajorMN;
+    const uint64_t desc_v = umma_desc_sw128_mn_sbo(0, kUpper, kGroupBytes);
     const int my_turn = kTurnBar + h, other_turn = kTurnBar + 1 - h;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -540,17 +558,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t < n) wait(&full[st_k], ph);
         if (active) {
           if (t == 1) wait(&o_free[h], (seg++ & 1) ^ 1);
-          if (t > 0) wait(&p_full[h], pv++ & 1);
+          if (t > 0) wait(&p_half[h], pv & 1);
         }
         tc_fence_after_sync();
         named_bar_sync(my_turn, 64);
+        const uint64_t v = desc_v + (ring + st_v * (kTile >> 4));
+        if (active && t > 0) {
+          if (elect_one() && ok) {
+            umma_bf16_tmem_a(d_o, d_s, v, idesc_o, t > 1);
+#pragma unroll
+            for (int x = 1; x < kFirst / 16; ++x)
+              umma_bf16_tmem_a(d_o, d_s + 8 * x, v + x * (2 * kGroupBytes >> 4), idesc_o, true);
+          }
+          __syncwarp();
+          wait(&p_full[h], pv++ & 1);
+          tc_fence_after_sync();
+        }
         if (elect_one()) {
           if (active) {
             if (ok && t > 0) {
-              const uint64_t v = umma_desc_sw128_mn_sbo(0, kUpper, kGroupBytes) + (ring + st_v * (kTile >> 4));
-              umma_bf16_tmem_a(d_o, d_s, v, idesc_o, t > 1);
 #pragma unroll
-              for (int x = 1; x < kKeys / 16; ++x)
+              for (int x = kFirst / 16; x < kKeys / 16; ++x)
                 umma_bf16_tmem_a(d_o, d_s + 8 * x, v + x * (2 * kGroupBytes >> 4), idesc_o, true);
             }
             // the scores overwrite the probabilities of the tile before, whose product was issued just now: MMAs of one
@@ -736,6 +764,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t u[64];
 #pragma unroll
         for (int x = 0; x < 64; ++x) {
+          if (x == kFirst / 2) {
+            if (ok) tmem_store<kFirst / 2>(tbase + col_s(h), u);
+            if (ok) tmem_wait_st();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_half[h]);
+          }
           float p0, p1;
           unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(sc[2 * x]), __uint_as_float(sc[2 * x + 1])), scale2, minus_m), p0, p1);
           p0 = ex2_approx(p0);
@@ -744,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
           u[x] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        if (ok) tmem_st64(tbase + col_s(h), u);
+        if (ok) tmem_store<64 - kFirst / 2>(tbase + col_s(h) + kFirst / 2, u + kFirst / 2);
         float s0, s1;
         unpack_f32x2(add_f32x2(add_f32x2(sum2[0], sum2[1]), add_f32x2(sum2[2], sum2[3])), s0, s1);
         l += s0 + s1;
