@@ -55,8 +55,9 @@ constexpr int kOffBar = kOffRing + kStages * kTile;
 constexpr int kItems = 4;                   // pieces announced ahead
 constexpr int kNumBars = 2 * kStages + 2 + 2 * 5 + 1 + 2 * kItems;
 constexpr int kOffItem = kOffBar + 256;
-constexpr int kOffOut = kOffItem + kItems * 64;  // per softmax warp 32 rows x 32 dimensions of bf16 output
-constexpr int kSmem = kOffOut + 8 * 2048;
+constexpr int kOutBytes = 4096;                  // per softmax warp 32 rows x 64 dimensions of bf16 output
+constexpr int kOffOut = kOffItem + kItems * 64;
+constexpr int kSmem = kOffOut + 8 * kOutBytes;
 // Registers per thread: at launch, and after the warpgroups have shared them out (128 threads that load and issue,
 // 256 softmax threads that hold a row of scores each).
 constexpr int kRegsLaunch = 168;
@@ -260,7 +261,20 @@ struct alignas(64) Piece {
 };
 static_assert(sizeof(Piece) == 64, "a piece's place in shared memory");
 
-// Walks a CTA's pieces in order.
+// last_at_most by a warp, 32 places at once: a search's loads wait for each other, and the CTA for its first piece.
+__device__ __forceinline__ int warp_last_at_most(const int32_t* a, int n, int x) {
+  int lo = 0;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int i = (threadIdx.x & 31) * step;
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, i == 0 || (i < n && a[lo + i] <= x)));
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return lo;
+}
+
+// Walks a CTA's pieces in order. A warp constructs it, one lane walks.
 class Walk {
  public:
   __device__ __forceinline__ Walk(const Params& p) : p_(p) {
@@ -274,19 +288,14 @@ class Walk {
     end_ = s.start(blockIdx.x + 1);
     if (x_ >= end_) return;
     // the last sequence whose first unit is at most x (empty ones before it are skipped by the search)
-    int lo = 0, hi = p.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.h_kv * p.pre[mid] <= x_) lo = mid; else hi = mid - 1;
-    }
-    b_ = lo;
+    b_ = warp_last_at_most(p.pre, p.B, x_ / p.h_kv);
     const int first = p.pre[b_];
     const int tiles = p.pre[b_ + 1] - first;
     const int off = x_ - p.h_kv * first;
     j_ = off / tiles;
     const int rem = off - j_ * tiles;
     const int base = p.base[b_];
-    i_ = base + last_at_most(p.cum + base, p.base[b_ + 1] - base, first + rem);
+    i_ = base + warp_last_at_most(p.cum + base, p.base[b_ + 1] - base, first + rem);
     t_ = first + rem - p.cum[i_];
   }
   __device__ __forceinline__ bool next(Piece& c) {
@@ -620,8 +629,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 3) {
     // =========================== announces the pieces ===========================
+    Walk walk(p);
     if (lane == 0) {
-      Walk walk(p);
       for (bool more = true; more; ++di) {
         Piece c{};
         more = walk.next(c);
@@ -788,75 +797,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[h]);
       }
-      // the piece's output
+      // the piece's output, into registers, so that the next products need not wait for its stores
       wait_warp(&o_full[h], pieces++ & 1);
       tc_fence_after_sync();
-      const bool some = l != 0.0f;  // (a query of NaN has a sum of NaN, and its output)
-      const int row = h * kHalf + r;
-      const int j = items[s].j, slot = items[s].slot, tok0 = items[s].k.tok0;
-      hand_back(s);
-      const float inv = some ? 1.0f / l : 0.0f;
-      if (slot < 0) {
-        // a thread's row is 256 bytes from its neighbour's: through shared memory, so that four lanes write 64 bytes of
-        // a row together (a store instruction then touches 8 lines instead of 32)
-        uint8_t* stage = smem + kOffOut + (warp - 4) * 2048;
-        const int64_t mine = live ? static_cast<int64_t>(tok0 + tok) * p.h_q + j * p.G + g : -1;
-#pragma unroll 1
-        for (int x = 0; x < 4; ++x) {
-          float v[32];
-          if (ok) {
-            tmem_ld32(tbase + col_o(h) + 32 * x, v);
-          } else {
-#pragma unroll
-            for (int y = 0; y < 32; ++y) v[y] = 0.0f;
-          }
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float a = some ? v[8 * y + 2 * e] * inv : 0.0f, b = some ? v[8 * y + 2 * e + 1] * inv : 0.0f;
-              const __nv_bfloat162 ab = __floats2bfloat162_rn(a, b);
-              w[e] = *reinterpret_cast<const uint32_t*>(&ab);
-            }
-            *reinterpret_cast<uint4*>(stage + lane * 64 + ((y ^ (lane >> 1)) & 3) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int rr = 8 * y + (lane >> 2);
-            const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((lane ^ (rr >> 1)) & 3) * 16);
-            const int64_t to = __shfl_sync(0xffffffffu, mine, rr);
-            if (to >= 0) *reinterpret_cast<uint4*>(p.out + to * kD + 32 * x + 8 * (lane & 3)) = w;
-          }
-          __syncwarp();
-        }
+      uint32_t o[128];
+      if (ok) {
+        tmem_ld128(tbase + col_o(h), o);
       } else {
-#pragma unroll 1
-        for (int x = 0; x < 4; ++x) {
-          float v[32];
-          if (ok) {
-            tmem_ld32(tbase + col_o(h) + 32 * x, v);
-          } else {
 #pragma unroll
-            for (int y = 0; y < 32; ++y) v[y] = 0.0f;
-          }
-          if (!live) continue;
-#pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            float4 f = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
-            if (!some) f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            *reinterpret_cast<float4*>(p.pieces_o + piece_at(slot, row, 32 * x + 4 * y)) = f;
-          }
-        }
-        if (live) {
-          p.pieces_m[static_cast<int64_t>(slot) * kRowTile + row] = m;
-          p.pieces_l[static_cast<int64_t>(slot) * kRowTile + row] = l;
-        }
+        for (int x = 0; x < 128; ++x) o[x] = 0u;
       }
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[h]);
+      const int row = h * kHalf + r;
+      const int j = items[s].j, slot = items[s].slot, tok0 = items[s].k.tok0;
+      hand_back(s);
+      if (l == 0.0f) {  // (a query of NaN has a sum of NaN, and its output)
+#pragma unroll
+        for (int x = 0; x < 128; ++x) o[x] = 0u;
+      }
+      if (slot < 0) {
+        // a thread's row is 256 bytes from its neighbour's: through shared memory, so that eight lanes write 128 bytes of
+        // a row together (a store instruction then touches 4 lines instead of 32)
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        uint8_t* stage = smem + kOffOut + (warp - 4) * kOutBytes;
+        const int64_t mine = live ? static_cast<int64_t>(tok0 + tok) * p.h_q + j * p.G + g : -1;
+        int64_t to[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) to[y] = __shfl_sync(0xffffffffu, mine, 4 * y + (lane >> 3));
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int at = 64 * x + 8 * y + 2 * e;
+              const __nv_bfloat162 ab = __floats2bfloat162_rn(__uint_as_float(o[at]) * inv, __uint_as_float(o[at + 1]) * inv);
+              w[e] = *reinterpret_cast<const uint32_t*>(&ab);
+            }
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((y ^ lane) & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const int rr = 4 * y + (lane >> 3);
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((lane ^ rr) & 7) * 16);
+            if (to[y] >= 0) *reinterpret_cast<uint4*>(p.out + to[y] * kD + 64 * x + 8 * (lane & 7)) = w;
+          }
+          __syncwarp();
+        }
+      } else if (live) {
+#pragma unroll
+        for (int x = 0; x < 16; ++x) st_global_v8(p.pieces_o + piece_at(slot, row, 8 * x), o + 8 * x);
+        p.pieces_m[static_cast<int64_t>(slot) * kRowTile + row] = m;
+        p.pieces_l[static_cast<int64_t>(slot) * kRowTile + row] = l;
+      }
     }
   }
 
