@@ -188,7 +188,6 @@ struct GqaRowsPlan {
   // shared prefix (then cu_q, seq_lens and out are not used): table, length
   const int32_t* prefix_table;
   int prefix_len, prefix_splits, prefix_blocks;
-  const int32_t* own_lens;  // [B] (simple form)
   int N, B, h_q, h_kv;
   float scale_log2;
   int num_sms;
