@@ -34,7 +34,7 @@
 #include <cstdint>
 
 #include "gqa_paged.cuh"
-#include "moe_device.cuh"
+#include "paged_device.cuh"
 #include "moe_launch.h"
 
 namespace moe {

@@ -22,7 +22,7 @@
 
 #include <cstdint>
 
-#include "moe_device.cuh"
+#include "paged_device.cuh"
 #include "moe_launch.h"
 
 namespace moe {
