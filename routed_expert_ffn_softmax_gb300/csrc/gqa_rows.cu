@@ -11,20 +11,28 @@
 //
 // Softmax: a thread owns a row (TMEM lane): its 128 scores come with one TMEM load and its probabilities leave with one
 // store, so the row's maximum and sum need no exchange. (TMEM instructions that meet the running products stall: with
-// two threads per row and four times the instructions, 16K prompts took 391 us instead of 357.) O stays in TMEM; it is
+// two threads per row and four times the instructions, 16K prompts took 391 us instead of 357.) The store is in two
+// parts, so that most of P . V starts before the last exponentials are done. O stays in TMEM; it is
 // rescaled only when a row's maximum has grown by more than 2^8 since the reference in use (probabilities are then at
 // most 2^8, exact to the same relative bf16 step, and sums stay far inside fp32), which after the first tiles is rare.
 //
 // Work split: the key tiles of all (sequence, head, block) segments form one list (causal blocks have different
 // lengths, windows bound them) and each CTA takes a contiguous range of it, so any mix of prompts balances to within
 // a tile. Which range holds what comes from a small table kernel, since lengths are only known on the device. A
-// segment cut between CTAs leaves (o, m, l) pieces that a third kernel joins in CTA order, one warp per row. For a
+// segment cut between CTAs leaves (o, m, l) pieces that a third kernel joins in CTA order, one warp per row (joined in
+// this kernel by whoever came last, pairs of pieces at a time, 8 chunks behind contexts took 61 us instead of 55). For a
 // shared prefix the host knows the sizes: equal splits per segment, joined the same way; the decode kernel adds the
 // result to the sequences' own keys.
 //
 // Per CTA, 12 warps: 0 TMA producer (Q per piece; K and V tiles alternate in a ring of 4 x 32 KB), 1 and 2 issue the
 // MMAs of the two halves in turn, 3 announces the pieces and writes zeros for blocks that see nothing, 4-7 and 8-11 the
 // softmax and output of the two halves.
+//
+// What bounds it: per tile a half's chain of scores, softmax and product, about 2850 cycles (products 1130 with their
+// issue, softmax 1475 of which 512 are exponentials, the rest hand-over; the last exponentials under the product). TMEM
+// holds two halves, so the tensor pipe is busy 68% of the time. GB300: 16K prompt behind a window of 4096 in 341 us (1412
+// TFLOP/s), six prompts of up to 4095 tokens in 171 (1095), a prefix of 32K for 255 sequences 174 (1590); a call with few
+// rows pays 7 us up to its first scores and 9 to join its pieces.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -75,7 +83,7 @@ __device__ constexpr uint32_t col_o(int h) { return 256u + 128u * h; }
 
 // What a segment costs beside its tiles (its queries' load, the first scores and the output, which no product
 // overlaps), in tiles: the CTAs' shares are cut so that those with many short segments get fewer tiles (ragged and
-// 16K prompts take 175 and 355 us at 2, 181 and 355 at 3).
+// 16K prompts take 184 and 365 us at 1, 172 and 342 at 2, 177 and 339 at 3).
 constexpr int kSegCost = 2;
 
 constexpr int kReaders = 3 + 2 * kSoft / 32;  // warps that read the announced pieces
