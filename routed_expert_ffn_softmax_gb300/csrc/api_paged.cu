@@ -19,14 +19,15 @@ constexpr size_t kTicketOffset = 8;
 constexpr size_t kDecodePartialBytes = sizeof(float) * static_cast<size_t>(moe::kPartialCtas) * 2 * moe::kGqaSlotFloats;
 
 // Splits of each of `segs` segments of a shared prefix of `tiles` key tiles over the CTAs: whole waves of pieces, each
-// its tiles and about 3 tiles' time of start and output, and for joining about 1/50 of a tile's time per piece.
+// its tiles and about 3 tiles' time of start and output, and for joining about 1/33 of a tile's time per piece (with 1/50
+// or 1/25 8 sequences behind 8K keys take 29.7 or 28.2 us instead of 28.3, 255 behind 32K 257 or 265 instead of 257).
 constexpr int kMaxPrefixPieces = 4 * moe::kRowsCtas;
 int prefix_splits(int64_t segs, int tiles) {
   int best = 1;
   double least = 0.0;
   for (int s = 1; s <= tiles && (s == 1 || segs * s <= kMaxPrefixPieces); ++s) {
     const int64_t waves = (segs * s + moe::kRowsCtas - 1) / moe::kRowsCtas;
-    const double cost = static_cast<double>(waves) * ((tiles + s - 1) / s + 3) + 0.02 * static_cast<double>(segs * s);
+    const double cost = static_cast<double>(waves) * ((tiles + s - 1) / s + 3) + 0.03 * static_cast<double>(segs * s);
     if (s == 1 || cost < least) {
       best = s;
       least = cost;
