@@ -802,3 +802,44 @@ def test_binding_refuses_shapes_and_types():
             moe.moe_qk_norm_rope(**{**qk, name: value})
     torch.cuda.synchronize()
     assert moe.workspace_status(ws) == 0
+
+
+def test_prefill_more_blocks_and_sequences_than_one_search_step():
+    """More than 32 x 32 row blocks of a sequence, and more sequences: sampled rows against 64 bits."""
+    n, h_q = 20001, 16
+    c = ref.Cache((n,), 1, 64, DEV)
+    q = randn(n, h_q, D, seed=3)
+    out, ws = torch.empty_like(q), moe.alloc_paged_workspace(n, 1, h_q, 1, D, device=DEV)
+    moe.moe_gqa_paged_prefill(q, i32([0, n]), c.k, c.v, c.table, i32([n]), SCALE, out, ws, window=300, n_sink=5)
+    rows = torch.cat([torch.arange(0, n, 97), torch.arange(n - 20, n)]).to(DEV)
+    see = ref.visible(rows[:, None], torch.arange(n, device=DEV), 300, 5)
+    ref.check(out[rows], *ref.attend(q[rows], *c.rows[0], see, SCALE), "sampled rows")
+    assert moe.workspace_status(ws) == 0 and torch.isfinite(out.float()).all()
+    g = np.random.default_rng(8)
+    lens = g.integers(1, 60, 2048)
+    run_prefill(lens.tolist(), [int(g.integers(0, m + 1)) for m in lens], 8, 1, 16)
+
+
+def test_all_attention_calls_at_once_on_three_streams():
+    lens = (3000, 200, 1500)
+    c = ref.Cache(lens, 2, 16, DEV)
+    lt, cu, shared = i32(lens), i32([0, 150, 151, 400]), c.table[0].contiguous()
+    q, qp = randn(3, 16, D, seed=1), randn(400, 16, D, seed=2)
+    ws = [moe.alloc_paged_workspace(400, 3, 16, 2, D, 3000, device=DEV) for _ in range(3)]
+    calls = [lambda o, s: moe.moe_gqa_paged_decode(q, c.k, c.v, c.table, lt, SCALE, o, ws[0], window=900, n_sink=4, stream=s),
+             lambda o, s: moe.moe_gqa_paged_prefill(qp, cu, c.k, c.v, c.table, lt, SCALE, o, ws[1], stream=s),
+             lambda o, s: moe.moe_gqa_prefix_decode(q, shared, 3000, c.k, c.v, c.table, lt, SCALE, o, ws[2], stream=s)]
+    like = [q, qp, q]
+    want = [torch.empty_like(x) for x in like]
+    for f, o in zip(calls, want):
+        f(o, None)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [[torch.zeros_like(x) for x in like] for _ in range(20)]
+    torch.cuda.synchronize()
+    for r in range(20):
+        for i in range(3):
+            calls[i](outs[r][i], streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for row in outs for o, w in zip(row, want))
+    assert all(moe.workspace_status(w) == 0 and not w[4:4096].any() for w in ws)
