@@ -178,6 +178,32 @@ __device__ __forceinline__ void load_row(const float* row, float (&v)[kVals]) {
   }
 }
 
+// A group's heads in a partial: per dimension beside each other, so that a thread moves up to four at once (one at a time,
+// merging two pieces of 16 heads took a CTA 4000 cycles).
+template <int kVals>
+__device__ __forceinline__ void store_heads(float* to, const float (&v)[kVals]) {
+  if constexpr (kVals >= 4) {
+#pragma unroll
+    for (int h = 0; h < kVals; h += 4) *reinterpret_cast<float4*>(to + h) = make_float4(v[h], v[h + 1], v[h + 2], v[h + 3]);
+  } else {
+#pragma unroll
+    for (int h = 0; h < kVals; ++h) to[h] = v[h];
+  }
+}
+template <int kVals>
+__device__ __forceinline__ void load_heads(const float* from, float (&v)[kVals]) {
+  if constexpr (kVals >= 4) {
+#pragma unroll
+    for (int h = 0; h < kVals; h += 4) {
+      const float4 f = __ldcg(reinterpret_cast<const float4*>(from + h));
+      v[h] = f.x, v[h + 1] = f.y, v[h + 2] = f.z, v[h + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < kVals; ++h) v[h] = __ldcg(from + h);
+  }
+}
+
 // The shared prefix's part of group j's heads for sequence b, and adding it to the running (M, L, O); this thread
 // holds dimension r.
 template <int kGP>
@@ -827,6 +853,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before_sync();
         mbar_arrive(&h_empty[hb]);
 
+        // A segment cut between CTAs: whether its other pieces have all been published is asked for now, and known by the
+        // time it is needed (with 16 heads it is asked for then: early, registers spill and short segments take 5% more).
+        constexpr bool kAskEarly = kGP <= 8;
+        const bool whole = pc.tl == 0 && pc.n == pc.nt;
+        auto cta_of = [&](int i) {  // the CTA whose range holds tile i
+          const int big = rm * (q_tiles + 1);
+          return i < big ? i / (q_tiles + 1) : rm + (i - big) / q_tiles;
+        };
+        int c_first = 0, c_last = 0;
+        auto ask = [&]() {
+          c_first = cta_of(pc.seg0);
+          c_last = cta_of(pc.seg0 + pc.nt - 1);
+          if (gt == 0) misc[8] = ld_acquire_gpu(&p.counters[c_first]) == c_last - c_first;
+        };
+        if (kAskEarly && !whole) ask();
+
         // the piece's last one or two O^T, in tile order
         auto drain_o = [&](int i, const float (&a)[kGP]) {
           const int sb = i & 1;
@@ -875,7 +917,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             l_tot[h] = (red_sum[h] + red_sum[kN + h]) + (red_sum[2 * kN + h] + red_sum[3 * kN + h]);
         }
 
-        const bool whole = pc.tl == 0 && pc.n == pc.nt;
         uint16_t* outp = p.out + (static_cast<int64_t>(pc.b) * p.h_q + static_cast<int64_t>(pc.j) * p.G) * kD + r;
         if (whole) {
           if constexpr (kPaged)
@@ -894,35 +935,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Segment cut between CTAs: its pieces are merged in CTA order by the CTA that completes
           // the set. If every other piece is already published, this one merges straight from its
           // registers; otherwise it publishes (o, m, l) and the last to arrive merges.
-          auto cta_of = [&](int i) {  // the CTA whose range holds tile i
-            const int big = rm * (q_tiles + 1);
-            return i < big ? i / (q_tiles + 1) : rm + (i - big) / q_tiles;
-          };
-          const int c_first = cta_of(pc.seg0);
-          const int c_last = cta_of(pc.seg0 + pc.nt - 1);
-          const int others = c_last - c_first;
-          if (gt == 0) misc[8] = ld_acquire_gpu(&p.counters[c_first]) == others;
-          named_bar_sync(2, kSoft);
+          if (!kAskEarly) {
+            ask();
+            named_bar_sync(2, kSoft);
+          }
           const bool direct = misc[8] != 0;
           bool merge = direct;
           if (!direct) {
             const int slot = pi == 0 ? 0 : 1;
             float* mine = p.partials + (cta * 2 + slot) * kSlotFloats;
-#pragma unroll
-            for (int h = 0; h < kGP; ++h) mine[h * kD + r] = o_acc[h];
+            store_heads(mine + r * kGP, o_acc);
             if (gt == 0) {
-#pragma unroll
-              for (int h = 0; h < kGP; ++h) {
-                mine[kN * kD + h] = m_run[h];
-                mine[kN * kD + kN + h] = l_tot[h];
-              }
+              store_heads(mine + kN * kD, m_run);
+              store_heads(mine + kN * kD + kN, l_tot);
             }
             named_bar_sync(2, kSoft);
             if (gt == 0) {
               // the fence after the barrier publishes the whole warpgroup's writes (cumulativity)
               __threadfence();
               const int old = atomicAdd(&p.counters[c_first], 1);
-              const int last = old == others;
+              const int last = old == c_last - c_first;
               if (last) p.counters[c_first] = 0;
               misc[8] = last;
             }
@@ -948,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int u = 0; u < kChunk; ++u) {
                 const int c = c0 + u;
                 if (c > c_last) continue;
-                if (direct && c == cta) {
+                if ((direct || kAskEarly) && c == cta) {
 #pragma unroll
                   for (int h = 0; h < kGP; ++h) {
                     mc[u][h] = m_run[h];
@@ -958,12 +990,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                   const int cslot = range_start(c) >= pc.seg0 ? 0 : 1;
                   const float* src = p.partials + (c * 2 + cslot) * kSlotFloats;
-#pragma unroll
-                  for (int h = 0; h < kGP; ++h) {
-                    mc[u][h] = __ldcg(src + kN * kD + h);
-                    lc[u][h] = __ldcg(src + kN * kD + kN + h);
-                    oc[u][h] = __ldcg(src + h * kD + r);
-                  }
+                  load_heads(src + kN * kD, mc[u]);
+                  load_heads(src + kN * kD + kN, lc[u]);
+                  load_heads(src + r * kGP, oc[u]);
                 }
               }
 #pragma unroll
@@ -972,8 +1001,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int h = 0; h < kGP; ++h) {
                   const float m_new = fmaxf(M[h], mc[u][h]);
-                  const float a_old = exp2f(M[h] - m_new);
-                  const float a_c = exp2f(mc[u][h] - m_new);
+                  const float a_old = kPaged ? ex2_approx(M[h] - m_new) : exp2f(M[h] - m_new);
+                  const float a_c = kPaged ? ex2_approx(mc[u][h] - m_new) : exp2f(mc[u][h] - m_new);
                   O[h] = O[h] * a_old + oc[u][h] * a_c;
                   L[h] = L[h] * a_old + lc[u][h] * a_c;
                   M[h] = m_new;
