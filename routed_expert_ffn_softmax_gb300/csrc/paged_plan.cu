@@ -151,14 +151,14 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PagedPlanArg
     const int col = ((ctx[b] + p.page_size - 1) >> p.page_shift) + k - base[b];
     p.block_table[static_cast<int64_t>(b) * p.max_pages + col] = p.free_pages[count - 1 - k];
   }
-  // token rows
+  // token rows (counted in 64 bits: n_rows may lie within a step of 2^31)
   const int rows = cu[p.B];
-  for (int t = first; t < p.n_rows; t += step) {
+  for (int64_t t = first; t < p.n_rows; t += step) {
     int32_t pos = 0, slot = -1;
     if (t < rows) {
-      const int b = interval_of(cu, p.B, t);
+      const int b = interval_of(cu, p.B, static_cast<int>(t));
       const int cb = ctx[b];
-      const int i = t - cu[b];
+      const int i = static_cast<int>(t) - cu[b];
       pos = static_cast<int32_t>(static_cast<uint32_t>(cb < 0 ? -1 - cb : cb) + static_cast<uint32_t>(i));
       if (cb >= 0) {
         const int idx = pos >> p.page_shift;
@@ -199,8 +199,8 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PagedPlanArg
 
 cudaError_t launch_paged_plan(const PagedPlanArgs& args, int num_sms, cudaStream_t stream) {
   // one token row per thread until the grid covers the device (each CTA repeats the scans)
-  const int want = (args.n_rows + plan::kThreads - 1) / plan::kThreads;
-  const int grid = want < 1 ? 1 : (want < num_sms ? want : num_sms);
+  const int64_t want = (static_cast<int64_t>(args.n_rows) + plan::kThreads - 1) / plan::kThreads;
+  const int grid = want < 1 ? 1 : (want < num_sms ? static_cast<int>(want) : num_sms);
   return launch_pdl(plan::paged_plan_kernel, dim3(grid), dim3(plan::kThreads), 0, stream, args);
 }
 

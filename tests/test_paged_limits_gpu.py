@@ -1,0 +1,45 @@
+"""The serving path over a paged key/value cache at the edges its header allows: the largest token row counts (needs a
+GPU)."""
+import torch
+
+import paged_reference as ref
+import routed_expert_ffn_softmax_gb300 as moe
+from test_paged_gpu import DEV, D, SCALE, i32, randn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from routed_expert_ffn_softmax_gb300 import build
+    build.build()
+    moe.load()
+    yield
+
+
+# ---------------------------------------------------------------- plan
+def test_plan_with_as_many_token_rows_as_32_bits_count():
+    """2^31 - 1 token rows, nearly all of them one sequence's: every row's position and slot, and the words around the
+    rows as they were."""
+    page, pages, n_rows, pad = 1024, 2 ** 21 - 1, 2 ** 31 - 1, 4096
+    new = [3, 2 ** 31 - 6000]
+    width = ref.up(new[1], page)
+    ws = moe.alloc_paged_workspace(device=DEV)
+    rows = [torch.full((n_rows + 2 * pad,), -5, dtype=torch.int32, device=DEV) for _ in range(2)]
+    positions, slots = (r[pad:pad + n_rows] for r in rows)
+    table, lens, cu, left = (torch.full(s, -1, dtype=torch.int32, device=DEV) for s in ((2, width), (2,), (3,), (1,)))
+    free = torch.arange(pages, dtype=torch.int32, device=DEV)
+    moe.moe_paged_plan(i32([0, 0]), i32(new), page, pages, free, i32([pages]), table, lens, cu, positions, slots, left, ws)
+    torch.cuda.synchronize()
+    assert moe.workspace_status(ws) == 0
+    assert lens.tolist() == new and cu.tolist() == [0, 3, sum(new)] and left.tolist() == [pages - 1 - width]
+    # pages come from the end of the list: sequence 0 has the last, sequence 1 those before it
+    assert table[0, 0] == pages - 1 and torch.equal(table[1], pages - 2 - torch.arange(width, dtype=torch.int32, device=DEV))
+    assert all((r[:pad] == -5).all() and (r[pad + n_rows:] == -5).all() for r in rows)
+    for at in range(0, n_rows, 1 << 27):
+        t = torch.arange(at, min(n_rows, at + (1 << 27)), device=DEV)
+        pos = torch.where(t < 3, t, t - 3)
+        slot = torch.where(t < 3, (pages - 1) * page + pos, (pages - 2 - pos // page) * page + pos % page)
+        real = t < sum(new)
+        assert torch.equal(positions[at:at + t.numel()], torch.where(real, pos, 0).to(torch.int32))
+        assert torch.equal(slots[at:at + t.numel()], torch.where(real, slot, -1).to(torch.int32))
