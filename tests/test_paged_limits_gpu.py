@@ -1,5 +1,6 @@
 """The serving path over a paged key/value cache at the edges its header allows: the largest token row counts (needs a
 GPU)."""
+import pytest
 import torch
 
 import paged_reference as ref
