@@ -29,7 +29,7 @@ __all__ = [
     "moe_expert_ffn_residual", "moe_ffn_forward_residual", "moe_set_decode_step_policy", "moe_ffn_forward_launches",
     "moe_test_expire_grid_barrier", "moe_set_expert_pass_tokens", "moe_test_expert_wait_limit",
     "moe_paged_workspace_size", "alloc_paged_workspace", "moe_paged_plan", "moe_qk_norm_rope", "moe_gqa_paged_decode",
-    "moe_gqa_paged_prefill", "moe_gqa_prefix_decode",
+    "moe_gqa_paged_prefill", "moe_gqa_prefix_decode", "moe_test_paged_give_up",
 ]
 
 MOE_W_BF16 = 0
@@ -381,3 +381,12 @@ def moe_gqa_prefix_decode(q, prefix_table, prefix_len: int, k_cache, v_cache, bl
                                                            scale, out, workspace, _raw(stream))
     if st:
         raise MoeError("moe_gqa_prefix_decode", st)
+
+
+def moe_test_paged_give_up(tile: int = -1) -> None:
+    """Failure-detection test hook: the row-block attention kernel's producers stop before this tile (-1: never), and what
+    waits for them gives up: nonzero workspace status (see include/paged/moe_paged_test.h)."""
+    f = load().moe_test_paged_give_up
+    f.argtypes = [ctypes.c_int]
+    f.restype = ctypes.c_int
+    _check("moe_test_paged_give_up", f(int(tile)))

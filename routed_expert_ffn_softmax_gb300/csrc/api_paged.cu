@@ -2,12 +2,14 @@
 // checks, workspace layout and launches.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
 #include "api_util.h"
 #include "moe_launch.h"
 #include "paged/moe_paged.h"
+#include "paged/moe_paged_test.h"
 
 namespace {
 
@@ -156,6 +158,9 @@ moe::GqaPlan decode_plan(const Attention& a, int sms) {
   return plan;
 }
 
+// moe_test_paged_give_up
+std::atomic<int> g_give_up_tile{-1};
+
 moe::GqaRowsPlan rows_plan(const Attention& a, const Layout& L, int sms) {
   char* ws = static_cast<char*>(a.workspace);
   moe::GqaRowsPlan plan{};
@@ -174,6 +179,7 @@ moe::GqaRowsPlan rows_plan(const Attention& a, const Layout& L, int sms) {
   plan.h_kv = a.h_kv;
   plan.scale_log2 = scale_log2(a.scale);
   plan.num_sms = sms < moe::kRowsCtas ? sms : moe::kRowsCtas;
+  plan.give_up_tile = g_give_up_tile.load(std::memory_order_relaxed);
   return plan;
 }
 
@@ -338,6 +344,12 @@ moe_status_t moe_gqa_prefix_decode(const uint16_t* q, const int32_t* prefix_tabl
     own.prefix.half_seqs = half_tokens(h_q / h_kv);
   }
   return cuda_status(moe::launch_gqa_decode(own, s));
+}
+
+moe_status_t moe_test_paged_give_up(int tile) {
+  if (tile < -1) return MOE_ERR_INVALID_ARG;
+  g_give_up_tile.store(tile, std::memory_order_relaxed);
+  return MOE_OK;
 }
 
 }  // extern "C"

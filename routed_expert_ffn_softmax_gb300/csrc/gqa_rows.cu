@@ -72,7 +72,7 @@ constexpr int kRegsLaunch = 168;
 constexpr int kRegsIo = 88;
 constexpr int kRegsSoftmax = 208;
 static_assert(128 * kRegsIo + 2 * kSoft * kRegsSoftmax <= kThreads * kRegsLaunch, "a larger share would wait forever");
-static_assert(kNumBars * 8 + 8 <= 256, "barrier area");
+static_assert(kNumBars * 8 + 12 <= 256, "barrier area");
 static_assert(kSmem <= 232448, "dynamic shared memory per CTA");
 static_assert(kRowTile == 2 * kHalf, "partials hold both halves");
 
@@ -115,6 +115,7 @@ struct Params {
   int prefix_len, prefix_splits, prefix_blocks;
   int N, B, h_q, h_kv, G, half_tokens, max_blocks, L_cap;
   float scale_log2;
+  int give_up_tile;  // failure-detection test: the producers stop before this tile (-1: never)
 };
 
 // Rows cu_q[b] .. of sequence b, 0 unless they lie within [0, N] in order.
@@ -407,6 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* d_full = mma_done + 1;      // [kItems]
   uint64_t* d_empty = d_full + kItems;  // [kItems]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(d_empty + kItems);
+  volatile uint32_t* turns_over = tmem_slot + 1;  // [2]: half 1's issuer has left the list; half 0's ends the turns
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -430,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&d_full[i], 1);
       mbar_init(&d_empty[i], kReaders);
     }
+    turns_over[0] = turns_over[1] = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
@@ -496,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int key = sp.key_tile(t) * kKeys + row0;
         const int z = id < 0 ? -1 : id * p.h_kv + j;
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, id != -2 && !is_v)) * static_cast<uint32_t>(rows) * 256u;
+        if (it == p.give_up_tile) ok = false;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           const int idx = 2 * it + kv;
@@ -555,9 +559,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t idesc_o = umma_idesc_bf16_m128(kD) | kIdescBMajorMN;
     const uint64_t desc_v = umma_desc_sw128_mn_sbo(0, kUpper, kGroupBytes);
     const int my_turn = kTurnBar + h, other_turn = kTurnBar + 1 - h;
+    // After a wait that ran out this warp waits for nothing more (only for its turns), issues nothing and hands nothing
+    // back: a stage it has not seen full is then never filled again over copies in flight, and the other roles' waits run
+    // out in their turn, once each.
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (!mbar_wait_soon(bar, parity)) ok = false;
+      if (ok && !mbar_wait_soon(bar, parity)) ok = false;
     };
     uint32_t pv = 0, seg = 0;    // products P . V issued, pieces begun
     uint32_t st_k = 0, ph = 0;   // ring place and phase of the next K tile; the V tile due is the one before
@@ -591,16 +598,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait(&p_full[h], pv++ & 1);
           tc_fence_after_sync();
         }
-        if (elect_one()) {
+        if (elect_one() && ok) {
           if (active) {
-            if (ok && t > 0) {
+            if (t > 0) {
 #pragma unroll
               for (int x = kFirst / 16; x < kKeys / 16; ++x)
                 umma_bf16_tmem_a(d_o, d_s + 8 * x, v + x * (2 * kGroupBytes >> 4), idesc_o, true);
             }
             // the scores overwrite the probabilities of the tile before, whose product was issued just now: MMAs of one
             // thread run in order
-            if (ok && t < n) {
+            if (t < n) {
               const uint64_t k = umma_desc_sw128_sbo(0, kGroupBytes) + (ring + st_k * (kTile >> 4));
 #pragma unroll
               for (int x = 0; x < kD / 16; ++x)
@@ -629,8 +636,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (h == 0) named_bar_sync(my_turn, 64);  // the turn that half 1 passed last
-    if (!ok && lane == 0) atomicExch(p.status, kStatusWaitFullTimeout);
+    // The turns have no limit of their own, so they go on until both issuers have left the list (one of them earlier, when
+    // its wait for a piece ran out): half 0 ends them after it has seen that half 1 has.
+    if (h == 0) {
+      for (bool over = false; !over;) {
+        named_bar_sync(my_turn, 64);
+        over = __any_sync(0xffffffffu, turns_over[0] != 0);
+        if (lane == 0) turns_over[1] = over;
+        __syncwarp();
+        named_bar_arrive(other_turn, 64);
+      }
+    } else {
+      if (lane == 0) turns_over[0] = 1;
+      __syncwarp();
+      for (;;) {
+        named_bar_sync(my_turn, 64);
+        if (turns_over[1] != 0) break;
+        named_bar_arrive(other_turn, 64);
+      }
+    }
+    if (__any_sync(0xffffffffu, !ok) && lane == 0) atomicExch(p.status, kStatusWaitFullTimeout);
     // every MMA has completed before TMEM is released
     if (elect_one()) umma_commit(mma_done);
     if (!mbar_wait_soon(mma_done, 0) && lane == 0) atomicExch(p.status, kStatusDrainTimeout);
@@ -676,14 +701,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = r - i * p.G;
     const bool neg = p.scale_log2 < 0.0f;
     const float scale = fabsf(p.scale_log2);
-    bool ok = true;
-    auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
-      const bool w = __all_sync(0xffffffffu, ok && mbar_wait_soon(bar, parity));
-      if (!w && ok) {
-        ok = false;
-        atomicExch(p.status, kStatusWaitFullTimeout);
-      }
+    bool ok = true;  // the same for the whole warp, which leaves when a wait has run out
+    auto settle = [&](bool done) {
+      ok = __all_sync(0xffffffffu, done);
+      if (!ok) atomicExch(p.status, kStatusWaitFullTimeout);
     };
+    auto wait_warp = [&](uint64_t* bar, uint32_t parity) { settle(mbar_wait_soon(bar, parity)); };
     uint32_t cnt = 0;     // tiles of this half so far
     uint32_t pieces = 0;  // and pieces
     int it = 0;           // tiles of the CTA so far
@@ -710,14 +733,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = t0; t < t1; ++t, ++it, ++cnt) {
         const int kb = sp.key_tile(t) * kKeys;
         wait_warp(&s_full[h], cnt & 1);
+        if (!ok) break;
         tc_fence_after_sync();
         uint32_t sc[128];
-        if (ok) {
-          tmem_ld128(tbase + col_s(h), sc);
-        } else {
-#pragma unroll
-          for (int x = 0; x < 128; ++x) sc[x] = 0u;
-        }
+        tmem_ld128(tbase + col_s(h), sc);
         if (neg) {
 #pragma unroll
           for (int x = 0; x < 128; ++x) sc[x] ^= 0x80000000u;
@@ -732,22 +751,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 32; ++x)
               if (!((see >> x) & 1u)) sc[32 * w + x] = __float_as_uint(-INFINITY);
           }
+          bool landed = true;
           if (h == 0 && !sp.sees(kb + r)) {
             // a key no row sees: its cache row is arbitrary (even NaN) and a zero probability times NaN is NaN, so
             // this row of the V tile is cleared (the wait orders the overwrite behind the tile's landing)
             const int idx = 2 * it + 1;
             const int st = idx % kStages;
-            if (mbar_wait_soon(&full[st], static_cast<uint32_t>((idx / kStages) & 1))) {
+            landed = mbar_wait_soon(&full[st], static_cast<uint32_t>((idx / kStages) & 1));
+            if (landed) {
               uint4* v0 = reinterpret_cast<uint4*>(smem + kOffRing + st * kTile + tile_row(r));
               uint4* v1 = v0 + kUpper / 16;
 #pragma unroll
               for (int x = 0; x < 8; ++x)  // neighbours in other banks
                 v0[x ^ (r & 7)] = v1[x ^ (r & 7)] = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-              atomicExch(p.status, kStatusWaitFullTimeout);
             }
             fence_proxy_async_smem();
           }
+          settle(landed);
+          if (!ok) break;
         }
         // four chains, so that their latency overlaps
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -763,7 +784,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the scores' commit covered the product before them
 #pragma unroll 1
           for (int x = 0; x < 8; ++x) {
-            if (!ok) break;
             float o[16];
             uint32_t u[16];
             tmem_ld16(tbase + col_o(h) + 16 * x, o);
@@ -782,8 +802,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 64; ++x) {
           if (x == kFirst / 2) {
-            if (ok) tmem_store<kFirst / 2>(tbase + col_s(h), u);
-            if (ok) tmem_wait_st();
+            tmem_store<kFirst / 2>(tbase + col_s(h), u);
+            tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_half[h]);
@@ -796,25 +816,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
           u[x] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        if (ok) tmem_store<64 - kFirst / 2>(tbase + col_s(h) + kFirst / 2, u + kFirst / 2);
+        tmem_store<64 - kFirst / 2>(tbase + col_s(h) + kFirst / 2, u + kFirst / 2);
         float s0, s1;
         unpack_f32x2(add_f32x2(add_f32x2(sum2[0], sum2[1]), add_f32x2(sum2[2], sum2[3])), s0, s1);
         l += s0 + s1;
-        if (ok) tmem_wait_st();
+        tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[h]);
       }
       // the piece's output, into registers, so that the next products need not wait for its stores
-      wait_warp(&o_full[h], pieces++ & 1);
+      if (ok) wait_warp(&o_full[h], pieces++ & 1);
+      if (!ok) break;
       tc_fence_after_sync();
       uint32_t o[128];
-      if (ok) {
-        tmem_ld128(tbase + col_o(h), o);
-      } else {
-#pragma unroll
-        for (int x = 0; x < 128; ++x) o[x] = 0u;
-      }
+      tmem_ld128(tbase + col_o(h), o);
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[h]);
@@ -1012,6 +1028,7 @@ cudaError_t launch_gqa_rows(const GqaRowsPlan& plan, cudaStream_t stream) {
   p.L_cap = plan.paged.max_pages * page;
   // a scale of 0 makes all scores equal; the mask's infinities need a factor other than 0
   p.scale_log2 = plan.scale_log2 == 0.0f ? 1e-30f : plan.scale_log2;
+  p.give_up_tile = plan.give_up_tile;
 
   constexpr int kMaxDev = 64;  // the shared-memory opt-in is per device: done once on each
   static std::atomic<bool> done[kMaxDev];

@@ -191,6 +191,7 @@ struct GqaRowsPlan {
   int N, B, h_q, h_kv;
   float scale_log2;
   int num_sms;
+  int give_up_tile;         // failure-detection test: the producers stop before this tile (-1: never)
 };
 cudaError_t launch_gqa_rows(const GqaRowsPlan& plan, cudaStream_t stream);
 

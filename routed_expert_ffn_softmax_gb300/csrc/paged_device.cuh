@@ -16,11 +16,12 @@ enum : int32_t {
   kStatusPlanNoRoom = 7,  // the plan left a sequence out
 };
 
-// The same wait in few instructions, for kernels whose many waits would crowd the instruction cache: limited by a count
-// of tries (each suspends the thread for some tens of nanoseconds, so about the same two seconds).
+// mbar_wait in few instructions, for kernels whose many waits would crowd the instruction cache: limited by a count of
+// tries. A try that fails takes 1.5 to 4 us on the GB300, whatever suspend time it is given, so the limit is 0.8 to 2.1 s.
+// (Reading the clock in this loop costs 16K prompts 3%.)
 __device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
-  for (int i = 0; i < (1 << 25); ++i)
+  for (int i = 0; i < (1 << 19); ++i)
     if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
