@@ -2,8 +2,10 @@
 side of the paged serving path, with g++ against the installed torch.
 
 Each .cu translation unit is compiled in parallel, then linked into a shared
-library against the shared CUDA runtime. The build is skipped when the libraries
-are newer than every source and header.
+library against the shared CUDA runtime. libmoe.so needs nothing of torch and comes first: where the
+torch headers that _paged.so is built against are missing, build() raises after libmoe.so is in
+place. Either library is built again when a source or header of its own is newer, _paged.so also when
+the installed torch or the interpreter is another one than it was built for.
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +25,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 PY_SOURCE = os.path.join(CSRC, "py_paged.cpp")
 PY_LIB = os.path.join(PKG, "_paged.so")
+PY_STAMP = os.path.join(BUILD, "py_paged.stamp")  # what _paged.so was built for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
@@ -39,28 +43,43 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return sources() + [PY_SOURCE] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(INCLUDE, "**", "*.h"), recursive=True) + [os.path.abspath(__file__)]
+def _headers():
+    return glob.glob(os.path.join(INCLUDE, "**", "*.h"), recursive=True) + [os.path.abspath(__file__)]
+
+
+def _newer(lib: str, deps) -> bool:
+    return os.path.exists(lib) and all(os.path.getmtime(d) <= os.path.getmtime(lib) for d in deps)
+
+
+def lib_up_to_date() -> bool:
+    return _newer(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + _headers())
+
+
+def _py_target() -> str:
+    import torch
+    return f"{torch.__version__} in {os.path.dirname(torch.__file__)}, Python {sys.version}"
+
+
+def py_up_to_date() -> bool:
+    if not (_newer(PY_LIB, [PY_SOURCE] + _headers()) and os.path.exists(PY_STAMP)):
+        return False
+    with open(PY_STAMP, encoding="utf-8") as f:
+        return f.read() == _py_target()
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(PY_LIB)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(PY_LIB))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return lib_up_to_date() and py_up_to_date()
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and up_to_date():
+    lib_stale, py_stale = force or not lib_up_to_date(), force or not py_up_to_date()
+    if not (lib_stale or py_stale):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    cc = nvcc()
-    objs = []
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-        cmd = [cc, *ARCH, *NVCC_FLAGS, *extra_flags, "-I", INCLUDE, "-c", src, "-o", obj]
+        cmd = [nvcc(), *ARCH, *NVCC_FLAGS, *extra_flags, "-I", INCLUDE, "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
@@ -69,16 +88,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        py_obj = ex.submit(_compile_py)
-        objs = list(ex.map(compile_one, sources()))
-        py_obj = py_obj.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_py(py_obj)
+        py_obj = ex.submit(_compile_py) if py_stale else None
+        if lib_stale:
+            objs = list(ex.map(compile_one, sources()))
+            tmp = LIB + f".tmp{os.getpid()}"
+            _run("linking libmoe.so", [nvcc(), *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs])
+            os.replace(tmp, LIB)
+        if py_obj is not None:
+            _link_py(py_obj.result())
     return LIB
 
 
@@ -108,8 +125,9 @@ def _link_py(obj: str) -> None:
         "g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libmoe.so", "-L", libs, "-lc10", "-lc10_cuda", "-ltorch_cpu",
         "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"])
     os.replace(tmp, PY_LIB)
+    with open(PY_STAMP, "w", encoding="utf-8") as f:
+        f.write(_py_target())
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose=True))
