@@ -12,6 +12,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -29,7 +30,10 @@ PY_STAMP = os.path.join(BUILD, "py_paged.stamp")  # what _paged.so was built for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
-              "-Xptxas", "-warn-spills"]
+              "-Xptxas", "-v,-warn-spills"]
+# Kernels whose warps share out their registers: source, kernel, and the constant in the source that counts what a thread
+# has at launch. With another count their launch is refused.
+REGISTERS = (("gqa_rows.cu", "gqa_rows_kernel", "kRegsLaunch"),)
 
 
 def nvcc() -> str:
@@ -71,6 +75,19 @@ def up_to_date() -> bool:
     return lib_up_to_date() and py_up_to_date()
 
 
+def check_registers(src: str, log: str) -> None:
+    """Raises when ptxas (its -v output in `log`) gave a kernel of REGISTERS another number than its source counts on."""
+    for name, kernel, constant in REGISTERS:
+        if os.path.basename(src) != name:
+            continue
+        with open(src, encoding="utf-8") as f:
+            want = re.search(rf"\bconstexpr int {constant} = (\d+);", f.read())
+        used = re.search(rf"Compiling entry function '[^']*{kernel}[^']*'.*?Used (\d+) registers", log, flags=re.S)
+        if not (want and used and want[1] == used[1]):
+            raise RuntimeError(f"{name}: {kernel} counts on {want and want[1]} registers a thread at launch, "
+                               f"the compiler gave it {used and used[1]}")
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     lib_stale, py_stale = force or not lib_up_to_date(), force or not py_up_to_date()
     if not (lib_stale or py_stale):
@@ -83,6 +100,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+        check_registers(src, r.stdout + r.stderr)
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr)
         return obj

@@ -1,5 +1,5 @@
-"""The in-tree build: the C library does not depend on torch's headers, and the Python side is built again for another
-torch (no GPU needed)."""
+"""The in-tree build: the C library does not depend on torch's headers, the Python side is built again for another torch,
+and a kernel that did not get the registers it counts on stops it (no GPU needed)."""
 import ctypes
 import os
 
@@ -53,3 +53,32 @@ def test_the_python_side_is_built_again_for_another_torch_or_interpreter(what, m
     else:
         monkeypatch.setattr(build.sys, "version", "2.7")
     assert build.lib_up_to_date() and not build.py_up_to_date() and not build.up_to_date()
+
+
+def ptxas(kernel, registers):
+    return f"""ptxas info    : Compiling entry function '_ZN3moe4rows18rows_tables_kernelENS0_6ParamsE' for 'sm_103a'
+ptxas info    : Used 32 registers, used 1 barriers, 9216 bytes smem
+ptxas info    : Compiling entry function '_ZN3moe4rows15{kernel}E14CUtensorMap_stS1_S1_NS0_6ParamsE' for 'sm_103a'
+ptxas info    : Function properties for _ZN3moe4rows15{kernel}E14CUtensorMap_stS1_S1_NS0_6ParamsE
+    0 bytes stack frame, 0 bytes spill stores, 0 bytes spill loads
+ptxas info    : Used {registers} registers, used 16 barriers
+"""
+
+
+def test_a_kernel_without_its_registers_stops_the_build():
+    src = os.path.join(build.CSRC, "gqa_rows.cu")
+    build.check_registers(src, ptxas("gqa_rows_kernel", 168))
+    for log in (ptxas("gqa_rows_kernel", 166), ptxas("another_kernel", 168), ""):
+        with pytest.raises(RuntimeError, match="gqa_rows_kernel counts on 168 registers"):
+            build.check_registers(src, log)
+    build.check_registers(os.path.join(build.CSRC, "paged_plan.cu"), "")
+
+
+def test_the_build_looks_at_the_registers(small, monkeypatch):
+    src = small / "gqa_rows.cu"
+    src.write_text("constexpr int kRegsLaunch = 255;\n__global__ void gqa_rows_kernel(int* p) { *p = 1; }\n")
+    monkeypatch.setattr(build, "sources", lambda: [str(src)])
+    monkeypatch.setattr(build, "_compile_py", lambda: "")
+    with pytest.raises(RuntimeError, match="counts on 255 registers"):
+        build.build()
+    assert not os.path.exists(build.LIB)
