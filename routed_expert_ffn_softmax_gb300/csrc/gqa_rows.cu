@@ -40,6 +40,7 @@
 #include <atomic>
 #include <cfloat>
 #include <cstdint>
+#include <limits>
 
 #include "gqa_paged.cuh"
 #include "paged_device.cuh"
@@ -1026,8 +1027,9 @@ cudaError_t launch_gqa_rows(const GqaRowsPlan& plan, cudaStream_t stream) {
   p.G = G;
   p.max_blocks = plan.N / (2 * p.half_tokens) + plan.B;
   p.L_cap = plan.paged.max_pages * page;
-  // a scale of 0 makes all scores equal; the mask's infinities need a factor other than 0
-  p.scale_log2 = plan.scale_log2 == 0.0f ? 1e-30f : plan.scale_log2;
+  // A scale of 0 makes all scores equal, but the mask's infinities need a factor other than 0: the least there is, which
+  // leaves no finite score above 5e-7.
+  p.scale_log2 = plan.scale_log2 == 0.0f ? std::numeric_limits<float>::denorm_min() : plan.scale_log2;
   p.give_up_tile = plan.give_up_tile;
 
   constexpr int kMaxDev = 64;  // the shared-memory opt-in is per device: done once on each

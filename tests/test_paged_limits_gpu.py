@@ -1,5 +1,5 @@
-"""The serving path over a paged key/value cache at the edges its header allows: the largest token row counts (needs a
-GPU)."""
+"""The serving path over a paged key/value cache at the edges its header allows: the largest token row counts, a
+scale of 0 (needs a GPU)."""
 import pytest
 import torch
 
@@ -44,3 +44,33 @@ def test_plan_with_as_many_token_rows_as_32_bits_count():
         real = t < sum(new)
         assert torch.equal(positions[at:at + t.numel()], torch.where(real, pos, 0).to(torch.int32))
         assert torch.equal(slots[at:at + t.numel()], torch.where(real, slot, -1).to(torch.int32))
+
+
+# ---------------------------------------------------------------- attention
+@pytest.mark.parametrize("size", [1.0, 1e15])
+def test_a_scale_of_zero_weighs_all_keys_alike(size):
+    """Whatever the scores: with queries and keys of 1e15 they reach 1e31."""
+    lens = (300, 70)
+    c = ref.Cache(lens, 2, 16, DEV)
+    for b, n in enumerate(lens):
+        c.rows[b][0] = (c.rows[b][0].float() * size).to(torch.bfloat16)
+        c.put(b, slice(0, n), *c.rows[b])
+    q = (randn(130, 16, D, seed=2).float() * size).to(torch.bfloat16)
+    ws = moe.alloc_paged_workspace(130, 130, 16, 2, D, 300, device=DEV)
+    out = torch.empty_like(q)
+    moe.moe_gqa_paged_prefill(q, i32([0, 60, 130]), c.k, c.v, c.table, i32(lens), 0.0, out, ws)
+    for b, (rows, n) in enumerate(((slice(0, 60), 300), (slice(60, 130), 70))):
+        pos = torch.arange(n - (rows.stop - rows.start), n, device=DEV)[:, None]
+        see = ref.visible(pos, torch.arange(n, device=DEV), 0, 0)
+        ref.check(out[rows], *ref.attend(q[rows], *c.rows[b], see, 0.0), f"prompt {b}")
+    out = torch.empty_like(q[:2])
+    moe.moe_gqa_paged_decode(q[:2], c.k, c.v, c.table, i32(lens), 0.0, out, ws)
+    for b, n in enumerate(lens):
+        ref.check(out[b:b + 1], *ref.attend(q[b:b + 1], *c.rows[b], torch.ones(1, n, dtype=torch.bool, device=DEV), 0.0), "one token")
+    moe.moe_gqa_prefix_decode(q[:2], c.table[0].contiguous(), 300, c.k, c.v, c.table[1:].expand(2, -1).contiguous(),
+                              i32([70, 0]), 0.0, out, ws)
+    for b, n in enumerate((70, 0)):
+        k, v = (torch.cat([c.rows[0][i], c.rows[1][i][:n]]) for i in (0, 1))
+        see = torch.ones(1, 300 + n, dtype=torch.bool, device=DEV)
+        ref.check(out[b:b + 1], *ref.attend(q[b:b + 1], k, v, see, 0.0), f"behind a prefix, {n} own keys")
+    assert moe.workspace_status(ws) == 0
