@@ -37,7 +37,8 @@
  * Workspace: one zero-filled allocation of moe_paged_workspace_size() bytes (256-byte aligned) serves
  * all calls of one stream, one after the other; every call leaves it ready for the next. Calls that can
  * overlap (other streams, graphs replayed side by side) need workspaces of their own. Its first 4 bytes
- * are a status word that calls set and never clear; zero it to reset it:
+ * are a status word that calls set and never clear; zero it to reset it. It keeps the code that matters most: 1-3 before
+ * all others, then the largest:
  *   1-3  a kernel gave up a bounded wait (does not happen in correct operation; outputs undefined, zero
  *        the whole workspace before reuse)
  *   4    a length was negative or past the block table (that sequence counts as empty)

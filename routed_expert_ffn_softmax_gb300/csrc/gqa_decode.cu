@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sum += nt[k];
       }
     }
-    if (bad) atomicExch(p.status, kStatusBadSeqLen);
+    if (bad) raise_status(p.status, kStatusBadSeqLen);
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int z = id < 0 ? -1 : id * p.h_kv + pc.j;
             const CUtensorMap* map = folded ? (is_v ? &tm16.v : &tm16.k) : (is_v ? &tmV : &tmK);
             tma_load_5d(dst, map, &full[st], 0, 0, 0, (key & (page - 1)) >> 3, z, policy);
-            if (id < 0) atomicExch(p.status, kStatusBadPage);
+            if (id < 0) raise_status(p.status, kStatusBadPage);
           }
           id = next;
         }

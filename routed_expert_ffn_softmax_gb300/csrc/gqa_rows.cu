@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kTableThreads) rows_tables_kernel(const Params
       bool bad;
       nb[k] = (tokens_of(p, b, &bad) + per - 1) / per;
       const int len = p.seq_lens[b];
-      if (bad || len < 0 || len > p.L_cap) atomicExch(p.status, kStatusBadSeqLen);
+      if (bad || len < 0 || len > p.L_cap) raise_status(p.status, kStatusBadSeqLen);
     }
   }
   // offsets that run over each other could ask for more blocks than N tokens make, and than 32 bits count: the tables
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kTableThreads) rows_tables_kernel(const Params
     const int b = 2 * tid + k;
     if (b < p.B) {
       base[b] = static_cast<int>(min(run, static_cast<int64_t>(p.max_blocks)));
-      if (run + nb[k] > p.max_blocks) atomicExch(p.status, kStatusBadSeqLen);
+      if (run + nb[k] > p.max_blocks) raise_status(p.status, kStatusBadSeqLen);
     }
     run += nb[k];
     if (b + 1 == p.B) base[p.B] = static_cast<int>(min(run, static_cast<int64_t>(p.max_blocks)));
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        if (id == -1) atomicExch(p.status, kStatusBadPage);
+        if (id == -1) raise_status(p.status, kStatusBadPage);
         id = next;
       }
     }

@@ -16,6 +16,17 @@ enum : int32_t {
   kStatusPlanNoRoom = 7,  // the plan left a sequence out
 };
 
+// Sets the status word to an input error's code (4 and up), unless it holds a larger one or that of a wait that ran out
+// (1 .. 3, which are written over anything: the workspace is then not fit for use).
+__device__ __forceinline__ void raise_status(int32_t* status, int32_t code) {
+  int32_t old = 0;
+  do {
+    const int32_t seen = atomicCAS(status, old, code);
+    if (seen == old) return;
+    old = seen;
+  } while (old > kStatusDrainTimeout && old < code);
+}
+
 // mbar_wait in few instructions, for kernels whose many waits would crowd the instruction cache: limited by a count of
 // tries. A try that fails takes 1.5 to 4 us on the GB300, whatever suspend time it is given, so the limit is 0.8 to 2.1 s.
 // (Reading the clock in this loop costs 16K prompts 3%.)

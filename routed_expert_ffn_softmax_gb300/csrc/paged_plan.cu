@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PagedPlanArg
   for (int k = 0; k < kPer; ++k)
     if (tid * kPer + k < p.B && c[k] >= 0) mine += need[k];
   if (mine) atomicAdd(&taken_s, mine);
-  if (status && blockIdx.x == 0) atomicMax(p.status, status);
+  if (status && blockIdx.x == 0) raise_status(p.status, status);
   __syncthreads();
   const int taken = taken_s;
 
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PagedPlanArg
         if (page_ok(id))
           slot = (id << p.page_shift) + (pos & (p.page_size - 1));
         else
-          atomicMax(p.status, kStatusBadPage);
+          raise_status(p.status, kStatusBadPage);
       }
     }
     p.positions[t] = pos;

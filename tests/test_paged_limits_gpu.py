@@ -1,5 +1,5 @@
 """The serving path over a paged key/value cache at the edges its header allows: the largest token row counts, a
-scale of 0 (needs a GPU)."""
+scale of 0, the precedence of the status word's codes (needs a GPU)."""
 import pytest
 import torch
 
@@ -74,3 +74,45 @@ def test_a_scale_of_zero_weighs_all_keys_alike(size):
         see = torch.ones(1, 300 + n, dtype=torch.bool, device=DEV)
         ref.check(out[b:b + 1], *ref.attend(q[b:b + 1], k, v, see, 0.0), f"behind a prefix, {n} own keys")
     assert moe.workspace_status(ws) == 0
+
+
+# ---------------------------------------------------------------- the status word
+@pytest.mark.parametrize("before", [0, 1, 2, 3, 4, 6, 7])
+def test_the_status_word_keeps_the_code_that_matters_most(before):
+    """1 to 3 stay whatever comes (the workspace is not fit for use); of the others the largest is kept."""
+    c = ref.Cache((40, 300), 2, 16, DEV)
+    q, qp = randn(2, 16, D), randn(30, 16, D)
+    out, outp = torch.empty_like(q), torch.empty_like(qp)
+    ws = moe.alloc_paged_workspace(30, 2, 16, 2, D, 40, device=DEV)
+    bad_pages = c.table.clone()
+    bad_pages[1, 3] = -1
+    good, lt, bad = c.table, i32([40, 300]), i32([-1, 300])
+    cu, one, rows = i32([0, 10, 30]), i32([1]), i32([0] * 4)
+    plan = lambda ctx, free: moe.moe_paged_plan(  # noqa: E731
+        i32([ctx]), one, 16, 50, i32([5]), i32([free]), i32([[3, 4]]), i32([0]), i32([0, 0]), rows, rows.clone(), i32([0]), ws)
+    calls = {
+        "one token, bad length": (4, lambda: moe.moe_gqa_paged_decode(q, c.k, c.v, good, bad, SCALE, out, ws)),
+        "one token, bad page": (6, lambda: moe.moe_gqa_paged_decode(q, c.k, c.v, bad_pages, lt, SCALE, out, ws)),
+        "prompt, bad length": (4, lambda: moe.moe_gqa_paged_prefill(qp, cu, c.k, c.v, good, bad, SCALE, outp, ws)),
+        "prompt, bad page": (6, lambda: moe.moe_gqa_paged_prefill(qp, cu, c.k, c.v, bad_pages, lt, SCALE, outp, ws)),
+        "prefix, bad page": (6, lambda: moe.moe_gqa_prefix_decode(q, i32([0, -1, 1]), 40, c.k, c.v, good, lt, SCALE, out, ws)),
+        "plan, bad length": (4, lambda: plan(-1, 1)),
+        "plan, no room": (7, lambda: plan(16, 0)),
+    }
+    for what, (code, call) in calls.items():
+        ws[:4] = torch.tensor([before, 0, 0, 0], dtype=torch.uint8, device=DEV)
+        call()
+        torch.cuda.synchronize()
+        assert moe.workspace_status(ws) == (before if 1 <= before <= 3 else max(before, code)), what
+    assert not ws[4:4096].any()
+
+
+def test_the_contiguous_cache_keeps_the_code_of_a_wait_too():
+    ws = moe.alloc_gqa_workspace(1, 8, 1, D, 64, DEV)
+    k = torch.zeros(1, 1, 64, D, dtype=torch.bfloat16, device=DEV)
+    q = randn(1, 8, D)
+    for before, after in ((0, 4), (1, 1), (3, 3), (4, 4)):
+        ws[:4] = torch.tensor([before, 0, 0, 0], dtype=torch.uint8, device=DEV)
+        moe.moe_gqa_decode(q, k, k, i32([65]), SCALE, torch.empty_like(q), ws)
+        torch.cuda.synchronize()
+        assert moe.workspace_status(ws) == after
