@@ -384,8 +384,8 @@ def moe_gqa_prefix_decode(q, prefix_table, prefix_len: int, k_cache, v_cache, bl
 
 
 def moe_test_paged_give_up(tile: int = -1) -> None:
-    """Failure-detection test hook: the row-block attention kernel's producers stop before this tile (-1: never), and what
-    waits for them gives up: nonzero workspace status (see include/paged/moe_paged_test.h)."""
+    """Failure-detection test hook: the paged attention kernels' producers stop before this tile (-1: never), and what waits
+    for them gives up: nonzero workspace status (see include/paged/moe_paged_test.h)."""
     f = load().moe_test_paged_give_up
     f.argtypes = [ctypes.c_int]
     f.restype = ctypes.c_int

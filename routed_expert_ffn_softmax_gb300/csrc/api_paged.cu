@@ -137,6 +137,9 @@ moe::PagedKv paged_of(const Attention& a) {
 
 float scale_log2(float scale) { return static_cast<float>(static_cast<double>(scale) * 1.4426950408889634); }
 
+// moe_test_paged_give_up
+std::atomic<int> g_give_up_tile{-1};
+
 moe::GqaPlan decode_plan(const Attention& a, int sms) {
   char* ws = static_cast<char*>(a.workspace);
   moe::GqaPlan plan{};
@@ -155,11 +158,9 @@ moe::GqaPlan decode_plan(const Attention& a, int sms) {
   plan.L_cap = a.max_pages * a.page_size;
   plan.scale_log2 = scale_log2(a.scale);
   plan.num_ctas = sms < moe::kPartialCtas ? sms : moe::kPartialCtas;
+  plan.give_up_tile = g_give_up_tile.load(std::memory_order_relaxed);
   return plan;
 }
-
-// moe_test_paged_give_up
-std::atomic<int> g_give_up_tile{-1};
 
 moe::GqaRowsPlan rows_plan(const Attention& a, const Layout& L, int sms) {
   char* ws = static_cast<char*>(a.workspace);

@@ -110,6 +110,7 @@ struct Params {
   float scale_log2;         // softmax scale * log2(e)
   PagedKv kv;               // paged kernels only
   PrefixPartials prefix;    // paged kernels only; o == null: no shared prefix
+  int give_up_tile;         // paged kernels only, failure-detection test: the producers stop before this tile (-1: never)
 };
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -474,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = pc.tl; t < pc.tl + pc.n; ++t, ++it) {
           const int next = t + 1 < pc.tl + pc.n ? entry(sp, pc.b, t + 1) : (more ? entry(nsp, np.b, 0) : -2);
           const int st = it % kStages;
+          if (it == p.give_up_tile) ok = false;
           wait_all(&empty[st], static_cast<uint32_t>(((it / kStages) & 1) ^ 1));
           if (!ok) break;
           const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, id != -2));
@@ -562,6 +564,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // =========================== MMA issuer ===========================
+    // After a wait that ran out it waits for nothing more, issues nothing and hands nothing back: a stage it has not seen
+    // full is then never filled again over copies in flight, and the other roles' waits run out, once each.
     if (lane == 0) {
       const uint32_t sbase = smem_addr(smem);
       const uint32_t idesc_s = umma_idesc_bf16_m128(kN);
@@ -588,9 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                       kPaged ? umma_desc_sw128_mn_sbo(v + s * 2 * kGroupBytes, kUpper, kGroupBytes)
                              : umma_desc_sw128_mn(v + s * 2048, kBox),
                       umma_desc_sw128(pt + (s >> 2) * 2048 + (s & 3) * 32), idesc_o, s > 0);
+          umma_commit(&o_full[sb]);
+          umma_commit(&empty[st]);
         }
-        umma_commit(&o_full[sb]);
-        umma_commit(&empty[st]);
       };
       int it = 0;
       int pi = 0;
@@ -615,9 +619,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         kPaged ? umma_desc_sw128_sbo(k + (s >> 2) * kUpper + (s & 3) * 32, kGroupBytes)
                                : umma_desc_sw128(k + (s >> 2) * kBox + (s & 3) * 32),
                         umma_desc_sw128(qs + (s >> 2) * 2048 + (s & 3) * 32), idesc_s, s > 0);
+            umma_commit(&s_full[sb]);
+            if (t == pc.n - 1) umma_commit(&q_empty[qb]);
           }
-          umma_commit(&s_full[sb]);
-          if (t == pc.n - 1) umma_commit(&q_empty[qb]);
           // the previous tile's O^T (across a piece boundary too: the finisher, not the softmax,
           // waits for a piece's last one)
           if (it > 0) issue_o(it - 1);
@@ -768,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (!valid) {
+          if (!valid && ok) {
             // keys past the sequence: the cache rows there are arbitrary (even NaN) and a zero
             // probability times NaN is NaN, so clear this key's row of the V tile
             // (the wait makes the tile's landing visible to this thread before it overwrites)
@@ -1152,6 +1156,7 @@ cudaError_t launch_gqa_decode(const GqaPlan& plan, cudaStream_t stream) {
   p.scale_log2 = plan.scale_log2;
   p.kv = plan.paged;
   p.prefix = plan.prefix;
+  p.give_up_tile = plan.give_up_tile;
   return paged ? launch<true>(tk, tv, tq, fold, p, plan.num_ctas, stream)
                : launch<false>(tk, tv, tq, FoldMaps<false>{}, p, plan.num_ctas, stream);
 }

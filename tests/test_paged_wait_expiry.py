@@ -1,4 +1,5 @@
-"""Failure detection in the row-block attention kernel's own waits (prompts, and the prefix a batch shares).
+"""Failure detection in the attention kernels' own waits over a paged cache: prompts, the prefix a batch shares, one token
+per sequence.
 
 Producers that stop in the middle of a piece leave the other roles waiting for tiles that never come. Their waits run out
 (status 1 or 2; never 3, because copies and products under way are waited for), each role waits at most once or twice, and
@@ -75,3 +76,31 @@ def test_producers_that_stop_end_the_call_within_a_few_limits(shared, tile):
     ws.zero_()
     run_prefill((300, 17), (83, 17), 16, 2, 16, ws=ws)
     run_prefix(1000, (5, 0, 300), 16, 2, 16, ws=ws)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tile", [0, 4])
+def test_one_token_producers_that_stop_end_the_call_within_a_few_limits(tile):
+    """255 sequences of 300 keys with 4 key/value heads: some 7 pieces a CTA, each with masked keys in its last tile. The
+    issuer's and the softmax's waits run out together, the finisher's for the piece's product after them."""
+    from test_paged_gpu import i32, run_decode
+    B, pages = 255, 255 * 5
+    k, v = (torch.randn(pages, 4, 64, D, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    q = torch.randn(B, 32, D, device=DEV, dtype=torch.bfloat16)
+    table, lens, out = i32(list(range(pages))).view(B, 5), i32([300] * B), torch.empty_like(q)
+    ws = moe.alloc_paged_workspace(B, B, 32, 4, D, device=DEV)
+    call = lambda ws: moe.moe_gqa_paged_decode(q, k, v, table, lens, D ** -0.5, out, ws)  # noqa: E731
+    call(ws)
+    torch.cuda.synchronize()
+    assert moe.workspace_status(ws) == 0
+    moe.moe_test_paged_give_up(tile)
+    try:
+        ms = timed(call, ws)
+    finally:
+        moe.moe_test_paged_give_up()
+    assert ms < 3 * LIMIT_MS, f"{ms:.1f} ms"
+    status = moe.workspace_status(ws)
+    assert status in (1, 2), f"expected a wait timeout (1 or 2), got {status}"
+    ws.zero_()
+    run_decode((300, 17, 0, 1000), 32, 4, 16, window=100, n_sink=3, ws=ws)
+    run_decode((300, 17, 0, 1000), 32, 4, 16, ws=ws)
