@@ -103,8 +103,10 @@ moe_status_t moe_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, in
  *   q_out     [N, h_q, d] bf16 out; must not overlap qkv
  *   k_cache, v_cache  get token n's key and value heads at slots[n]; a token whose slot is outside
  *             [0, num_pages * page_size) is not stored (its q_out is written). Slots of one call are distinct.
- * In fp32 with one rounding to bf16 at the end; the angle is reduced exactly modulo a turn (64-bit fixed point), so
- * far positions lose nothing. values are copied. |inv_freq| must be finite. d = 128, 0 <= N, N = 0 is a no-op.
+ * In fp32 with one rounding to bf16 at the end. The angle is reduced modulo a turn in 64-bit fixed point, so far positions
+ * as such lose nothing: it is off by less than |pos| * max(1, |inv_freq|) * 2^-53 turns (the 64-bit rounding of inv_freq in
+ * turns). |inv_freq| must be finite. Squares are summed in fp32: a normed row whose squares sum past 2^128 comes out as 0.
+ * Values are copied. d = 128, 0 <= N, N = 0 is a no-op.
  */
 moe_status_t moe_qk_norm_rope(const uint16_t* qkv, int64_t row_stride, int N, int h_q, int h_kv, int d,
                               const uint16_t* q_weight, const uint16_t* k_weight, float eps, const float* inv_freq,

@@ -15,8 +15,9 @@
 // 64 + 8 heads.)
 //
 // The angle: inv_freq / (2 pi) is kept as a 64-bit fraction of a turn (computed in fp64, rounded once), so
-// pos * fraction modulo 2^64 is the angle modulo one turn without any loss for large pos (error below
-// pos * 2^-53 turns), and sin and cos are taken of a reduced argument.
+// pos * fraction modulo 2^64 is the angle modulo one turn without any loss for large pos, and sin and cos are taken of a
+// reduced argument. What remains is the fraction's error: 1 / (2 pi) and the product round in fp64 (2^-53 of |inv_freq| /
+// (2 pi) each), and so does the step into [0, 1) (2^-54), in all below max(1, |inv_freq|) * 2^-53 turns for each position.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -1,5 +1,5 @@
-"""The serving path over a paged key/value cache at the edges its header allows: the largest token row counts, a
-scale of 0, the precedence of the status word's codes (needs a GPU)."""
+"""The serving path over a paged key/value cache at the edges its header allows: the largest token row counts, large
+frequencies at far positions, a scale of 0, the precedence of the status word's codes (needs a GPU)."""
 import pytest
 import torch
 
@@ -44,6 +44,64 @@ def test_plan_with_as_many_token_rows_as_32_bits_count():
         real = t < sum(new)
         assert torch.equal(positions[at:at + t.numel()], torch.where(real, pos, 0).to(torch.int32))
         assert torch.equal(slots[at:at + t.numel()], torch.where(real, slot, -1).to(torch.int32))
+
+
+# ---------------------------------------------------------------- norm and rotation
+def turns_per_position(inv_freq, bits=200):
+    """inv_freq / (2 pi) modulo 1 of fp32 values, as whole numbers of 2^-bits turns (pi by Machin's formula)."""
+    one = 1 << (bits + 400)
+
+    def arctan_inverse(n):
+        term, total, k = one // n, one // n, 1
+        while term:
+            term //= -n * n
+            k += 2
+            total += term // k
+        return total
+
+    two_pi = 8 * (4 * arctan_inverse(5) - arctan_inverse(239))
+    out = []
+    for f in inv_freq.tolist():
+        num, den = f.as_integer_ratio()
+        out.append((num * one * (one >> 400) // (den * two_pi)) % (1 << bits))
+    return out
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("largest", [1.0, 7.0, 1000.0])
+def test_the_angle_of_large_frequencies_at_far_positions(largest, interleaved):
+    """Off by less than |pos| max(1, |inv_freq|) 2^-53 turns, against whole-number arithmetic; positive and negative
+    frequencies, positions near 2^31 and below 0. (2^-19 of |a| + |b| for the fp32 sine, cosine and sums, as in run_qk; 1%
+    for the square of the angle's error, which is below 2^-9.)"""
+    g = torch.Generator().manual_seed(3)
+    N, bits = 60, 200
+    inv = (largest * torch.rand(D // 2, generator=g)).float() * (1 - 2 * (torch.arange(D // 2) % 2))
+    pos = torch.cat([2 ** 31 - 1 - torch.randint(0, 10 ** 6, (N // 2,), generator=g), -torch.randint(1, 10 ** 9, (N // 2,), generator=g)])
+    x = torch.randn(N, 3, D, generator=g).to(torch.bfloat16)
+    q, k = torch.empty(N, 1, D, dtype=torch.bfloat16, device=DEV), torch.empty(4, 1, 16, D, dtype=torch.bfloat16, device=DEV)
+    moe.moe_qk_norm_rope(x.view(N, -1).to(DEV), None, None, 0.0, inv.to(DEV), pos.to(torch.int32).to(DEV), i32([-1] * N), q, k,
+                         k.clone(), interleaved=interleaved)
+    turn = turns_per_position(inv, bits)
+    angle = torch.tensor([[(t * p % (1 << bits)) / (1 << bits) for t in turn] for p in pos.tolist()], dtype=torch.float64)
+    angle = angle * (2 * torch.pi)
+    first, second = (slice(0, D, 2), slice(1, D, 2)) if interleaved else (slice(0, D // 2), slice(D // 2, D))
+    a, b = x[:, 0, first].double(), x[:, 0, second].double()
+    off = 2 * torch.pi * pos.abs().double()[:, None] * inv.abs().double().clamp(min=1.0) * 2.0 ** -53
+    for at, want in ((first, a * angle.cos() - b * angle.sin()), (second, b * angle.cos() + a * angle.sin())):
+        over = (q[:, 0, at].cpu().double() - want).abs() - (2.0 ** -8 * want.abs() + (2.0 ** -19 + 1.01 * off) * (a.abs() + b.abs()))
+        assert over.max() <= 0, f"off by {over.max():.3g}"
+
+
+@pytest.mark.parametrize("rot", [128, 32])
+def test_rows_whose_squares_overflow_come_out_as_zero(rot):
+    x = randn(3, 3 * D, seed=1)
+    x[1] *= 2.0 ** 64
+    w, inv = torch.ones(D, dtype=torch.bfloat16, device=DEV), torch.ones(rot // 2, device=DEV)
+    q, k = torch.empty(3, 1, D, dtype=torch.bfloat16, device=DEV), torch.full((1, 1, 16, D), 7.0, dtype=torch.bfloat16, device=DEV)
+    v = k.clone()
+    moe.moe_qk_norm_rope(x, w, w, 1e-6, inv, i32([5, 6, 7]), i32([0, 1, 2]), q, k, v)
+    assert not q[1].any() and not k[0, 0, 1].any() and torch.equal(v[0, 0, 1], x[1, 2 * D:])
+    assert q[0].any() and q[2].any() and torch.isfinite(q.float()).all()
 
 
 # ---------------------------------------------------------------- attention
