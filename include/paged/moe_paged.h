@@ -27,8 +27,10 @@
  * so pages behind a window can be given to other sequences. Rows that some query of the sequence sees
  * must hold finite values.
  *
- * Numerics: scores and softmax in fp32, probabilities rounded to bf16 for the probability x value
- * product, sums in fp32, the output rounded once to bf16 (nearest even).
+ * Numerics: scores and softmax in fp32, 2^x by the hardware's approximation (2^-22 relative),
+ * probabilities rounded to bf16 for the probability x value product (the tensor cores take both factors in
+ * one type, and values are bf16), sums in fp32, for one token per sequence the last division to 2^-22, the
+ * output rounded once to bf16 (nearest even).
  *
  * Conventions: those of moe.h (device pointers owned by the caller, asynchronous on `stream`, host-side
  * checks before any launch, no exceptions across the boundary, graph capturable). Results are

@@ -15,7 +15,10 @@
 // Numerics: scores and the online softmax in fp32 (base-2 exponent, scale * log2(e) folded into
 // the scores, the hardware's approximate 2^x at about 2^-22 relative error), probabilities rounded
 // to bf16 for the second product (its operands must share one 16-bit type with V), fp32
-// accumulation, output rounded once to bf16.
+// accumulation, output rounded once to bf16. Over a paged cache the joins of pieces take the same 2^x
+// and the last division __fdividef (2 ulp; sums stay below 2^40, far from where it gives 0), both far below the output's
+// rounding: with exp2f and the exact division 64 sequences behind a window take 32.7 us instead of 31.7, 255 short ones of
+// 16 heads a group 57 instead of 50.6, one sequence 9.4 instead of 9.0.
 //
 // Work split: the key tiles of all (sequence, key/value head) segments form one list; each CTA
 // (one per SM) takes a contiguous range of it (stream-K), so long and short sequences balance to

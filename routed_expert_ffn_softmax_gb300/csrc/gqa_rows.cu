@@ -15,6 +15,8 @@
 // parts, so that most of P . V starts before the last exponentials are done. O stays in TMEM; it is
 // rescaled only when a row's maximum has grown by more than 2^8 since the reference in use (probabilities are then at
 // most 2^8, exact to the same relative bf16 step, and sums stay far inside fp32), which after the first tiles is rare.
+// Probabilities are rounded to bf16, since both factors of a tcgen05 product have one type and V's is bf16; 2^x is the
+// hardware's approximation (2^-22 relative); everything else stays in fp32 until the output's one rounding.
 //
 // Work split: the key tiles of all (sequence, head, block) segments form one list (causal blocks have different
 // lengths, windows bound them) and each CTA takes a contiguous range of it, so any mix of prompts balances to within
