@@ -1,5 +1,5 @@
 """The serving path over a paged key/value cache at the edges its header allows: the largest token row counts, large
-frequencies at far positions, a scale of 0, the precedence of the status word's codes (needs a GPU)."""
+frequencies at far positions, a scale of 0, bad pages, the precedence of the status word's codes (needs a GPU)."""
 import pytest
 import torch
 
@@ -132,6 +132,45 @@ def test_a_scale_of_zero_weighs_all_keys_alike(size):
         see = torch.ones(1, 300 + n, dtype=torch.bool, device=DEV)
         ref.check(out[b:b + 1], *ref.attend(q[b:b + 1], k, v, see, 0.0), f"behind a prefix, {n} own keys")
     assert moe.workspace_status(ws) == 0
+
+
+def zeroed(c, b, idx):
+    """Sequence b's rows with those of its idx-th page zero."""
+    rows = [r.clone() for r in c.rows[b]]
+    for r in rows:
+        r[idx * c.page:(idx + 1) * c.page] = 0
+    return rows
+
+
+# sequence 1 has 1000 keys; behind a window of 200 the first visible one of it is 800, 32 keys into a tile, so that up to 32
+# sink keys are copied into the rows before it in boxes of 16
+BAD_PAGES = [(16, 0, 0, 0), (16, 0, 0, 61), (64, 0, 0, 15), (1024, 0, 0, 0), (16, 200, 3, 0), (16, 200, 20, 1), (16, 200, 3, 50),
+             (64, 200, 3, 0), (64, 200, 3, 12), (256, 200, 30, 0), (256, 200, 30, 3), (16, 200, 140, 8), (64, 200, 140, 2)]
+
+
+@pytest.mark.parametrize("entry", [-1, 10 ** 6, -2 ** 31, 2 ** 31 - 1])
+@pytest.mark.parametrize("page,window,n_sink,idx", BAD_PAGES)
+def test_a_bad_page_reads_as_zeros(page, window, n_sink, idx, entry):
+    lens = (40, 1000, 64)
+    c = ref.Cache(lens, 2, page, DEV, seed=idx)
+    c.table[1, idx] = entry
+    rows = [c.rows[0], zeroed(c, 1, idx), c.rows[2]]
+    ws = moe.alloc_paged_workspace(90, 3, 16, 2, D, device=DEV)
+    q = randn(90, 16, D, seed=1)
+    out = torch.empty_like(q)
+    for what, new in (("one token", (1, 1, 1)), ("prompt", (20, 50, 20))):
+        ws[:4] = 0
+        cu = [0, new[0], new[0] + new[1], sum(new)]
+        if what == "prompt":
+            moe.moe_gqa_paged_prefill(q, i32(cu), c.k, c.v, c.table, i32(lens), SCALE, out, ws, window=window, n_sink=n_sink)
+        else:
+            moe.moe_gqa_paged_decode(q[:3], c.k, c.v, c.table, i32(lens), SCALE, out[:3], ws, window=window, n_sink=n_sink)
+        assert moe.workspace_status(ws) == 6, what
+        for b, n in enumerate(lens):
+            pos = torch.arange(n - new[b], n, device=DEV)[:, None]
+            see = ref.visible(pos, torch.arange(n, device=DEV), window, n_sink)
+            at = slice(cu[b], cu[b + 1])
+            ref.check(out[at], *ref.attend(q[at], *rows[b], see, SCALE), f"{what}, sequence {b}")
 
 
 # ---------------------------------------------------------------- the status word
