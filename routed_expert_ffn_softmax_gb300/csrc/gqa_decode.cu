@@ -73,7 +73,7 @@ constexpr int kPBytes = kN * kKeys * 2;       // 4 KB
 constexpr int kThreads = 320;
 constexpr int kSoft = 128;                    // softmax threads (warps 2..5); finisher: warps 6..9
 constexpr int kScan = 256;                    // threads of the sequence prefix (warps 2..9)
-constexpr int kSlotFloats = kGqaSlotFloats;   // partial of one piece: o[16][128], m[16], l[16]
+constexpr int kSlotFloats = kGqaSlotFloats;   // partial of one piece: o[128][kGP], m[16], l[16]
 constexpr int kNumBars = 2 * kStages + 2 * 9 + 1;
 
 // TMEM columns: S^T of buffer k at 32k, O^T of buffer k at 32k + 16, so a tile's scores and the

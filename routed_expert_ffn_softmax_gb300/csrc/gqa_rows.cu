@@ -30,11 +30,12 @@
 // MMAs of the two halves in turn, 3 announces the pieces and writes zeros for blocks that see nothing, 4-7 and 8-11 the
 // softmax and output of the two halves.
 //
-// What bounds it: per tile a half's chain of scores, softmax and product, about 2850 cycles (products 1130 with their
-// issue, softmax 1475 of which 512 are exponentials, the rest hand-over; the last exponentials under the product). TMEM
-// holds two halves, so the tensor pipe is busy 68% of the time. GB300: 16K prompt behind a window of 4096 in 341 us (1412
-// TFLOP/s), six prompts of up to 4095 tokens in 171 (1095), a prefix of 32K for 255 sequences 174 (1590); a call with few
-// rows pays 7 us up to its first scores and 9 to join its pieces.
+// What bounds it: per tile a half's chain of scores, softmax and product, about 2580 cycles (products 1150 with their
+// issue, softmax 1180 of which 512 are exponentials, the rest hand-over; the last exponentials under the product). TMEM
+// holds two halves, so the tensor pipe is busy 74% of the time. GB300, whole calls: a 16K prompt behind a window of 4096 in
+// 329 us (1463 TFLOP/s) and six prompts of up to 4095 tokens in 166 (1127) when replayed for milliseconds, 357 and 175
+// (1350, 1068) timed over seconds, under the power cap; a prefix of 32K for 255 sequences 161 of the call's 243 (1700, this
+// kernel alone). A call with few rows pays 7 us up to its first scores and 9 to join its pieces.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -86,7 +87,7 @@ __device__ constexpr uint32_t col_o(int h) { return 256u + 128u * h; }
 
 // What a segment costs beside its tiles (its queries' load, the first scores and the output, which no product
 // overlaps), in tiles: the CTAs' shares are cut so that those with many short segments get fewer tiles (ragged and
-// 16K prompts take 184 and 365 us at 1, 172 and 342 at 2, 177 and 339 at 3).
+// 16K prompts take 168 and 340 us at 1, 166 and 329 at 2, 172 and 323 at 3).
 constexpr int kSegCost = 2;
 
 constexpr int kReaders = 3 + 2 * kSoft / 32;  // warps that read the announced pieces
@@ -94,8 +95,8 @@ constexpr int kReaders = 3 + 2 * kSoft / 32;  // warps that read the announced p
 constexpr int kTurnBar = 1;  // named barriers 1 and 2: the issuers' turns
 
 // Keys of a tile whose probabilities are handed over first: their part of P . V runs under the exponentials of the rest,
-// which take a warp 4 cycles each (16K and ragged prompts take 356 and 175 us with the tile as one, 341 and 173 with 64
-// keys first, 340 and 171 with 96).
+// which take a warp 4 cycles each (16K and ragged prompts take 334 and 169 us with 64 keys first, 329 and 166 with 96; the
+// tile as one costs 4% and 2% more than that).
 constexpr int kFirst = 96;
 
 constexpr float kGrowth = 8.0f;  // log2 of how far a row's maximum may outgrow its reference

@@ -104,7 +104,7 @@ cudaError_t launch_expert_ffn(const ExpertFfnPlan& plan, cudaStream_t stream);
 
 // Decode-phase GQA attention (gqa_decode.cu) over a key/value cache [B, h_kv, L_cap, 128].
 constexpr int kGqaMaxSeqs = 2048;  // sequences per call (the tile prefix lives in shared memory)
-constexpr int kGqaSlotFloats = 16 * 128 + 2 * 16;  // one stream-K partial: o[16][128], m[16], l[16]
+constexpr int kGqaSlotFloats = 16 * 128 + 2 * 16;  // one stream-K partial (see store_heads): o[128][heads], m, l
 struct PagedKv {
   const int32_t* block_table;  // [B, max_pages]; null: the contiguous cache
   int num_pages, page_shift, max_pages;
