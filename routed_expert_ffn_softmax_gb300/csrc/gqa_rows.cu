@@ -40,6 +40,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cfloat>
 #include <cstdint>
@@ -119,6 +120,7 @@ struct Params {
   int prefix_len, prefix_splits, prefix_blocks;
   int N, B, h_q, h_kv, G, half_tokens, max_blocks, L_cap;
   float scale_log2;
+  int piece_waits;   // limits of a wait that may last as long as a piece
   int give_up_tile;  // failure-detection test: the producers stop before this tile (-1: never)
 };
 
@@ -453,10 +455,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   // registers or waits for its table look-ups.
   Piece* items = reinterpret_cast<Piece*>(smem + kOffItem);
   int di = 0;
+  // A reader that has nothing to do for a piece, and the warp that announces them, wait for others to finish one.
+  auto wait_piece = [&](uint64_t* bar, uint32_t parity) {
+    bool done = false;
+#pragma unroll 1
+    for (int i = 0; i < p.piece_waits && !done; ++i) done = mbar_wait_soon(bar, parity);
+    return done;
+  };
   // The next piece's place, kItems when there is none; its reader copies what it needs and hands the place back.
   auto next_piece = [&]() -> int {
     const int s = di % kItems;
-    const bool got = __all_sync(0xffffffffu, mbar_wait_soon(&d_full[s], static_cast<uint32_t>((di / kItems) & 1)));
+    const bool got = __all_sync(0xffffffffu, wait_piece(&d_full[s], static_cast<uint32_t>((di / kItems) & 1)));
     if (!got && lane == 0) atomicExch(p.status, kStatusWaitFullTimeout);
     ++di;
     return got && items[s].n > 0 ? s : kItems;
@@ -672,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Piece c{};
         more = walk.next(c);
         const int s = di % kItems;
-        if (!mbar_wait_soon(&d_empty[s], static_cast<uint32_t>(((di / kItems) & 1) ^ 1))) {
+        if (!wait_piece(&d_empty[s], static_cast<uint32_t>(((di / kItems) & 1) ^ 1))) {
           atomicExch(p.status, kStatusWaitEmptyTimeout);
           break;
         }
@@ -1033,6 +1042,8 @@ cudaError_t launch_gqa_rows(const GqaRowsPlan& plan, cudaStream_t stream) {
   // A scale of 0 makes all scores equal, but the mask's infinities need a factor other than 0: the least there is, which
   // leaves no finite score above 5e-7.
   p.scale_log2 = plan.scale_log2 == 0.0f ? std::numeric_limits<float>::denorm_min() : plan.scale_log2;
+  // a tile takes some 1.3 us, so 2^18 of them less than half a wait's limit
+  p.piece_waits = 1 + (std::max(p.L_cap, p.prefix_len) / kKeys >> 18);
   p.give_up_tile = plan.give_up_tile;
 
   constexpr int kMaxDev = 64;  // the shared-memory opt-in is per device: done once on each
