@@ -121,7 +121,9 @@ moe_status_t moe_qk_norm_rope(const uint16_t* qkv, int64_t row_stride, int N, in
  *   q [B, h_q, d] bf16, seq_lens [B] int32 (the new token included), out [B, h_q, d] bf16
  * Heads are grouped as in moe_gqa_decode (query head hq reads key/value head hq / (h_q / h_kv)). Supported:
  * d = 128, h_q a multiple of h_kv, h_q / h_kv <= 16, 0 <= B <= 2048 (B = 0 is a no-op), scale finite. q, the
- * caches and out 16-byte aligned, out apart from all inputs. Each visible row is read once per call.
+ * caches and out 16-byte aligned, out apart from all inputs. Work is counted in 32 bits: with N query tokens in
+ * all, (N / (2 (128 / G)) + B) * h_kv * (max_pages * page_size / 128 + 9) < 2^31, G = h_q / h_kv. Each visible row
+ * is read once per call.
  */
 moe_status_t moe_gqa_paged_decode(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache,
                                   const int32_t* block_table, const int32_t* seq_lens, int B, int h_q, int h_kv,
