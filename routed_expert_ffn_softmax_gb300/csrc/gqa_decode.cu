@@ -113,7 +113,7 @@ struct Params {
   float scale_log2;         // softmax scale * log2(e)
   PagedKv kv;               // paged kernels only
   PrefixPartials prefix;    // paged kernels only; o == null: no shared prefix
-  int give_up_tile;         // paged kernels only, failure-detection test: the producers stop before this tile (-1: never)
+  int give_up_tile;         // paged kernels only, failure-detection test: no piece from this tile on is loaded (-1: all are)
 };
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -457,7 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         nsp = span_of(lens[np.b], p.L_cap, p.kv);
         id = entry(nsp, np.b, np.tl);
       }
-      for (int x = beg; x < end && ok; ++pi) {
+      const int stop = p.give_up_tile < 0 ? end : beg + min(end - beg, p.give_up_tile);
+      for (int x = beg; x < stop && ok; ++pi) {
         pc = np;
         sp = nsp;
         const bool more = x + pc.n < end;
@@ -478,7 +479,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = pc.tl; t < pc.tl + pc.n; ++t, ++it) {
           const int next = t + 1 < pc.tl + pc.n ? entry(sp, pc.b, t + 1) : (more ? entry(nsp, np.b, 0) : -2);
           const int st = it % kStages;
-          if (it == p.give_up_tile) ok = false;
           wait_all(&empty[st], static_cast<uint32_t>(((it / kStages) & 1) ^ 1));
           if (!ok) break;
           const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, id != -2));
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         x += pc.n;
       }
       if (lane == 0) {
-        if (!ok) atomicExch(p.status, kStatusWaitEmptyTimeout);
+        if (!ok || stop < end) atomicExch(p.status, kStatusWaitEmptyTimeout);
         const int n = it < kStages ? it : kStages;
         for (int i = it - n; i < it; ++i)
           if (!mbar_wait(&full[i % kStages], static_cast<uint32_t>((i / kStages) & 1))) {
@@ -595,9 +595,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                       kPaged ? umma_desc_sw128_mn_sbo(v + s * 2 * kGroupBytes, kUpper, kGroupBytes)
                              : umma_desc_sw128_mn(v + s * 2048, kBox),
                       umma_desc_sw128(pt + (s >> 2) * 2048 + (s & 3) * 32), idesc_o, s > 0);
-          umma_commit(&o_full[sb]);
-          umma_commit(&empty[st]);
         }
+        if (!ok) return;
+        umma_commit(&o_full[sb]);
+        umma_commit(&empty[st]);
       };
       int it = 0;
       int pi = 0;
@@ -622,9 +623,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         kPaged ? umma_desc_sw128_sbo(k + (s >> 2) * kUpper + (s & 3) * 32, kGroupBytes)
                                : umma_desc_sw128(k + (s >> 2) * kBox + (s & 3) * 32),
                         umma_desc_sw128(qs + (s >> 2) * 2048 + (s & 3) * 32), idesc_s, s > 0);
-            umma_commit(&s_full[sb]);
-            if (t == pc.n - 1) umma_commit(&q_empty[qb]);
           }
+          if (!ok) break;
+          umma_commit(&s_full[sb]);
+          if (t == pc.n - 1) umma_commit(&q_empty[qb]);
           // the previous tile's O^T (across a piece boundary too: the finisher, not the softmax,
           // waits for a piece's last one)
           if (it > 0) issue_o(it - 1);

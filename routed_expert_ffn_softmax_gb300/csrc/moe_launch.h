@@ -123,7 +123,7 @@ struct PrefixPartials {
 struct GqaPlan {
   PagedKv paged;
   PrefixPartials prefix;
-  int give_up_tile;         // paged, failure-detection test: the producers stop before this tile (-1: never)
+  int give_up_tile;         // paged, failure-detection test: no piece from this tile on is loaded (-1: all are)
   const uint16_t* q;        // [B, h_q, 128] bf16
   const uint16_t* k_cache;  // [B, h_kv, L_cap, 128] bf16
   const uint16_t* v_cache;  // [B, h_kv, L_cap, 128] bf16
