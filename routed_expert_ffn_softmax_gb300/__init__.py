@@ -1,8 +1,8 @@
 """Routed-expert MoE FFN, decode GQA attention and the serving path over a paged key/value cache
-for the GB300 (sm_103a): Python binding of libmoe.so.
+(bf16 or 4 bits) for the GB300 (sm_103a): Python binding of libmoe.so.
 
 Every function here has the name of the C entry point it calls (include/moe.h,
-include/moe_gqa.h, include/paged/moe_paged.h)
+include/moe_gqa.h, include/paged/moe_paged.h, moe_norm.h, moe_kv4.h)
 and only marshals arguments: torch tensors in, device pointers and sizes out.
 All arithmetic runs in the library's CUDA kernels. There is no fallback: if
 libmoe.so is missing or cannot be loaded, importing the binding's functions
@@ -29,7 +29,8 @@ __all__ = [
     "moe_expert_ffn_residual", "moe_ffn_forward_residual", "moe_set_decode_step_policy", "moe_ffn_forward_launches",
     "moe_test_expire_grid_barrier", "moe_set_expert_pass_tokens", "moe_test_expert_wait_limit",
     "moe_paged_workspace_size", "alloc_paged_workspace", "moe_paged_plan", "moe_qk_norm_rope", "moe_gqa_paged_decode",
-    "moe_gqa_paged_prefill", "moe_gqa_prefix_decode", "moe_test_paged_give_up",
+    "moe_gqa_paged_prefill", "moe_gqa_prefix_decode", "moe_test_paged_give_up", "moe_add_rms_norm", "moe_qk_norm_mrope",
+    "moe_qk_norm_rope_kv4", "moe_gqa_kv4_decode", "moe_kv4_load", "alloc_kv4_cache",
 ]
 
 MOE_W_BF16 = 0
@@ -86,8 +87,14 @@ def load() -> ctypes.CDLL:
         lib.moe_gqa_paged_decode.argtypes = [P] * 5 + [i] * 7 + [f32, i, i, P, P, z, P]
         lib.moe_gqa_paged_prefill.argtypes = [P] * 6 + [i] * 8 + [f32, i, i, P, P, z, P]
         lib.moe_gqa_prefix_decode.argtypes = [P, P, i, P, P, P, P] + [i] * 7 + [f32, P, P, z, P]
+        lib.moe_add_rms_norm.argtypes = [P, i64, P, P, f32, i, i, P, P, P, P, P]
+        lib.moe_qk_norm_mrope.argtypes = [P, i64, i, i, i, i, P, P, f32, P, P, i, i, P, i64, i, P, P, P, P, i, i, P]
+        lib.moe_qk_norm_rope_kv4.argtypes = [P, i64, i, i, i, i, P, P, f32, P, P, i, i, P, i64, i, P, P, P, i, i, P]
+        lib.moe_gqa_kv4_decode.argtypes = [P] * 4 + [i] * 7 + [f32, i, i, P, P, z, P]
+        lib.moe_kv4_load.argtypes = [P] * 4 + [i] * 6 + [P, P, P, i, i, P, z, P]
         for f in ("moe_paged_plan", "moe_qk_norm_rope", "moe_gqa_paged_decode", "moe_gqa_paged_prefill",
-                  "moe_gqa_prefix_decode"):
+                  "moe_gqa_prefix_decode", "moe_add_rms_norm", "moe_qk_norm_mrope", "moe_qk_norm_rope_kv4",
+                  "moe_gqa_kv4_decode", "moe_kv4_load"):
             getattr(lib, f).restype = i
         for f in ("moe_set_decode_step_policy", "moe_ffn_forward_launches"):
             getattr(lib, f).restype = i
@@ -381,6 +388,62 @@ def moe_gqa_prefix_decode(q, prefix_table, prefix_len: int, k_cache, v_cache, bl
                                                            scale, out, workspace, _raw(stream))
     if st:
         raise MoeError("moe_gqa_prefix_decode", st)
+
+
+# ---------------------------------------------------------------- norms and rotations (include/paged/moe_norm.h)
+def moe_add_rms_norm(x, residual, weight, eps: float, residual_out, y=None, q=None, scales=None, stream=None) -> None:
+    """x [N, H] bf16 (rows may be strided; None: nothing is added), residual [N, H] bf16, weight [H] bf16 or None; out:
+    residual_out [N, H] bf16 (may be residual; None: not stored), and the norm of the sum as y [N, H] bf16 and / or
+    as q [N, H] int8 with scales [N, H / 128] f32."""
+    st = (_native or _load_native()).moe_add_rms_norm(x, residual, weight, eps, residual_out, y, q, scales, _raw(stream))
+    if st:
+        raise MoeError("moe_add_rms_norm", st)
+
+
+def moe_qk_norm_mrope(qkv, q_weight, k_weight, eps: float, inv_freq, pair_axis, positions, slots, q_out, k_cache, v_cache,
+                      interleaved: bool = False, stream=None) -> None:
+    """moe_qk_norm_rope with positions [n_axes, N] int32 (rows may be strided): pair i turns by the axis pair_axis[i]
+    ([rot_dim / 2] int32; outside [0, n_axes): not at all)."""
+    st = (_native or _load_native()).moe_qk_norm_mrope(qkv, q_weight, k_weight, eps, inv_freq, pair_axis, positions, slots, q_out,
+                                                       k_cache, v_cache, interleaved, _raw(stream))
+    if st:
+        raise MoeError("moe_qk_norm_mrope", st)
+
+
+# ---------------------------------------------------------------- a cache held in 4 bits (include/paged/moe_kv4.h)
+def alloc_kv4_cache(num_pages: int, h_kv: int, page_size: int, device="cuda") -> torch.Tensor:
+    """An uninitialised 4-bit cache of one layer, keys and values: [num_pages, h_kv, page_size / 16, 2304] bytes."""
+    if page_size not in (16, 32, 64, 128, 256, 512, 1024):
+        raise ValueError("page_size must be a power of two, 16 .. 1024")
+    return torch.empty(num_pages, h_kv, page_size // 16, 2304, dtype=torch.uint8, device=device)
+
+
+def moe_qk_norm_rope_kv4(qkv, q_weight, k_weight, eps: float, inv_freq, pair_axis, positions, slots, q_out, kv4_cache,
+                         interleaved: bool = False, stream=None) -> None:
+    """moe_qk_norm_rope with the keys and values stored to kv4_cache in 4 bits. positions [N] int32 with pair_axis None,
+    or [n_axes, N] with pair_axis as in moe_qk_norm_mrope."""
+    st = (_native or _load_native()).moe_qk_norm_rope_kv4(qkv, q_weight, k_weight, eps, inv_freq, pair_axis, positions, slots,
+                                                          q_out, kv4_cache, interleaved, _raw(stream))
+    if st:
+        raise MoeError("moe_qk_norm_rope_kv4", st)
+
+
+def moe_gqa_kv4_decode(q, kv4_cache, block_table, seq_lens, scale: float, out, workspace, window: int = 0, n_sink: int = 0,
+                       stream=None) -> None:
+    """moe_gqa_paged_decode over a 4-bit cache [num_pages, h_kv, page_size / 16, 2304]."""
+    st = (_native or _load_native()).moe_gqa_kv4_decode(q, kv4_cache, block_table, seq_lens, scale, out, workspace, window,
+                                                        n_sink, _raw(stream))
+    if st:
+        raise MoeError("moe_gqa_kv4_decode", st)
+
+
+def moe_kv4_load(kv4_cache, block_table, first, seq_lens, k_cache, v_cache, dst_table, workspace, stream=None) -> None:
+    """Rows first[b] .. seq_lens[b] - 1 (first None: from 0) of the 4-bit cache's pages block_table [B, max_pages] as bf16
+    rows of k_cache and v_cache [pages, h_kv, page_size, d] at the pages dst_table [B, dst_max_pages]. All lists int32."""
+    st = (_native or _load_native()).moe_kv4_load(kv4_cache, block_table, first, seq_lens, k_cache, v_cache, dst_table,
+                                                  workspace, _raw(stream))
+    if st:
+        raise MoeError("moe_kv4_load", st)
 
 
 def moe_test_paged_give_up(tile: int = -1) -> None:

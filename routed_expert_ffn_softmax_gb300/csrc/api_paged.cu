@@ -1,5 +1,6 @@
-// C ABI of the serving path over a paged key/value cache (include/paged/moe_paged.h): host-side argument
-// checks, workspace layout and launches.
+// C ABI of the serving path over a paged key/value cache (include/paged/moe_paged.h), of the same over a cache held in 4
+// bits (moe_kv4.h) and of the layer step's norms and rotations (moe_norm.h): host-side argument checks, workspace layout
+// and launches.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -8,8 +9,11 @@
 
 #include "api_util.h"
 #include "moe_launch.h"
+#include "paged/moe_kv4.h"
+#include "paged/moe_norm.h"
 #include "paged/moe_paged.h"
 #include "paged/moe_paged_test.h"
+#include "step_launch.h"
 
 namespace {
 
@@ -184,6 +188,32 @@ moe::GqaRowsPlan rows_plan(const Attention& a, const Layout& L, int sms) {
   return plan;
 }
 
+// The three calls that norm, rotate and store heads; a's page_shift is set here.
+moe_status_t qk_norm_rope(moe::QkNormRopeArgs a, int d, int page_size, moe_stream_t stream) {
+  if (a.N < 0 || a.h_q < 1 || a.h_kv < 1 || d < 1 || a.rot < 0 || a.rot > d || a.rot % 16 || a.interleaved < 0 ||
+      a.interleaved > 1 || !std::isfinite(a.eps) || a.eps < 0.0f)
+    return MOE_ERR_INVALID_ARG;
+  if (a.n_axes < 1 || (a.n_axes > 1 && a.axis_stride < a.N)) return MOE_ERR_INVALID_ARG;
+  if (d != 128 || a.n_axes > 16) return MOE_ERR_UNSUPPORTED;
+  const int64_t heads = static_cast<int64_t>(a.h_q) + 2 * static_cast<int64_t>(a.h_kv);
+  if (heads * d > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (a.row_stride < heads * d || a.row_stride % 8) return MOE_ERR_INVALID_ARG;
+  const moe_status_t st = check_pages(a.h_kv, a.num_pages, page_size, 1);
+  if (st != MOE_OK) return st;
+  if (a.N == 0) return MOE_OK;
+  if (!a.qkv || !a.positions || !a.slots || !a.q_out || (!a.kv4 && (!a.k_cache || !a.v_cache)) || (a.rot > 0 && !a.inv_freq))
+    return MOE_ERR_INVALID_ARG;
+  const void* vectors[] = {a.qkv, a.q_out, a.k_cache, a.v_cache, a.kv4, a.q_weight, a.k_weight};
+  for (const void* v : vectors)
+    if (!aligned(v, 16)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(a.inv_freq, 4) || !aligned(a.positions, 4) || !aligned(a.slots, 4) || !aligned(a.pair_axis, 4))
+    return MOE_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  if (sms < 1) return MOE_ERR_CUDA;
+  a.page_shift = page_shift(page_size);
+  return cuda_status(moe::launch_qk_norm_rope(a, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -242,44 +272,49 @@ moe_status_t moe_qk_norm_rope(const uint16_t* qkv, int64_t row_stride, int N, in
                               int rot_dim, int interleaved, const int32_t* positions, const int32_t* slots,
                               uint16_t* q_out, uint16_t* k_cache, uint16_t* v_cache, int num_pages, int page_size,
                               moe_stream_t stream) {
-  if (N < 0 || h_q < 1 || h_kv < 1 || d < 1 || rot_dim < 0 || rot_dim > d || rot_dim % 16 || interleaved < 0 ||
-      interleaved > 1 || !std::isfinite(eps) || eps < 0.0f)
-    return MOE_ERR_INVALID_ARG;
-  if (d != 128) return MOE_ERR_UNSUPPORTED;
-  const int64_t heads = static_cast<int64_t>(h_q) + 2 * static_cast<int64_t>(h_kv);
-  if (heads * d > INT32_MAX) return MOE_ERR_UNSUPPORTED;
-  if (row_stride < heads * d || row_stride % 8) return MOE_ERR_INVALID_ARG;
-  const moe_status_t st = check_pages(h_kv, num_pages, page_size, 1);
-  if (st != MOE_OK) return st;
+  return qk_norm_rope({qkv, q_weight, k_weight, inv_freq, positions, slots, q_out, k_cache, v_cache, row_stride, eps, N, h_q,
+                       h_kv, rot_dim, interleaved, num_pages, 0, nullptr, 0, 1, nullptr}, d, page_size, stream);
+}
+
+moe_status_t moe_qk_norm_mrope(const uint16_t* qkv, int64_t row_stride, int N, int h_q, int h_kv, int d,
+                               const uint16_t* q_weight, const uint16_t* k_weight, float eps, const float* inv_freq,
+                               const int32_t* pair_axis, int rot_dim, int interleaved, const int32_t* positions,
+                               int64_t axis_stride, int n_axes, const int32_t* slots, uint16_t* q_out,
+                               uint16_t* k_cache, uint16_t* v_cache, int num_pages, int page_size,
+                               moe_stream_t stream) {
+  if (N > 0 && rot_dim > 0 && !pair_axis) return MOE_ERR_INVALID_ARG;
+  return qk_norm_rope({qkv, q_weight, k_weight, inv_freq, positions, slots, q_out, k_cache, v_cache, row_stride, eps, N, h_q,
+                       h_kv, rot_dim, interleaved, num_pages, 0, pair_axis, axis_stride, n_axes, nullptr}, d, page_size, stream);
+}
+
+moe_status_t moe_qk_norm_rope_kv4(const uint16_t* qkv, int64_t row_stride, int N, int h_q, int h_kv, int d,
+                                  const uint16_t* q_weight, const uint16_t* k_weight, float eps,
+                                  const float* inv_freq, const int32_t* pair_axis, int rot_dim, int interleaved,
+                                  const int32_t* positions, int64_t axis_stride, int n_axes, const int32_t* slots,
+                                  uint16_t* q_out, uint8_t* kv4_cache, int num_pages, int page_size,
+                                  moe_stream_t stream) {
+  if (!pair_axis && n_axes != 1) return MOE_ERR_INVALID_ARG;
+  if (N > 0 && !kv4_cache) return MOE_ERR_INVALID_ARG;
+  return qk_norm_rope({qkv, q_weight, k_weight, inv_freq, positions, slots, q_out, nullptr, nullptr, row_stride, eps, N, h_q,
+                       h_kv, rot_dim, interleaved, num_pages, 0, pair_axis, axis_stride, n_axes, kv4_cache}, d, page_size, stream);
+}
+
+moe_status_t moe_add_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual, const uint16_t* weight,
+                              float eps, int N, int H, uint16_t* residual_out, uint16_t* y, int8_t* q, float* scales,
+                              moe_stream_t stream) {
+  if (N < 0 || H < 1 || !std::isfinite(eps) || eps < 0.0f || !q != !scales || (!y && !q)) return MOE_ERR_INVALID_ARG;
+  if (H % (q ? 128 : 8) || H > 32768) return MOE_ERR_UNSUPPORTED;
+  if (x && (x_stride < H || x_stride % 8)) return MOE_ERR_INVALID_ARG;
   if (N == 0) return MOE_OK;
-  if (!qkv || !positions || !slots || !q_out || !k_cache || !v_cache || (rot_dim > 0 && !inv_freq))
-    return MOE_ERR_INVALID_ARG;
-  if (!aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
-      !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(inv_freq, 4) || !aligned(positions, 4) ||
-      !aligned(slots, 4))
-    return MOE_ERR_INVALID_ARG;
+  if (!residual) return MOE_ERR_INVALID_ARG;
+  const void* vectors[] = {x, residual, weight, residual_out, y, q};
+  for (const void* v : vectors)
+    if (!aligned(v, 16)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
   const int sms = sm_count();
   if (sms < 1) return MOE_ERR_CUDA;
-  moe::QkNormRopeArgs a{};
-  a.qkv = qkv;
-  a.q_weight = q_weight;
-  a.k_weight = k_weight;
-  a.inv_freq = inv_freq;
-  a.positions = positions;
-  a.slots = slots;
-  a.q_out = q_out;
-  a.k_cache = k_cache;
-  a.v_cache = v_cache;
-  a.row_stride = row_stride;
-  a.eps = eps;
-  a.N = N;
-  a.h_q = h_q;
-  a.h_kv = h_kv;
-  a.rot = rot_dim;
-  a.interleaved = interleaved;
-  a.num_pages = num_pages;
-  a.page_shift = page_shift(page_size);
-  return cuda_status(moe::launch_qk_norm_rope(a, sms, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(moe::launch_add_rms_norm({x, residual, weight, residual_out, y, q, scales, x_stride, eps, N, H}, sms,
+                                              reinterpret_cast<cudaStream_t>(stream)));
 }
 
 moe_status_t moe_gqa_paged_decode(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache,
@@ -345,6 +380,48 @@ moe_status_t moe_gqa_prefix_decode(const uint16_t* q, const int32_t* prefix_tabl
     own.prefix.half_seqs = half_tokens(h_q / h_kv);
   }
   return cuda_status(moe::launch_gqa_decode(own, s));
+}
+
+moe_status_t moe_gqa_kv4_decode(const uint16_t* q, const uint8_t* kv4_cache, const int32_t* block_table,
+                                const int32_t* seq_lens, int B, int h_q, int h_kv, int d, int num_pages,
+                                int page_size, int max_pages, float scale, int window, int n_sink, uint16_t* out,
+                                void* workspace, size_t ws_bytes, moe_stream_t stream) {
+  const uint16_t* cache = reinterpret_cast<const uint16_t*>(kv4_cache);
+  const Attention a{q, cache, cache, block_table, seq_lens, B, B, h_q, h_kv, d, num_pages, page_size, max_pages,
+                    scale, window, n_sink, 0, out, workspace, ws_bytes};
+  const moe_status_t st = check_attention(a);
+  if (st != MOE_OK || B == 0) return st;
+  const int sms = sm_count();
+  if (sms < 1) return MOE_ERR_CUDA;
+  const moe::GqaPlan plan = decode_plan(a, sms);
+  return cuda_status(moe::launch_kv4_decode({plan.paged, q, kv4_cache, seq_lens, out, plan.partials, plan.counters, plan.status, B,
+                                             h_q, h_kv, plan.L_cap, plan.scale_log2, plan.num_ctas, plan.give_up_tile},
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_kv4_load(const uint8_t* kv4_cache, const int32_t* block_table, const int32_t* first,
+                          const int32_t* seq_lens, int B, int h_kv, int d, int num_pages, int page_size,
+                          int max_pages, uint16_t* k_cache, uint16_t* v_cache, const int32_t* dst_table, int dst_pages,
+                          int dst_max_pages, void* workspace, size_t ws_bytes, moe_stream_t stream) {
+  if (B < 0 || h_kv < 1 || d < 1) return MOE_ERR_INVALID_ARG;
+  if (d != 128 || B > moe::kGqaMaxSeqs) return MOE_ERR_UNSUPPORTED;
+  moe_status_t st = check_pages(h_kv, num_pages, page_size, max_pages);
+  if (st == MOE_OK) st = check_pages(h_kv, dst_pages, page_size, dst_max_pages);
+  if (st != MOE_OK) return st;
+  const int64_t widest = max_pages > dst_max_pages ? max_pages : dst_max_pages;
+  if (static_cast<double>(B) * h_kv * (page_size / 16) * widest > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (B == 0) return MOE_OK;
+  if (!kv4_cache || !block_table || !seq_lens || !k_cache || !v_cache || !dst_table || !workspace) return MOE_ERR_INVALID_ARG;
+  if (!aligned(kv4_cache, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_table, 4) ||
+      !aligned(dst_table, 4) || !aligned(first, 4) || !aligned(seq_lens, 4) || !aligned(workspace, kAlign))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < kCtrlBytes) return MOE_ERR_WORKSPACE;
+  const int sms = sm_count();
+  if (sms < 1) return MOE_ERR_CUDA;
+  return cuda_status(moe::launch_kv4_load({kv4_cache, block_table, dst_table, first, seq_lens, k_cache, v_cache,
+                                           static_cast<int32_t*>(workspace), B, h_kv, num_pages, dst_pages, max_pages,
+                                           dst_max_pages, page_shift(page_size)},
+                                          sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 moe_status_t moe_test_paged_give_up(int tile) {

@@ -169,6 +169,11 @@ struct QkNormRopeArgs {
   int64_t row_stride;
   float eps;
   int N, h_q, h_kv, rot, interleaved, num_pages, page_shift;
+  // positions with several axes: the axis of each pair (null: one axis), rows of positions axis_stride apart
+  const int32_t* pair_axis;    // [rot / 2]
+  int64_t axis_stride;
+  int n_axes;
+  uint8_t* kv4;                // the cache in 4 bits, instead of k_cache and v_cache
 };
 cudaError_t launch_qk_norm_rope(const QkNormRopeArgs& args, int num_sms, cudaStream_t stream);
 

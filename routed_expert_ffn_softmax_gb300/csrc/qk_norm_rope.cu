@@ -16,6 +16,15 @@
 // of 64 + 8 heads in 59 us interleaved and 69 in halves of 32, where the full rotation in halves takes 56 (44.6 at the copy
 // rate).
 //
+// Positions with several axes (kAxes; include/paged/moe_norm.h): the lanes that compute a pair's sine and cosine look up the
+// pair's axis once and load that axis's position per token; nothing else differs.
+//
+// A 4-bit cache (kFour; include/paged/moe_kv4.h): keys and values are rounded to bf16 as for the bf16 cache, then the 8 (or
+// 4) lanes that hold a group of 32 dimensions share its largest magnitude, taken of the bits as whole numbers (two groups
+// in one shuffle; NaN stands above infinity), and lanes that hold parts of the same stored bytes exchange them, so that a
+// head's 64 bytes of codes leave in 8- or 16-byte stores. The bf16 quotient of a value and its scale that is not a half is
+// 2^-9 of itself or more away from one, so the fp32 division decides every code exactly.
+//
 // The angle: inv_freq / (2 pi) is kept as a 64-bit fraction of a turn (computed in fp64, rounded once), so
 // pos * fraction modulo 2^64 is the angle modulo one turn without any loss for large pos, and sin and cos are taken of a
 // reduced argument. What remains is the fraction's error: 1 / (2 pi) and the product round in fp64 (2^-53 of |inv_freq| /
@@ -27,6 +36,7 @@
 
 #include "paged_device.cuh"
 #include "moe_launch.h"
+#include "step_launch.h"
 
 namespace moe {
 namespace qk {
@@ -73,9 +83,102 @@ __device__ __forceinline__ uint64_t turn_fraction(float inv_freq) {
   return static_cast<uint64_t>(__double2ull_rn(f * 18446744073709551616.0));
 }
 
+// The scale of a group whose largest magnitude has these bf16 bits (in the upper half): a 7th of it, in bf16.
+__device__ __forceinline__ uint32_t scale_bits(uint32_t top) {
+  const __nv_bfloat16 s = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 7.0f));
+  return *reinterpret_cast<const uint16_t*>(&s);
+}
+// round(x / s) within -7 .. 7, plus 8 (a NaN quotient: 8).
+__device__ __forceinline__ uint32_t code4(float x, float s) {
+  const int c = s == 0.0f ? 0 : __float2int_rn(__fdiv_rn(x, s));  // (0 for NaN)
+  return static_cast<uint32_t>(min(max(c, -7), 7) + 8);
+}
+// The magnitudes' bits of two packed bf16 values, and the larger of two such in each half.
+__device__ __forceinline__ uint32_t magnitudes(uint32_t v) { return v & 0x7fff7fffu; }
+
+// Head j's block in the 4-bit cache of the token at this slot, at the token's place: keys or values.
+struct Kv4Row {
+  uint8_t* codes;
+  uint8_t* scales;
+};
+__device__ __forceinline__ Kv4Row kv4_row(const QkNormRopeArgs& p, int slot, int j, bool is_v) {
+  const int in_page = slot & ((1 << p.page_shift) - 1);
+  const int64_t block = ((static_cast<int64_t>(slot >> p.page_shift) * p.h_kv + j) << (p.page_shift - 4)) + (in_page >> 4);
+  uint8_t* at = p.kv4 + block * kKv4Block + (is_v ? kKv4Values : 0);
+  return {at + (in_page & 15) * kKv4RowBytes, at + kKv4Scales + (in_page & 15) * 8};
+}
+
+// A head's 128 values in 4 bits, from the 16 lanes that hold 8 of them each (all of a half-warp, lane l dimensions 8 l ..):
+// four lanes share a group, and lanes l, l + 4, l + 8, l + 12 hold the four groups' parts of the same 16 bytes.
+__device__ __forceinline__ void store4_eight(const QkNormRopeArgs& p, const uint4& o, int slot, bool stored, int j, bool is_v,
+                                             int l) {
+  const uint32_t half_warp = 0xffffu << (threadIdx.x & 16);
+  const uint32_t v[4] = {o.x, o.y, o.z, o.w};
+  uint32_t top = __vmaxu2(__vmaxu2(magnitudes(v[0]), magnitudes(v[1])), __vmaxu2(magnitudes(v[2]), magnitudes(v[3])));
+  top = max(top << 16, top & 0xffff0000u);
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) top = max(top, __shfl_xor_sync(half_warp, top, d, 16));
+  const uint32_t sb = scale_bits(top);
+  const float s = __uint_as_float(sb << 16);
+  float x[8];
+  unpack8(o, x);
+  uint32_t c = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c |= code4(x[i], s) << (4 * i);
+  uint32_t cw[4], sw[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    cw[w] = __shfl_sync(half_warp, c, (l & 3) + 4 * w, 16);
+    sw[w] = __shfl_sync(half_warp, sb, 4 * w, 16);
+  }
+  if (!stored || l >= 4) return;
+  const Kv4Row row = kv4_row(p, slot, j, is_v);
+  *reinterpret_cast<uint4*>(row.codes + 16 * l) =
+      make_uint4(__byte_perm(cw[0], cw[1], 0x5410), __byte_perm(cw[2], cw[3], 0x5410), __byte_perm(cw[0], cw[1], 0x7632),
+                 __byte_perm(cw[2], cw[3], 0x7632));
+  if (l == 0) *reinterpret_cast<uint2*>(row.scales) = make_uint2(sw[0] | sw[1] << 16, sw[2] | sw[3] << 16);
+}
+
+// The same where lane l holds dimensions 4 l .. + 3 (a) and 64 + 4 l .. + 3 (b): eight lanes share two groups, lanes l and
+// l + 8 the same 8 bytes.
+__device__ __forceinline__ void store4_halves(const QkNormRopeArgs& p, const uint2& a, const uint2& b, int slot, bool stored,
+                                              int j, bool is_v, int l) {
+  const uint32_t half_warp = 0xffffu << (threadIdx.x & 16);
+  const uint32_t ma = __vmaxu2(magnitudes(a.x), magnitudes(a.y)), mb = __vmaxu2(magnitudes(b.x), magnitudes(b.y));
+  uint32_t top = __vmaxu2(__byte_perm(ma, mb, 0x5410), __byte_perm(ma, mb, 0x7632));  // group of a, group of b
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) top = __vmaxu2(top, __shfl_xor_sync(half_warp, top, d, 16));
+  const uint32_t sa = scale_bits(top << 16), sb = scale_bits(top & 0xffff0000u);
+  const float fa = __uint_as_float(sa << 16), fb = __uint_as_float(sb << 16);
+  auto four = [](const uint2& v, float s) {
+    return code4(__uint_as_float(v.x << 16), s) | code4(__uint_as_float(v.x & 0xffff0000u), s) << 4 |
+           code4(__uint_as_float(v.y << 16), s) << 8 | code4(__uint_as_float(v.y & 0xffff0000u), s) << 12;
+  };
+  const uint32_t c = four(a, fa) | four(b, fb) << 16;  // lanes below 8: groups 0 and 2, the others 1 and 3
+  const uint32_t co = __shfl_xor_sync(half_warp, c, 8, 16);
+  const uint32_t s = sa | sb << 16;
+  const uint32_t so = __shfl_xor_sync(half_warp, s, 8, 16);
+  if (!stored || l >= 8) return;
+  const Kv4Row row = kv4_row(p, slot, j, is_v);
+  *reinterpret_cast<uint2*>(row.codes + 8 * l) = make_uint2(__byte_perm(c, co, 0x5410), __byte_perm(c, co, 0x7632));
+  if (l == 0) *reinterpret_cast<uint2*>(row.scales) = make_uint2(__byte_perm(s, so, 0x5410), __byte_perm(s, so, 0x7632));
+}
+
+// The axis of pair x: what it adds to the positions' address, and whether it turns.
+struct PairAxis {
+  int64_t offset = 0;
+  bool turns = true;
+  __device__ __forceinline__ PairAxis(const QkNormRopeArgs& p, int x, bool there) {
+    if (!there) return;
+    const int axis = p.pair_axis[x];
+    turns = static_cast<uint32_t>(axis) < static_cast<uint32_t>(p.n_axes);
+    offset = turns ? axis * p.axis_stride : 0;
+  }
+};
+
 constexpr int kUnroll = 4;
 
-template <bool kInterleaved>
+template <bool kInterleaved, bool kAxes, bool kFour>
 __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(const QkNormRopeArgs p, int parts, int part_heads) {
   __shared__ __align__(16) float cs[kThreads / 32][2][kD / 2];  // cos, sin of each warp's token
   const int lane = threadIdx.x & 31;
@@ -89,6 +192,12 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(const QkNormR
   uint64_t turn[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) turn[i] = lane + 32 * i < half ? turn_fraction(p.inv_freq[lane + 32 * i]) : 0;
+  PairAxis axis[2] = {{p, lane, kAxes && lane < half}, {p, lane + 32, kAxes && lane + 32 < half}};
+  if constexpr (kAxes) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (!axis[i].turns) turn[i] = 0;
+  }
   // the lane's role in the rotation: first (a) or second (b) of its pairs, or untouched
   const bool rotates = 8 * l < p.rot;
   const bool second = !kInterleaved && 8 * l >= half;
@@ -114,7 +223,9 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(const QkNormR
     const int first = static_cast<int>(it - static_cast<int64_t>(n) * parts) * part_heads;
     const int last = min(heads, first + part_heads);
     const uint16_t* src = p.qkv + static_cast<int64_t>(n) * p.row_stride + 8 * l;
-    const int pos = p.positions[n];
+    int pos[2];
+    pos[0] = p.positions[n + (kAxes ? axis[0].offset : 0)];
+    pos[1] = kAxes ? p.positions[n + axis[1].offset] : pos[0];
     const int slot = p.slots[n];
     uint4 v[kUnroll];
     auto load = [&](int h0) {
@@ -129,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(const QkNormR
     for (int i = 0; i < 2; ++i) {
       const int x = lane + 32 * i;
       if (x < half) {
-        const uint64_t a = turn[i] * static_cast<uint64_t>(static_cast<int64_t>(pos));
+        const uint64_t a = turn[i] * static_cast<uint64_t>(static_cast<int64_t>(pos[i]));
         // signed fraction of a turn in [-1/2, 1/2) times two, for sincospi; converted with one rounding
         const float f = static_cast<float>(static_cast<int64_t>(a)) * (1.0f / 9223372036854775808.0f);
         float s, c;
@@ -198,6 +309,8 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(const QkNormR
         }
         if (is_q) {
           *reinterpret_cast<uint4*>(p.q_out + (static_cast<int64_t>(n) * p.h_q + h) * kD + 8 * l) = o;
+        } else if (kFour) {
+          store4_eight(p, o, slot, stored, is_v ? h - p.h_q - p.h_kv : h - p.h_q, is_v, l);
         } else if (stored) {
           const int j = is_v ? h - p.h_q - p.h_kv : h - p.h_q;
           *reinterpret_cast<uint4*>((is_v ? p.v_cache : p.k_cache) + row + (static_cast<int64_t>(j) << p.page_shift) * kD) = o;
@@ -212,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(const QkNormR
 // arithmetic two values an instruction.
 constexpr int kUnrollHalves = 4;
 
+template <bool kAxes, bool kFour>
 __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_halves_kernel(const QkNormRopeArgs p, int parts, int part_heads) {
   __shared__ __align__(16) float cs[kThreads / 32][2][kD / 2];  // cos, sin of each warp's token
   const int lane = threadIdx.x & 31;
@@ -221,7 +335,13 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_halves_kernel(const 
   pdl_wait_predecessor();
   pdl_allow_successor();
 
-  const uint64_t turn[2] = {turn_fraction(p.inv_freq[lane]), turn_fraction(p.inv_freq[lane + 32])};
+  uint64_t turn[2] = {turn_fraction(p.inv_freq[lane]), turn_fraction(p.inv_freq[lane + 32])};
+  const PairAxis axis[2] = {{p, lane, kAxes}, {p, lane + 32, kAxes}};
+  if constexpr (kAxes) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (!axis[i].turns) turn[i] = 0;
+  }
   const uint2 ones = make_uint2(0x3f803f80u, 0x3f803f80u);
   uint2 w[2][2] = {{ones, ones}, {ones, ones}};  // [q, k][first, second half]
   if (p.q_weight) {
@@ -247,7 +367,9 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_halves_kernel(const 
     const int first = static_cast<int>(it - static_cast<int64_t>(n) * parts) * part_heads;
     const int last = min(heads, first + part_heads);
     const uint16_t* src = p.qkv + static_cast<int64_t>(n) * p.row_stride + 4 * l;
-    const int pos = p.positions[n];
+    int pos[2];
+    pos[0] = p.positions[n + (kAxes ? axis[0].offset : 0)];
+    pos[1] = kAxes ? p.positions[n + axis[1].offset] : pos[0];
     const int slot = p.slots[n];
     uint2 v[kUnrollHalves][2];
     auto load = [&](int h0) {
@@ -261,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_halves_kernel(const 
     load(first);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint64_t a = turn[i] * static_cast<uint64_t>(static_cast<int64_t>(pos));
+      const uint64_t a = turn[i] * static_cast<uint64_t>(static_cast<int64_t>(pos[i]));
       // signed fraction of a turn in [-1/2, 1/2) times two, for sincospi; converted with one rounding
       const float f = static_cast<float>(static_cast<int64_t>(a)) * (1.0f / 9223372036854775808.0f);
       sincospif(f, &my[1][lane + 32 * i], &my[0][lane + 32 * i]);
@@ -323,6 +445,8 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_halves_kernel(const 
         uint16_t* to = nullptr;
         if (is_q) {
           to = p.q_out + (static_cast<int64_t>(n) * p.h_q + h) * kD + 4 * l;
+        } else if (kFour) {
+          store4_halves(p, o[u][0], o[u][1], slot, stored, is_v ? h - p.h_q - p.h_kv : h - p.h_q, is_v, l);
         } else if (stored) {
           const int j = is_v ? h - p.h_q - p.h_kv : h - p.h_q;
           to = (is_v ? p.v_cache : p.k_cache) + row + (static_cast<int64_t>(j) << p.page_shift) * kD;
@@ -359,8 +483,17 @@ cudaError_t launch_qk_norm_rope(const QkNormRopeArgs& args, int num_sms, cudaStr
   const int64_t blocks = (static_cast<int64_t>(args.N) * parts + qk::kThreads / 32 - 1) / (qk::kThreads / 32);
   const int64_t resident = warps / (qk::kThreads / 32);
   const int grid = static_cast<int>(blocks < resident ? blocks : resident);
-  auto kernel = halves ? qk::qk_norm_rope_halves_kernel
-                       : (args.interleaved ? qk::qk_norm_rope_kernel<true> : qk::qk_norm_rope_kernel<false>);
+  using Kernel = void (*)(QkNormRopeArgs, int, int);
+  const bool axes = args.pair_axis != nullptr, four = args.kv4 != nullptr;
+  static constexpr Kernel kHalves[2][2] = {
+      {qk::qk_norm_rope_halves_kernel<false, false>, qk::qk_norm_rope_halves_kernel<false, true>},
+      {qk::qk_norm_rope_halves_kernel<true, false>, qk::qk_norm_rope_halves_kernel<true, true>}};
+  static constexpr Kernel kGeneral[2][2][2] = {
+      {{qk::qk_norm_rope_kernel<false, false, false>, qk::qk_norm_rope_kernel<false, false, true>},
+       {qk::qk_norm_rope_kernel<false, true, false>, qk::qk_norm_rope_kernel<false, true, true>}},
+      {{qk::qk_norm_rope_kernel<true, false, false>, qk::qk_norm_rope_kernel<true, false, true>},
+       {qk::qk_norm_rope_kernel<true, true, false>, qk::qk_norm_rope_kernel<true, true, true>}}};
+  const Kernel kernel = halves ? kHalves[axes][four] : kGeneral[args.interleaved][axes][four];
   return launch_pdl(kernel, dim3(grid), dim3(qk::kThreads), 0, stream, args, parts, part_heads);
 }
 
