@@ -33,7 +33,8 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--ex
               "-Xptxas", "-v,-warn-spills"]
 # Kernels whose warps share out their registers: source, kernel, and the constant in the source that counts what a thread
 # has at launch. With another count their launch is refused.
-REGISTERS = (("gqa_rows.cu", "gqa_rows_kernel", "kRegsLaunch"),)
+REGISTERS = (("gqa_rows.cu", "gqa_rows_kernel", "kRegsLaunch"),
+             ("kv4_decode.cu", "kv4_decode_kernelILi1E", "kRegsLaunch"), ("kv4_decode.cu", "kv4_decode_kernelILi2E", "kRegsLaunch"))
 
 
 def nvcc() -> str:

@@ -45,30 +45,51 @@ using gqa::kKeys;
 using gqa::span_of;
 
 constexpr int kD = 128;
-constexpr int kWarps = 8;                  // that compute; the last warp loads
-constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kWork = 32 * kWarps;
-constexpr int kChunk = kKv4Tokens;         // keys of a warp in a tile
-constexpr int kChunks = kKeys / kChunk;
+constexpr int kChunk = kKv4Tokens;         // keys of one matrix instruction
+constexpr int kChunks = kKeys / kChunk;    // of a tile
 constexpr int kStageBytes = kChunks * kKv4Block;
-constexpr int kRow = kD + 4;               // floats of a head's outputs in the join buffer (no bank conflicts)
-constexpr float kHigh = 15.0f;             // log2 of what p s may reach
+constexpr int kRow = kD + 4;               // floats of a head's outputs handed over (no bank conflicts)
+constexpr float kMost = 32768.0f;          // what p s may reach
+constexpr float kRaise = 14.5f;            // log2 of the p s from which a head's reference is raised when one is too large
 constexpr float kStart = 6.0f;             // log2 of the largest p s right after a reference is set
-constexpr float kLeastScale = -60.0f;      // log2: smaller value scales count as this when the reference is set
-static_assert(kChunks == kWarps && kFold == kChunk, "a warp takes a chunk of each tile");
+constexpr float kLeastScale = 8.6736174e-19f;  // 2^-60: smaller value scales count as this where references are concerned
+static_assert(kFold == kChunk, "sink keys are folded in whole chunks");
 
+// Warps 0..3: two that load, two that prepare queries and finish pieces; the others work.
+constexpr int kWarps = 8;                  // that work
+constexpr int kThreads = 32 * (4 + kWarps);
+// Registers per thread at launch; the warpgroups share out what the launch has.
+constexpr int kRegsLaunch = 168;
+constexpr int kRegsHelp = 104;
+constexpr int kRegsWork = 200;
+static_assert(128 * kRegsHelp + 32 * kWarps * kRegsWork <= kThreads * kRegsLaunch, "a larger share would wait forever");
+
+// kNT: eights of heads. GB300, us for 12 warps instead of 8: 16 sequences of up to 32K keys 62.5 instead of 65.5, but 255 of up
+// to 4K 92 instead of 85 and one sequence 11.0 instead of 9.3.
 template <int kNT>
-struct Smem {
+struct Split {
+  // Chunks a warp takes at once. With 16 heads one, two spill: 64 sequences behind a window 26.4 us instead of 28.9 (24 of up to
+  // 32K keys 81.5 instead of 79.3); with 8 heads two, as the code around them costs as much as one.
+  static constexpr int kUnit = kNT == 1 ? 2 : 1;
+  static constexpr int kUnits = kChunks / kUnit;         // of a tile
+  static constexpr int kTiles = kWarps / kUnits;         // tiles the warps are at together
   static constexpr int kStages = kNT == 1 ? 9 : 7;
+    // shared memory
+  static constexpr int kJoinFloats = kWarps * 8 * kNT * kRow;
+  static constexpr int kMost = kJoinFloats * 4 / (128 + 512 * 8 * kNT);  // parts of a cut segment that fit there
+  static_assert(kMost >= kWarps && kMost <= 32, "both are joined alike, a lane copies a part");
   static constexpr int kJoin = kStages * kStageBytes;                    // [kWarps][8 kNT][kRow] floats
-  static constexpr int kRef = kJoin + kWarps * 8 * kNT * kRow * 4;       // [2][2][kWarps][16] floats: R, sum
-  static constexpr int kBars = kRef + 2 * 2 * kWarps * 16 * 4;           // full, empty
-  static constexpr int kBad = kBars + 2 * kStages * 8;                   // [kStages] chunks that read as zeros
-  static constexpr int kMisc = (kBad + kStages * 4 + 15) / 16 * 16;      // 16 ints
-  static constexpr int kPre = kMisc + 64;
+  static constexpr int kRef = kJoin + kJoinFloats * 4;                   // [2][kWarps][16] floats: reference, sum
+  static constexpr int kQ = kRef + 2 * kWarps * 16 * 4;                  // [2] queries as operands
+  static constexpr int kQBytes = kNT * (4 * 32 * 16 + 8 * 4 * 4 + 8 * 4);
+  static constexpr int kBars = (kQ + 2 * kQBytes + 15) / 16 * 16;
+  static constexpr int kBad = kBars + (2 * kStages + 7) * 8;             // [2][kStages] chunks that read as zeros, the last tile there
+  static constexpr int kMisc = (kBad + 2 * kStages * 4 + 15) / 16 * 16;      // 32 ints
+  static constexpr int kPre = kMisc + 128;
   static constexpr int kLens = kPre + (kGqaMaxSeqs + 4) * 4;
   static constexpr int kBytes = kLens + kGqaMaxSeqs * 4;
   static_assert(kBytes <= 232448, "dynamic shared memory per CTA");
+  static_assert(kQ % 16 == 0 && kRef % 16 == 0, "vector loads");
 };
 
 struct Params {
@@ -85,10 +106,11 @@ struct Params {
   int give_up_tile;
 };
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                                        const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 // An 8 x 8 matrix of 16-bit elements, a row's pair per lane, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -113,8 +135,16 @@ __device__ __forceinline__ uint32_t sub2(uint32_t v, uint32_t bias) {
   const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&bias));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-__device__ __forceinline__ uint32_t code_lo(uint32_t v) { return sub2((v & 0x000f000fu) | 0x64006400u, 0x64086408u); }
-__device__ __forceinline__ uint32_t code_hi(uint32_t v) { return sub2((v & 0x00f000f0u) | 0x54005400u, 0x54805480u); }
+// (v & mask) | more in one instruction: with both as immediates the compiler takes two.
+template <uint32_t kMask>
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t more) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(v), "n"(kMask), "r"(more));
+  return d;
+}
+
+// Orders this thread's plain accesses, to shared and global memory, before copies that are issued after a barrier.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
   asm volatile(
@@ -124,15 +154,32 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// A warp's queries of up to 8 kNT heads as mma operands, and what goes with them.
+// log2 of the largest of a key's value scales.
+__device__ __forceinline__ float log_scale(const uint2& v) {
+  const uint32_t m = __vmaxu2(v.x, v.y);
+  return lg2_approx(max3_f32(bf_lo(m), bf_hi(m), kLeastScale));
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// The queries of up to 8 kNT heads as mma operands, and what goes with them: in shared memory, written by one warp per piece,
+// and in the working warps' registers.
 template <int kNT>
 struct Queries {
-  uint32_t b[kNT][4][2][2];  // [heads][group of dims][k16 step][register]
+  uint32_t b[kNT][4][4];     // [heads][group of dims][k16 step, register]
   float start[kNT][4][2];    // -8 sum(q) of the group for heads 2 t, 2 t + 1 (in accumulator units)
   float unit[kNT][2];        // accumulator units to log2 scores
+  uint32_t exp_low, exp_high;  // fp16 1024 and 64 twice, in registers
 
-  // q at the group's first head; a lane (g, t) holds head g's dimensions 32 w + 8 t .. + 7.
-  __device__ __forceinline__ void load(const uint16_t* q, int G, float scale_log2, int lane) {
+  static __device__ __forceinline__ uint4* operands(uint8_t* at) { return reinterpret_cast<uint4*>(at); }
+  static __device__ __forceinline__ float* starts(uint8_t* at) { return reinterpret_cast<float*>(at + kNT * 4 * 32 * 16); }
+  static __device__ __forceinline__ float* units(uint8_t* at) { return starts(at) + kNT * 32; }
+
+  // q at the group's first head; lane (g, t) takes head g's dimensions 32 w + 8 t .. + 7.
+  static __device__ __forceinline__ void prepare(uint8_t* at, const uint16_t* q, int G, float scale_log2, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
@@ -155,7 +202,6 @@ struct Queries {
       const int e = top == 0 ? 0 : min(max(static_cast<int>(top >> 23) - 127, -100), 100);
       const float to = __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
       const float back = scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 24 - 13 + e) << 23);
-      float sum[4];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const uint32_t x[4] = {v[w].x, v[w].y, v[w].z, v[w].w};
@@ -165,25 +211,38 @@ struct Queries {
           f[2 * i] = bf_lo(x[i]) * to;
           f[2 * i + 1] = bf_hi(x[i]) * (to * 0.0625f);
         }
-        sum[w] = 0.0f;
+        uint32_t h[4];
+        float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const __half2 h = __floats2half2_rn(f[i], f[i + 4]);
-          b[nt][w][i >> 1][i & 1] = *reinterpret_cast<const uint32_t*>(&h);
-          const float2 r = __half22float2(h);
-          sum[w] = fmaf(r.x + r.y, (i & 1) ? 16.0f : 1.0f, sum[w]);
+          h[i] = half2_bits(f[i], f[i + 4]);
+          const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+          sum = fmaf(r.x + r.y, (i & 1) ? 16.0f : 1.0f, sum);
         }
-        sum[w] += __shfl_xor_sync(0xffffffffu, sum[w], 1);
-        sum[w] += __shfl_xor_sync(0xffffffffu, sum[w], 2);
+        operands(at)[(nt * 4 + w) * 32 + lane] = make_uint4(h[0], h[1], h[2], h[3]);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (t == 0) starts(at)[(nt * 4 + w) * 8 + g] = sum * -4.76837158203125e-07f;  // -8 2^-24
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int from = 4 * (2 * t + h);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) start[nt][w][h] = __shfl_sync(0xffffffffu, sum[w], from) * -4.76837158203125e-07f;  // -8 2^-24
-        unit[nt][h] = __shfl_sync(0xffffffffu, back, from);
-      }
+      if (t == 0) units(at)[nt * 8 + g] = back;
     }
+  }
+  __device__ __forceinline__ void load(uint8_t* at, int lane) {
+    const int t = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint4 v = operands(at)[(nt * 4 + w) * 32 + lane];
+        b[nt][w][0] = v.x, b[nt][w][1] = v.y, b[nt][w][2] = v.z, b[nt][w][3] = v.w;
+        const float2 s = *reinterpret_cast<const float2*>(starts(at) + (nt * 4 + w) * 8 + 2 * t);
+        start[nt][w][0] = s.x, start[nt][w][1] = s.y;
+      }
+      const float2 u = *reinterpret_cast<const float2*>(units(at) + nt * 8 + 2 * t);
+      unit[nt][0] = u.x, unit[nt][1] = u.y;
+    }
+    asm volatile("mov.u32 %0, 0x64006400;" : "=r"(exp_low));
+    asm volatile("mov.u32 %0, 0x54005400;" : "=r"(exp_high));
   }
 };
 
@@ -204,69 +263,86 @@ struct State {
     }
   }
 
-  // 16 keys at `at` in shared memory; see0, see1: whether the query sees keys g and g + 8; zero: all read as zeros.
-  __device__ __forceinline__ void add(const Queries<kNT>& q, const uint8_t* at, bool see0, bool see1, bool zero, int lane) {
+  // kCount times 16 keys at `at` in shared memory; bias: 0 for a key (g and g + 8 of each 16) that the query sees, -infinity
+  // for others, whose scales are 0.
+  template <int kCount>
+  __device__ __forceinline__ void add(const Queries<kNT>& q, const uint8_t* at, const float (&bias)[kCount][2], int lane) {
     const int g = lane >> 2, t = lane & 3;
-    const uint4 k0 = *reinterpret_cast<const uint4*>(at + g * kKv4RowBytes + 16 * t);
-    const uint4 k1 = *reinterpret_cast<const uint4*>(at + (g + 8) * kKv4RowBytes + 16 * t);
-    uint2 ks0 = *reinterpret_cast<const uint2*>(at + kKv4Scales + 8 * g);
-    uint2 ks1 = *reinterpret_cast<const uint2*>(at + kKv4Scales + 8 * (g + 8));
-    const uint8_t* va = at + kKv4Values;
-    uint2 vs0 = *reinterpret_cast<const uint2*>(va + kKv4Scales + 8 * g);
-    uint2 vs1 = *reinterpret_cast<const uint2*>(va + kKv4Scales + 8 * (g + 8));
-    if (zero) ks0 = ks1 = vs0 = vs1 = make_uint2(0u, 0u);
-    if (!see0) vs0 = make_uint2(0u, 0u);  // what stands in rows not seen may be NaN
-    if (!see1) vs1 = make_uint2(0u, 0u);
+    float x[kCount][kNT][4];
+    uint2 vs[kCount][2];
+#pragma unroll
+    for (int c = 0; c < kCount; ++c) {
+      const uint8_t* ka = at + c * kKv4Block;
+      const uint4 k0 = *reinterpret_cast<const uint4*>(ka + g * kKv4RowBytes + 16 * t);
+      const uint4 k1 = *reinterpret_cast<const uint4*>(ka + (g + 8) * kKv4RowBytes + 16 * t);
+      const uint2 ks0 = *reinterpret_cast<const uint2*>(ka + kKv4Scales + 8 * g);
+      const uint2 ks1 = *reinterpret_cast<const uint2*>(ka + kKv4Scales + 8 * (g + 8));
+      vs[c][0] = *reinterpret_cast<const uint2*>(ka + kKv4Values + kKv4Scales + 8 * g);
+      vs[c][1] = *reinterpret_cast<const uint2*>(ka + kKv4Values + kKv4Scales + 8 * (g + 8));
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[c][nt][i] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t sel = (w & 1) ? 0x7632u : 0x5410u;
+        const uint32_t r0 = __byte_perm(w < 2 ? k0.x : k0.y, w < 2 ? k0.z : k0.w, sel);
+        const uint32_t r1 = __byte_perm(w < 2 ? k1.x : k1.y, w < 2 ? k1.z : k1.w, sel);
+        const uint32_t r0h = r0 >> 8, r1h = r1 >> 8;
+        const float s0 = (w & 1) ? bf_hi(w < 2 ? ks0.x : ks0.y) : bf_lo(w < 2 ? ks0.x : ks0.y);
+        const float s1 = (w & 1) ? bf_hi(w < 2 ? ks1.x : ks1.y) : bf_lo(w < 2 ? ks1.x : ks1.y);
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          const float from[4] = {q.start[nt][w][0], q.start[nt][w][1], q.start[nt][w][0], q.start[nt][w][1]};
+          float acc[4];
+          mma_f16(acc, r0 & 0x000f000fu, r1 & 0x000f000fu, r0 & 0x00f000f0u, r1 & 0x00f000f0u, q.b[nt][w][0], q.b[nt][w][1], from);
+          mma_f16(acc, r0h & 0x000f000fu, r1h & 0x000f000fu, r0h & 0x00f000f0u, r1h & 0x00f000f0u, q.b[nt][w][2], q.b[nt][w][3],
+                  acc);
+          x[c][nt][0] = fmaf(acc[0], s0, x[c][nt][0]);
+          x[c][nt][1] = fmaf(acc[1], s0, x[c][nt][1]);
+          x[c][nt][2] = fmaf(acc[2], s1, x[c][nt][2]);
+          x[c][nt][3] = fmaf(acc[3], s1, x[c][nt][3]);
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[c][nt][i] = fmaf(x[c][nt][i], q.unit[nt][i & 1], bias[c][i >> 1]);
+    }
 
-    float x[kNT][4];
+    float p[kCount][kNT][4];
+    auto weigh = [&]() {
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
+      for (int c = 0; c < kCount; ++c)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[nt][i] = 0.0f;
+        for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const uint32_t sel = (w & 1) ? 0x7632u : 0x5410u;
-      const uint32_t r0 = __byte_perm(w < 2 ? k0.x : k0.y, w < 2 ? k0.z : k0.w, sel);
-      const uint32_t r1 = __byte_perm(w < 2 ? k1.x : k1.y, w < 2 ? k1.z : k1.w, sel);
-      const uint32_t r0h = r0 >> 8, r1h = r1 >> 8;
-      const float s0 = (w & 1) ? bf_hi(w < 2 ? ks0.x : ks0.y) : bf_lo(w < 2 ? ks0.x : ks0.y);
-      const float s1 = (w & 1) ? bf_hi(w < 2 ? ks1.x : ks1.y) : bf_lo(w < 2 ? ks1.x : ks1.y);
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-        float acc[4] = {q.start[nt][w][0], q.start[nt][w][1], q.start[nt][w][0], q.start[nt][w][1]};
-        mma_f16(acc, r0 & 0x000f000fu, r1 & 0x000f000fu, r0 & 0x00f000f0u, r1 & 0x00f000f0u, q.b[nt][w][0][0], q.b[nt][w][0][1]);
-        mma_f16(acc, r0h & 0x000f000fu, r1h & 0x000f000fu, r0h & 0x00f000f0u, r1h & 0x00f000f0u, q.b[nt][w][1][0],
-                q.b[nt][w][1][1]);
-        x[nt][0] = fmaf(acc[0], s0, x[nt][0]);
-        x[nt][1] = fmaf(acc[1], s0, x[nt][1]);
-        x[nt][2] = fmaf(acc[2], s1, x[nt][2]);
-        x[nt][3] = fmaf(acc[3], s1, x[nt][3]);
-      }
-    }
-    // log2 of the largest value scale of the lane's two keys
-    auto log_scale = [](const uint2& v) {
-      const uint32_t m = __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu);
-      return fmaxf(lg2_approx(__uint_as_float(max(m << 16, m & 0xffff0000u))), kLeastScale);
+          for (int i = 0; i < 4; ++i) p[c][nt][i] = ex2_approx(x[c][nt][i] - ref[nt][i & 1]);
     };
-    const float g0 = log_scale(vs0), g1 = log_scale(vs1);
-    bool grows = false;
+    weigh();
+    // Whether the lane's largest weight times its largest value scale (scales are not negative) is small enough. NaN is not.
+    auto larger = [](uint32_t a, uint32_t b) { return __vmaxu2(a, b); };
+    uint32_t m = larger(larger(vs[0][0].x, vs[0][0].y), larger(vs[0][1].x, vs[0][1].y));
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
+    for (int c = 1; c < kCount; ++c) m = larger(m, larger(larger(vs[c][0].x, vs[c][0].y), larger(vs[c][1].x, vs[c][1].y)));
+    float top_p = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[nt][i] = (i < 2 ? see0 : see1) ? x[nt][i] * q.unit[nt][i & 1] : -INFINITY;
-        grows |= x[nt][i] + (i < 2 ? g0 : g1) > ref[nt][i & 1] + kHigh;
-      }
-    }
-    if (__any_sync(0xffffffffu, grows)) {
+    for (int c = 0; c < kCount; ++c)
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) top_p = max3_nan(max3_nan(top_p, p[c][nt][0], p[c][nt][1]), p[c][nt][2], p[c][nt][3]);
+    const bool fits = top_p * max3_f32(bf_lo(m), bf_hi(m), kLeastScale) <= kMost;
+    if (!__all_sync(0xffffffffu, fits)) {
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float top = fmaxf(x[nt][h] + g0, x[nt][h + 2] + g1);
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kCount; ++c)
+            top = max3_f32(top, x[c][nt][h] + log_scale(vs[c][0]), x[c][nt][h + 2] + log_scale(vs[c][1]));
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-          if (top > ref[nt][h] + kHigh) {
+          if (top > ref[nt][h] + kRaise) {
             const float a = ex2_approx(ref[nt][h] - (top - kStart));
             ref[nt][h] = top - kStart;
             sum[nt][h] *= a;
@@ -277,51 +353,141 @@ struct State {
             }
           }
         }
-    }
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[nt][i] = ex2_approx(x[nt][i] - ref[nt][i & 1]);
-      sum[nt][0] += x[nt][0] + x[nt][2];
-      sum[nt][1] += x[nt][1] + x[nt][3];
+      weigh();
     }
 
-    const uint8_t* vr = va + 2 * t * kKv4RowBytes + 8 * g;
-    const uint2 v0 = *reinterpret_cast<const uint2*>(vr);
-    const uint2 v1 = *reinterpret_cast<const uint2*>(vr + kKv4RowBytes);
-    const uint2 v2 = *reinterpret_cast<const uint2*>(vr + 8 * kKv4RowBytes);
-    const uint2 v3 = *reinterpret_cast<const uint2*>(vr + 9 * kKv4RowBytes);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const uint32_t sel = (w & 1) ? 0x7632u : 0x5410u;
-      const uint32_t a = __byte_perm(w < 2 ? v0.x : v0.y, w < 2 ? v1.x : v1.y, sel);
-      const uint32_t b = __byte_perm(w < 2 ? v2.x : v2.y, w < 2 ? v3.x : v3.y, sel);
-      const uint32_t ah = a >> 8, bh = b >> 8;
-      const uint32_t c0 = code_lo(a), c1 = code_hi(a), c2 = code_lo(b), c3 = code_hi(b);
-      const uint32_t d0 = code_lo(ah), d1 = code_hi(ah), d2 = code_lo(bh), d3 = code_hi(bh);
-      const float s0 = (w & 1) ? bf_hi(w < 2 ? vs0.x : vs0.y) : bf_lo(w < 2 ? vs0.x : vs0.y);
-      const float s1 = (w & 1) ? bf_hi(w < 2 ? vs1.x : vs1.y) : bf_lo(w < 2 ? vs1.x : vs1.y);
+    for (int c = 0; c < kCount; ++c) {
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
-        const uint32_t p0 = transpose8(half2_bits(x[nt][0] * s0, x[nt][1] * s0));
-        const uint32_t p1 = transpose8(half2_bits(x[nt][2] * s1, x[nt][3] * s1));
-        mma_f16(o[nt][2 * w], c0, c1, c2, c3, p0, p1);
-        mma_f16(o[nt][2 * w + 1], d0, d1, d2, d3, p0, p1);
+        sum[nt][0] += p[c][nt][0] + p[c][nt][2];
+        sum[nt][1] += p[c][nt][1] + p[c][nt][3];
       }
+      const uint8_t* vr = at + c * kKv4Block + kKv4Values + 2 * t * kKv4RowBytes + 8 * g;
+      const uint2 v0 = *reinterpret_cast<const uint2*>(vr);
+      const uint2 v1 = *reinterpret_cast<const uint2*>(vr + kKv4RowBytes);
+      const uint2 v2 = *reinterpret_cast<const uint2*>(vr + 8 * kKv4RowBytes);
+      const uint2 v3 = *reinterpret_cast<const uint2*>(vr + 9 * kKv4RowBytes);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t sel = (w & 1) ? 0x7632u : 0x5410u;
+        const uint32_t a = __byte_perm(w < 2 ? v0.x : v0.y, w < 2 ? v1.x : v1.y, sel);
+        const uint32_t b = __byte_perm(w < 2 ? v2.x : v2.y, w < 2 ? v3.x : v3.y, sel);
+        const uint32_t ah = a >> 8, bh = b >> 8;
+        auto low = [&](uint32_t v) { return sub2(and_or<0x000f000fu>(v, q.exp_low), 0x64086408u); };
+        auto high = [&](uint32_t v) { return sub2(and_or<0x00f000f0u>(v, q.exp_high), 0x54805480u); };
+        const uint32_t c0 = low(a), c1 = high(a), c2 = low(b), c3 = high(b), d0 = low(ah), d1 = high(ah), d2 = low(bh), d3 = high(bh);
+        const float s0 = (w & 1) ? bf_hi(w < 2 ? vs[c][0].x : vs[c][0].y) : bf_lo(w < 2 ? vs[c][0].x : vs[c][0].y);
+        const float s1 = (w & 1) ? bf_hi(w < 2 ? vs[c][1].x : vs[c][1].y) : bf_lo(w < 2 ? vs[c][1].x : vs[c][1].y);
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          const uint32_t p0 = transpose8(half2_bits(p[c][nt][0] * s0, p[c][nt][1] * s0));
+          const uint32_t p1 = transpose8(half2_bits(p[c][nt][2] * s1, p[c][nt][3] * s1));
+          mma_f16(o[nt][2 * w], c0, c1, c2, c3, p0, p1, o[nt][2 * w]);
+          mma_f16(o[nt][2 * w + 1], d0, d1, d2, d3, p0, p1, o[nt][2 * w + 1]);
+        }
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ int atom_add_acq_rel(int32_t* p, int v) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
+
+// What a warp has joined of the parts of four heads, first .. first + 3: lane (x, y), y the lowest two bits, holds the running
+// reference and sum of head first + y; each lane four dimensions of all four.
+struct Joined {
+  float ref, sum;
+  float4 o[4];
+  __device__ __forceinline__ void clear() {
+    ref = -FLT_MAX;
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  // n <= kMost parts: references of the four heads at `refs` (`step` floats from one part to the next; they are overwritten),
+  // sums at `sums`, this lane's dimensions of the outputs at `outs` (o_step to the next part's, head_step to the next head's).
+  // Every head's factors are found at once, the lanes sharing the parts: one head after the other, with all parts to a lane,
+  // joining 8 warps' 16 heads took 10000 cycles.
+  template <int kMost>
+  __device__ __forceinline__ void add(float* refs, const float* sums, int step, int n, const float* outs, int o_step, int head_step,
+                                      int lane) {
+    constexpr int kPer = (kMost + 7) / 8;
+    const int x = lane >> 2, y = lane & 3;
+    float m[kPer], l[kPer];
+    float top = ref;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const bool in = x + 8 * i < n;
+      m[i] = in ? refs[(x + 8 * i) * step + y] : -INFINITY;
+      l[i] = in ? sums[(x + 8 * i) * step + y] : 0.0f;
+      top = fmaxf(top, m[i]);
+    }
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    float more = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const float a = ex2_approx(m[i] - top);
+      more = fmaf(l[i], a, more);
+      if (x + 8 * i < n) refs[(x + 8 * i) * step + y] = a;
+    }
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) more += __shfl_xor_sync(0xffffffffu, more, d);
+    const float old = ex2_approx(ref - top);
+    sum = fmaf(sum, old, more);
+    ref = top;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = __shfl_sync(0xffffffffu, old, k);
+      o[k] = make_float4(o[k].x * f, o[k].y * f, o[k].z * f, o[k].w * f);
+    }
+#pragma unroll 4
+    for (int u = 0; u < n; ++u) {
+      const float4 a4 = *reinterpret_cast<const float4*>(refs + u * step);
+      const float a[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(outs + u * o_step + k * head_step);
+        o[k] = make_float4(fmaf(v.x, a[k], o[k].x), fmaf(v.y, a[k], o[k].y), fmaf(v.z, a[k], o[k].z), fmaf(v.w, a[k], o[k].w));
+      }
+    }
+    __syncwarp();
+  }
+  // out: this lane's dimensions of the group's first head
+  __device__ __forceinline__ void store(uint16_t* out, int first, int G) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int head = first + k;
+      const float l = __shfl_sync(0xffffffffu, sum, k);
+      if (head >= G) continue;
+      const __nv_bfloat162 a = __floats2bfloat162_rn(__fdividef(o[k].x, l), __fdividef(o[k].y, l));
+      const __nv_bfloat162 b = __floats2bfloat162_rn(__fdividef(o[k].z, l), __fdividef(o[k].w, l));
+      *reinterpret_cast<uint2*>(out + head * kD) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
     }
   }
 };
 
 template <int kNT>
 __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p) {
-  using S = Smem<kNT>;
+  using S = Split<kNT>;
   constexpr int kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   float* join = reinterpret_cast<float*>(smem + S::kJoin);
   float* refs = reinterpret_cast<float*>(smem + S::kRef);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBars);
   uint64_t* empty = full + kStages;
+  uint64_t* q_full = empty + kStages;  // [2] queries of a piece
+  uint64_t* q_empty = q_full + 2;      // [2]
+  uint64_t* h_full = q_empty + 2;      // a piece handed over
+  uint64_t* h_empty = h_full + 1;
+  uint64_t* m_full = h_empty + 1;      // partials of a cut segment
   uint32_t* bad_chunks = reinterpret_cast<uint32_t*>(smem + S::kBad);
+  int* last_tile = reinterpret_cast<int*>(bad_chunks + kStages);
   int* misc = reinterpret_cast<int*>(smem + S::kMisc);
   int* pre = reinterpret_cast<int*>(smem + S::kPre);
   int* lens = reinterpret_cast<int*>(smem + S::kLens);
@@ -330,53 +496,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kWarps);
+      mbar_init(&empty[s], S::kUnits);
+      last_tile[s] = -1;
     }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&q_full[b], 1);
+      mbar_init(&q_empty[b], kWarps);
+    }
+    mbar_init(h_full, kWarps);
+    mbar_init(h_empty, 2);
+    mbar_init(m_full, 1);
     fence_mbar_init();
-  }
-  // ---- tiles of the sequences before, by the working warps, at most 8 sequences a thread
-  const int per = (p.B + kWork - 1) / kWork;
-  const int i0 = tid * per;
-  const int i1 = warp < kWarps ? min(p.B, i0 + per) : 0;
-  pdl_wait_predecessor();
-  pdl_allow_successor();
-  if (warp < kWarps) {
-    int sum = 0;
-    bool bad = false;
-    for (int i = i0; i < i1; ++i) {
-      const int len = p.seq_lens[i];
-      bad |= len < 0 || len > p.L_cap;
-      lens[i] = len;
-      sum += span_of(len, p.L_cap, p.kv).nt;
-    }
-    if (bad) raise_status(p.status, kStatusBadSeqLen);
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += n;
-    }
-    if (lane == 31) misc[warp] = incl;
-    named_bar_sync(1, kWork);
-    int run = incl - sum;
-    for (int w = 0; w < warp; ++w) run += misc[w];
-    if (tid == kWork - 1) pre[p.B] = run + sum;
-    for (int i = i0; i < i1; ++i) {
-      pre[i] = run;
-      run += span_of(lens[i], p.L_cap, p.kv).nt;
-    }
   }
   __syncthreads();
 
-  // The first min(tiles, CTAs) CTAs share the tiles, each at least one (tile counts fit 32 bits: the host checks).
-  const int total = p.h_kv * pre[p.B];
+  // The first NC CTAs share the tiles: as many as there are with kTiles tiles each, which a CTA works on together (tile counts
+  // fit 32 bits: the host checks).
   const int grid = gridDim.x, cta = blockIdx.x;
-  const int NC = min(total, grid);
-  const int q_tiles = NC > 0 ? total / NC : 0;
-  const int rm = NC > 0 ? total - q_tiles * NC : 0;
+  int q_tiles = 0, rm = 0, beg = 0, end = 0;
   auto range_start = [&](int c) { return c * q_tiles + min(c, rm); };
-  const int beg = cta < NC ? range_start(cta) : 0;
-  const int end = cta < NC ? range_start(cta + 1) : 0;
+  auto find_range = [&]() {
+    const int total = p.h_kv * pre[p.B];
+    const int NC = min((total + S::kTiles - 1) / S::kTiles, grid);
+    if (NC == 0) return;
+    q_tiles = total / NC;
+    rm = total - q_tiles * NC;
+    if (cta >= NC) return;
+    beg = range_start(cta);
+    end = range_start(cta + 1);
+  };
 
   // The piece of the range that starts at tile x: sequence b, key/value head j, first tile tl of the segment's nt, n tiles
   // here, the segment's first tile in the list.
@@ -411,227 +559,322 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
     r.n = min(end - x, r.nt);
     return r;
   };
-
-  if (warp == kWarps) {
-    // =========================== loads ===========================
-    // Lane lp brings the run of chunks lp of a tile: a page's rows, at most a tile's; 16 keys where sink keys are folded in.
-    // The next tile's table entry is read while this one's stage is waited for.
-    const uint64_t policy = l2_policy_evict_first();
-    const int page = 1 << p.kv.page_shift;
-    const int rows = min(page, kKeys);
-    int it = 0;
-    bool ok = true;
-    // the run's page in tile t of sequence b: -2 nothing to load, -1 a bad entry (reads as zeros)
-    auto entry = [&](const DecodeSpan& sp, int b, int t) {
-      const int n = t == 0 && sp.fold > 0 ? kFold : rows;
-      const int key = sp.key_of(t, lane * n);
-      if (lane * n >= kKeys || !sp.sees_any(key, n)) return -2;
-      const int id = p.kv.block_table[static_cast<int64_t>(b) * p.kv.max_pages + (key >> p.kv.page_shift)];
-      return static_cast<uint32_t>(id) < static_cast<uint32_t>(p.kv.num_pages) ? id : -1;
-    };
-    Piece pc{}, np{};
-    DecodeSpan sp{}, nsp{};
-    int id = -2;
-    if (beg < end) {
-      np = locate(beg);
-      nsp = span_of(lens[np.b], p.L_cap, p.kv);
-      id = entry(nsp, np.b, np.tl);
+  bool ok = true;  // no wait of this warp has run out (the same for all its lanes); then it waits for nothing more
+  auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
+    if (!__all_sync(0xffffffffu, ok && mbar_wait(bar, parity))) {
+      if (ok && lane == 0) atomicExch(p.status, code);
+      ok = false;
     }
-    const int stop = p.give_up_tile < 0 ? end : beg + min(end - beg, p.give_up_tile);
-    for (int x = beg; x < stop && ok;) {
-      pc = np;
-      sp = nsp;
-      const bool more = x + pc.n < end;
-      if (more) {
-        np = after(pc, x + pc.n);
-        if (np.b != pc.b) nsp = span_of(lens[np.b], p.L_cap, p.kv);
+  };
+
+  if (warp < 4) {
+    reg_dealloc<kRegsHelp>();
+    // ---- tiles of the sequences before
+    pdl_wait_predecessor();
+    pdl_allow_successor();
+    const int per = (p.B + 127) / 128;
+    const int i0 = tid * per, i1 = min(p.B, i0 + per);
+    int sum = 0;
+    bool bad_len = false;
+    for (int i = i0; i < i1; ++i) {
+      const int len = p.seq_lens[i];
+      bad_len |= len < 0 || len > p.L_cap;
+      lens[i] = len;
+      sum += span_of(len, p.L_cap, p.kv).nt;
+    }
+    if (bad_len) raise_status(p.status, kStatusBadSeqLen);
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += n;
+    }
+    if (lane == 31) misc[warp] = incl;
+    named_bar_sync(3, 128);
+    int run = incl - sum;
+    for (int w = 0; w < warp; ++w) run += misc[w];
+    if (tid == 127) pre[p.B] = run + sum;
+    for (int i = i0; i < i1; ++i) {
+      pre[i] = run;
+      run += span_of(lens[i], p.L_cap, p.kv).nt;
+    }
+    named_bar_sync(3, 128);
+    named_bar_arrive(4, kThreads);  // the working warps may look at it
+    find_range();
+    if (warp < 2) {
+      // =========================== loads ===========================
+      // The two warps take four tiles in turn: lane 8 i + r finds tile i and its run r of chunks (a page's rows, at most a tile's; 16 keys
+      // where sink keys are folded in), reads that page's table entry four tiles early, and issues the copy when the tile's
+      // stage is free. One tile after the other, the chain of searches and loads took this warp 1300 cycles a tile, twice
+      // the memory's time.
+      const uint64_t policy = l2_policy_evict_first();
+      const int page = 1 << p.kv.page_shift;
+      struct Run {
+        int64_t block;   // the first chunk's place in the cache, without the page's
+        int id, chunks;  // the page's table entry; 0 chunks: nothing to load
+      };
+      auto run_at = [&](int i0) {
+        Run r{0, 0, 0};
+        const int x = beg + i0 + (lane >> 3);
+        if (x >= end) return r;
+        const Piece pc = locate(x);
+        const DecodeSpan sp = span_of(lens[pc.b], p.L_cap, p.kv);
+        const int n = pc.tl == 0 && sp.fold > 0 ? kFold : min(page, kKeys);
+        const int row = (lane & 7) * n;
+        const int key = sp.key_of(pc.tl, row);
+        if (row >= kKeys || !sp.sees_any(key, n)) return r;
+        r.id = __ldg(p.kv.block_table + static_cast<int64_t>(pc.b) * p.kv.max_pages + (key >> p.kv.page_shift));
+        r.block = (static_cast<int64_t>(pc.j) << (p.kv.page_shift - 4)) + ((key & (page - 1)) / kChunk);
+        r.chunks = n / kChunk;
+        return r;
+      };
+      const int stop = (p.give_up_tile < 0 ? end : beg + min(end - beg, p.give_up_tile)) - beg;
+      Run next = run_at(4 * warp);
+      for (int i0 = 4 * warp; i0 < stop && ok; i0 += 8) {
+        const Run run = next;
+        next = run_at(i0 + 8);
+        const bool mine = run.chunks > 0;
+        const bool there = mine && static_cast<uint32_t>(run.id) < static_cast<uint32_t>(p.kv.num_pages);
+        const uint8_t* src = p.cache + ((static_cast<int64_t>(run.id) * p.h_kv << (p.kv.page_shift - 4)) + run.block) * kKv4Block;
+        const uint32_t bytes = static_cast<uint32_t>(run.chunks * kKv4Block);
+        // the tile's bytes, and its chunks that read as zeros
+        uint32_t all = there ? bytes : 0, bad = mine && !there ? ((1u << run.chunks) - 1) << ((lane & 7) * run.chunks) : 0;
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) {
+          all += __shfl_xor_sync(0xffffffffu, all, d);
+          bad |= __shfl_xor_sync(0xffffffffu, bad, d);
+        }
+        if (mine && !there && i0 + (lane >> 3) < stop) raise_status(p.status, kStatusBadPage);
+        for (int it = i0; it < min(i0 + 4, stop); ++it) {
+          const int st = it % kStages;
+          wait(&empty[st], static_cast<uint32_t>(((it / kStages) & 1) ^ 1), kStatusWaitEmptyTimeout);
+          if (!ok) break;
+          if (lane == 8 * (it - i0)) {
+            bad_chunks[st] = bad;
+            last_tile[st] = it;
+            mbar_arrive_expect_tx(&full[st], all);
+          }
+          __syncwarp();
+          if (lane >> 3 == it - i0 && there)
+            bulk_load(smem + st * kStageBytes + (lane & 7) * bytes, src, bytes, &full[st], policy);
+        }
       }
-      for (int t = pc.tl; t < pc.tl + pc.n; ++t, ++it) {
-        const int next = t + 1 < pc.tl + pc.n ? entry(sp, pc.b, t + 1) : (more ? entry(nsp, np.b, 0) : -2);
-        const int st = it % kStages;
-        ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], static_cast<uint32_t>(((it / kStages) & 1) ^ 1)));
-        if (!ok) break;
-        const int n = t == 0 && sp.fold > 0 ? kFold : rows;
-        const int chunks = n / kChunk;
-        const uint32_t loads = __popc(__ballot_sync(0xffffffffu, id >= 0));
-        const uint32_t bad = __ballot_sync(0xffffffffu, id == -1);
-        if (lane == 0) {
-          uint32_t mask = 0;
-          for (int r = 0; r < kChunks / chunks; ++r)
-            if (bad >> r & 1) mask |= ((1u << chunks) - 1) << (r * chunks);
-          bad_chunks[st] = mask;
-          mbar_arrive_expect_tx(&full[st], loads * static_cast<uint32_t>(chunks * kKv4Block));
+      // no copy may outlive its CTA: the last of each stage
+      named_bar_sync(2, 64);
+      if (tid == 0) {
+        if (stop < end - beg) atomicExch(p.status, kStatusWaitEmptyTimeout);
+        for (int st = 0; st < kStages; ++st)
+          if (last_tile[st] >= 0 && !mbar_wait(&full[st], static_cast<uint32_t>((last_tile[st] / kStages) & 1))) {
+            atomicExch(p.status, kStatusDrainTimeout);
+            break;
+          }
+      }
+      __syncwarp();
+    } else {
+      // =========================== queries, pieces finished ===========================
+      // Two warps. The first also prepares the queries, two pieces ahead. Of a piece a warp takes every other head, a lane four
+      // dimensions of it.
+      const int half = warp - 2;
+      const int d4 = 4 * lane;
+      struct Ahead {
+        Piece pc;
+        int x, pi;
+      } ahead{};
+      ahead.x = beg;
+      auto prepare_next = [&]() {
+        if (half != 0 || ahead.x >= end) return;
+        ahead.pc = ahead.pi == 0 ? locate(beg) : after(ahead.pc, ahead.x);
+        const int slot = ahead.pi & 1;
+        wait(&q_empty[slot], ((ahead.pi >> 1) & 1) ^ 1, kStatusWaitEmptyTimeout);
+        Queries<kNT>::prepare(smem + S::kQ + slot * S::kQBytes,
+                              p.q + (static_cast<int64_t>(ahead.pc.b) * p.h_q + static_cast<int64_t>(ahead.pc.j) * p.G) * kD, p.G,
+                              p.scale_log2, lane);
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(&q_full[slot]);
+        ahead.x += ahead.pc.n;
+        ++ahead.pi;
+      };
+      prepare_next();
+      prepare_next();
+      int pi = 0;
+      uint32_t merges = 0, copied = ~0u;  // batches joined, the last whose copies this warp issued
+      Piece pc{};
+      for (int x = beg; x < end; x += pc.n, ++pi) {
+        pc = x == beg ? locate(x) : after(pc, x);
+        wait(h_full, pi & 1, kStatusWaitFullTimeout);
+        const bool whole = pc.tl == 0 && pc.n == pc.nt;
+        uint16_t* out = p.out + (static_cast<int64_t>(pc.b) * p.h_q + static_cast<int64_t>(pc.j) * p.G) * kD + d4;
+        float* mine = p.partials + (static_cast<int64_t>(cta) * 2 + (pi == 0 ? 0 : 1)) * kGqaSlotFloats;
+        Joined all;
+        // the warps' parts
+        for (int h = 4 * half; h < p.G; h += 8) {
+          float* r = refs + h;
+          all.clear();
+          all.add<kWarps>(r, r + kWarps * 16, 16, kWarps, join + h * kRow + d4, 8 * kNT * kRow, kRow, lane);
+          if (whole) {
+            all.store(out, h, p.G);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (h + k < p.G) *reinterpret_cast<float4*>(mine + 32 + (h + k) * kD + d4) = all.o[k];
+            if (lane < 4) {
+              mine[h + lane] = all.ref;
+              mine[16 + h + lane] = all.sum;
+            }
+          }
+        }
+        if (!whole) {
+          // A segment cut between CTAs: the last to publish its piece joins them all, in CTA order. Their partials (references
+          // and sums of 16 heads, then the heads' outputs) come with bulk copies into the hand-over buffer, as many as fit it
+          // at once: with loads into registers a warp had a few of them under way, and 20 pieces took 8 us.
+          fence_proxy_async_all();  // (they are read with copies)
+          auto cta_of = [&](int i) {
+            const int big = rm * (q_tiles + 1);
+            return i < big ? i / (q_tiles + 1) : rm + (i - big) / q_tiles;
+          };
+          const int c_first = cta_of(pc.seg0), c_last = cta_of(pc.seg0 + pc.nt - 1);
+          named_bar_sync(1, 64);
+          if (tid == 64) {
+            // publishes what the barrier gathered (cumulativity), and sees what those before published
+            const bool last = atom_add_acq_rel(&p.counters[c_first], 1) == c_last - c_first;
+            if (last) p.counters[c_first] = 0;
+            misc[16] = last;
+          }
+          __syncwarp();
+          named_bar_sync(1, 64);
+          if (misc[16]) {
+            const int part = 32 + kD * p.G;  // floats
+            for (int h0 = 0; h0 < p.G; h0 += 8) {  // (both warps take every turn: they meet in it)
+              const int h = h0 + 4 * half;
+              all.clear();
+              for (int c0 = c_first; c0 <= c_last; c0 += S::kMost) {
+                const int n = min(S::kMost, c_last + 1 - c0);
+                if (h0 == 0 || c_last - c_first >= S::kMost) {  // (else they are there already)
+                  // what was read and written there plainly comes before the copies
+                  fence_proxy_async_all();
+                  named_bar_sync(1, 64);
+                  if (half == 0 && ok) {
+                    if (lane == 0) mbar_arrive_expect_tx(m_full, static_cast<uint32_t>(n * part) * 4u);
+                    __syncwarp();
+                    if (lane < n) {
+                      const int c = c0 + lane;
+                      bulk_load(join + lane * part,
+                                p.partials + (static_cast<int64_t>(c) * 2 + (range_start(c) >= pc.seg0 ? 0 : 1)) * kGqaSlotFloats,
+                                static_cast<uint32_t>(part) * 4u, m_full, l2_policy_evict_first());
+                    }
+                    copied = merges;
+                  }
+                  wait(m_full, merges & 1, kStatusWaitFullTimeout);
+                  ++merges;
+                }
+                if (h < p.G) all.add<S::kMost>(join + h, join + 16 + h, part, n, join + 32 + h * kD + d4, part, kD, lane);
+              }
+              if (h < p.G) all.store(out, h, p.G);
+            }
+          }
+          named_bar_sync(1, 64);  // misc[16] is written again by the next cut piece, the buffer by the next piece
         }
         __syncwarp();
-        if (id >= 0) {
-          const int key = sp.key_of(t, lane * n);
-          const int64_t block = ((static_cast<int64_t>(id) * p.h_kv + pc.j) << (p.kv.page_shift - 4)) + ((key & (page - 1)) / kChunk);
-          bulk_load(smem + st * kStageBytes + lane * chunks * kKv4Block, p.cache + block * kKv4Block,
-                    static_cast<uint32_t>(chunks * kKv4Block), &full[st], policy);
-        } else if (id == -1) {
-          raise_status(p.status, kStatusBadPage);
-        }
-        id = next;
+        if (lane == 0) mbar_arrive(h_empty);
+        prepare_next();
       }
-      x += pc.n;
-    }
-    if (lane == 0) {
-      if (!ok || stop < end) atomicExch(p.status, kStatusWaitEmptyTimeout);
-      // no copy may outlive its CTA
-      const int n = min(it, kStages);
-      for (int i = it - n; i < it; ++i)
-        if (!mbar_wait(&full[i % kStages], static_cast<uint32_t>((i / kStages) & 1))) {
-          atomicExch(p.status, kStatusDrainTimeout);
-          break;
-        }
-    }
-    __syncwarp();
-    return;
-  }
-
-  // =========================== work ===========================
-  const int g = lane >> 2, t4 = lane & 3;
-  Queries<kNT> q;
-  State<kNT> s;
-  bool ok = true;
-  int it = 0, turn = 0;
-  Piece pc{};
-  for (int x = beg; x < end; turn ^= 1) {
-    pc = x == beg ? locate(x) : after(pc, x);
-    const DecodeSpan sp = span_of(lens[pc.b], p.L_cap, p.kv);
-    q.load(p.q + (static_cast<int64_t>(pc.b) * p.h_q + static_cast<int64_t>(pc.j) * p.G) * kD, p.G, p.scale_log2, lane);
-    s.clear();
-    for (int t = pc.tl; t < pc.tl + pc.n; ++t, ++it) {
-      const int st = it % kStages;
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[st], static_cast<uint32_t>((it / kStages) & 1)));
-      if (!ok) {
-        if (lane == 0) atomicExch(p.status, kStatusWaitFullTimeout);
-        break;
+      if (!ok && copied != ~0u && !mbar_wait(m_full, copied & 1) && lane == 0) atomicExch(p.status, kStatusDrainTimeout);
+      // ---- sequences with no keys (or a bad length) attend to nothing: output 0
+      for (int b = cta; b < p.B; b += grid) {
+        if (pre[b + 1] != pre[b]) continue;
+        uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(b) * p.h_q * kD);
+        for (int i = tid - 64; i < p.h_q * kD / 8; i += 64) o[i] = make_uint4(0u, 0u, 0u, 0u);
       }
-      const int key = sp.key_of(t, warp * kChunk);
-      if (sp.sees_any(key, kChunk))
-        s.add(q, smem + st * kStageBytes + warp * kKv4Block, sp.sees(key + g), sp.sees(key + g + 8), bad_chunks[st] >> warp & 1,
-              lane);
+    }
+  } else {
+    // =========================== work ===========================
+    // Warp (i, c) takes unit c of tiles i, i + kTiles, ... of the CTA's list, whatever piece they belong to; a piece's part is
+    // handed over when the next one begins, and nothing is waited for but the hand-over buffer.
+    reg_alloc<kRegsWork>();
+    named_bar_sync(4, kThreads);
+    find_range();
+    const int w = warp - 4;
+    const int g = lane >> 2, t4 = lane & 3;
+    const int c0 = w % S::kUnits * S::kUnit;
+    Queries<kNT> q;
+    State<kNT> s;
+    Piece pc{};
+    int it = w / S::kUnits, pi = 0;
+    for (int x = beg; x < end; x += pc.n, ++pi) {
+      pc = x == beg ? locate(x) : after(pc, x);
+      const int slot = pi & 1;
+      const int first = x - beg;  // the piece's first tile in this CTA's count
+      wait(&q_full[slot], (pi >> 1) & 1, kStatusWaitFullTimeout);
+      const bool any = it < first + pc.n;
+      if (any) q.load(smem + S::kQ + slot * S::kQBytes, lane);
+      s.clear();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
-    }
-
-    // ---- the warps' states joined: references first, then outputs on a common one
-    float* my_ref = refs + turn * 2 * kWarps * 16;
-    float* my_sum = my_ref + kWarps * 16;
+      if (lane == 0) mbar_arrive(&q_empty[slot]);
+      if (any) {
+        const DecodeSpan sp = span_of(lens[pc.b], p.L_cap, p.kv);
+        // the tiles whose keys the query sees all (a folded one is not among them)
+        const int from = max(pc.tl, (sp.lo + kKeys - 1) / kKeys - sp.w0 + sp.ns) - pc.tl + first;
+        const int to = min(pc.tl + pc.n, sp.len / kKeys - sp.w0 + sp.ns) - pc.tl + first;
+        for (; it < first + pc.n; it += S::kTiles) {
+          const int st = it % kStages;
+          wait(&full[st], static_cast<uint32_t>((it / kStages) & 1), kStatusWaitFullTimeout);
+          if (!ok) break;
+          uint8_t* at = smem + st * kStageBytes + c0 * kKv4Block;
+          const uint32_t bad = bad_chunks[st];
+          float bias[S::kUnit][2] = {};
+          bool none = false;
+          if (it < from || it >= to || bad != 0) {
+            // some keys are not seen, or read as zeros: their scales become 0 (what stands there may be NaN)
+            none = true;
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
+            for (int c = 0; c < S::kUnit; ++c) {
+              const int key = sp.key_of(pc.tl + it - first, (c0 + c) * kChunk);
+              const bool zero = bad >> (c0 + c) & 1;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float v = s.sum[nt][h];
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-        if (g == 0) {
-          my_ref[warp * 16 + 8 * nt + 2 * t4 + h] = s.ref[nt][h];
-          my_sum[warp * 16 + 8 * nt + 2 * t4 + h] = v;
-        }
-      }
-    named_bar_sync(1, kWork);
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int head = 8 * nt + 2 * t4 + h;
-        float top = my_ref[head];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, my_ref[w * 16 + head]);
-        const float a = ex2_approx(s.ref[nt][h] - top);
-        float* to = join + (warp * 8 * kNT + head) * kRow + 4 * g;
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          *reinterpret_cast<float4*>(to + 32 * w) = make_float4(s.o[nt][2 * w][h] * a, s.o[nt][2 * w][h + 2] * a,
-                                                                s.o[nt][2 * w + 1][h] * a, s.o[nt][2 * w + 1][h + 2] * a);
-      }
-    named_bar_sync(1, kWork);
-
-    // ---- thread: four dimensions of a head (of two, with 16)
-    const bool whole = pc.tl == 0 && pc.n == pc.nt;
-    const int d4 = 4 * (tid & 31);
-    uint16_t* out = p.out + (static_cast<int64_t>(pc.b) * p.h_q + static_cast<int64_t>(pc.j) * p.G) * kD + d4;
-    auto store = [&](int head, const float4& o, float l) {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(__fdividef(o.x, l), __fdividef(o.y, l));
-      const __nv_bfloat162 b = __floats2bfloat162_rn(__fdividef(o.z, l), __fdividef(o.w, l));
-      *reinterpret_cast<uint2*>(out + head * kD) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    };
-    const int slot = x == beg ? 0 : 1;
-    float* mine = p.partials + (static_cast<int64_t>(cta) * 2 + slot) * kGqaSlotFloats;
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      const int head = 8 * nt + warp;
-      if (head >= p.G) continue;
-      float top = my_ref[head];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, my_ref[w * 16 + head]);
-      float l = 0.0f;
-      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        l += my_sum[w * 16 + head] * ex2_approx(my_ref[w * 16 + head] - top);
-        const float4 v = *reinterpret_cast<const float4*>(join + (w * 8 * kNT + head) * kRow + d4);
-        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
-      }
-      if (whole) {
-        store(head, o, l);
-      } else {
-        *reinterpret_cast<float4*>(mine + head * kD + d4) = o;
-        if (lane == 0) {
-          mine[16 * kD + head] = top;
-          mine[16 * kD + 16 + head] = l;
-        }
-      }
-    }
-    if (!whole) {
-      // a segment cut between CTAs: the last to publish its piece joins them all, in CTA order
-      auto cta_of = [&](int i) {
-        const int big = rm * (q_tiles + 1);
-        return i < big ? i / (q_tiles + 1) : rm + (i - big) / q_tiles;
-      };
-      const int c_first = cta_of(pc.seg0), c_last = cta_of(pc.seg0 + pc.nt - 1);
-      named_bar_sync(1, kWork);
-      if (tid == 0) {
-        __threadfence();  // publishes what the barrier gathered
-        const bool last = atomicAdd(&p.counters[c_first], 1) == c_last - c_first;
-        if (last) p.counters[c_first] = 0;
-        misc[8] = last;
-      }
-      named_bar_sync(1, kWork);
-      if (misc[8]) {
-        __threadfence();
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          const int head = 8 * nt + warp;
-          if (head >= p.G) continue;
-          float top = -FLT_MAX, l = 0.0f;
-          float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int c = c_first; c <= c_last; ++c) {
-            const float* src = p.partials + (static_cast<int64_t>(c) * 2 + (range_start(c) >= pc.seg0 ? 0 : 1)) * kGqaSlotFloats;
-            const float m = __ldcg(src + 16 * kD + head), lc = __ldcg(src + 16 * kD + 16 + head);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + head * kD + d4));
-            const float now = fmaxf(top, m);
-            const float a = ex2_approx(top - now), b = ex2_approx(m - now);
-            o = make_float4(o.x * a + v.x * b, o.y * a + v.y * b, o.z * a + v.z * b, o.w * a + v.w * b);
-            l = l * a + lc * b;
-            top = now;
+              for (int r = 0; r < 2; ++r) {
+                const bool see = sp.sees(key + g + 8 * r);
+                bias[c][r] = see ? 0.0f : -INFINITY;
+                none &= !see;
+                if (t4 < 2 && (zero || !see))
+                  *reinterpret_cast<uint2*>(at + c * kKv4Block + t4 * kKv4Values + kKv4Scales + 8 * (g + 8 * r)) = make_uint2(0u, 0u);
+              }
+            }
+            none = __all_sync(0xffffffffu, none);
+            fence_proxy_async_smem();
+            __syncwarp();
           }
-          store(head, o, l);
+          if (!none) s.add(q, at, bias, lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[st]);
         }
       }
-      named_bar_sync(1, kWork);  // misc[8] is written again by the next cut piece
+      // ---- hand over
+      wait(h_empty, (pi & 1) ^ 1, kStatusWaitEmptyTimeout);
+      if (ok) {
+        float* ref = refs + w * 16;
+        float* l_of = ref + kWarps * 16;
+        float* to_o = join + w * 8 * kNT * kRow + 4 * g;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int head = 8 * nt + 2 * t4 + h;
+            float v = s.sum[nt][h];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+            if (g == 0) {
+              ref[head] = s.ref[nt][h];
+              l_of[head] = v;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<float4*>(to_o + head * kRow + 32 * k) =
+                  make_float4(s.o[nt][2 * k][h], s.o[nt][2 * k][h + 2], s.o[nt][2 * k + 1][h], s.o[nt][2 * k + 1][h + 2]);
+          }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(h_full);
     }
-    x += pc.n;
-  }
-
-  // ---- sequences with no keys (or a bad length) attend to nothing: output 0
-  for (int b = cta; b < p.B; b += grid) {
-    if (pre[b + 1] != pre[b]) continue;
-    uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(b) * p.h_q * kD);
-    for (int i = tid; i < p.h_q * kD / 8; i += kWork) o[i] = make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -643,11 +886,15 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= kMaxDev || !done[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(kv4_decode_kernel<kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<kNT>::kBytes);
+    cudaFuncAttributes attr{};
+    e = cudaFuncGetAttributes(&attr, kv4_decode_kernel<kNT>);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the shares count on it
+    e = cudaFuncSetAttribute(kv4_decode_kernel<kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Split<kNT>::kBytes);
     if (e != cudaSuccess) return e;
     if (dev < kMaxDev) done[dev].store(true, std::memory_order_release);
   }
-  return launch_pdl(kv4_decode_kernel<kNT>, dim3(grid), dim3(kThreads), Smem<kNT>::kBytes, stream, p);
+  return launch_pdl(kv4_decode_kernel<kNT>, dim3(grid), dim3(kThreads), Split<kNT>::kBytes, stream, p);
 }
 
 }  // namespace kv4

@@ -108,24 +108,40 @@ class Kv4:
                 self.table[b, i] = -7 if i % 2 else 1 << 30
 
 
-def attend(q, k, v, see, scale):
-    """q [h_q, 128], k and v [L, h_kv, 128] in 64 bits, see [L] -> (output, sum of p |v|, largest p * |v|) in 64 bits."""
+def attend(q, k, v, see, scale, k_scales=None):
+    """q [h_q, 128], k and v [L, h_kv, 128] in 64 bits, see [L], k_scales [L, h_kv, 4] -> (output, sum of p |v|, largest
+    p * |v|, what the scores' fp32 sums may do) in 64 bits.
+
+    The last: a group's sum is of products n q of at most 15 |q| and its offset -8 sum(q), in fp32; two matrix instructions of
+    eight products a lane's pair each, the start, the scale, the sum over groups and the unit are 8 roundings or truncations of
+    at most 2^-23 of 15 sum|q| each, so a score is off by at most d = |scale| 15 2^-20 sum_w s_w sum_w|q|. A weight p changes
+    by p (exp(d) - 1) at most, e for short, the output then by (sum(e |v|) + |o| sum(e)) / (1 - sum(e)).
+    """
     h_q, d = q.shape
     L, h_kv, _ = k.shape
     if not bool(see.any()):
         z = torch.zeros(h_q, d, dtype=torch.float64, device=q.device)
-        return z, z.clone(), z.clone()
+        return z, z.clone(), z.clone(), z.clone()
     k, v = k[see].permute(1, 0, 2), v[see].permute(1, 0, 2)
-    p = torch.softmax(q.double().view(h_kv, -1, d) @ k.transpose(1, 2) * scale, -1)
+    qq = q.double().view(h_kv, -1, d)
+    p = torch.softmax(qq @ k.transpose(1, 2) * scale, -1)
     top = (p[..., None] * v.abs().amax(-1)[:, None, :, None]).amax(2).expand(-1, -1, d)
-    return (p @ v).reshape(h_q, d), (p @ v.abs()).reshape(h_q, d), top.reshape(h_q, d)
+    out = p @ v
+    slack = torch.zeros_like(out)
+    if k_scales is not None:
+        off = qq.abs().unflatten(-1, (4, 32)).sum(-1) @ k_scales[see].double().permute(1, 2, 0) * abs(scale) * 15 * 2.0 ** -20
+        e = p * off.clamp(max=700).expm1()
+        total = e.sum(-1, keepdim=True)
+        slack = (e @ v.abs() + out.abs() * total) / (1 - total)
+        slack = torch.where(total < 0.5, slack, torch.inf)  # scores of tens of thousands: fp32 does not settle the weights
+    return tuple(x.reshape(h_q, d) for x in (out, p @ v.abs(), top, slack))
 
 
-def check(got, want, size, top, keys, what):
+def check(got, want, size, top, slack, keys, what):
     """A probability times a value scale is rounded to fp16 once (half a step, 2^-11, of p |v|; where it is small next to
     the largest, 2^-31 of that, times a code of up to 8 against the largest value's 1 at least, for each key), the output
-    to bf16 once (2^-8), and 2^-12 of sum p |v| + 1e-6 stand for the fp32 scores, the approximate 2^x and the fp32 sums."""
+    to bf16 once (2^-8); 2^-12 of sum p |v| + 1e-6 stand for the approximate 2^x and the fp32 sums, slack for the scores."""
     g = got.double()
     assert torch.isfinite(g).all(), f"{what}: non-finite output"
-    over = (g - want).abs() - ((2.0 ** -11 + 2.0 ** -12) * size + keys * 2.0 ** -28 * top + 2.0 ** -8 * want.abs() + 1e-6)
+    over = (g - want).abs() - ((2.0 ** -11 + 2.0 ** -12) * size + keys * 2.0 ** -28 * top + slack + 2.0 ** -8 * want.abs() + 1e-6)
     assert over.max() <= 0, f"{what}: {(over > 0).sum()} values out of bound, by {over.max():.3g}"

@@ -200,8 +200,7 @@ def decode(c, lens, h_q, scale=SCALE, window=0, n_sink=0, seed=1, hide=True, ws=
 def check_decode(c, lens, q, out, sees, scale=SCALE, what=""):
     for b, n in enumerate(lens):
         k, v = c.values(b)
-        want, size, top = step.attend(q[b], k, v, sees[b], scale)
-        step.check(out[b], want, size, top, max(n, 1), f"{what} sequence {b} of {n}")
+        step.check(out[b], *step.attend(q[b], k, v, sees[b], scale, c.rows[b][0][1]), max(n, 1), f"{what} sequence {b} of {n}")
 
 
 LENS = [1, 0, 15, 16, 17, 127, 128, 129, 255, 700, 1, 2000]
@@ -236,8 +235,7 @@ def test_decode_many_sequences():
     q, out, sees = decode(c, lens, 2, hide=False)
     for b in list(range(40)) + list(range(2008, 2048)):
         k, v = c.values(b)
-        want, size, top = step.attend(q[b], k, v, sees[b], SCALE)
-        step.check(out[b], want, size, top, max(lens[b], 1), f"sequence {b}")
+        step.check(out[b], *step.attend(q[b], k, v, sees[b], SCALE, c.rows[b][0][1]), max(lens[b], 1), f"sequence {b}")
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.1, 3.0])
@@ -255,6 +253,21 @@ def test_decode_scales_of_values_far_apart(spread):
     check_decode(c, lens, *decode(c, lens, 8, scale=SCALE / 10 ** spread), scale=SCALE / 10 ** spread)
 
 
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("decades", [1, 3, 5])
+def test_decode_value_scales_far_apart(decades, window):
+    """Value scales over up to ten powers of ten beside ordinary scores: between keys, groups and sequences."""
+    lens = [700, 90, 33, 3000]
+    c = step.Kv4(lens, 2, 16, DEV, seed=decades)
+    g = torch.Generator().manual_seed(decades)
+    for b, n in enumerate(lens):
+        k, (codes, s) = c.rows[b]
+        s = (s.float() * 10 ** (decades * (2 * torch.rand(n, 2, 4, generator=g) - 1)).to(DEV)).to(torch.bfloat16)
+        c.rows[b] = [k, (codes, s)]
+        c.put(b, slice(0, n), *c.rows[b])
+    check_decode(c, lens, *decode(c, lens, 16, window=window, n_sink=1))
+
+
 @pytest.mark.parametrize("factor", [2.0 ** -60, 2.0 ** -20, 2.0 ** 20, 2.0 ** 60])
 def test_decode_sizes_of_queries_and_values(factor):
     """Queries times a factor and the scale by its inverse change nothing; values times a factor only the output's size."""
@@ -270,8 +283,8 @@ def test_decode_sizes_of_queries_and_values(factor):
         _, big, sees = decode(c, lens, 8, hide=False, q=q)
         for b, n in enumerate(lens):
             k, v = c.values(b)
-            want, size, top = step.attend(q[b], k, v / factor, sees[b], SCALE)
-            step.check(big[b].double() / factor, want, size, top, n, "values")
+            want = step.attend(q[b], k, v / factor, sees[b], SCALE, c.rows[b][0][1])
+            step.check(big[b].double() / factor, *want, n, "values")
 
 
 def test_decode_query_components_far_apart():

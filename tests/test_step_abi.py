@@ -183,7 +183,7 @@ def test_attend_of_one_token():
     q = torch.randn(4, 128, generator=g).to(torch.bfloat16)
     k, v = (torch.randn(30, 2, 128, generator=g).double() for _ in range(2))
     see = torch.arange(30) % 3 > 0
-    out, size, top = step.attend(q, k, v, see, 0.1)
+    out, size, top, _ = step.attend(q, k, v, see, 0.1)
     x = torch.nn.functional.scaled_dot_product_attention(
         q.double()[None, :, None], k[see].permute(1, 0, 2)[None], v[see].permute(1, 0, 2)[None], scale=0.1, enable_gqa=True)
     assert torch.allclose(out, x[0, :, 0]) and (size >= out.abs()).all() and (size >= top / 129).all()
