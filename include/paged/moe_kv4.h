@@ -19,7 +19,7 @@
  * What is stored for x (already rounded to bf16, as the bf16 cache would hold it): s = max |x| / 7 over the 32
  * dimensions, rounded to bf16, and c = round(x / s) of the exact quotient, halves to even, within -7 .. 7; s = 0 gives
  * c = 0. The error is at most half a scale, a 14th of the group's largest value, and 2^-8 of the value more where the
- * scale was rounded down. A group that holds a NaN or an infinity reads back as NaN.
+ * scale was rounded down. A group that holds a NaN or an infinity has a NaN scale and reads back as NaN.
  *
  * Conventions, masks, workspace and status word: those of moe_paged.h (the same workspace serves its calls and these).
  * The cache is 16-byte aligned.

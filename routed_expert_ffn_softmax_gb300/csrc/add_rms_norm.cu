@@ -8,9 +8,9 @@
 // part of the weight from row to row and has the next row's loads under way while it works on one.
 //
 // The codes: the norm's factor is the same for all of a group, so q does not depend on it, and 127 t is exact in fp32
-// (8 + 8 + 7 bits). The quotient of a number of 23 bits and one of 16 that is not a half is 2^-17 of itself or more
-// away from one, so a multiplication by the rounded reciprocal (2^-22) decides all codes but those next to a half,
-// which take the division.
+// (8 + 8 + 7 bits). A multiplication with the rounded 127 / T is off by 127 2^-23 < 2^-16 and decides every code but those
+// next to a half; a thread that holds one within 2^-14 (one warp in 30) divides all of its eight, which is exact: a quotient
+// of a number of 23 bits and one of 16 that is not a half is 2^-17 or more away from one.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -40,16 +40,30 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// round(127 t / T), halves to even; inv = 127 / T rounded.
-__device__ __forceinline__ int code8(float t, float top, float inv) {
-  const float f = t * inv;
-  float n = rintf(f);
-  if (!(fabsf(f - n) <= 0.5f - 1.0f / 4096)) n = rintf(__fdiv_rn(t * 127.0f, top));  // (so do an inv of infinity, and NaN)
-  return static_cast<int>(n);
+// round(127 t / T) of eight values, halves to even, as bytes; inv = 127 / T rounded.
+__device__ __forceinline__ uint2 codes8(const float (&t)[8], float top, float inv) {
+  constexpr float kMagic = 12582912.0f;  // 1.5 2^23: a sum with it has the rounded number in its low bits
+  uint32_t c[8];
+  bool near_half = false;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float v = fmaf(t[k], inv, kMagic);
+    const float e = fmaf(t[k], inv, -(v - kMagic));
+    near_half |= !(fabsf(e) <= 0.5f - 1.0f / 16384);  // (so do an inv of infinity, and NaN)
+    c[k] = __float_as_uint(v);
+  }
+  if (near_half) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) c[k] = static_cast<uint32_t>(__float2int_rn(__fdiv_rn(t[k] * 127.0f, top)));  // (0 for NaN)
+  }
+  auto four = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+  };
+  return make_uint2(four(c[0], c[1], c[2], c[3]), four(c[4], c[5], c[6], c[7]));
 }
 
 template <int kVecs, bool kAdd, bool kInt8>
-__global__ void __launch_bounds__(kMaxThreads) add_rms_norm_kernel(const AddRmsNormArgs p) {
+__global__ void __launch_bounds__(kMaxThreads, kVecs <= 2 ? 2 : 1) add_rms_norm_kernel(const AddRmsNormArgs p) {
   __shared__ float sums[2][kMaxThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int warps = blockDim.x >> 5;
@@ -132,11 +146,9 @@ __global__ void __launch_bounds__(kMaxThreads) add_rms_norm_kernel(const AddRmsN
         for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float big = __uint_as_float(top);
         const float inv = top ? 127.0f / big : 0.0f;
-        uint32_t c[2] = {0, 0};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) c[k >> 2] |= (static_cast<uint32_t>(code8(t[k], big, inv)) & 0xffu) << (8 * (k & 3));
+        const uint2 codes = codes8(t, big, inv);
         if (mine[i]) {
-          *reinterpret_cast<uint2*>(p.q + to) = make_uint2(c[0], c[1]);
+          *reinterpret_cast<uint2*>(p.q + to) = codes;
           if ((lane & 15) == 0) p.scales[to >> 7] = top ? big * factor / 127.0f : 1.0f;
         }
       }
