@@ -10,10 +10,14 @@
 //     O [16 dims x 8 heads] += codes(V)^T [16 x 16 keys] . (p s) [16 x 8]  s the value scale of the group the dims are in
 // K's scales multiply the four group sums in fp32; V's scales go into the probabilities, once per group.
 //
-// Unpacking. 16 bits of a row hold four codes of a group; two such of the same row (K) or of two keys (V) in one register
-// give all four fp16 pairs with four masks and a shift. K's are left as fp16 subnormals n 2^-24 (n 2^-20 for the odd codes,
+// Unpacking is what the kernel spends its time on (the integer pipe takes 2 cycles an instruction). 16 bits of a row hold four
+// codes of a group; two such of the same row (K) or of two keys (V) in one register give all four fp16 pairs with four masks
+// and a shift. K's are left as fp16 subnormals n 2^-24 (n 2^-20 for the odd codes,
 // whose queries are a 16th): exact products, n = c + 8, and -8 sum(q) is where the accumulator starts. V's are turned into
-// exact c by an exponent and a subtraction, as a sum over many keys must not carry an offset.
+// exact c by an exponent and a subtraction, as a sum over many keys must not carry an offset (as subnormals too, corrected by a
+// product with -8, a key of large weight and code 0 left 2^-20 of its weight; it was no faster). K's codes as e4m3 bytes, two
+// masks for eight, with the queries in two e4m3 parts: the instruction is made of conversions and fp16 products, 16 sequences
+// of up to 32K keys took 78 us instead of 65.
 //
 // Range. p s must fit fp16, whatever the scales are: the softmax reference R of a head bounds score + log2(largest scale of
 // the key) instead of the score alone, p = 2^(score - R) is held in fp32, and R is raised (outputs and sums rescaled) only
@@ -22,8 +26,18 @@
 // Work split: as in gqa_decode.cu, the key tiles (128 keys) of all segments form one list of which each CTA takes a
 // contiguous share; the pieces of a cut segment are joined in CTA order by the last to arrive.
 //
-// Per CTA: 8 warps, each with 16 keys of a tile and a running (R, sum, O) of its own, joined through shared memory at the
-// end of a piece; one warp that brings tiles with bulk copies, a page's 16 tokens of keys and values in one, 2304 bytes.
+// Per CTA, 12 warps, which share out the registers:
+//   0, 1   bring tiles with bulk copies, 16 tokens of keys and values or whole runs of a page in one (2304 bytes a chunk);
+//   2, 3   prepare the queries as operands, two pieces ahead; join the working warps' parts of a piece, write its output or
+//          its partial, and join a cut segment;
+//   4..11  work: each takes 16 or 32 keys of a tile, with a running (R, sum, O) of its own, and goes on to the next piece as
+//          soon as its part is handed over.
+// (One warp that loads, 8 or 11 that work and join through barriers: 255 sequences of up to 4K keys took 125 us, now 85.)
+//
+// GB300: 16 sequences of up to 32K keys, 4 heads a group, in 65 us (4.5 TB/s, 66% of a copy; 155 us in bf16); 24 with 16 heads
+// a group in 82 (2.9 TB/s, 170 TFLOP/s); 64 behind a window of 1024 in 26; one sequence of 512 visible keys in 9.3. The
+// working warps are at it 76% of the time, the integer pipe then 68% busy; the rest is the start (lengths, table, first tile:
+// 3 us), the last pieces' joins, and a hand-over per piece.
 #include <cuda_fp16.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

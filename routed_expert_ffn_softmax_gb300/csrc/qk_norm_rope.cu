@@ -23,7 +23,7 @@
 // 4) lanes that hold a group of 32 dimensions share its largest magnitude, taken of the bits as whole numbers (two groups
 // in one shuffle; NaN stands above infinity), and lanes that hold parts of the same stored bytes exchange them, so that a
 // head's 64 bytes of codes leave in 8- or 16-byte stores. Every code is that of the exact quotient: see code4. 9603 tokens of
-// 32 + 2 8 heads in STORE_US us (their bf16 store takes 44.7); with divisions 63.
+// 32 + 2 8 heads in 55.7 us (their bf16 store takes 44.7); with divisions 63.
 //
 // The angle: inv_freq / (2 pi) is kept as a 64-bit fraction of a turn (computed in fp64, rounded once), so
 // pos * fraction modulo 2^64 is the angle modulo one turn without any loss for large pos, and sin and cos are taken of a
