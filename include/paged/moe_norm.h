@@ -46,8 +46,8 @@ moe_status_t moe_add_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_
  *   positions  [n_axes] rows of N int32, axis_stride elements apart
  *   pair_axis  [rot_dim / 2] int32: pair i of token n turns by positions[pair_axis[i], n] * inv_freq[i]; a pair
  *              whose axis is outside [0, n_axes) does not turn
- * 1 <= n_axes <= 16, axis_stride >= N (any with one axis). Everything else as in moe_qk_norm_rope; with one axis the
- * results are its results.
+ * 1 <= n_axes <= 16, axis_stride >= 0 (0: the axes share their positions). Everything else as in moe_qk_norm_rope; with one
+ * axis the results are its results.
  */
 moe_status_t moe_qk_norm_mrope(const uint16_t* qkv, int64_t row_stride, int N, int h_q, int h_kv, int d,
                                const uint16_t* q_weight, const uint16_t* k_weight, float eps, const float* inv_freq,

@@ -193,7 +193,7 @@ moe_status_t qk_norm_rope(moe::QkNormRopeArgs a, int d, int page_size, moe_strea
   if (a.N < 0 || a.h_q < 1 || a.h_kv < 1 || d < 1 || a.rot < 0 || a.rot > d || a.rot % 16 || a.interleaved < 0 ||
       a.interleaved > 1 || !std::isfinite(a.eps) || a.eps < 0.0f)
     return MOE_ERR_INVALID_ARG;
-  if (a.n_axes < 1 || (a.n_axes > 1 && a.axis_stride < a.N)) return MOE_ERR_INVALID_ARG;
+  if (a.n_axes < 1 || a.axis_stride < 0) return MOE_ERR_INVALID_ARG;
   if (d != 128 || a.n_axes > 16) return MOE_ERR_UNSUPPORTED;
   const int64_t heads = static_cast<int64_t>(a.h_q) + 2 * static_cast<int64_t>(a.h_kv);
   if (heads * d > INT32_MAX) return MOE_ERR_UNSUPPORTED;
@@ -302,11 +302,11 @@ moe_status_t moe_qk_norm_rope_kv4(const uint16_t* qkv, int64_t row_stride, int N
 moe_status_t moe_add_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual, const uint16_t* weight,
                               float eps, int N, int H, uint16_t* residual_out, uint16_t* y, int8_t* q, float* scales,
                               moe_stream_t stream) {
-  if (N < 0 || H < 1 || !std::isfinite(eps) || eps < 0.0f || !q != !scales || (!y && !q)) return MOE_ERR_INVALID_ARG;
+  if (N < 0 || H < 1 || !std::isfinite(eps) || eps < 0.0f) return MOE_ERR_INVALID_ARG;
   if (H % (q ? 128 : 8) || H > 32768) return MOE_ERR_UNSUPPORTED;
   if (x && (x_stride < H || x_stride % 8)) return MOE_ERR_INVALID_ARG;
-  if (N == 0) return MOE_OK;
-  if (!residual) return MOE_ERR_INVALID_ARG;
+  if (N == 0) return MOE_OK;  // (tensors without elements have null pointers)
+  if (!residual || !q != !scales || (!y && !q)) return MOE_ERR_INVALID_ARG;
   const void* vectors[] = {x, residual, weight, residual_out, y, q};
   for (const void* v : vectors)
     if (!aligned(v, 16)) return MOE_ERR_INVALID_ARG;

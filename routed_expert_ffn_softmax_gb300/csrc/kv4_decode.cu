@@ -617,10 +617,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
     find_range();
     if (warp < 2) {
       // =========================== loads ===========================
-      // The two warps take four tiles in turn: lane 8 i + r finds tile i and its run r of chunks (a page's rows, at most a tile's; 16 keys
-      // where sink keys are folded in), reads that page's table entry four tiles early, and issues the copy when the tile's
-      // stage is free. One tile after the other, the chain of searches and loads took this warp 1300 cycles a tile, twice
-      // the memory's time.
+      // The two warps take four tiles in turn: lane 8 i + r finds tile i and its run r of chunks (a page's rows, at most a
+      // tile's; 16 keys where sink keys are folded in), reads that page's table entry a turn early, and issues the copy when
+      // the tile's stage is free. One tile after the other, the chain of searches and loads took a warp 1300 cycles a tile,
+      // twice the memory's time.
       const uint64_t policy = l2_policy_evict_first();
       const int page = 1 << p.kv.page_shift;
       struct Run {
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
         const int row = (lane & 7) * n;
         const int key = sp.key_of(pc.tl, row);
         if (row >= kKeys || !sp.sees_any(key, n)) return r;
-        r.id = __ldg(p.kv.block_table + static_cast<int64_t>(pc.b) * p.kv.max_pages + (key >> p.kv.page_shift));
+        r.id = p.kv.block_table[static_cast<int64_t>(pc.b) * p.kv.max_pages + (key >> p.kv.page_shift)];
         r.block = (static_cast<int64_t>(pc.j) << (p.kv.page_shift - 4)) + ((key & (page - 1)) / kChunk);
         r.chunks = n / kChunk;
         return r;
@@ -686,8 +686,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
       __syncwarp();
     } else {
       // =========================== queries, pieces finished ===========================
-      // Two warps. The first also prepares the queries, two pieces ahead. Of a piece a warp takes every other head, a lane four
-      // dimensions of it.
+      // Two warps. The first also prepares the queries, two pieces ahead. Of a piece a warp takes four of every eight heads, a
+      // lane four dimensions.
       const int half = warp - 2;
       const int d4 = 4 * lane;
       struct Ahead {

@@ -40,11 +40,9 @@ def place():
 def pack_rows(codes):
     """codes [..., 128] in -8 .. 7 -> [..., 64] bytes."""
     byte, bit = place()
-    out = torch.zeros(*codes.shape[:-1], 64, dtype=torch.int32, device=codes.device)
-    n = (codes + 8).to(torch.int32)
-    for d in range(128):
-        out[..., byte[d]] |= n[..., d] << int(bit[d])
-    return out.to(torch.uint8)
+    n = (codes + 8).to(torch.uint8)
+    low, high = (torch.argsort(byte + 64 * (bit != b)).to(codes.device)[:64] for b in (0, 4))
+    return n[..., low] | n[..., high] << 4
 
 
 def unpack_rows(raw):

@@ -380,6 +380,87 @@ def test_decode_graph_and_streams():
     assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
 
 
+@pytest.mark.parametrize("h_q,h_kv,page,window", [(32, 4, 16, 0), (64, 4, 32, 300), (16, 16, 128, 0)])
+def test_decode_ragged_batches_repeat_exactly(h_q, h_kv, page, window):
+    """Many whole and cut pieces per CTA: checked once, then 30 more calls give the same bits."""
+    g = torch.Generator().manual_seed(h_q)
+    lens = torch.randint(0, 1200, (100,), generator=g).tolist()
+    lens[7], lens[8] = 0, 9000
+    c = step.Kv4(lens, h_kv, page, DEV, seed=h_q)
+    q, out, sees = decode(c, lens, h_q, window=window, n_sink=5, hide=False)
+    check_decode(c, lens, q, out, sees)
+    ws, n, again = moe.alloc_paged_workspace(100, 100, h_q, h_kv, D, device=DEV), i32(lens), torch.empty_like(out)
+    for _ in range(30):
+        again.fill_(float("nan"))
+        moe.moe_gqa_kv4_decode(q, c.raw, c.table, n, SCALE, again, ws, window=window, n_sink=5)
+        assert torch.equal(again, out)
+    assert moe.workspace_status(ws) == 0
+
+
+def test_decode_one_sequence_over_all_ctas():
+    """More parts of a cut segment than are joined at once, for 1, 5, 8, 9 and 16 heads."""
+    n = 128 * 152 * 2 + 77
+    c = step.Kv4([n], 1, 64, DEV)
+    for h_q in (1, 5, 8, 9, 16):
+        check_decode(c, [n], *decode(c, [n], h_q, hide=False))
+
+
+def test_calls_without_work():
+    """No tokens, no sequences, sequences without keys."""
+    raw = moe.alloc_kv4_cache(2, 2, 16, DEV)
+    ws = moe.alloc_paged_workspace(4, 4, 8, 2, D, device=DEV)
+    none = lambda *s, t=torch.bfloat16: torch.empty(*s, dtype=t, device=DEV)  # noqa: E731
+    k, v = none(2, 2, 16, D), none(2, 2, 16, D)
+    moe.moe_qk_norm_rope_kv4(none(0, 12 * D), None, None, 0.0, None, None, none(0, t=torch.int32), none(0, t=torch.int32),
+                             none(0, 8, D), raw)
+    moe.moe_qk_norm_mrope(none(0, 12 * D), None, None, 0.0, None, None, none(3, 0, t=torch.int32), none(0, t=torch.int32),
+                          none(0, 8, D), k, v)
+    moe.moe_kv4_load(raw, none(0, 2, t=torch.int32), None, none(0, t=torch.int32), k, v, none(0, 2, t=torch.int32), ws)
+    moe.moe_gqa_kv4_decode(none(0, 8, D), raw, none(0, 2, t=torch.int32), none(0, t=torch.int32), SCALE, none(0, 8, D), ws)
+    moe.moe_add_rms_norm(none(0, 256), none(0, 256), none(256), 1e-6, None, none(0, 256))
+    out = torch.full((3, 8, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+    table = i32([[1 << 30, -1]] * 3)
+    moe.moe_gqa_kv4_decode(randn(3, 8, D), raw, table, i32([0, 0, 0]), SCALE, out, ws)
+    before = k.clone()
+    moe.moe_kv4_load(raw, table, i32([0, 5, 32]), i32([0, 5, 7]), k, v, table, ws)
+    torch.cuda.synchronize()
+    assert moe.workspace_status(ws) == 0 and not out.any() and torch.equal(before.view(torch.int16), k.view(torch.int16))
+
+
+def test_a_captured_step_follows_its_inputs():
+    """Norm, store, attention and norm again, captured once: replays with other inputs in place give the eager results."""
+    B, h_q, h_kv, page, H = 5, 16, 2, 16, 256
+    lens = [40, 17, 1, 300, 128]
+    c = step.Kv4(lens, h_kv, page, DEV)
+    ws = moe.alloc_paged_workspace(B, B, h_q, h_kv, D, device=DEV)
+    n, pos = i32(lens), i32([x - 1 for x in lens])
+    slots = i32([int(c.table[b, (x - 1) // page]) * page + (x - 1) % page for b, x in enumerate(lens)])
+    inv = (1e6 ** (-torch.arange(0, D, 2).double() / D)).float().to(DEV)
+    x, res, qkv = randn(B, H), randn(B, H, seed=1), randn(B, (h_q + 2 * h_kv) * D, seed=2)
+    y, q, out = torch.empty_like(x), randn(B, h_q, D), randn(B, h_q, D)
+
+    def run():
+        moe.moe_add_rms_norm(x, res, None, 1e-6, res, y)
+        moe.moe_qk_norm_rope_kv4(qkv, None, None, 0.0, inv, None, pos, slots, q, c.raw)
+        moe.moe_gqa_kv4_decode(q, c.raw, c.table, n, SCALE, out, ws)
+
+    saved = [t.clone() for t in (x, res, qkv)]
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        run()
+    for seed in (10, 11, 12):
+        news = [saved[0] * 0 + randn(B, H, seed=seed), randn(B, H, seed=seed + 100), randn(*qkv.shape, seed=seed + 200)]
+        got = []
+        for call in (g.replay, run):
+            for t, v in zip((x, res, qkv), news):
+                t.copy_(v)
+            call()
+            torch.cuda.synchronize()
+            got.append([t.clone() for t in (res, y, q, out, c.raw)])
+        assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 def test_decode_cache_past_32_bits():
     page, h_kv = 1024, 2
     num_pages = (5 << 30) // (h_kv * page * 144)

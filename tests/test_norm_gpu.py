@@ -204,7 +204,8 @@ def test_one_axis_gives_the_one_axis_call(rot, interleaved):
     want += [torch.full((4, h_kv, 16, D), -9.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
     moe.moe_qk_norm_rope(qkv, *w, EPS, inv, pos, slots, *want, interleaved=interleaved)
     pairs = torch.arange(rot // 2, dtype=torch.int32, device=DEV)
-    for positions, pair in ((pos, pairs * 0), (pos[None], pairs * 0), (pos[None].repeat(3, 1), pairs % 3)):
+    for positions, pair in ((pos, pairs * 0), (pos[None], pairs * 0), (pos[None].repeat(3, 1), pairs % 3),
+                            (pos[None].expand(4, N), pairs % 4)):
         got = rotate(qkv, h_q, h_kv, w, positions, inv, pair, slots, 16, 4, interleaved)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 

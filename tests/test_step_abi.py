@@ -68,7 +68,7 @@ ROPE_CASES = [
     (dict(rot_dim=8), INVALID), (dict(rot_dim=144), INVALID), (dict(interleaved=2), INVALID), (dict(eps=float("inf")), INVALID),
     (dict(row_stride=1279), INVALID), (dict(row_stride=1284), INVALID), (dict(page_size=8), INVALID),
     (dict(page_size=48), INVALID), (dict(num_pages=0), INVALID), (dict(num_pages=1 << 27), UNSUPPORTED),
-    (dict(n_axes=0), INVALID), (dict(n_axes=17), UNSUPPORTED), (dict(axis_stride=3), INVALID), (dict(positions=None), INVALID),
+    (dict(n_axes=0), INVALID), (dict(n_axes=17), UNSUPPORTED), (dict(axis_stride=-1), INVALID), (dict(positions=None), INVALID),
     (dict(slots=None), INVALID), (dict(q_out=None), INVALID), (dict(inv_freq=None), INVALID), (dict(pair_axis=None), INVALID),
     (dict(pair_axis=F + 2), INVALID), (dict(positions=F + 1), INVALID), (dict(qkv=F + 8), INVALID), (dict(q_out=F + 8), INVALID),
     (dict(h_q=1 << 24, row_stride=1 << 40), UNSUPPORTED)]
