@@ -803,7 +803,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
   } else {
     // =========================== work ===========================
     // Warp (i, c) takes unit c of tiles i, i + kTiles, ... of the CTA's list, whatever piece they belong to; a piece's part is
-    // handed over when the next one begins, and nothing is waited for but the hand-over buffer.
+    // handed over when the next one begins, and nothing is waited for but the hand-over buffer. After a wait that ran out a
+    // warp leaves and hands nothing back: the others' waits then run out with it, once each.
     reg_alloc<kRegsWork>();
     named_bar_sync(4, kThreads);
     find_range();
@@ -819,6 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
       const int slot = pi & 1;
       const int first = x - beg;  // the piece's first tile in this CTA's count
       wait(&q_full[slot], (pi >> 1) & 1, kStatusWaitFullTimeout);
+      if (!ok) break;
       const bool any = it < first + pc.n;
       if (any) q.load(smem + S::kQ + slot * S::kQBytes, lane);
       s.clear();
@@ -863,29 +865,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
         }
       }
       // ---- hand over
-      wait(h_empty, (pi & 1) ^ 1, kStatusWaitEmptyTimeout);
-      if (ok) {
-        float* ref = refs + w * 16;
-        float* l_of = ref + kWarps * 16;
-        float* to_o = join + w * 8 * kNT * kRow + 4 * g;
+      if (ok) wait(h_empty, (pi & 1) ^ 1, kStatusWaitEmptyTimeout);
+      if (!ok) break;
+      float* ref = refs + w * 16;
+      float* l_of = ref + kWarps * 16;
+      float* to_o = join + w * 8 * kNT * kRow + 4 * g;
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
+      for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int head = 8 * nt + 2 * t4 + h;
-            float v = s.sum[nt][h];
+        for (int h = 0; h < 2; ++h) {
+          const int head = 8 * nt + 2 * t4 + h;
+          float v = s.sum[nt][h];
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-            if (g == 0) {
-              ref[head] = s.ref[nt][h];
-              l_of[head] = v;
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<float4*>(to_o + head * kRow + 32 * k) =
-                  make_float4(s.o[nt][2 * k][h], s.o[nt][2 * k][h + 2], s.o[nt][2 * k + 1][h], s.o[nt][2 * k + 1][h + 2]);
+          for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+          if (g == 0) {
+            ref[head] = s.ref[nt][h];
+            l_of[head] = v;
           }
-      }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<float4*>(to_o + head * kRow + 32 * k) =
+                make_float4(s.o[nt][2 * k][h], s.o[nt][2 * k][h + 2], s.o[nt][2 * k + 1][h], s.o[nt][2 * k + 1][h + 2]);
+        }
       __syncwarp();
       if (lane == 0) mbar_arrive(h_full);
     }
