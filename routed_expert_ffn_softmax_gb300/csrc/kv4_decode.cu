@@ -45,6 +45,7 @@
 #include <atomic>
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 
 #include "gqa_paged.cuh"
 #include "paged_device.cuh"
@@ -83,10 +84,13 @@ static_assert(128 * kRegsHelp + 32 * kWarps * kRegsWork <= kThreads * kRegsLaunc
 template <int kNT>
 struct Split {
   // Chunks a warp takes at once. With 16 heads one, two spill: 64 sequences behind a window 26.4 us instead of 28.9 (24 of up to
-  // 32K keys 81.5 instead of 79.3); with 8 heads two, as the code around them costs as much as one.
+  // 32K keys 81.5 instead of 79.3). With 8 heads two, as the code around them costs as much as one; four where the sequences'
+  // segments have kLong tiles on average: us for two and four with 128 sequences of up to 2K keys 36.1 and 38.9, 64 of up to
+  // 4K 33.6 and 32.3, 32 of up to 8K 33.5 and 31.1, 8 of up to 32K 32.6 and 31.0 (4 key/value heads, lengths from half of it).
   static constexpr int kUnit = kNT == 1 ? 2 : 1;
-  static constexpr int kUnits = kChunks / kUnit;         // of a tile
-  static constexpr int kTiles = kWarps / kUnits;         // tiles the warps are at together
+  static constexpr int kLongUnit = kNT == 1 ? 4 : 1;
+  static constexpr int kLong = 20;
+  static constexpr int tiles_at_once(bool longs) { return kWarps * (longs ? kLongUnit : kUnit) / kChunks; }
   static constexpr int kStages = kNT == 1 ? 9 : 7;
     // shared memory
   static constexpr int kJoinFloats = kWarps * 8 * kNT * kRow;
@@ -157,6 +161,9 @@ __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t more) {
   return d;
 }
 
+__device__ __forceinline__ void mbar_arrive_many(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
+}
 // Orders this thread's plain accesses, to shared and global memory, before copies that are issued after a barrier.
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
@@ -510,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], S::kUnits);
+      mbar_init(&empty[s], kChunks);
       last_tile[s] = -1;
     }
     for (int b = 0; b < 2; ++b) {
@@ -524,14 +531,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
   }
   __syncthreads();
 
-  // The first NC CTAs share the tiles: as many as there are with kTiles tiles each, which a CTA works on together (tile counts
-  // fit 32 bits: the host checks).
+  // The first NC CTAs share the tiles: as many as there are with as many tiles as a CTA works on together (tile counts fit 32
+  // bits: the host checks).
   const int grid = gridDim.x, cta = blockIdx.x;
   int q_tiles = 0, rm = 0, beg = 0, end = 0;
+  bool longs = false;  // long segments
   auto range_start = [&](int c) { return c * q_tiles + min(c, rm); };
   auto find_range = [&]() {
     const int total = p.h_kv * pre[p.B];
-    const int NC = min((total + S::kTiles - 1) / S::kTiles, grid);
+    longs = S::kLongUnit != S::kUnit && pre[p.B] >= S::kLong * p.B;
+    const int together = S::tiles_at_once(longs);
+    const int NC = min((total + together - 1) / together, grid);
     if (NC == 0) return;
     q_tiles = total / NC;
     rm = total - q_tiles * NC;
@@ -808,87 +818,95 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
     reg_alloc<kRegsWork>();
     named_bar_sync(4, kThreads);
     find_range();
-    const int w = warp - 4;
-    const int g = lane >> 2, t4 = lane & 3;
-    const int c0 = w % S::kUnits * S::kUnit;
-    Queries<kNT> q;
-    State<kNT> s;
-    Piece pc{};
-    int it = w / S::kUnits, pi = 0;
-    for (int x = beg; x < end; x += pc.n, ++pi) {
-      pc = x == beg ? locate(x) : after(pc, x);
-      const int slot = pi & 1;
-      const int first = x - beg;  // the piece's first tile in this CTA's count
-      wait(&q_full[slot], (pi >> 1) & 1, kStatusWaitFullTimeout);
-      if (!ok) break;
-      const bool any = it < first + pc.n;
-      if (any) q.load(smem + S::kQ + slot * S::kQBytes, lane);
-      s.clear();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_empty[slot]);
-      if (any) {
-        const DecodeSpan sp = span_of(lens[pc.b], p.L_cap, p.kv);
-        // the tiles whose keys the query sees all (a folded one is not among them)
-        const int from = max(pc.tl, (sp.lo + kKeys - 1) / kKeys - sp.w0 + sp.ns) - pc.tl + first;
-        const int to = min(pc.tl + pc.n, sp.len / kKeys - sp.w0 + sp.ns) - pc.tl + first;
-        for (; it < first + pc.n; it += S::kTiles) {
-          const int st = it % kStages;
-          wait(&full[st], static_cast<uint32_t>((it / kStages) & 1), kStatusWaitFullTimeout);
-          if (!ok) break;
-          uint8_t* at = smem + st * kStageBytes + c0 * kKv4Block;
-          const uint32_t bad = bad_chunks[st];
-          float bias[S::kUnit][2] = {};
-          bool none = false;
-          if (it < from || it >= to || bad != 0) {
-            // some keys are not seen, or read as zeros: their scales become 0 (what stands there may be NaN)
-            none = true;
+    auto work = [&](auto chunks) {
+      constexpr int kUnit = decltype(chunks)::value, kUnits = kChunks / kUnit, kTiles = kWarps / kUnits;
+      const int w = warp - 4;
+      const int g = lane >> 2, t4 = lane & 3;
+      const int c0 = w % kUnits * kUnit;
+      Queries<kNT> q;
+      State<kNT> s;
+      Piece pc{};
+      int it = w / kUnits, pi = 0;
+      for (int x = beg; x < end; x += pc.n, ++pi) {
+        pc = x == beg ? locate(x) : after(pc, x);
+        const int slot = pi & 1;
+        const int first = x - beg;  // the piece's first tile in this CTA's count
+        wait(&q_full[slot], (pi >> 1) & 1, kStatusWaitFullTimeout);
+        if (!ok) break;
+        const bool any = it < first + pc.n;
+        if (any) q.load(smem + S::kQ + slot * S::kQBytes, lane);
+        s.clear();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_empty[slot]);
+        if (any) {
+          const DecodeSpan sp = span_of(lens[pc.b], p.L_cap, p.kv);
+          // the tiles whose keys the query sees all (a folded one is not among them)
+          const int from = max(pc.tl, (sp.lo + kKeys - 1) / kKeys - sp.w0 + sp.ns) - pc.tl + first;
+          const int to = min(pc.tl + pc.n, sp.len / kKeys - sp.w0 + sp.ns) - pc.tl + first;
+          for (; it < first + pc.n; it += kTiles) {
+            const int st = it % kStages;
+            wait(&full[st], static_cast<uint32_t>((it / kStages) & 1), kStatusWaitFullTimeout);
+            if (!ok) break;
+            uint8_t* at = smem + st * kStageBytes + c0 * kKv4Block;
+            const uint32_t bad = bad_chunks[st];
+            float bias[kUnit][2] = {};
+            bool none = false;
+            if (it < from || it >= to || bad != 0) {
+              // some keys are not seen, or read as zeros: their scales become 0 (what stands there may be NaN)
+              none = true;
 #pragma unroll
-            for (int c = 0; c < S::kUnit; ++c) {
-              const int key = sp.key_of(pc.tl + it - first, (c0 + c) * kChunk);
-              const bool zero = bad >> (c0 + c) & 1;
+              for (int c = 0; c < kUnit; ++c) {
+                const int key = sp.key_of(pc.tl + it - first, (c0 + c) * kChunk);
+                const bool zero = bad >> (c0 + c) & 1;
 #pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const bool see = sp.sees(key + g + 8 * r);
-                bias[c][r] = see ? 0.0f : -INFINITY;
-                none &= !see;
-                if (t4 < 2 && (zero || !see))
-                  *reinterpret_cast<uint2*>(at + c * kKv4Block + t4 * kKv4Values + kKv4Scales + 8 * (g + 8 * r)) = make_uint2(0u, 0u);
+                for (int r = 0; r < 2; ++r) {
+                  const bool see = sp.sees(key + g + 8 * r);
+                  bias[c][r] = see ? 0.0f : -INFINITY;
+                  none &= !see;
+                  if (t4 < 2 && (zero || !see))
+                    *reinterpret_cast<uint2*>(at + c * kKv4Block + t4 * kKv4Values + kKv4Scales + 8 * (g + 8 * r)) = make_uint2(0u, 0u);
+                }
               }
+              none = __all_sync(0xffffffffu, none);
+              fence_proxy_async_smem();
+              __syncwarp();
             }
-            none = __all_sync(0xffffffffu, none);
-            fence_proxy_async_smem();
+            if (!none) s.add(q, at, bias, lane);
             __syncwarp();
+            if (lane == 0) mbar_arrive_many(&empty[st], kUnit);
           }
-          if (!none) s.add(q, at, bias, lane);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[st]);
         }
+        // ---- hand over
+        if (ok) wait(h_empty, (pi & 1) ^ 1, kStatusWaitEmptyTimeout);
+        if (!ok) break;
+        float* ref = refs + w * 16;
+        float* l_of = ref + kWarps * 16;
+        float* to_o = join + w * 8 * kNT * kRow + 4 * g;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int head = 8 * nt + 2 * t4 + h;
+            float v = s.sum[nt][h];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+            if (g == 0) {
+              ref[head] = s.ref[nt][h];
+              l_of[head] = v;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<float4*>(to_o + head * kRow + 32 * k) =
+                  make_float4(s.o[nt][2 * k][h], s.o[nt][2 * k][h + 2], s.o[nt][2 * k + 1][h], s.o[nt][2 * k + 1][h + 2]);
+          }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(h_full);
       }
-      // ---- hand over
-      if (ok) wait(h_empty, (pi & 1) ^ 1, kStatusWaitEmptyTimeout);
-      if (!ok) break;
-      float* ref = refs + w * 16;
-      float* l_of = ref + kWarps * 16;
-      float* to_o = join + w * 8 * kNT * kRow + 4 * g;
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int head = 8 * nt + 2 * t4 + h;
-          float v = s.sum[nt][h];
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-          if (g == 0) {
-            ref[head] = s.ref[nt][h];
-            l_of[head] = v;
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<float4*>(to_o + head * kRow + 32 * k) =
-                make_float4(s.o[nt][2 * k][h], s.o[nt][2 * k][h + 2], s.o[nt][2 * k + 1][h], s.o[nt][2 * k + 1][h + 2]);
-        }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(h_full);
+    };
+    if (longs) {
+      work(std::integral_constant<int, S::kLongUnit>());
+    } else {
+      work(std::integral_constant<int, S::kUnit>());
     }
   }
 }
