@@ -17,7 +17,7 @@
 // exact c by an exponent and a subtraction, as a sum over many keys must not carry an offset (as subnormals too, corrected by a
 // product with -8, a key of large weight and code 0 left 2^-20 of its weight; it was no faster). K's codes as e4m3 bytes, two
 // masks for eight, with the queries in two e4m3 parts: the instruction is made of conversions and fp16 products, 16 sequences
-// of up to 32K keys took 78 us instead of 65.
+// of up to 32K keys took 78 us instead of the 65 of that time.
 //
 // Range. p s must fit fp16, whatever the scales are: the softmax reference R of a head bounds score + log2(largest scale of
 // the key) instead of the score alone, p = 2^(score - R) is held in fp32, and R is raised (outputs and sums rescaled) only
@@ -30,14 +30,14 @@
 //   0, 1   bring tiles with bulk copies, 16 tokens of keys and values or whole runs of a page in one (2304 bytes a chunk);
 //   2, 3   prepare the queries as operands, two pieces ahead; join the working warps' parts of a piece, write its output or
 //          its partial, and join a cut segment;
-//   4..11  work: each takes 16 or 32 keys of a tile, with a running (R, sum, O) of its own, and goes on to the next piece as
+//   4..11  work: each takes 32 or 64 keys of a tile, with a running (R, sum, O) of its own, and goes on to the next piece as
 //          soon as its part is handed over.
 // (One warp that loads, 8 or 11 that work and join through barriers: 255 sequences of up to 4K keys took 125 us, now 85.)
 //
-// GB300: 16 sequences of up to 32K keys, 4 heads a group, in 65 us (4.5 TB/s, 66% of a copy; 155 us in bf16); 24 with 16 heads
-// a group in 82 (2.9 TB/s, 170 TFLOP/s); 64 behind a window of 1024 in 26; one sequence of 512 visible keys in 9.3. The
-// working warps are at it 76% of the time, the integer pipe then 68% busy; the rest is the start (lengths, table, first tile:
-// 3 us), the last pieces' joins, and a hand-over per piece.
+// GB300: 16 sequences of up to 32K keys, 4 heads a group, in 60 us (4.9 TB/s, 72% of a copy; 155 us in bf16); 24 with 16 heads
+// a group in 74 (3.2 TB/s, 180 TFLOP/s); 64 behind a window of 1024 in 27; one sequence of 512 visible keys in 9.3. With two
+// chunks a warp the working warps were at it 76% of the time, the integer pipe then 68% busy; the rest is the start (lengths,
+// table, first tile: 3 us), the last pieces' joins, and a hand-over per piece.
 #include <cuda_fp16.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -79,16 +79,17 @@ constexpr int kRegsHelp = 104;
 constexpr int kRegsWork = 200;
 static_assert(128 * kRegsHelp + 32 * kWarps * kRegsWork <= kThreads * kRegsLaunch, "a larger share would wait forever");
 
-// kNT: eights of heads. GB300, us for 12 warps instead of 8: 16 sequences of up to 32K keys 62.5 instead of 65.5, but 255 of up
-// to 4K 92 instead of 85 and one sequence 11.0 instead of 9.3.
+// kNT: eights of heads. (With 12 warps that work and 128 registers at launch, two chunks each: 16 sequences of up to 32K keys
+// 62.5 us instead of 65.4, but 255 of up to 4K 92 instead of 85 and one sequence 11.0 instead of 9.3; with 16 heads the same as 8.)
 template <int kNT>
 struct Split {
-  // Chunks a warp takes at once. With 16 heads one, two spill: 64 sequences behind a window 26.4 us instead of 28.9 (24 of up to
-  // 32K keys 81.5 instead of 79.3). With 8 heads two, as the code around them costs as much as one; four where the sequences'
-  // segments have kLong tiles on average: us for two and four with 128 sequences of up to 2K keys 36.1 and 38.9, 64 of up to
-  // 4K 33.6 and 32.3, 32 of up to 8K 33.5 and 31.1, 8 of up to 32K 32.6 and 31.0 (4 key/value heads, lengths from half of it).
-  static constexpr int kUnit = kNT == 1 ? 2 : 1;
-  static constexpr int kLongUnit = kNT == 1 ? 4 : 1;
+  // Chunks a warp takes at once: two, as the code around them costs as much as one (with 16 heads: 24 sequences of up to 32K keys
+  // 74.0 us instead of 74.9 with two for these alone, 64 behind a window 26.8 instead of 26.4). Four with up to 8 heads where the
+  // sequences' segments have kLong tiles on average: us for two and four with 128 sequences of up to 2K keys 36.1 and 38.9, 64 of
+  // up to 4K 33.6 and 32.3, 32 of up to 8K 33.5 and 31.1, 8 of up to 32K 32.6 and 31.0 (4 key/value heads, lengths from half of
+  // it). With 16 heads four spill.
+  static constexpr int kUnit = 2;
+  static constexpr int kLongUnit = kNT == 1 ? 4 : 2;
   static constexpr int kLong = 20;
   static constexpr int tiles_at_once(bool longs) { return kWarps * (longs ? kLongUnit : kUnit) / kChunks; }
   static constexpr int kStages = kNT == 1 ? 9 : 7;
@@ -186,13 +187,13 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   return d;
 }
 
-// The queries of up to 8 kNT heads as mma operands, and what goes with them: in shared memory, written by one warp per piece,
-// and in the working warps' registers.
+// The queries of up to 8 kNT heads as mma operands, and what goes with them, in shared memory: written by one warp per piece,
+// read per use (in registers, they took those that keep four chunks, or two with 16 heads, under way: 24 sequences of up to
+// 32K keys with 16 heads 81 us instead of 76).
 template <int kNT>
 struct Queries {
-  uint32_t b[kNT][4][4];     // [heads][group of dims][k16 step, register]
-  float start[kNT][4][2];    // -8 sum(q) of the group for heads 2 t, 2 t + 1 (in accumulator units)
-  float unit[kNT][2];        // accumulator units to log2 scores
+  uint8_t* at;               // per 8 heads and group of dimensions: operands [lane], -8 sum(q) [head]; units [head]
+  float unit[kNT][2];        // accumulator units to log2 scores, for heads 2 t, 2 t + 1
   uint32_t exp_low, exp_high;  // fp16 1024 and 64 twice, in registers
 
   static __device__ __forceinline__ uint4* operands(uint8_t* at) { return reinterpret_cast<uint4*>(at); }
@@ -248,18 +249,16 @@ struct Queries {
       if (t == 0) units(at)[nt * 8 + g] = back;
     }
   }
-  __device__ __forceinline__ void load(uint8_t* at, int lane) {
-    const int t = lane & 3;
+  // One group's: two registers for each of two k16 steps, and where the accumulators of heads 2 t, 2 t + 1 start.
+  __device__ __forceinline__ uint4 operand(int nt, int w, int lane) const { return operands(at)[(nt * 4 + w) * 32 + lane]; }
+  __device__ __forceinline__ float2 start(int nt, int w, int lane) const {
+    return *reinterpret_cast<const float2*>(starts(at) + (nt * 4 + w) * 8 + 2 * (lane & 3));
+  }
+  __device__ __forceinline__ void take(uint8_t* from, int lane) {
+    at = from;
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint4 v = operands(at)[(nt * 4 + w) * 32 + lane];
-        b[nt][w][0] = v.x, b[nt][w][1] = v.y, b[nt][w][2] = v.z, b[nt][w][3] = v.w;
-        const float2 s = *reinterpret_cast<const float2*>(starts(at) + (nt * 4 + w) * 8 + 2 * t);
-        start[nt][w][0] = s.x, start[nt][w][1] = s.y;
-      }
-      const float2 u = *reinterpret_cast<const float2*>(units(at) + nt * 8 + 2 * t);
+      const float2 u = *reinterpret_cast<const float2*>(units(at) + nt * 8 + 2 * (lane & 3));
       unit[nt][0] = u.x, unit[nt][1] = u.y;
     }
     asm volatile("mov.u32 %0, 0x64006400;" : "=r"(exp_low));
@@ -291,45 +290,58 @@ struct State {
     const int g = lane >> 2, t = lane & 3;
     float x[kCount][kNT][4];
     uint2 vs[kCount][2];
+    uint4 k0[kCount], k1[kCount];
+    uint2 ks0[kCount], ks1[kCount];
 #pragma unroll
     for (int c = 0; c < kCount; ++c) {
       const uint8_t* ka = at + c * kKv4Block;
-      const uint4 k0 = *reinterpret_cast<const uint4*>(ka + g * kKv4RowBytes + 16 * t);
-      const uint4 k1 = *reinterpret_cast<const uint4*>(ka + (g + 8) * kKv4RowBytes + 16 * t);
-      const uint2 ks0 = *reinterpret_cast<const uint2*>(ka + kKv4Scales + 8 * g);
-      const uint2 ks1 = *reinterpret_cast<const uint2*>(ka + kKv4Scales + 8 * (g + 8));
+      k0[c] = *reinterpret_cast<const uint4*>(ka + g * kKv4RowBytes + 16 * t);
+      k1[c] = *reinterpret_cast<const uint4*>(ka + (g + 8) * kKv4RowBytes + 16 * t);
+      ks0[c] = *reinterpret_cast<const uint2*>(ka + kKv4Scales + 8 * g);
+      ks1[c] = *reinterpret_cast<const uint2*>(ka + kKv4Scales + 8 * (g + 8));
       vs[c][0] = *reinterpret_cast<const uint2*>(ka + kKv4Values + kKv4Scales + 8 * g);
       vs[c][1] = *reinterpret_cast<const uint2*>(ka + kKv4Values + kKv4Scales + 8 * (g + 8));
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[c][nt][i] = 0.0f;
+    }
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < 4; ++w) {
+      uint4 qb[kNT];
+      float2 st[kNT];
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        qb[nt] = q.operand(nt, w, lane);
+        st[nt] = q.start(nt, w, lane);
+      }
+#pragma unroll
+      for (int c = 0; c < kCount; ++c) {
         const uint32_t sel = (w & 1) ? 0x7632u : 0x5410u;
-        const uint32_t r0 = __byte_perm(w < 2 ? k0.x : k0.y, w < 2 ? k0.z : k0.w, sel);
-        const uint32_t r1 = __byte_perm(w < 2 ? k1.x : k1.y, w < 2 ? k1.z : k1.w, sel);
+        const uint32_t r0 = __byte_perm(w < 2 ? k0[c].x : k0[c].y, w < 2 ? k0[c].z : k0[c].w, sel);
+        const uint32_t r1 = __byte_perm(w < 2 ? k1[c].x : k1[c].y, w < 2 ? k1[c].z : k1[c].w, sel);
         const uint32_t r0h = r0 >> 8, r1h = r1 >> 8;
-        const float s0 = (w & 1) ? bf_hi(w < 2 ? ks0.x : ks0.y) : bf_lo(w < 2 ? ks0.x : ks0.y);
-        const float s1 = (w & 1) ? bf_hi(w < 2 ? ks1.x : ks1.y) : bf_lo(w < 2 ? ks1.x : ks1.y);
+        const float s0 = (w & 1) ? bf_hi(w < 2 ? ks0[c].x : ks0[c].y) : bf_lo(w < 2 ? ks0[c].x : ks0[c].y);
+        const float s1 = (w & 1) ? bf_hi(w < 2 ? ks1[c].x : ks1[c].y) : bf_lo(w < 2 ? ks1[c].x : ks1[c].y);
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
-          const float from[4] = {q.start[nt][w][0], q.start[nt][w][1], q.start[nt][w][0], q.start[nt][w][1]};
+          const float from[4] = {st[nt].x, st[nt].y, st[nt].x, st[nt].y};
           float acc[4];
-          mma_f16(acc, r0 & 0x000f000fu, r1 & 0x000f000fu, r0 & 0x00f000f0u, r1 & 0x00f000f0u, q.b[nt][w][0], q.b[nt][w][1], from);
-          mma_f16(acc, r0h & 0x000f000fu, r1h & 0x000f000fu, r0h & 0x00f000f0u, r1h & 0x00f000f0u, q.b[nt][w][2], q.b[nt][w][3],
-                  acc);
+          mma_f16(acc, r0 & 0x000f000fu, r1 & 0x000f000fu, r0 & 0x00f000f0u, r1 & 0x00f000f0u, qb[nt].x, qb[nt].y, from);
+          mma_f16(acc, r0h & 0x000f000fu, r1h & 0x000f000fu, r0h & 0x00f000f0u, r1h & 0x00f000f0u, qb[nt].z, qb[nt].w, acc);
           x[c][nt][0] = fmaf(acc[0], s0, x[c][nt][0]);
           x[c][nt][1] = fmaf(acc[1], s0, x[c][nt][1]);
           x[c][nt][2] = fmaf(acc[2], s1, x[c][nt][2]);
           x[c][nt][3] = fmaf(acc[3], s1, x[c][nt][3]);
         }
       }
+    }
+#pragma unroll
+    for (int c = 0; c < kCount; ++c)
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[c][nt][i] = fmaf(x[c][nt][i], q.unit[nt][i & 1], bias[c][i >> 1]);
-    }
 
     float p[kCount][kNT][4];
     auto weigh = [&]() {
@@ -834,10 +846,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
         wait(&q_full[slot], (pi >> 1) & 1, kStatusWaitFullTimeout);
         if (!ok) break;
         const bool any = it < first + pc.n;
-        if (any) q.load(smem + S::kQ + slot * S::kQBytes, lane);
+        if (any) q.take(smem + S::kQ + slot * S::kQBytes, lane);
         s.clear();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_empty[slot]);
         if (any) {
           const DecodeSpan sp = span_of(lens[pc.b], p.L_cap, p.kv);
           // the tiles whose keys the query sees all (a folded one is not among them)
@@ -877,7 +887,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
           }
         }
         // ---- hand over
-        if (ok) wait(h_empty, (pi & 1) ^ 1, kStatusWaitEmptyTimeout);
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_empty[slot]);
+        wait(h_empty, (pi & 1) ^ 1, kStatusWaitEmptyTimeout);
         if (!ok) break;
         float* ref = refs + w * 16;
         float* l_of = ref + kWarps * 16;
