@@ -93,7 +93,13 @@ struct Split {
   static constexpr int kLong = 20;
   static constexpr int tiles_at_once(bool longs) { return kWarps * (longs ? kLongUnit : kUnit) / kChunks; }
   static constexpr int kStages = kNT == 1 ? 9 : 7;
-    // shared memory
+  // The two loading warps take kTurn tiles in turn, and an mbarrier tells apart only neighbouring phases: neither may get to
+  // tile t + 2 kStages of a stage while tile t there is still worked on. The warps that are behind with t are so with every
+  // tiles_at_once-th tile after it. The loader whose tile t + kStages is stops there; the other's next turn starts at most
+  // kTurn tiles later, and it stops at the first of those tiles, fewer than tiles_at_once on.
+  static constexpr int kTurn = 4;
+  static_assert(tiles_at_once(kLongUnit != kUnit) <= kTurn && kStages >= kTurn + tiles_at_once(kLongUnit != kUnit), "stages reused early");
+  // shared memory
   static constexpr int kJoinFloats = kWarps * 8 * kNT * kRow;
   static constexpr int kMost = kJoinFloats * 4 / (128 + 512 * 8 * kNT);  // parts of a cut segment that fit there
   static_assert(kMost >= kWarps && kMost <= 32, "both are joined alike, a lane copies a part");
@@ -665,10 +671,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
         return r;
       };
       const int stop = (p.give_up_tile < 0 ? end : beg + min(end - beg, p.give_up_tile)) - beg;
-      Run next = run_at(4 * warp);
-      for (int i0 = 4 * warp; i0 < stop && ok; i0 += 8) {
+      Run next = run_at(S::kTurn * warp);
+      for (int i0 = S::kTurn * warp; i0 < stop && ok; i0 += 2 * S::kTurn) {
         const Run run = next;
-        next = run_at(i0 + 8);
+        next = run_at(i0 + 2 * S::kTurn);
         const bool mine = run.chunks > 0;
         const bool there = mine && static_cast<uint32_t>(run.id) < static_cast<uint32_t>(p.kv.num_pages);
         const uint8_t* src = p.cache + ((static_cast<int64_t>(run.id) * p.h_kv << (p.kv.page_shift - 4)) + run.block) * kKv4Block;
@@ -681,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
           bad |= __shfl_xor_sync(0xffffffffu, bad, d);
         }
         if (mine && !there && i0 + (lane >> 3) < stop) raise_status(p.status, kStatusBadPage);
-        for (int it = i0; it < min(i0 + 4, stop); ++it) {
+        for (int it = i0; it < min(i0 + S::kTurn, stop); ++it) {
           const int st = it % kStages;
           wait(&empty[st], static_cast<uint32_t>(((it / kStages) & 1) ^ 1), kStatusWaitEmptyTimeout);
           if (!ok) break;
