@@ -93,12 +93,14 @@ struct Split {
   static constexpr int kLong = 20;
   static constexpr int tiles_at_once(bool longs) { return kWarps * (longs ? kLongUnit : kUnit) / kChunks; }
   static constexpr int kStages = kNT == 1 ? 9 : 7;
-  // The two loading warps take kTurn tiles in turn, and an mbarrier tells apart only neighbouring phases: neither may get to
-  // tile t + 2 kStages of a stage while tile t there is still worked on. The warps that are behind with t are so with every
-  // tiles_at_once-th tile after it. The loader whose tile t + kStages is stops there; the other's next turn starts at most
-  // kTurn tiles later, and it stops at the first of those tiles, fewer than tiles_at_once on.
+  // The two loading warps take kTurn tiles in turn, and an mbarrier tells apart only neighbouring phases. So neither loader may
+  // get to tile t + 2 kStages of a stage while tile t there is still worked on, nor a working warp to tile t + kStages while t
+  // is not loaded. What keeps them: the working warps that are behind with t are so with every kTogether-th tile after it, a
+  // turn holds one of those, and a warp needs a tile of every second turn. (tests/test_kv4_schedule_model.py visits every state
+  // of these numbers; 5 or 8 stages with 3 tiles together fail.)
   static constexpr int kTurn = 4;
-  static_assert(tiles_at_once(kLongUnit != kUnit) <= kTurn && kStages >= kTurn + tiles_at_once(kLongUnit != kUnit), "stages reused early");
+  static constexpr int kTogether = tiles_at_once(kLongUnit != kUnit);
+  static_assert(kTurn % kTogether == 0 && kStages > kTurn + kTogether, "phases apart by two");
   // shared memory
   static constexpr int kJoinFloats = kWarps * 8 * kNT * kRow;
   static constexpr int kMost = kJoinFloats * 4 / (128 + 512 * 8 * kNT);  // parts of a cut segment that fit there

@@ -1,10 +1,10 @@
 """A model of the ring of tiles in attention over the 4-bit cache (no GPU needed): two loading warps take four tiles in turn,
-groups of working warps take every n-th tile, and a stage's barrier tells apart only neighbouring phases. Under random
-interleavings no stage is filled again before its tile has been worked on, for the numbers of stages and groups the kernel
-uses; with fewer stages than its static_assert asks for, the model shows one that is."""
+groups of working warps take every n-th tile, and a stage's barriers tell apart only neighbouring phases. Every reachable
+state of their progress is visited: no stage is filled again before its tile has been worked on, and no tile worked on before
+it is there, for the numbers of stages and groups the kernel uses; with others that its static_assert refuses, some are."""
 import os
-import random
 import re
+from collections import deque
 
 import pytest
 
@@ -14,57 +14,62 @@ SOURCE = os.path.join(os.path.dirname(moe.__file__), "csrc", "kv4_decode.cu")
 TURN = 4
 
 
-def refilled_early(stages, groups, seed, tiles=60, steps=3000):
-    """Whether a loader fills a stage whose tile is still worked on; one actor moves at a time, by weights that change now and
-    then, so that some fall far behind."""
-    rng = random.Random(seed)
-    actors = range(2 + groups)
-    pick = lambda: [rng.random() ** 4 + 1e-3 for _ in actors]  # noqa: E731
-    weights = pick()
-    done = [0] * stages   # completed phases of a stage's `empty` barrier
-    held = {}             # stage -> the tile in it
-    load = [0, TURN]      # each loader's next tile
-    work = list(range(groups))
-    for _ in range(steps):
-        if rng.random() < 0.02:
-            weights = pick()
-        a = rng.choices(actors, weights)[0]
-        if a < 2:
-            t = load[a]
-            st = t % stages
-            # the wait for the parity of the phase that frees the stage passes when the current phase has the other parity
-            if t < tiles and (done[st] & 1) != (((t // stages) & 1) ^ 1):
-                if st in held or done[st] != t // stages:
-                    return True
-                held[st] = t
-                load[a] = t + 1 if (t + 1) % TURN else t + 1 + TURN
-        else:
-            t = work[a - 2]
-            st = t % stages
-            if t < tiles and held.get(st) == t:
-                del held[st]
-                done[st] += 1
-                work[a - 2] += groups
-    return False
+def search(stages, groups, tiles=60):
+    """None, or what happens too early. A state is each loader's next tile and each group's."""
+    start = (0, TURN) + tuple(range(groups))
+    seen, queue = {start}, deque([start])
+
+    def phases(t, through):  # completed phases of the barrier of t's stage
+        return sum(through(u) for u in range(t % stages, t + 2 * stages + 1, stages))
+
+    while queue:
+        s = queue.popleft()
+        loaded = lambda u: u < s[u // TURN % 2]  # noqa: E731
+        worked = lambda u: u < s[2 + u % groups]  # noqa: E731
+        for i, t in enumerate(s):
+            if t >= tiles:
+                continue
+            # a wait for the parity of a phase passes when the current phase has the other parity
+            if i < 2:
+                done = phases(t, worked)
+                if done & 1 == (t // stages & 1) ^ 1:
+                    continue
+                if done != t // stages:
+                    return "filled", t, s
+                to = t + 1 if (t + 1) % TURN else t + 1 + TURN
+            else:
+                full = phases(t, loaded)
+                if full & 1 == t // stages & 1:
+                    continue
+                if full != t // stages + 1:
+                    return "worked on", t, s
+                to = t + groups
+            n = s[:i] + (to,) + s[i + 1:]
+            if n not in seen:
+                seen.add(n)
+                queue.append(n)
+    assert any(min(s) >= tiles for s in seen), "the ring stands still"
+    return None
 
 
 def constant(name):
     with open(SOURCE, encoding="utf-8") as f:
-        m = re.search(rf"constexpr int {name} = ([^;]+);", f.read())
-    return m[1]
+        return re.search(rf"constexpr int {name} = ([^;]+);", f.read())[1]
 
 
 def test_the_kernels_numbers():
-    """The pairs below are the kernel's: its stages, and the tiles its working warps are at together."""
+    """The pairs below are the kernel's: its stages, and the tiles its working warps are at together (8 warps, 2 or 4 of a tile's
+    8 chunks each)."""
     assert constant("kWarps") == "8" and constant("kUnit") == "2" and constant("kLongUnit") == "kNT == 1 ? 4 : 2"
     assert constant("kStages") == "kNT == 1 ? 9 : 7" and constant("kTurn") == str(TURN)
 
 
 @pytest.mark.parametrize("stages,groups", [(9, 2), (9, 4), (7, 2)])
-def test_no_stage_is_filled_early(stages, groups):
-    assert stages >= TURN + groups
-    assert not any(refilled_early(stages, groups, seed) for seed in range(400))
+def test_nothing_is_early(stages, groups):
+    assert TURN % groups == 0 and stages > TURN + groups
+    assert search(stages, groups) is None
 
 
-def test_the_model_finds_too_few_stages():
-    assert sum(refilled_early(5, 3, seed) for seed in range(50)) > 10
+@pytest.mark.parametrize("stages,groups", [(5, 3), (8, 3), (7, 4), (4, 2)])
+def test_the_model_finds_what_is_early(stages, groups):
+    assert search(stages, groups)[0] in ("filled", "worked on")
