@@ -13,17 +13,17 @@
 // token's 64 sines and cosines and share them through shared memory, and kUnroll pairs of heads are loaded before the
 // first is worked on. (A block per token, with two block barriers around the sines, took 115 us for 8191 tokens of
 // 64 + 8 heads.) Partial and interleaved rotations take the first kernel below, with the partner shuffled in: 8191 tokens
-// of 64 + 8 heads in 59 us interleaved and 69 in halves of 32, where the full rotation in halves takes 56 (44.6 at the copy
-// rate).
+// of 64 + 8 heads in 55 us interleaved and 65 in halves of 32, where the full rotation in halves takes 53 (44.6 at the copy
+// rate; 5.7 TB/s).
 //
 // Positions with several axes (kAxes; include/paged/moe_norm.h): the lanes that compute a pair's sine and cosine look up the
-// pair's axis once and load that axis's position per token; nothing else differs.
+// pair's axis once and load that axis's position per token; nothing else differs (8191 tokens of 64 + 8 heads: 55 us).
 //
 // A 4-bit cache (kFour; include/paged/moe_kv4.h): keys and values are rounded to bf16 as for the bf16 cache, then the 8 (or
 // 4) lanes that hold a group of 32 dimensions share its largest magnitude, taken of the bits as whole numbers (two groups
 // in one shuffle; NaN stands above infinity), and lanes that hold parts of the same stored bytes exchange them, so that a
-// head's 64 bytes of codes leave in 8- or 16-byte stores. Every code is that of the exact quotient: see code4. 9603 tokens of
-// 32 + 2 8 heads in 55.7 us (their bf16 store takes 44.7); with divisions 63.
+// head's 64 bytes of codes leave in 8- or 16-byte stores. Every code is that of the exact quotient: see codes2. 9603 tokens of
+// 32 + 2 8 heads in 49.6 us (4.2 TB/s; their bf16 store takes 41.6, and with divisions it was 7 more).
 //
 // The angle: inv_freq / (2 pi) is kept as a 64-bit fraction of a turn (computed in fp64, rounded once), so
 // pos * fraction modulo 2^64 is the angle modulo one turn without any loss for large pos, and sin and cos are taken of a
@@ -32,6 +32,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "paged_device.cuh"
@@ -93,19 +94,27 @@ __device__ __forceinline__ uint32_t scale_bits(uint32_t top) {
 }
 // What x is multiplied with for its code: 1 / s, 0 for s = 0.
 __device__ __forceinline__ float code_factor(float s) { return s == 0.0f ? 0.0f : __frcp_rn(s); }
-// round(x / s) + 8, halves to even, in the lowest 4 bits. x and s have 8 bits each, so a quotient (at most 7.04) that is not a
-// half is 2^-10 or more away from one, and x * factor is within 2^-20 of it: rounding that to multiples of 2^-11 first makes
-// a half of what is one and no half of what is none. (Infinite and NaN groups get some code.)
-__device__ __forceinline__ uint32_t code4(float x, float factor) {
-  const float near = __fadd_rn(__fadd_rn(x * factor, 6144.0f), -6144.0f);  // 1.5 2^12
-  return __float_as_uint(near + 12582920.0f);                               // 1.5 2^23 + 8
+// round(x / s) + 8, halves to even, in the lowest 4 bits, of two values. x and s have 8 bits each, so a quotient (at most 7.04)
+// that is not a half is 2^-10 or more away from one, and x times the rounded factor is within 2^-21 of it: rounding that to
+// multiples of 2^-11 first makes a half of what is one and no half of what is none. (Infinite and NaN groups get some code.)
+__device__ __forceinline__ void codes2(uint64_t x, uint64_t factor, uint32_t& a, uint32_t& b) {
+  uint64_t v = fma_f32x2(x, factor, pack_f32x2(6144.0f, 6144.0f));  // 1.5 2^12
+  v = add_f32x2(v, pack_f32x2(-6144.0f, -6144.0f));
+  v = add_f32x2(v, pack_f32x2(12582920.0f, 12582920.0f));           // 1.5 2^23 + 8
+  float fa, fb;
+  unpack_f32x2(v, fa, fb);
+  a = __float_as_uint(fa);
+  b = __float_as_uint(fb);
+}
+__device__ __forceinline__ uint64_t pair_of(uint32_t v) {  // two packed bf16 values in fp32
+  return pack_f32x2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 // The same for scales below 2^-100, whose reciprocals may overflow and whose few bits let quotients pass 7.
 __device__ __forceinline__ uint32_t code4_tiny(float x, float s) {
   return static_cast<uint32_t>(min(max(s == 0.0f ? 0 : __float2int_rn(__fdiv_rn(x, s)), -7), 7) + 8);
 }
 constexpr float kTinyScale = 7.8886e-31f;  // 2^-100
-// Four codes, one behind the other (what code4 has above a code's 4 bits are multiples of 2^16).
+// Four codes, one behind the other (what codes2 has above a code's 4 bits are multiples of 2^16).
 __device__ __forceinline__ uint32_t nibbles(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return (a + (b << 4) + (c << 8) + (d << 12)) & 0xffffu;
 }
@@ -113,22 +122,23 @@ __device__ __forceinline__ uint32_t nibbles(uint32_t a, uint32_t b, uint32_t c, 
 // The magnitudes' bits of two packed bf16 values, and the larger of two such in each half.
 __device__ __forceinline__ uint32_t magnitudes(uint32_t v) { return v & 0x7fff7fffu; }
 
-// Head j's block in the 4-bit cache of the token at this slot, at the token's place: keys or values.
-struct Kv4Row {
-  uint8_t* codes;
-  uint8_t* scales;
-};
-__device__ __forceinline__ Kv4Row kv4_row(const QkNormRopeArgs& p, int slot, int j, bool is_v) {
+// The 4-bit cache at a token's place of head 0; what a head adds.
+__device__ __forceinline__ uint8_t* kv4_token(const QkNormRopeArgs& p, int slot) {
   const int in_page = slot & ((1 << p.page_shift) - 1);
-  const int64_t block = ((static_cast<int64_t>(slot >> p.page_shift) * p.h_kv + j) << (p.page_shift - 4)) + (in_page >> 4);
-  uint8_t* at = p.kv4 + block * kKv4Block + (is_v ? kKv4Values : 0);
-  return {at + (in_page & 15) * kKv4RowBytes, at + kKv4Scales + (in_page & 15) * 8};
+  const int64_t block = (static_cast<int64_t>(slot >> p.page_shift) * p.h_kv << (p.page_shift - 4)) + (in_page >> 4);
+  return p.kv4 + block * kKv4Block + (in_page & 15) * kKv4RowBytes;
+}
+__device__ __forceinline__ int64_t kv4_head(const QkNormRopeArgs& p, int j) {
+  return (static_cast<int64_t>(j) << (p.page_shift - 4)) * kKv4Block;
+}
+// The 8 bytes of a row's scales, seen from its codes: 64 bytes of codes and 8 of scales a row, 16 rows.
+__device__ __forceinline__ uint8_t* kv4_scales(uint8_t* codes, int slot) {
+  return codes + kKv4Scales - (slot & 15) * (kKv4RowBytes - 8);
 }
 
 // A head's 128 values in 4 bits, from the 16 lanes that hold 8 of them each (all of a half-warp, lane l dimensions 8 l ..):
 // four lanes share a group, and lanes l, l + 4, l + 8, l + 12 hold the four groups' parts of the same 16 bytes.
-__device__ __forceinline__ void store4_eight(const QkNormRopeArgs& p, const uint4& o, int slot, bool stored, int j, bool is_v,
-                                             int l) {
+__device__ __forceinline__ void store4_eight(uint8_t* codes, const uint4& o, int slot, bool stored, int l) {
   const uint32_t half_warp = 0xffffu << (threadIdx.x & 16);
   const uint32_t v[4] = {o.x, o.y, o.z, o.w};
   uint32_t top = __vmaxu2(__vmaxu2(magnitudes(v[0]), magnitudes(v[1])), __vmaxu2(magnitudes(v[2]), magnitudes(v[3])));
@@ -137,13 +147,13 @@ __device__ __forceinline__ void store4_eight(const QkNormRopeArgs& p, const uint
   for (int d = 1; d < 4; d <<= 1) top = max(top, __shfl_xor_sync(half_warp, top, d, 16));
   const uint32_t sb = scale_bits(top);
   const float s = __uint_as_float(sb << 16);
-  float x[8];
-  unpack8(o, x);
   uint32_t n[8];
   const float factor = code_factor(s);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) n[i] = code4(x[i], factor);
+  for (int i = 0; i < 4; ++i) codes2(pair_of(v[i]), pack_f32x2(factor, factor), n[2 * i], n[2 * i + 1]);
   if (s < kTinyScale) {
+    float x[8];
+    unpack8(o, x);
 #pragma unroll
     for (int i = 0; i < 8; ++i) n[i] = code4_tiny(x[i], s);
   }
@@ -155,17 +165,15 @@ __device__ __forceinline__ void store4_eight(const QkNormRopeArgs& p, const uint
     sw[w] = __shfl_sync(half_warp, sb, 4 * w, 16);
   }
   if (!stored || l >= 4) return;
-  const Kv4Row row = kv4_row(p, slot, j, is_v);
-  *reinterpret_cast<uint4*>(row.codes + 16 * l) =
+  *reinterpret_cast<uint4*>(codes + 16 * l) =
       make_uint4(__byte_perm(cw[0], cw[1], 0x5410), __byte_perm(cw[2], cw[3], 0x5410), __byte_perm(cw[0], cw[1], 0x7632),
                  __byte_perm(cw[2], cw[3], 0x7632));
-  if (l == 0) *reinterpret_cast<uint2*>(row.scales) = make_uint2(sw[0] | sw[1] << 16, sw[2] | sw[3] << 16);
+  if (l == 0) *reinterpret_cast<uint2*>(kv4_scales(codes, slot)) = make_uint2(sw[0] | sw[1] << 16, sw[2] | sw[3] << 16);
 }
 
 // The same where lane l holds dimensions 4 l .. + 3 (a) and 64 + 4 l .. + 3 (b): eight lanes share two groups, lanes l and
 // l + 8 the same 8 bytes.
-__device__ __forceinline__ void store4_halves(const QkNormRopeArgs& p, const uint2& a, const uint2& b, int slot, bool stored,
-                                              int j, bool is_v, int l) {
+__device__ __forceinline__ void store4_halves(uint8_t* codes, const uint2& a, const uint2& b, int slot, bool stored, int l) {
   const uint32_t half_warp = 0xffffu << (threadIdx.x & 16);
   const uint32_t ma = __vmaxu2(magnitudes(a.x), magnitudes(a.y)), mb = __vmaxu2(magnitudes(b.x), magnitudes(b.y));
   uint32_t top = __vmaxu2(__byte_perm(ma, mb, 0x5410), __byte_perm(ma, mb, 0x7632));  // group of a, group of b
@@ -174,13 +182,13 @@ __device__ __forceinline__ void store4_halves(const QkNormRopeArgs& p, const uin
   const uint32_t sa = scale_bits(top << 16), sb = scale_bits(top & 0xffff0000u);
   const float fa = __uint_as_float(sa << 16), fb = __uint_as_float(sb << 16);
   auto four = [](const uint2& v, float s) {
-    const float x[4] = {__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                        __uint_as_float(v.y & 0xffff0000u)};
     const float factor = code_factor(s);
     uint32_t n[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) n[i] = code4(x[i], factor);
+    codes2(pair_of(v.x), pack_f32x2(factor, factor), n[0], n[1]);
+    codes2(pair_of(v.y), pack_f32x2(factor, factor), n[2], n[3]);
     if (s < kTinyScale) {
+      const float x[4] = {__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                          __uint_as_float(v.y & 0xffff0000u)};
 #pragma unroll
       for (int i = 0; i < 4; ++i) n[i] = code4_tiny(x[i], s);
     }
@@ -191,9 +199,8 @@ __device__ __forceinline__ void store4_halves(const QkNormRopeArgs& p, const uin
   const uint32_t s = sa | sb << 16;
   const uint32_t so = __shfl_xor_sync(half_warp, s, 8, 16);
   if (!stored || l >= 8) return;
-  const Kv4Row row = kv4_row(p, slot, j, is_v);
-  *reinterpret_cast<uint2*>(row.codes + 8 * l) = make_uint2(__byte_perm(c, co, 0x5410), __byte_perm(c, co, 0x7632));
-  if (l == 0) *reinterpret_cast<uint2*>(row.scales) = make_uint2(__byte_perm(s, so, 0x5410), __byte_perm(s, so, 0x7632));
+  *reinterpret_cast<uint2*>(codes + 8 * l) = make_uint2(__byte_perm(c, co, 0x5410), __byte_perm(c, co, 0x7632));
+  if (l == 0) *reinterpret_cast<uint2*>(kv4_scales(codes, slot)) = make_uint2(__byte_perm(s, so, 0x5410), __byte_perm(s, so, 0x7632));
 }
 
 // The axis of pair x: what it adds to the positions' address, and whether it turns.
@@ -208,10 +215,57 @@ struct PairAxis {
   }
 };
 
+// The work of a warp: whole tokens in `rounds` rounds over all warps, and then the next `each` of the list of the remaining
+// tokens' units, `token` a token: one for a pair of heads, kKv4Cost for one behind the first `cheap`.
+constexpr int kKv4Cost = 2;
+struct Shares {
+  int rounds, each, token, cheap;
+  int first;  // of the remaining tokens
+  template <bool kFour>
+  __device__ __forceinline__ int pair_at(int units) const {
+    return !kFour || units <= cheap ? units : cheap + (units - cheap + kKv4Cost - 1) / kKv4Cost;
+  }
+};
+struct Walk {
+  int n, from, to;  // a token, units of it
+  int rounds, left;
+  __device__ __forceinline__ Walk(const Shares& s) : rounds(s.rounds), left(s.each) {
+    const int warp = static_cast<int>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    if (rounds == 0) rest(s, warp);
+    else whole(s, warp);
+  }
+  __device__ __forceinline__ void whole(const Shares& s, int token) {
+    n = token;
+    from = 0;
+    to = s.token;
+  }
+  // (The list has fewer than 2^32 units: so many heads do not fit the memory.)
+  __device__ __forceinline__ void rest(const Shares& s, int warp) {
+    const uint32_t at = static_cast<uint32_t>(warp) * static_cast<uint32_t>(s.each);
+    const uint32_t token = at / static_cast<uint32_t>(s.token);
+    n = s.first + static_cast<int>(token);
+    from = static_cast<int>(at - token * static_cast<uint32_t>(s.token));
+    to = min(s.token, from + left);
+  }
+  __device__ __forceinline__ bool more(int N) const { return n < N; }
+  __device__ __forceinline__ void next(const Shares& s, int N) {
+    if (rounds > 0) {
+      const int step = static_cast<int>(gridDim.x) * (kThreads / 32);
+      if (--rounds == 0) rest(s, n + step - s.first);
+      else whole(s, n + step);
+    } else {
+      left -= to - from;
+      n = left > 0 ? n + 1 : N;
+      from = 0;
+      to = min(s.token, left);
+    }
+  }
+};
+
 constexpr int kUnroll = 4;
 
 template <bool kInterleaved, bool kAxes, bool kFour>
-__global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(const QkNormRopeArgs p, int parts, int part_heads) {
+__global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(const QkNormRopeArgs p, const Shares shares) {
   __shared__ __align__(16) float cs[kThreads / 32][2][kD / 2];  // cos, sin of each warp's token
   const int lane = threadIdx.x & 31;
   const int l = lane & 15;       // dimensions 8 l .. 8 l + 7
@@ -248,12 +302,9 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(const QkNormR
     wkp = *reinterpret_cast<const uint4*>(p.k_weight + 8 * partner);
   }
 
-  const int64_t items = static_cast<int64_t>(p.N) * parts;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
-    const int n = static_cast<int>(it / parts);
-    const int first = static_cast<int>(it - static_cast<int64_t>(n) * parts) * part_heads;
-    const int last = min(heads, first + part_heads);
+  for (Walk walk(shares); walk.more(p.N); walk.next(shares, p.N)) {
+    const int n = walk.n;
+    const int first = 2 * shares.pair_at<kFour>(walk.from), last = min(heads, 2 * shares.pair_at<kFour>(walk.to));
     const uint16_t* src = p.qkv + static_cast<int64_t>(n) * p.row_stride + 8 * l;
     int pos[2];
     pos[0] = p.positions[n + (kAxes ? axis[0].offset : 0)];
@@ -294,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(const QkNormR
     // this token's row of head 0 in the caches
     const int64_t row = ((static_cast<int64_t>(slot >> p.page_shift) * p.h_kv << p.page_shift) +
                          (slot & ((1 << p.page_shift) - 1))) * kD + 8 * l;
+    uint8_t* token4 = kFour ? kv4_token(p, stored ? slot : 0) : nullptr;
     for (int h0 = first; h0 < last; h0 += 2 * kUnroll) {
       uint4 w[kUnroll];
 #pragma unroll
@@ -342,7 +394,8 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(const QkNormR
         if (is_q) {
           *reinterpret_cast<uint4*>(p.q_out + (static_cast<int64_t>(n) * p.h_q + h) * kD + 8 * l) = o;
         } else if (kFour) {
-          store4_eight(p, o, slot, stored, is_v ? h - p.h_q - p.h_kv : h - p.h_q, is_v, l);
+          const int j = is_v ? h - p.h_q - p.h_kv : h - p.h_q;
+          store4_eight(token4 + kv4_head(p, j) + (is_v ? kKv4Values : 0), o, slot, stored, l);
         } else if (stored) {
           const int j = is_v ? h - p.h_q - p.h_kv : h - p.h_q;
           *reinterpret_cast<uint4*>((is_v ? p.v_cache : p.k_cache) + row + (static_cast<int64_t>(j) << p.page_shift) * kD) = o;
@@ -358,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(const QkNormR
 constexpr int kUnrollHalves = 4;
 
 template <bool kAxes, bool kFour>
-__global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_halves_kernel(const QkNormRopeArgs p, int parts, int part_heads) {
+__global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_halves_kernel(const QkNormRopeArgs p, const Shares shares) {
   __shared__ __align__(16) float cs[kThreads / 32][2][kD / 2];  // cos, sin of each warp's token
   const int lane = threadIdx.x & 31;
   const int l = lane & 15;
@@ -384,7 +437,6 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_halves_kernel(const 
     w[1][0] = *reinterpret_cast<const uint2*>(p.k_weight + 4 * l);
     w[1][1] = *reinterpret_cast<const uint2*>(p.k_weight + 64 + 4 * l);
   }
-  auto pair = [](uint32_t v) { return pack_f32x2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)); };
   auto round2 = [](uint64_t v) {
     float a, b;
     unpack_f32x2(v, a, b);
@@ -392,12 +444,9 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_halves_kernel(const 
     return *reinterpret_cast<const uint32_t*>(&r);
   };
   const int heads = p.h_q + 2 * p.h_kv;
-  const int64_t items = static_cast<int64_t>(p.N) * parts;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
-    const int n = static_cast<int>(it / parts);
-    const int first = static_cast<int>(it - static_cast<int64_t>(n) * parts) * part_heads;
-    const int last = min(heads, first + part_heads);
+  for (Walk walk(shares); walk.more(p.N); walk.next(shares, p.N)) {
+    const int n = walk.n;
+    const int first = 2 * shares.pair_at<kFour>(walk.from), last = min(heads, 2 * shares.pair_at<kFour>(walk.to));
     const uint16_t* src = p.qkv + static_cast<int64_t>(n) * p.row_stride + 4 * l;
     int pos[2];
     pos[0] = p.positions[n + (kAxes ? axis[0].offset : 0)];
@@ -435,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_halves_kernel(const 
     // this token's row of head 0 in the caches
     const int64_t row = ((static_cast<int64_t>(slot >> p.page_shift) * p.h_kv << p.page_shift) +
                          (slot & ((1 << p.page_shift) - 1))) * kD + 4 * l;
+    uint8_t* token4 = kFour ? kv4_token(p, stored ? slot : 0) : nullptr;
     for (int h0 = first; h0 < last; h0 += 2 * kUnrollHalves) {
       uint2 o[kUnrollHalves][2];
 #pragma unroll
@@ -449,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_halves_kernel(const 
         const int h = h0 + 2 * u + hw;
         const bool is_q = h < p.h_q;
         const bool is_v = h >= p.h_q + p.h_kv;
-        uint64_t x[4] = {pair(o[u][0].x), pair(o[u][0].y), pair(o[u][1].x), pair(o[u][1].y)};
+        uint64_t x[4] = {pair_of(o[u][0].x), pair_of(o[u][0].y), pair_of(o[u][1].x), pair_of(o[u][1].y)};
         uint64_t sq = mul_f32x2(x[0], x[0]);
 #pragma unroll
         for (int i = 1; i < 4; ++i) sq = fma_f32x2(x[i], x[i], sq);
@@ -464,10 +514,10 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_halves_kernel(const 
             const float r = rsqrtf(sum * (1.0f / kD) + p.eps);
             const uint64_t r2 = pack_f32x2(r, r);
             const uint2 wa = is_q ? w[0][0] : w[1][0], wb = is_q ? w[0][1] : w[1][1];
-            x[0] = mul_f32x2(x[0], mul_f32x2(r2, pair(wa.x)));
-            x[1] = mul_f32x2(x[1], mul_f32x2(r2, pair(wa.y)));
-            x[2] = mul_f32x2(x[2], mul_f32x2(r2, pair(wb.x)));
-            x[3] = mul_f32x2(x[3], mul_f32x2(r2, pair(wb.y)));
+            x[0] = mul_f32x2(x[0], mul_f32x2(r2, pair_of(wa.x)));
+            x[1] = mul_f32x2(x[1], mul_f32x2(r2, pair_of(wa.y)));
+            x[2] = mul_f32x2(x[2], mul_f32x2(r2, pair_of(wb.x)));
+            x[3] = mul_f32x2(x[3], mul_f32x2(r2, pair_of(wb.y)));
           }
           o[u][0].x = round2(fma_f32x2(x[0], c[0], mul_f32x2(x[2], ns[0])));
           o[u][0].y = round2(fma_f32x2(x[1], c[1], mul_f32x2(x[3], ns[1])));
@@ -478,7 +528,8 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_halves_kernel(const 
         if (is_q) {
           to = p.q_out + (static_cast<int64_t>(n) * p.h_q + h) * kD + 4 * l;
         } else if (kFour) {
-          store4_halves(p, o[u][0], o[u][1], slot, stored, is_v ? h - p.h_q - p.h_kv : h - p.h_q, is_v, l);
+          const int j = is_v ? h - p.h_q - p.h_kv : h - p.h_q;
+          store4_halves(token4 + kv4_head(p, j) + (is_v ? kKv4Values : 0), o[u][0], o[u][1], slot, stored, l);
         } else if (stored) {
           const int j = is_v ? h - p.h_q - p.h_kv : h - p.h_q;
           to = (is_v ? p.v_cache : p.k_cache) + row + (static_cast<int64_t>(j) << p.page_shift) * kD;
@@ -495,28 +546,38 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_halves_kernel(const 
 }  // namespace qk
 
 cudaError_t launch_qk_norm_rope(const QkNormRopeArgs& args, int num_sms, cudaStream_t stream) {
-  // A token's heads are cut into equal runs (of pairs of heads), each a warp's work: the runs that make the rounds over
-  // the resident warps cheapest, counting a run's start (positions, sines, the first loads) as 4 pairs. 8191 tokens of
-  // 72 heads: 61 us uncut (a third of the warps idle in the last round), 56 us (5.4 TB/s) as chosen here.
+  // Whole tokens in rounds over the warps, as long as there is one for each, in the caches' order; what remains is cut into
+  // equal shares, a warp each, of one token where that is hardly more per warp (a start costs as much as some pairs), else
+  // across tokens. (Every token cut alike, so that the last round was partly empty: 2000 tokens of 72 heads 17.9 us instead of
+  // 16.1, 8191 56.9 instead of 53.2. Shares across tokens alone: 16000 105 us instead of 99, warps far apart in the caches.)
+  // A 4-bit cache has shares across tokens alone, with its heads counted twice: 9603 tokens of 48 heads 49.6 us, in rounds 52.
+  // More than a block an SM costs calls that follow one another closely 1 us, so few tokens' warps take two pairs where that
+  // avoids it: 64 tokens of 40 heads 3.9 -> 3.2 us (for a 4-bit cache, whose pairs take longer, it does not pay).
   const bool halves = args.rot == qk::kD && !args.interleaved;
-  const int64_t warps = static_cast<int64_t>(num_sms) * (halves ? 3 : 2) * (qk::kThreads / 32);
+  const bool axes = args.pair_axis != nullptr, four = args.kv4 != nullptr;
+  constexpr int kPerBlock = qk::kThreads / 32;
+  const int64_t sm_warps = static_cast<int64_t>(num_sms) * kPerBlock, warps = sm_warps * (halves ? 3 : 2);
   const int pairs = (args.h_q + 2 * args.h_kv + 1) / 2;
-  int parts = 1, part_heads = 2 * pairs;
-  int64_t least = 0;
-  for (int run = pairs; run >= 1; run -= run > 64 ? run / 64 : 1) {
-    const int n = (pairs + run - 1) / run;
-    const int64_t cost = (args.N * static_cast<int64_t>(n) + warps - 1) / warps * (run + 4);
-    if (least == 0 || cost < least) {
-      least = cost;
-      parts = n;
-      part_heads = 2 * run;
+  qk::Shares shares;
+  shares.rounds = four ? 0 : static_cast<int>(args.N / warps);
+  shares.first = static_cast<int>(shares.rounds * warps);
+  const int64_t rest = args.N - shares.first;
+  shares.cheap = four ? args.h_q / 2 : pairs;
+  shares.token = shares.cheap + (pairs - shares.cheap) * qk::kKv4Cost;
+  shares.each = static_cast<int>((rest * shares.token + warps - 1) / warps);
+  if (rest > 0 && rest <= warps) {
+    const int parts = static_cast<int>(std::min<int64_t>(warps / rest, pairs));
+    int cut = (pairs + parts - 1) / parts;
+    if (!four && cut == 1 && rest * pairs > sm_warps && rest * ((pairs + 1) / 2) <= sm_warps) cut = 2;
+    const int even = static_cast<int>((rest * pairs + warps - 1) / warps);
+    if (even <= 2 || cut <= even + (four ? 0 : 1) + 4 * even / pairs) {
+      shares.each = cut;
+      shares.cheap = shares.token = (pairs + cut - 1) / cut * cut;
     }
   }
-  const int64_t blocks = (static_cast<int64_t>(args.N) * parts + qk::kThreads / 32 - 1) / (qk::kThreads / 32);
-  const int64_t resident = warps / (qk::kThreads / 32);
-  const int grid = static_cast<int>(blocks < resident ? blocks : resident);
-  using Kernel = void (*)(QkNormRopeArgs, int, int);
-  const bool axes = args.pair_axis != nullptr, four = args.kv4 != nullptr;
+  const int64_t used = shares.rounds > 0 ? warps : (rest * shares.token + shares.each - 1) / shares.each;
+  const int grid = static_cast<int>((used + kPerBlock - 1) / kPerBlock);
+  using Kernel = void (*)(QkNormRopeArgs, qk::Shares);
   static constexpr Kernel kHalves[2][2] = {
       {qk::qk_norm_rope_halves_kernel<false, false>, qk::qk_norm_rope_halves_kernel<false, true>},
       {qk::qk_norm_rope_halves_kernel<true, false>, qk::qk_norm_rope_halves_kernel<true, true>}};
@@ -526,7 +587,7 @@ cudaError_t launch_qk_norm_rope(const QkNormRopeArgs& args, int num_sms, cudaStr
       {{qk::qk_norm_rope_kernel<true, false, false>, qk::qk_norm_rope_kernel<true, false, true>},
        {qk::qk_norm_rope_kernel<true, true, false>, qk::qk_norm_rope_kernel<true, true, true>}}};
   const Kernel kernel = halves ? kHalves[axes][four] : kGeneral[args.interleaved][axes][four];
-  return launch_pdl(kernel, dim3(grid), dim3(qk::kThreads), 0, stream, args, parts, part_heads);
+  return launch_pdl(kernel, dim3(grid), dim3(qk::kThreads), 0, stream, args, shares);
 }
 
 }  // namespace moe

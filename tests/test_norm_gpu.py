@@ -227,6 +227,39 @@ def test_pairs_of_no_axis_do_not_turn():
         assert torch.equal(q[..., still], x[:, :h_q][..., still]) and not torch.equal(q, x[:, :h_q])
 
 
+@pytest.mark.parametrize("rot,interleaved", [(128, False), (64, False), (128, True)])
+@pytest.mark.parametrize("h_q,h_kv", [(32, 4), (3, 1), (20, 20)])
+@pytest.mark.parametrize("four", [False, True])
+def test_many_tokens_are_as_few(rot, interleaved, h_q, h_kv, four):
+    """A call's work is shared out by its size; every token is as in a call of a few."""
+    page, heads = 64, h_q + 2 * h_kv
+    w = randn(D, seed=1)
+    inv = (10000.0 ** (-torch.arange(rot // 2) * 2 / rot)).float().to(DEV)
+    for N in (61, 500, 1217, 2000, 2433, 3649, 5000, 7400):
+        qkv = randn(N, heads * D, seed=N)
+        positions = torch.arange(N, dtype=torch.int32, device=DEV) * 7
+        slots = torch.randperm(N, generator=torch.Generator().manual_seed(2)).to(torch.int32).to(DEV)
+        outs = []
+        for step_tokens in (N, 97):
+            q = torch.full((N, h_q, D), -9.0, dtype=torch.bfloat16, device=DEV)
+            if four:
+                cache = (moe.alloc_kv4_cache((N + page - 1) // page, h_kv, page).fill_(7),)  # (rows behind N stay)
+            else:
+                cache = tuple(torch.full(((N + page - 1) // page, h_kv, page, D), -9.0, dtype=torch.bfloat16, device=DEV)
+                              for _ in range(2))
+            for at in range(0, N, step_tokens):
+                to = min(N, at + step_tokens)
+                part = (qkv[at:to], w, w, EPS, inv)
+                if four:
+                    moe.moe_qk_norm_rope_kv4(*part, None, positions[at:to], slots[at:to], q[at:to], *cache,
+                                             interleaved=interleaved)
+                else:
+                    moe.moe_qk_norm_rope(*part, positions[at:to], slots[at:to], q[at:to], *cache, interleaved=interleaved)
+            outs.append((q, *cache))
+        for a, b in zip(*outs):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), N
+
+
 # ---------------------------------------------------------------- around the experts
 def test_a_layer_step_with_the_experts():
     """Residual and norm in front of the routed experts and behind them, as a layer runs them."""
