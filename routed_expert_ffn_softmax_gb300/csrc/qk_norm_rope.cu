@@ -84,18 +84,28 @@ __device__ __forceinline__ uint64_t turn_fraction(float inv_freq) {
   return static_cast<uint64_t>(__double2ull_rn(f * 18446744073709551616.0));
 }
 
-// The scale of a group whose largest magnitude has these bf16 bits (in the upper half): a 7th of it, in bf16. (The product
-// with the rounded 1/7 is within 2^-23 of the 7th, which is representable or 2^-12 or more away from where rounding turns.)
-// NaN for infinity.
-__device__ __forceinline__ uint32_t scale_bits(uint32_t top) {
-  if (top >= 0x7f800000u) return 0x7fc0u;
-  const __nv_bfloat16 s = __float2bfloat16_rn(__uint_as_float(top) * (1.0f / 7.0f));
-  return *reinterpret_cast<const uint16_t*>(&s);
+__device__ __forceinline__ uint64_t pair_of(uint32_t v) {  // two packed bf16 values in fp32
+  return pack_f32x2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
-// What x is multiplied with for its code: 1 / s, 0 for s = 0.
-__device__ __forceinline__ float code_factor(float s) { return s == 0.0f ? 0.0f : __frcp_rn(s); }
+
+// The scales of two groups whose largest magnitudes are packed here: a 7th, in bf16. (The product with the rounded 1/7 is within
+// 2^-23 of the 7th, which is representable or 2^-12 or more away from where rounding turns.) Infinity times 0 makes it NaN.
+__device__ __forceinline__ uint32_t scales2(uint32_t top) {
+  const uint64_t x = pair_of(top);
+  const uint64_t seventh = fma_f32x2(x, pack_f32x2(1.0f / 7.0f, 1.0f / 7.0f), mul_f32x2(x, pack_f32x2(0.0f, 0.0f)));
+  float a, b;
+  unpack_f32x2(seventh, a, b);
+  const __nv_bfloat162 s = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&s);
+}
+// What x is multiplied with for its code: 1 / s, within 2^-23. (Infinity for scales that code4_tiny deals with.)
+__device__ __forceinline__ float code_factor(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
 // round(x / s) + 8, halves to even, in the lowest 4 bits, of two values. x and s have 8 bits each, so a quotient (at most 7.04)
-// that is not a half is 2^-10 or more away from one, and x times the rounded factor is within 2^-21 of it: rounding that to
+// that is not a half is 2^-10 or more away from one, and x times the factor is within 2^-20 of it: rounding that to
 // multiples of 2^-11 first makes a half of what is one and no half of what is none. (Infinite and NaN groups get some code.)
 __device__ __forceinline__ void codes2(uint64_t x, uint64_t factor, uint32_t& a, uint32_t& b) {
   uint64_t v = fma_f32x2(x, factor, pack_f32x2(6144.0f, 6144.0f));  // 1.5 2^12
@@ -106,47 +116,45 @@ __device__ __forceinline__ void codes2(uint64_t x, uint64_t factor, uint32_t& a,
   a = __float_as_uint(fa);
   b = __float_as_uint(fb);
 }
-__device__ __forceinline__ uint64_t pair_of(uint32_t v) {  // two packed bf16 values in fp32
-  return pack_f32x2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-}
 // The same for scales below 2^-100, whose reciprocals may overflow and whose few bits let quotients pass 7.
 __device__ __forceinline__ uint32_t code4_tiny(float x, float s) {
   return static_cast<uint32_t>(min(max(s == 0.0f ? 0 : __float2int_rn(__fdiv_rn(x, s)), -7), 7) + 8);
 }
 constexpr float kTinyScale = 7.8886e-31f;  // 2^-100
-// Four codes, one behind the other (what codes2 has above a code's 4 bits are multiples of 2^16).
-__device__ __forceinline__ uint32_t nibbles(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  return (a + (b << 4) + (c << 8) + (d << 12)) & 0xffffu;
+// Eight codes, one behind the other in fours: the first four in the lower half. (What codes2 has above a code's 4 bits are
+// multiples of 2^16.)
+__device__ __forceinline__ uint32_t nibbles8(const uint32_t (&n)[8]) {
+  const uint32_t a = n[0] + (n[1] << 4) + (n[2] << 8) + (n[3] << 12), b = n[4] + (n[5] << 4) + (n[6] << 8) + (n[7] << 12);
+  return __byte_perm(a, b, 0x5410);
 }
 
 // The magnitudes' bits of two packed bf16 values, and the larger of two such in each half.
 __device__ __forceinline__ uint32_t magnitudes(uint32_t v) { return v & 0x7fff7fffu; }
 
-// The 4-bit cache at a token's place of head 0; what a head adds.
-__device__ __forceinline__ uint8_t* kv4_token(const QkNormRopeArgs& p, int slot) {
-  const int in_page = slot & ((1 << p.page_shift) - 1);
-  const int64_t block = (static_cast<int64_t>(slot >> p.page_shift) * p.h_kv << (p.page_shift - 4)) + (in_page >> 4);
-  return p.kv4 + block * kKv4Block + (in_page & 15) * kKv4RowBytes;
-}
-__device__ __forceinline__ int64_t kv4_head(const QkNormRopeArgs& p, int j) {
-  return (static_cast<int64_t>(j) << (p.page_shift - 4)) * kKv4Block;
-}
-// The 8 bytes of a row's scales, seen from its codes: 64 bytes of codes and 8 of scales a row, 16 rows.
-__device__ __forceinline__ uint8_t* kv4_scales(uint8_t* codes, int slot) {
-  return codes + kKv4Scales - (slot & 15) * (kKv4RowBytes - 8);
-}
+// Where a token's rows are in the 4-bit cache: those of head 0, what a head adds, and a row's scales seen from its codes.
+struct Kv4Place {
+  uint8_t* codes;
+  int64_t head;
+  int scales;
+  __device__ __forceinline__ Kv4Place(const QkNormRopeArgs& p, int slot) {
+    const int in_page = slot & ((1 << p.page_shift) - 1);
+    head = static_cast<int64_t>(kKv4Block) << (p.page_shift - 4);
+    codes = p.kv4 + static_cast<int64_t>(slot >> p.page_shift) * p.h_kv * head + (in_page >> 4) * kKv4Block +
+            (in_page & 15) * kKv4RowBytes;
+    scales = kKv4Scales - (in_page & 15) * (kKv4RowBytes - 8);
+  }
+};
 
-// A head's 128 values in 4 bits, from the 16 lanes that hold 8 of them each (all of a half-warp, lane l dimensions 8 l ..):
+// Two heads' 128 values each in 4 bits, from the 16 lanes that hold 8 of them each (all of a warp, lane l dimensions 8 l ..):
 // four lanes share a group, and lanes l, l + 4, l + 8, l + 12 hold the four groups' parts of the same 16 bytes.
-__device__ __forceinline__ void store4_eight(uint8_t* codes, const uint4& o, int slot, bool stored, int l) {
-  const uint32_t half_warp = 0xffffu << (threadIdx.x & 16);
+__device__ __forceinline__ void store4_eight(uint8_t* codes, int scales, const uint4& o, bool stored, int l) {
   const uint32_t v[4] = {o.x, o.y, o.z, o.w};
   uint32_t top = __vmaxu2(__vmaxu2(magnitudes(v[0]), magnitudes(v[1])), __vmaxu2(magnitudes(v[2]), magnitudes(v[3])));
   top = max(top << 16, top & 0xffff0000u);
 #pragma unroll
-  for (int d = 1; d < 4; d <<= 1) top = max(top, __shfl_xor_sync(half_warp, top, d, 16));
-  const uint32_t sb = scale_bits(top);
-  const float s = __uint_as_float(sb << 16);
+  for (int d = 1; d < 4; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const uint32_t sb = scales2(top);  // (in the upper half)
+  const float s = __uint_as_float(sb & 0xffff0000u);
   uint32_t n[8];
   const float factor = code_factor(s);
 #pragma unroll
@@ -157,50 +165,46 @@ __device__ __forceinline__ void store4_eight(uint8_t* codes, const uint4& o, int
 #pragma unroll
     for (int i = 0; i < 8; ++i) n[i] = code4_tiny(x[i], s);
   }
-  const uint32_t c = nibbles(n[0], n[1], n[2], n[3]) | nibbles(n[4], n[5], n[6], n[7]) << 16;
+  const uint32_t c = nibbles8(n);
   uint32_t cw[4], sw[4];
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    cw[w] = __shfl_sync(half_warp, c, (l & 3) + 4 * w, 16);
-    sw[w] = __shfl_sync(half_warp, sb, 4 * w, 16);
+    cw[w] = __shfl_sync(0xffffffffu, c, (l & 3) + 4 * w, 16);
+    sw[w] = __shfl_sync(0xffffffffu, sb, 4 * w, 16);
   }
   if (!stored || l >= 4) return;
   *reinterpret_cast<uint4*>(codes + 16 * l) =
       make_uint4(__byte_perm(cw[0], cw[1], 0x5410), __byte_perm(cw[2], cw[3], 0x5410), __byte_perm(cw[0], cw[1], 0x7632),
                  __byte_perm(cw[2], cw[3], 0x7632));
-  if (l == 0) *reinterpret_cast<uint2*>(kv4_scales(codes, slot)) = make_uint2(sw[0] | sw[1] << 16, sw[2] | sw[3] << 16);
+  if (l == 0)
+    *reinterpret_cast<uint2*>(codes + scales) = make_uint2(__byte_perm(sw[0], sw[1], 0x7632), __byte_perm(sw[2], sw[3], 0x7632));
 }
 
 // The same where lane l holds dimensions 4 l .. + 3 (a) and 64 + 4 l .. + 3 (b): eight lanes share two groups, lanes l and
 // l + 8 the same 8 bytes.
-__device__ __forceinline__ void store4_halves(uint8_t* codes, const uint2& a, const uint2& b, int slot, bool stored, int l) {
-  const uint32_t half_warp = 0xffffu << (threadIdx.x & 16);
+__device__ __forceinline__ void store4_halves(uint8_t* codes, int scales, const uint2& a, const uint2& b, bool stored, int l) {
   const uint32_t ma = __vmaxu2(magnitudes(a.x), magnitudes(a.y)), mb = __vmaxu2(magnitudes(b.x), magnitudes(b.y));
   uint32_t top = __vmaxu2(__byte_perm(ma, mb, 0x5410), __byte_perm(ma, mb, 0x7632));  // group of a, group of b
 #pragma unroll
-  for (int d = 1; d < 8; d <<= 1) top = __vmaxu2(top, __shfl_xor_sync(half_warp, top, d, 16));
-  const uint32_t sa = scale_bits(top << 16), sb = scale_bits(top & 0xffff0000u);
-  const float fa = __uint_as_float(sa << 16), fb = __uint_as_float(sb << 16);
-  auto four = [](const uint2& v, float s) {
-    const float factor = code_factor(s);
-    uint32_t n[4];
-    codes2(pair_of(v.x), pack_f32x2(factor, factor), n[0], n[1]);
-    codes2(pair_of(v.y), pack_f32x2(factor, factor), n[2], n[3]);
-    if (s < kTinyScale) {
-      const float x[4] = {__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                          __uint_as_float(v.y & 0xffff0000u)};
+  for (int d = 1; d < 8; d <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const uint32_t s = scales2(top);
+  const float sa = __uint_as_float(s << 16), sb = __uint_as_float(s & 0xffff0000u);
+  const float fa = code_factor(sa), fb = code_factor(sb);
+  const uint32_t v[4] = {a.x, a.y, b.x, b.y};
+  uint32_t n[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) n[i] = code4_tiny(x[i], s);
-    }
-    return nibbles(n[0], n[1], n[2], n[3]);
-  };
-  const uint32_t c = four(a, fa) | four(b, fb) << 16;  // lanes below 8: groups 0 and 2, the others 1 and 3
-  const uint32_t co = __shfl_xor_sync(half_warp, c, 8, 16);
-  const uint32_t s = sa | sb << 16;
-  const uint32_t so = __shfl_xor_sync(half_warp, s, 8, 16);
+  for (int i = 0; i < 4; ++i) codes2(pair_of(v[i]), i < 2 ? pack_f32x2(fa, fa) : pack_f32x2(fb, fb), n[2 * i], n[2 * i + 1]);
+  if (fminf(sa, sb) < kTinyScale) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      n[i] = code4_tiny(__uint_as_float(i & 1 ? v[i >> 1] & 0xffff0000u : v[i >> 1] << 16), i < 4 ? sa : sb);
+  }
+  const uint32_t c = nibbles8(n);  // lanes below 8: groups 0 and 2, the others 1 and 3
+  const uint32_t co = __shfl_xor_sync(0xffffffffu, c, 8);
+  const uint32_t so = __shfl_xor_sync(0xffffffffu, s, 8);
   if (!stored || l >= 8) return;
   *reinterpret_cast<uint2*>(codes + 8 * l) = make_uint2(__byte_perm(c, co, 0x5410), __byte_perm(c, co, 0x7632));
-  if (l == 0) *reinterpret_cast<uint2*>(kv4_scales(codes, slot)) = make_uint2(__byte_perm(s, so, 0x5410), __byte_perm(s, so, 0x7632));
+  if (l == 0) *reinterpret_cast<uint2*>(codes + scales) = make_uint2(__byte_perm(s, so, 0x5410), __byte_perm(s, so, 0x7632));
 }
 
 // The axis of pair x: what it adds to the positions' address, and whether it turns.
@@ -345,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(const QkNormR
     // this token's row of head 0 in the caches
     const int64_t row = ((static_cast<int64_t>(slot >> p.page_shift) * p.h_kv << p.page_shift) +
                          (slot & ((1 << p.page_shift) - 1))) * kD + 8 * l;
-    uint8_t* token4 = kFour ? kv4_token(p, stored ? slot : 0) : nullptr;
+    const Kv4Place place(p, stored ? slot : 0);
     for (int h0 = first; h0 < last; h0 += 2 * kUnroll) {
       uint4 w[kUnroll];
 #pragma unroll
@@ -353,52 +357,55 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(const QkNormR
       if (h0 + 2 * kUnroll < last) load(h0 + 2 * kUnroll);
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        if (h0 + 2 * u >= last) break;
-        const int h = h0 + 2 * u + hw;
+        const int pair = h0 + 2 * u;  // its first head
+        if (pair >= last) break;
+        const int h = pair + hw;
         const bool is_q = h < p.h_q;
-        const bool is_v = h >= p.h_q + p.h_kv;
         uint4 o = w[u];
-        float x[8], y[8];
-        unpack8(o, x);
-        float ss = 0.0f;
+        if (pair < p.h_q + p.h_kv) {  // not both values
+          float x[8], y[8];
+          unpack8(o, x);
+          float ss = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+          for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
-        for (int d = 8; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-        if (!kInterleaved) {
-          uint4 q;
-          q.x = __shfl_sync(0xffffffffu, o.x, partner, 16);
-          q.y = __shfl_sync(0xffffffffu, o.y, partner, 16);
-          q.z = __shfl_sync(0xffffffffu, o.z, partner, 16);
-          q.w = __shfl_sync(0xffffffffu, o.w, partner, 16);
-          unpack8(q, y);
-        }
-        if (h >= last) continue;
-        if (!is_v) {
-          if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
-            const float r = rsqrtf(ss * (1.0f / kD) + p.eps);
-            float wx[8], wy[8];
-            unpack8(is_q ? wq : wk, wx);
-            unpack8(is_q ? wqp : wkp, wy);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              x[i] *= r * wx[i];
-              if (!kInterleaved) y[i] *= r * wy[i];
-            }
+          for (int d = 8; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+          if (!kInterleaved) {
+            uint4 q;
+            q.x = __shfl_sync(0xffffffffu, o.x, partner, 16);
+            q.y = __shfl_sync(0xffffffffu, o.y, partner, 16);
+            q.z = __shfl_sync(0xffffffffu, o.z, partner, 16);
+            q.w = __shfl_sync(0xffffffffu, o.w, partner, 16);
+            unpack8(q, y);
           }
-          float z[8];
+          if (h < p.h_q + p.h_kv) {
+            if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
+              const float r = rsqrtf(ss * (1.0f / kD) + p.eps);
+              float wx[8], wy[8];
+              unpack8(is_q ? wq : wk, wx);
+              unpack8(is_q ? wqp : wkp, wy);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = rotates ? fmaf(x[i], c8[i], (kInterleaved ? x[i ^ 1] : y[i]) * s8[i]) : x[i];
-          o = pack8(z);
+              for (int i = 0; i < 8; ++i) {
+                x[i] *= r * wx[i];
+                if (!kInterleaved) y[i] *= r * wy[i];
+              }
+            }
+            float z[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = rotates ? fmaf(x[i], c8[i], (kInterleaved ? x[i ^ 1] : y[i]) * s8[i]) : x[i];
+            o = pack8(z);
+          }
         }
-        if (is_q) {
+        if (pair < p.h_q && is_q && h < last)
           *reinterpret_cast<uint4*>(p.q_out + (static_cast<int64_t>(n) * p.h_q + h) * kD + 8 * l) = o;
-        } else if (kFour) {
+        if (pair + 1 >= p.h_q) {
+          const bool is_v = h >= p.h_q + p.h_kv;
           const int j = is_v ? h - p.h_q - p.h_kv : h - p.h_q;
-          store4_eight(token4 + kv4_head(p, j) + (is_v ? kKv4Values : 0), o, slot, stored, l);
-        } else if (stored) {
-          const int j = is_v ? h - p.h_q - p.h_kv : h - p.h_q;
-          *reinterpret_cast<uint4*>((is_v ? p.v_cache : p.k_cache) + row + (static_cast<int64_t>(j) << p.page_shift) * kD) = o;
+          const bool stores = stored && !is_q && h < last;
+          if constexpr (kFour)
+            store4_eight(place.codes + j * place.head + (is_v ? kKv4Values : 0), place.scales, o, stores, l);
+          else if (stores)
+            *reinterpret_cast<uint4*>((is_v ? p.v_cache : p.k_cache) + row + (static_cast<int64_t>(j) << p.page_shift) * kD) = o;
         }
       }
     }
@@ -484,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_halves_kernel(const 
     // this token's row of head 0 in the caches
     const int64_t row = ((static_cast<int64_t>(slot >> p.page_shift) * p.h_kv << p.page_shift) +
                          (slot & ((1 << p.page_shift) - 1))) * kD + 4 * l;
-    uint8_t* token4 = kFour ? kv4_token(p, stored ? slot : 0) : nullptr;
+    const Kv4Place place(p, stored ? slot : 0);
     for (int h0 = first; h0 < last; h0 += 2 * kUnrollHalves) {
       uint2 o[kUnrollHalves][2];
 #pragma unroll
@@ -495,48 +502,52 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_halves_kernel(const 
       if (h0 + 2 * kUnrollHalves < last) load(h0 + 2 * kUnrollHalves);
 #pragma unroll
       for (int u = 0; u < kUnrollHalves; ++u) {
-        if (h0 + 2 * u >= last) break;
-        const int h = h0 + 2 * u + hw;
+        const int first_h = h0 + 2 * u;
+        if (first_h >= last) break;
+        const int h = first_h + hw;
         const bool is_q = h < p.h_q;
-        const bool is_v = h >= p.h_q + p.h_kv;
-        uint64_t x[4] = {pair_of(o[u][0].x), pair_of(o[u][0].y), pair_of(o[u][1].x), pair_of(o[u][1].y)};
-        uint64_t sq = mul_f32x2(x[0], x[0]);
+        if (first_h < p.h_q + p.h_kv) {  // not both values
+          uint64_t x[4] = {pair_of(o[u][0].x), pair_of(o[u][0].y), pair_of(o[u][1].x), pair_of(o[u][1].y)};
+          uint64_t sq = mul_f32x2(x[0], x[0]);
 #pragma unroll
-        for (int i = 1; i < 4; ++i) sq = fma_f32x2(x[i], x[i], sq);
-        float s0, s1;
-        unpack_f32x2(sq, s0, s1);
-        float sum = s0 + s1;
+          for (int i = 1; i < 4; ++i) sq = fma_f32x2(x[i], x[i], sq);
+          float s0, s1;
+          unpack_f32x2(sq, s0, s1);
+          float sum = s0 + s1;
 #pragma unroll
-        for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (h >= last) continue;
-        if (!is_v) {
-          if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
-            const float r = rsqrtf(sum * (1.0f / kD) + p.eps);
-            const uint64_t r2 = pack_f32x2(r, r);
-            const uint2 wa = is_q ? w[0][0] : w[1][0], wb = is_q ? w[0][1] : w[1][1];
-            x[0] = mul_f32x2(x[0], mul_f32x2(r2, pair_of(wa.x)));
-            x[1] = mul_f32x2(x[1], mul_f32x2(r2, pair_of(wa.y)));
-            x[2] = mul_f32x2(x[2], mul_f32x2(r2, pair_of(wb.x)));
-            x[3] = mul_f32x2(x[3], mul_f32x2(r2, pair_of(wb.y)));
+          for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          if (h < p.h_q + p.h_kv) {
+            if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
+              const float r = rsqrtf(sum * (1.0f / kD) + p.eps);
+              const uint64_t r2 = pack_f32x2(r, r);
+              const uint2 wa = is_q ? w[0][0] : w[1][0], wb = is_q ? w[0][1] : w[1][1];
+              x[0] = mul_f32x2(x[0], mul_f32x2(r2, pair_of(wa.x)));
+              x[1] = mul_f32x2(x[1], mul_f32x2(r2, pair_of(wa.y)));
+              x[2] = mul_f32x2(x[2], mul_f32x2(r2, pair_of(wb.x)));
+              x[3] = mul_f32x2(x[3], mul_f32x2(r2, pair_of(wb.y)));
+            }
+            o[u][0].x = round2(fma_f32x2(x[0], c[0], mul_f32x2(x[2], ns[0])));
+            o[u][0].y = round2(fma_f32x2(x[1], c[1], mul_f32x2(x[3], ns[1])));
+            o[u][1].x = round2(fma_f32x2(x[2], c[0], mul_f32x2(x[0], s[0])));
+            o[u][1].y = round2(fma_f32x2(x[3], c[1], mul_f32x2(x[1], s[1])));
           }
-          o[u][0].x = round2(fma_f32x2(x[0], c[0], mul_f32x2(x[2], ns[0])));
-          o[u][0].y = round2(fma_f32x2(x[1], c[1], mul_f32x2(x[3], ns[1])));
-          o[u][1].x = round2(fma_f32x2(x[2], c[0], mul_f32x2(x[0], s[0])));
-          o[u][1].y = round2(fma_f32x2(x[3], c[1], mul_f32x2(x[1], s[1])));
         }
-        uint16_t* to = nullptr;
-        if (is_q) {
-          to = p.q_out + (static_cast<int64_t>(n) * p.h_q + h) * kD + 4 * l;
-        } else if (kFour) {
-          const int j = is_v ? h - p.h_q - p.h_kv : h - p.h_q;
-          store4_halves(token4 + kv4_head(p, j) + (is_v ? kKv4Values : 0), o[u][0], o[u][1], slot, stored, l);
-        } else if (stored) {
-          const int j = is_v ? h - p.h_q - p.h_kv : h - p.h_q;
-          to = (is_v ? p.v_cache : p.k_cache) + row + (static_cast<int64_t>(j) << p.page_shift) * kD;
-        }
-        if (to) {
+        if (first_h < p.h_q && is_q && h < last) {
+          uint16_t* to = p.q_out + (static_cast<int64_t>(n) * p.h_q + h) * kD + 4 * l;
           *reinterpret_cast<uint2*>(to) = o[u][0];
           *reinterpret_cast<uint2*>(to + 64) = o[u][1];
+        }
+        if (first_h + 1 >= p.h_q) {
+          const bool is_v = h >= p.h_q + p.h_kv;
+          const int j = is_v ? h - p.h_q - p.h_kv : h - p.h_q;
+          const bool stores = stored && !is_q && h < last;
+          if constexpr (kFour) {
+            store4_halves(place.codes + j * place.head + (is_v ? kKv4Values : 0), place.scales, o[u][0], o[u][1], stores, l);
+          } else if (stores) {
+            uint16_t* to = (is_v ? p.v_cache : p.k_cache) + row + (static_cast<int64_t>(j) << p.page_shift) * kD;
+            *reinterpret_cast<uint2*>(to) = o[u][0];
+            *reinterpret_cast<uint2*>(to + 64) = o[u][1];
+          }
         }
       }
     }
