@@ -4,8 +4,8 @@
 //   y = x * rsqrt(mean(x^2) + eps) * w,   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = pos * inv_freq
 //
 // Each value is read once and written once (2 B each way), so HBM bounds it. A head's 128 values are 16 lanes of
-// 16 bytes, so a warp holds two heads and one load or store instruction moves 512 contiguous bytes; the mean is
-// four shuffles. The partner of a rotated pair sits rot / 2 dimensions away in another lane and comes by
+// 16 bytes, so a warp holds two heads and one load or store instruction moves 512 contiguous bytes; the mean comes by
+// shuffles. The partner of a rotated pair sits rot / 2 dimensions away in another lane and comes by
 // shuffling the packed bf16 inputs (four shuffles for eight values); the partner's norm factor is the same, its
 // weight is kept beside the lane's own. Only the result is rounded.
 //
@@ -13,17 +13,20 @@
 // token's 64 sines and cosines and share them through shared memory, and kUnroll pairs of heads are loaded before the
 // first is worked on. (A block per token, with two block barriers around the sines, took 115 us for 8191 tokens of
 // 64 + 8 heads.) Partial and interleaved rotations take the first kernel below, with the partner shuffled in: 8191 tokens
-// of 64 + 8 heads in 55 us interleaved and 65 in halves of 32, where the full rotation in halves takes 53 (44.6 at the copy
+// of 64 + 8 heads in 53 us interleaved and 60 in halves of 32, where the full rotation in halves takes 53 (44.6 at the copy
 // rate; 5.7 TB/s).
 //
+// Four heads' sums of squares are reduced together (9 shuffles instead of 16, one root instead of four): halves of 32 65 -> 60 us.
+// The next heads are loaded after that in the kernel for full rotations, which has no registers for both.
+//
 // Positions with several axes (kAxes; include/paged/moe_norm.h): the lanes that compute a pair's sine and cosine look up the
-// pair's axis once and load that axis's position per token; nothing else differs (8191 tokens of 64 + 8 heads: 55 us).
+// pair's axis once and load that axis's position per token; nothing else differs (8191 tokens of 64 + 8 heads: 54 us).
 //
 // A 4-bit cache (kFour; include/paged/moe_kv4.h): keys and values are rounded to bf16 as for the bf16 cache, then the 8 (or
 // 4) lanes that hold a group of 32 dimensions share its largest magnitude, taken of the bits as whole numbers (two groups
 // in one shuffle; NaN stands above infinity), and lanes that hold parts of the same stored bytes exchange them, so that a
 // head's 64 bytes of codes leave in 8- or 16-byte stores. Every code is that of the exact quotient: see codes2. 9603 tokens of
-// 32 + 2 8 heads in 49.6 us (4.2 TB/s; their bf16 store takes 41.6, and with divisions it was 7 more).
+// 32 + 2 8 heads in 47 us (4.4 TB/s, issue-bound; their bf16 store takes 42).
 //
 // The angle: inv_freq / (2 pi) is kept as a 64-bit fraction of a turn (computed in fp64, rounded once), so
 // pos * fraction modulo 2^64 is the angle modulo one turn without any loss for large pos, and sin and cos are taken of a
@@ -266,6 +269,21 @@ struct Walk {
   }
 };
 
+// The norm factors of four heads from the 16 lanes' parts of their sums of squares (each half-warp its own four): two halving
+// steps leave a lane one head's sum, so that a factor is computed once and its root taken once. The order of the additions is
+// the same for each.
+__device__ __forceinline__ void norm_factors(float eps, int l, float (&part)[4]) {
+  const bool hi8 = l & 8, hi4 = l & 4;
+  const float a = (hi8 ? part[2] : part[0]) + __shfl_xor_sync(0xffffffffu, hi8 ? part[0] : part[2], 8);
+  const float b = (hi8 ? part[3] : part[1]) + __shfl_xor_sync(0xffffffffu, hi8 ? part[1] : part[3], 8);
+  float sum = (hi4 ? b : a) + __shfl_xor_sync(0xffffffffu, hi4 ? a : b, 4);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+  const float f = rsqrtf(sum * (1.0f / kD) + eps);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) part[u] = __shfl_sync(0xffffffffu, f, 4 * u, 16);
+}
+
 constexpr int kUnroll = 4;
 
 template <bool kInterleaved, bool kAxes, bool kFour>
@@ -355,6 +373,17 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(const QkNormR
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) w[u] = v[u];
       if (h0 + 2 * kUnroll < last) load(h0 + 2 * kUnroll);
+      float factor[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        float x[8], ss = 0.0f;
+        unpack8(w[u], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+        factor[u] = ss;
+        asm("" : "+r"(w[u].x), "+r"(w[u].y), "+r"(w[u].z), "+r"(w[u].w));  // (unpacked again, not kept)
+      }
+      norm_factors(p.eps, l, factor);
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int pair = h0 + 2 * u;  // its first head
@@ -365,11 +394,6 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(const QkNormR
         if (pair < p.h_q + p.h_kv) {  // not both values
           float x[8], y[8];
           unpack8(o, x);
-          float ss = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-          for (int d = 8; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
           if (!kInterleaved) {
             uint4 q;
             q.x = __shfl_sync(0xffffffffu, o.x, partner, 16);
@@ -380,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(const QkNormR
           }
           if (h < p.h_q + p.h_kv) {
             if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
-              const float r = rsqrtf(ss * (1.0f / kD) + p.eps);
+              const float r = factor[u];
               float wx[8], wy[8];
               unpack8(is_q ? wq : wk, wx);
               unpack8(is_q ? wqp : wkp, wy);
@@ -499,27 +523,32 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_halves_kernel(const 
         o[u][0] = v[u][0];
         o[u][1] = v[u][1];
       }
+      float factor[kUnrollHalves];
+#pragma unroll
+      for (int u = 0; u < kUnrollHalves; ++u) {
+        const uint64_t x[4] = {pair_of(o[u][0].x), pair_of(o[u][0].y), pair_of(o[u][1].x), pair_of(o[u][1].y)};
+        uint64_t sq = mul_f32x2(x[0], x[0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) sq = fma_f32x2(x[i], x[i], sq);
+        float s0, s1;
+        unpack_f32x2(sq, s0, s1);
+        factor[u] = s0 + s1;
+      }
+      norm_factors(p.eps, l, factor);
       if (h0 + 2 * kUnrollHalves < last) load(h0 + 2 * kUnrollHalves);
 #pragma unroll
       for (int u = 0; u < kUnrollHalves; ++u) {
+        // (unpacked again, not kept)
+        asm volatile("" : "+r"(o[u][0].x), "+r"(o[u][0].y), "+r"(o[u][1].x), "+r"(o[u][1].y) : : "memory");
         const int first_h = h0 + 2 * u;
         if (first_h >= last) break;
         const int h = first_h + hw;
         const bool is_q = h < p.h_q;
         if (first_h < p.h_q + p.h_kv) {  // not both values
           uint64_t x[4] = {pair_of(o[u][0].x), pair_of(o[u][0].y), pair_of(o[u][1].x), pair_of(o[u][1].y)};
-          uint64_t sq = mul_f32x2(x[0], x[0]);
-#pragma unroll
-          for (int i = 1; i < 4; ++i) sq = fma_f32x2(x[i], x[i], sq);
-          float s0, s1;
-          unpack_f32x2(sq, s0, s1);
-          float sum = s0 + s1;
-#pragma unroll
-          for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
           if (h < p.h_q + p.h_kv) {
             if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
-              const float r = rsqrtf(sum * (1.0f / kD) + p.eps);
-              const uint64_t r2 = pack_f32x2(r, r);
+              const uint64_t r2 = pack_f32x2(factor[u], factor[u]);
               const uint2 wa = is_q ? w[0][0] : w[1][0], wb = is_q ? w[0][1] : w[1][1];
               x[0] = mul_f32x2(x[0], mul_f32x2(r2, pair_of(wa.x)));
               x[1] = mul_f32x2(x[1], mul_f32x2(r2, pair_of(wa.y)));
@@ -560,8 +589,9 @@ cudaError_t launch_qk_norm_rope(const QkNormRopeArgs& args, int num_sms, cudaStr
   // Whole tokens in rounds over the warps, as long as there is one for each, in the caches' order; what remains is cut into
   // equal shares, a warp each, of one token where that is hardly more per warp (a start costs as much as some pairs), else
   // across tokens. (Every token cut alike, so that the last round was partly empty: 2000 tokens of 72 heads 17.9 us instead of
-  // 16.1, 8191 56.9 instead of 53.2. Shares across tokens alone: 16000 105 us instead of 99, warps far apart in the caches.)
-  // A 4-bit cache has shares across tokens alone, with its heads counted twice: 9603 tokens of 48 heads 49.6 us, in rounds 52.
+  // 16.1, 8191 56.9 instead of 53.2; shares across tokens alone: 16000 105 instead of 99, warps far apart in the caches.)
+  // A 4-bit cache has shares across tokens alone, with its heads counted twice: 9603 tokens of 48 heads
+  // 49.6 us instead of 52 in rounds.
   // More than a block an SM costs calls that follow one another closely 1 us, so few tokens' warps take two pairs where that
   // avoids it: 64 tokens of 40 heads 3.9 -> 3.2 us (for a 4-bit cache, whose pairs take longer, it does not pay).
   const bool halves = args.rot == qk::kD && !args.interleaved;
