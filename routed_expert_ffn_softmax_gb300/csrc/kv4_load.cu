@@ -2,7 +2,8 @@
 //
 // 144 bytes are read and 512 written per token and head, so HBM's writes bound it. The work is listed as blocks of 16
 // tokens of a head: every CTA repeats the scan over the sequences' block counts (as the plan's kernel does), and each warp
-// takes a block at a time, 16 lanes of 8 dimensions to a row, so that one store instruction writes two whole rows.
+// takes a block at a time, 16 lanes of 8 dimensions to a row, so that one store instruction writes two whole rows. GB300: 9603
+// tokens of 8 heads in 10.7 us (4.7 TB/s; a third of it is the launch and the scan).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
