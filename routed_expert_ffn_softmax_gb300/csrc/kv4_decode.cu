@@ -24,7 +24,8 @@
 // when a product would pass 2^15. R starts 2^6 below the largest, so products keep fp16's full precision down to 2^-20 of it.
 //
 // Work split: as in gqa_decode.cu, the key tiles (128 keys) of all segments form one list of which each CTA takes a
-// contiguous share; the pieces of a cut segment are joined in CTA order by the last to arrive.
+// contiguous share, here with some units more for a segment's start; the pieces of a cut segment are joined in CTA order by the
+// last to arrive.
 //
 // Per CTA, 12 warps, which share out the registers:
 //   0, 1   bring tiles with bulk copies, 16 tokens of keys and values or whole runs of a page in one (2304 bytes a chunk);
@@ -32,10 +33,11 @@
 //          its partial, and join a cut segment;
 //   4..11  work: each takes 32 or 64 keys of a tile, with a running (R, sum, O) of its own, and goes on to the next piece as
 //          soon as its part is handed over.
-// (One warp that loads, 8 or 11 that work and join through barriers: 255 sequences of up to 4K keys took 125 us, now 85.)
+// (One warp that loads, 8 or 11 that work and join through barriers: 255 sequences of up to 4K keys took 125 us, then 85.)
 //
 // GB300: 16 sequences of up to 32K keys, 4 heads a group, in 60 us (4.9 TB/s, 72% of a copy; 155 us in bf16); 24 with 16 heads
-// a group in 74 (3.2 TB/s, 180 TFLOP/s); 64 behind a window of 1024 in 27; one sequence of 512 visible keys in 9.3. With two
+// a group in 74 (3.2 TB/s, 180 TFLOP/s); 64 behind a window of 1024 in 25; 255 of up to 4K in 74 (3.9 TB/s); one
+// sequence of 512 visible keys in 9.3. With two
 // chunks a warp the working warps were at it 76% of the time, the integer pipe then 68% busy; the rest is the start (lengths,
 // table, first tile: 3 us), the last pieces' joins, and a hand-over per piece.
 #include <cuda_fp16.h>
@@ -91,6 +93,12 @@ struct Split {
   static constexpr int kUnit = 2;
   static constexpr int kLongUnit = kNT == 1 ? 4 : 2;
   static constexpr int kLong = 20;
+  // A piece costs a CTA about as much as some tiles (queries, a first tile to wait for, hand-over, join): so many units a segment
+  // counts besides its own tiles, where CTAs have kSegmentFrom tiles on average. (With none, CTAs whose share was many short
+  // segments came last: 255 sequences of up to 4K keys 85 us instead of 74, with 16 heads 133 instead of 106; 64 of up to 1K with
+  // 16 heads 30 instead of 21. 4 units for all: 24 long ones 74.2 instead of 73.7, 16 long ones 60.5 instead of 59.7.)
+  static constexpr int kSegment = kNT == 1 ? 2 : 3;
+  static constexpr int kSegmentFrom = 2;
   static constexpr int tiles_at_once(bool longs) { return kWarps * (longs ? kLongUnit : kUnit) / kChunks; }
   static constexpr int kStages = kNT == 1 ? 9 : 7;
   // The two loading warps take kTurn tiles in turn, and an mbarrier tells apart only neighbouring phases. So neither loader may
@@ -114,7 +122,8 @@ struct Split {
   static constexpr int kMisc = (kBad + 2 * kStages * 4 + 15) / 16 * 16;      // 32 ints
   static constexpr int kPre = kMisc + 128;
   static constexpr int kLens = kPre + (kGqaMaxSeqs + 4) * 4;
-  static constexpr int kBytes = kLens + kGqaMaxSeqs * 4;
+  static constexpr int kPreUnits = kLens + kGqaMaxSeqs * 4;
+  static constexpr int kBytes = kPreUnits + (kGqaMaxSeqs + 4) * 4;
   static_assert(kBytes <= 232448, "dynamic shared memory per CTA");
   static_assert(kQ % 16 == 0 && kRef % 16 == 0, "vector loads");
 };
@@ -532,6 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
   int* misc = reinterpret_cast<int*>(smem + S::kMisc);
   int* pre = reinterpret_cast<int*>(smem + S::kPre);
   int* lens = reinterpret_cast<int*>(smem + S::kLens);
+  int* pre_units = reinterpret_cast<int*>(smem + S::kPreUnits);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -552,22 +562,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
   __syncthreads();
 
   // The first NC CTAs share the tiles: as many as there are with as many tiles as a CTA works on together (tile counts fit 32
-  // bits: the host checks).
+  // bits: the host checks, with 8 more a segment). The list that is cut into equal shares has a unit for each tile and `extra`
+  // units in front of each segment's tiles.
   const int grid = gridDim.x, cta = blockIdx.x;
-  int q_tiles = 0, rm = 0, beg = 0, end = 0;
+  int q_units = 0, rm = 0, beg = 0, end = 0, extra = 0;
   bool longs = false;  // long segments
-  auto range_start = [&](int c) { return c * q_tiles + min(c, rm); };
+  auto range_start = [&](int c) { return c * q_units + min(c, rm); };
+  // Where segment j of sequence b begins in units, and the first tile at unit x or behind it.
+  auto segment_unit = [&](int b, int j, int nt, int seg0) { return extra == 0 ? seg0 : p.h_kv * pre_units[b] + j * (nt + extra); };
+  auto tile_at = [&](int x) {
+    if (extra == 0) return x;
+    if (x >= p.h_kv * pre_units[p.B]) return p.h_kv * pre[p.B];
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.h_kv * pre_units[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    const int nt = pre[lo + 1] - pre[lo], off = x - p.h_kv * pre_units[lo];
+    const int j = off / (nt + extra);
+    return p.h_kv * pre[lo] + j * nt + max(0, off - j * (nt + extra) - extra);
+  };
   auto find_range = [&]() {
     const int total = p.h_kv * pre[p.B];
     longs = S::kLongUnit != S::kUnit && pre[p.B] >= S::kLong * p.B;
     const int together = S::tiles_at_once(longs);
     const int NC = min((total + together - 1) / together, grid);
     if (NC == 0) return;
-    q_tiles = total / NC;
-    rm = total - q_tiles * NC;
+    extra = total >= S::kSegmentFrom * grid ? S::kSegment : 0;
+    const int units = extra > 0 ? p.h_kv * pre_units[p.B] : total;
+    q_units = units / NC;
+    rm = units - q_units * NC;
     if (cta >= NC) return;
-    beg = range_start(cta);
-    end = range_start(cta + 1);
+    const int at = tile_at(range_start(cta + (lane >> 4)));
+    beg = __shfl_sync(0xffffffffu, at, 0);
+    end = __shfl_sync(0xffffffffu, at, 16);
   };
 
   // The piece of the range that starts at tile x: sequence b, key/value head j, first tile tl of the segment's nt, n tiles
@@ -618,30 +646,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
     pdl_allow_successor();
     const int per = (p.B + 127) / 128;
     const int i0 = tid * per, i1 = min(p.B, i0 + per);
-    int sum = 0;
+    int64_t sum = 0;  // tiles, and sequences that have some in the upper half
     bool bad_len = false;
+    auto counts = [](int nt) { return nt + (static_cast<int64_t>(nt > 0) << 32); };
     for (int i = i0; i < i1; ++i) {
       const int len = p.seq_lens[i];
       bad_len |= len < 0 || len > p.L_cap;
       lens[i] = len;
-      sum += span_of(len, p.L_cap, p.kv).nt;
+      sum += counts(span_of(len, p.L_cap, p.kv).nt);
     }
     if (bad_len) raise_status(p.status, kStatusBadSeqLen);
-    int incl = sum;
+    int64_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, incl, o);
+      const int64_t n = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += n;
     }
-    if (lane == 31) misc[warp] = incl;
+    int64_t* sums = reinterpret_cast<int64_t*>(misc);
+    if (lane == 31) sums[warp] = incl;
     named_bar_sync(3, 128);
-    int run = incl - sum;
-    for (int w = 0; w < warp; ++w) run += misc[w];
-    if (tid == 127) pre[p.B] = run + sum;
+    int64_t run = incl - sum;
+    for (int w = 0; w < warp; ++w) run += sums[w];
+    auto note = [&](int i) {
+      pre[i] = static_cast<int>(run);
+      pre_units[i] = static_cast<int>(run) + S::kSegment * static_cast<int>(run >> 32);
+    };
     for (int i = i0; i < i1; ++i) {
-      pre[i] = run;
-      run += span_of(lens[i], p.L_cap, p.kv).nt;
+      note(i);
+      run += counts(span_of(lens[i], p.L_cap, p.kv).nt);
     }
+    if (tid == 127) note(p.B);
     named_bar_sync(3, 128);
     named_bar_arrive(4, kThreads);  // the working warps may look at it
     find_range();
@@ -773,10 +807,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
           // at once: with loads into registers a warp had a few of them under way, and 20 pieces took 8 us.
           fence_proxy_async_all();  // (they are read with copies)
           auto cta_of = [&](int i) {
-            const int big = rm * (q_tiles + 1);
-            return i < big ? i / (q_tiles + 1) : rm + (i - big) / q_tiles;
+            const int big = rm * (q_units + 1);
+            return i < big ? i / (q_units + 1) : rm + (i - big) / q_units;
           };
-          const int c_first = cta_of(pc.seg0), c_last = cta_of(pc.seg0 + pc.nt - 1);
+          const int unit0 = segment_unit(pc.b, pc.j, pc.nt, pc.seg0);
+          const int c_first = cta_of(unit0 + extra), c_last = cta_of(unit0 + extra + pc.nt - 1);
           named_bar_sync(1, 64);
           if (tid == 64) {
             // publishes what the barrier gathered (cumulativity), and sees what those before published
@@ -803,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
                     if (lane < n) {
                       const int c = c0 + lane;
                       bulk_load(join + lane * part,
-                                p.partials + (static_cast<int64_t>(c) * 2 + (range_start(c) >= pc.seg0 ? 0 : 1)) * kGqaSlotFloats,
+                                p.partials + (static_cast<int64_t>(c) * 2 + (range_start(c) >= unit0 ? 0 : 1)) * kGqaSlotFloats,
                                 static_cast<uint32_t>(part) * 4u, m_full, l2_policy_evict_first());
                     }
                     copied = merges;

@@ -3,6 +3,7 @@ groups of working warps take every n-th tile, and a stage's barriers tell apart 
 state of their progress is visited: no stage is filled again before its tile has been worked on, and no tile worked on before
 it is there, for the numbers of stages and groups the kernel uses; with others that its static_assert refuses, some are."""
 import os
+import random
 import re
 from collections import deque
 
@@ -76,3 +77,77 @@ def test_nothing_is_early(stages, groups):
 @pytest.mark.parametrize("stages,groups", [(5, 3), (8, 3), (7, 4), (4, 2)])
 def test_the_model_finds_what_is_early(stages, groups):
     assert search(stages, groups, 28)[0] in ("filled", "worked on")
+
+
+def _split(nts, h_kv, grid, segment, per_cta, together):
+    """The kernel's shares: (pieces of each CTA, range_start, unit0 of a segment, extra), every division as there."""
+    pre, units = [0], [0]
+    for nt in nts:
+        pre.append(pre[-1] + nt)
+        units.append(units[-1] + nt + (segment if nt else 0))
+    total = h_kv * pre[-1]
+    ctas = min(-(-total // together), grid)
+    if ctas == 0:
+        return [], None, None, 0
+    extra = segment if total >= per_cta * grid else 0
+    n_units = h_kv * units[-1] if extra else total
+    share, more = divmod(n_units, ctas)
+
+    def range_start(c):
+        return c * share + min(c, more)
+
+    def sequence_at(prefix, x):
+        return max(b for b in range(len(nts)) if h_kv * prefix[b] <= x)
+
+    def tile_at(x):
+        if not extra:
+            return x
+        if x >= h_kv * units[-1]:
+            return total
+        b = sequence_at(units, x)
+        j, off = divmod(x - h_kv * units[b], nts[b] + extra)
+        return h_kv * pre[b] + j * nts[b] + max(0, off - extra)
+
+    def unit0(b, j, seg0):
+        return h_kv * units[b] + j * (nts[b] + extra) if extra else seg0
+
+    def cta_of(i):
+        big = more * (share + 1)
+        return i // (share + 1) if i < big else more + (i - big) // share
+
+    pieces = []
+    for c in range(ctas):
+        x, end = tile_at(range_start(c)), tile_at(range_start(c + 1))
+        mine = []
+        while x < end:
+            b = sequence_at(pre, x)
+            j, tl = divmod(x - h_kv * pre[b], nts[b])
+            n = min(end - x, nts[b] - tl)
+            mine.append((b, j, tl, n, x - tl))
+            x += n
+        pieces.append(mine)
+    return pieces, range_start, lambda b, j, seg0: (unit0(b, j, seg0), extra), cta_of
+
+
+@pytest.mark.parametrize("segment", [0, 3])
+def test_shares_cover_all_tiles_and_cut_segments_find_their_parts(segment):
+    rng = random.Random(segment)
+    for _ in range(1500):
+        h_kv, grid = rng.randint(1, 5), rng.randint(1, 12)
+        nts = [rng.choice([0, 1, 2, rng.randint(1, 40)]) for _ in range(rng.randint(1, 9))]
+        pieces, range_start, unit0, cta_of = _split(nts, h_kv, grid, segment, rng.randint(0, 4), rng.choice([2, 4]))
+        seen, cut = {}, {}
+        for c, mine in enumerate(pieces):
+            for i, (b, j, tl, n, seg0) in enumerate(mine):
+                for t in range(tl, tl + n):
+                    assert seen.setdefault((b, j, t), c) == c
+                if n < nts[b]:
+                    cut.setdefault((b, j, seg0), []).append((c, 0 if i == 0 else 1))
+        assert len(seen) == h_kv * sum(nts)
+        firsts = set()
+        for (b, j, seg0), parts in cut.items():
+            at, extra = unit0(b, j, seg0)
+            first, last = cta_of(at + extra), cta_of(at + extra + nts[b] - 1)
+            assert parts == [(c, 0 if range_start(c) >= at else 1) for c in range(first, last + 1)]
+            assert first not in firsts  # a counter of its own
+            firsts.add(first)
