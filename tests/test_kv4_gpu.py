@@ -397,6 +397,15 @@ def test_decode_ragged_batches_repeat_exactly(h_q, h_kv, page, window):
     assert moe.workspace_status(ws) == 0
 
 
+@pytest.mark.parametrize("h_q", [8, 32])
+def test_decode_short_and_empty_sequences_share_the_sms(h_q):
+    """Runs of empty sequences in front, between and behind; segments of fewer tiles than a start counts for."""
+    g = torch.Generator().manual_seed(h_q)
+    lens = [0] * 60 + torch.randint(0, 300, (90,), generator=g).tolist() + [0] * 40 + [5000, 1, 0, 129] * 3 + [0] * 9
+    c = step.Kv4(lens, 2, 16, DEV, seed=h_q)
+    check_decode(c, lens, *decode(c, lens, h_q))
+
+
 def test_decode_one_sequence_over_all_ctas():
     """More parts of a cut segment than are joined at once, for 1, 5, 8, 9 and 16 heads."""
     n = 128 * 152 * 2 + 77
