@@ -37,7 +37,7 @@
 //
 // GB300: 16 sequences of up to 32K keys, 4 heads a group, in 60 us (4.9 TB/s, 72% of a copy; 155 us in bf16); 24 with 16 heads
 // a group in 74 (3.2 TB/s, 180 TFLOP/s); 64 behind a window of 1024 in 25; 255 of up to 4K in 74 (3.9 TB/s); one
-// sequence of 512 visible keys in 9.3. With two
+// sequence of 512 visible keys in 7.5. With two
 // chunks a warp the working warps were at it 76% of the time, the integer pipe then 68% busy; the rest is the start (lengths,
 // table, first tile: 3 us), the last pieces' joins, and a hand-over per piece.
 #include <cuda_fp16.h>
@@ -99,6 +99,10 @@ struct Split {
   // 16 heads 30 instead of 21. 4 units for all: 24 long ones 74.2 instead of 73.7, 16 long ones 60.5 instead of 59.7.)
   static constexpr int kSegment = kNT == 1 ? 2 : 3;
   static constexpr int kSegmentFrom = 2;
+  // Where there is a CTA for each segment and none has more tiles than this, each is a CTA's whole work: joining pieces takes
+  // longer. (us without and with: one sequence of 512 visible keys of 5 tiles 9.4 and 7.5, of 8 tiles 8.4 and 9.0; 32 of up to 1K
+  // keys 13.5 and 10.1; 4 of up to 512 with 16 heads 15.2 and 9.1.)
+  static constexpr int kWhole = 8;
   static constexpr int tiles_at_once(bool longs) { return kWarps * (longs ? kLongUnit : kUnit) / kChunks; }
   static constexpr int kStages = kNT == 1 ? 9 : 7;
   // The two loading warps take kTurn tiles in turn, and an mbarrier tells apart only neighbouring phases. So neither loader may
@@ -563,13 +567,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
 
   // The first NC CTAs share the tiles: as many as there are with as many tiles as a CTA works on together (tile counts fit 32
   // bits: the host checks, with 8 more a segment). The list that is cut into equal shares has a unit for each tile and `extra`
-  // units in front of each segment's tiles.
+  // units in front of each segment's tiles; or one unit for each segment.
   const int grid = gridDim.x, cta = blockIdx.x;
   int q_units = 0, rm = 0, beg = 0, end = 0, extra = 0;
+  bool whole_segments = false;
   bool longs = false;  // long segments
   auto range_start = [&](int c) { return c * q_units + min(c, rm); };
   // Where segment j of sequence b begins in units, and the first tile at unit x or behind it.
-  auto segment_unit = [&](int b, int j, int nt, int seg0) { return extra == 0 ? seg0 : p.h_kv * pre_units[b] + j * (nt + extra); };
+  auto units_of = [&](int nt) { return whole_segments ? 1 : nt + extra; };
+  auto segment_unit = [&](int b, int j, int nt, int seg0) { return extra == 0 ? seg0 : p.h_kv * pre_units[b] + j * units_of(nt); };
   auto tile_at = [&](int x) {
     if (extra == 0) return x;
     if (x >= p.h_kv * pre_units[p.B]) return p.h_kv * pre[p.B];
@@ -579,16 +585,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
       if (p.h_kv * pre_units[mid] <= x) lo = mid; else hi = mid - 1;
     }
     const int nt = pre[lo + 1] - pre[lo], off = x - p.h_kv * pre_units[lo];
-    const int j = off / (nt + extra);
-    return p.h_kv * pre[lo] + j * nt + max(0, off - j * (nt + extra) - extra);
+    const int j = off / units_of(nt);
+    return p.h_kv * pre[lo] + j * nt + max(0, off - j * units_of(nt) - extra);
   };
   auto find_range = [&]() {
     const int total = p.h_kv * pre[p.B];
     longs = S::kLongUnit != S::kUnit && pre[p.B] >= S::kLong * p.B;
     const int together = S::tiles_at_once(longs);
-    const int NC = min((total + together - 1) / together, grid);
+    whole_segments = misc[17] != 0;
+    const int NC = whole_segments ? p.h_kv * pre_units[p.B] : min((total + together - 1) / together, grid);
     if (NC == 0) return;
-    extra = total >= S::kSegmentFrom * grid ? S::kSegment : 0;
+    extra = whole_segments ? 1 : total >= S::kSegmentFrom * grid ? S::kSegment : 0;
     const int units = extra > 0 ? p.h_kv * pre_units[p.B] : total;
     q_units = units / NC;
     rm = units - q_units * NC;
@@ -648,12 +655,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
     const int i0 = tid * per, i1 = min(p.B, i0 + per);
     int64_t sum = 0;  // tiles, and sequences that have some in the upper half
     bool bad_len = false;
+    int most = 0;
     auto counts = [](int nt) { return nt + (static_cast<int64_t>(nt > 0) << 32); };
     for (int i = i0; i < i1; ++i) {
       const int len = p.seq_lens[i];
       bad_len |= len < 0 || len > p.L_cap;
       lens[i] = len;
-      sum += counts(span_of(len, p.L_cap, p.kv).nt);
+      const int nt = span_of(len, p.L_cap, p.kv).nt;
+      sum += counts(nt);
+      most = max(most, nt);
     }
     if (bad_len) raise_status(p.status, kStatusBadSeqLen);
     int64_t incl = sum;
@@ -663,13 +673,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
       if (lane >= o) incl += n;
     }
     int64_t* sums = reinterpret_cast<int64_t*>(misc);
+    most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 31) sums[warp] = incl;
+    if (lane == 0) misc[8 + warp] = most;
     named_bar_sync(3, 128);
     int64_t run = incl - sum;
     for (int w = 0; w < warp; ++w) run += sums[w];
+    const bool whole = max(max(misc[8], misc[9]), max(misc[10], misc[11])) <= S::kWhole &&
+                       p.h_kv * static_cast<int>((sums[0] + sums[1] + sums[2] + sums[3]) >> 32) <= grid;
+    if (tid == 0) misc[17] = whole;
     auto note = [&](int i) {
       pre[i] = static_cast<int>(run);
-      pre_units[i] = static_cast<int>(run) + S::kSegment * static_cast<int>(run >> 32);
+      pre_units[i] = whole ? static_cast<int>(run >> 32) : static_cast<int>(run) + S::kSegment * static_cast<int>(run >> 32);
     };
     for (int i = i0; i < i1; ++i) {
       note(i);

@@ -79,17 +79,21 @@ def test_the_model_finds_what_is_early(stages, groups):
     assert search(stages, groups, 28)[0] in ("filled", "worked on")
 
 
-def _split(nts, h_kv, grid, segment, per_cta, together):
-    """The kernel's shares: (pieces of each CTA, range_start, unit0 of a segment, extra), every division as there."""
+def _split(nts, h_kv, grid, segment, per_cta, together, whole):
+    """The kernel's shares: (pieces of each CTA, range_start, unit0 of a segment, cta_of), every division as there."""
+    whole = max(nts) <= whole and h_kv * sum(nt > 0 for nt in nts) <= grid
     pre, units = [0], [0]
     for nt in nts:
         pre.append(pre[-1] + nt)
-        units.append(units[-1] + nt + (segment if nt else 0))
+        units.append(units[-1] + (nt > 0 if whole else nt + (segment if nt else 0)))
     total = h_kv * pre[-1]
-    ctas = min(-(-total // together), grid)
+    ctas = h_kv * units[-1] if whole else min(-(-total // together), grid)
     if ctas == 0:
         return [], None, None, 0
-    extra = segment if total >= per_cta * grid else 0
+    extra = 1 if whole else segment if total >= per_cta * grid else 0
+
+    def units_of(nt):
+        return 1 if whole else nt + extra
     n_units = h_kv * units[-1] if extra else total
     share, more = divmod(n_units, ctas)
 
@@ -105,11 +109,11 @@ def _split(nts, h_kv, grid, segment, per_cta, together):
         if x >= h_kv * units[-1]:
             return total
         b = sequence_at(units, x)
-        j, off = divmod(x - h_kv * units[b], nts[b] + extra)
+        j, off = divmod(x - h_kv * units[b], units_of(nts[b]))
         return h_kv * pre[b] + j * nts[b] + max(0, off - extra)
 
     def unit0(b, j, seg0):
-        return h_kv * units[b] + j * (nts[b] + extra) if extra else seg0
+        return h_kv * units[b] + j * units_of(nts[b]) if extra else seg0
 
     def cta_of(i):
         big = more * (share + 1)
@@ -135,7 +139,10 @@ def test_shares_cover_all_tiles_and_cut_segments_find_their_parts(segment):
     for _ in range(1500):
         h_kv, grid = rng.randint(1, 5), rng.randint(1, 12)
         nts = [rng.choice([0, 1, 2, rng.randint(1, 40)]) for _ in range(rng.randint(1, 9))]
-        pieces, range_start, unit0, cta_of = _split(nts, h_kv, grid, segment, rng.randint(0, 4), rng.choice([2, 4]))
+        if rng.random() < 0.2:
+            nts = [nt % 9 for nt in nts]
+        pieces, range_start, unit0, cta_of = _split(nts, h_kv, grid, segment, rng.randint(0, 4), rng.choice([2, 4]),
+                                                    rng.choice([0, 8, 40]))
         seen, cut = {}, {}
         for c, mine in enumerate(pieces):
             for i, (b, j, tl, n, seg0) in enumerate(mine):
