@@ -24,8 +24,8 @@
 // when a product would pass 2^15. R starts 2^6 below the largest, so products keep fp16's full precision down to 2^-20 of it.
 //
 // Work split: as in gqa_decode.cu, the key tiles (128 keys) of all segments form one list of which each CTA takes a
-// contiguous share, here with some units more for a segment's start; the pieces of a cut segment are joined in CTA order by the
-// last to arrive.
+// contiguous share, here with some units more for a segment's start, or with few tiles a part of one segment; the pieces of a cut
+// segment are joined in CTA order by the last to arrive.
 //
 // Per CTA, 12 warps, which share out the registers:
 //   0, 1   bring tiles with bulk copies, 16 tokens of keys and values or whole runs of a page in one (2304 bytes a chunk);
@@ -36,10 +36,9 @@
 // (One warp that loads, 8 or 11 that work and join through barriers: 255 sequences of up to 4K keys took 125 us, then 85.)
 //
 // GB300: 16 sequences of up to 32K keys, 4 heads a group, in 60 us (4.9 TB/s, 72% of a copy; 155 us in bf16); 24 with 16 heads
-// a group in 74 (3.2 TB/s, 180 TFLOP/s); 64 behind a window of 1024 in 25; 255 of up to 4K in 74 (3.9 TB/s); one
-// sequence of 512 visible keys in 7.5. With two
-// chunks a warp the working warps were at it 76% of the time, the integer pipe then 68% busy; the rest is the start (lengths,
-// table, first tile: 3 us), the last pieces' joins, and a hand-over per piece.
+// a group in 74 (3.2 TB/s, 180 TFLOP/s); 64 behind a window of 1024 in 25; 255 of up to 4K in 74 (3.9 TB/s); one sequence of 512
+// visible keys in 7.5. With two chunks a warp the working warps were at it 76% of the time in the first of these, the integer pipe
+// then 68% busy; the rest is the start (lengths, table, first tile: 3 us), the last pieces' joins, and a hand-over per piece.
 #include <cuda_fp16.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -99,10 +98,13 @@ struct Split {
   // 16 heads 30 instead of 21. 4 units for all: 24 long ones 74.2 instead of 73.7, 16 long ones 60.5 instead of 59.7.)
   static constexpr int kSegment = kNT == 1 ? 2 : 3;
   static constexpr int kSegmentFrom = 2;
-  // Where there is a CTA for each segment and none has more tiles than this, each is a CTA's whole work: joining pieces takes
-  // longer. (us without and with: one sequence of 512 visible keys of 5 tiles 9.4 and 7.5, of 8 tiles 8.4 and 9.0; 32 of up to 1K
-  // keys 13.5 and 10.1; 4 of up to 512 with 16 heads 15.2 and 9.1.)
+  // With few tiles a CTA has tiles of one segment only: all of it where there is a CTA for each segment and none has more than
+  // kWhole tiles, as joining pieces takes longer (us without and with: one sequence of 512 visible keys of 5 tiles 9.4 and 7.5, of
+  // 8 tiles 8.4 and 9.0; 32 of up to 1K keys 13.5 and 10.1; 4 of up to 512 with 16 heads 15.2 and 9.1); else as many as make the
+  // CTAs do, up to kOwn (one of 1300 keys 10.1 and 8.7, 4 of up to 4K 12.1 and 9.6, with 16 heads 16.0 and 12.3).
   static constexpr int kWhole = 8;
+  static constexpr int kWholeTiles = 1 << 20;
+  static constexpr int kOwn = 6;
   static constexpr int tiles_at_once(bool longs) { return kWarps * (longs ? kLongUnit : kUnit) / kChunks; }
   static constexpr int kStages = kNT == 1 ? 9 : 7;
   // The two loading warps take kTurn tiles in turn, and an mbarrier tells apart only neighbouring phases. So neither loader may
@@ -567,17 +569,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
 
   // The first NC CTAs share the tiles: as many as there are with as many tiles as a CTA works on together (tile counts fit 32
   // bits: the host checks, with 8 more a segment). The list that is cut into equal shares has a unit for each tile and `extra`
-  // units in front of each segment's tiles; or one unit for each segment.
+  // units in front of each segment's tiles; or, with few tiles, a unit for each `own` tiles of a segment, or part of them.
   const int grid = gridDim.x, cta = blockIdx.x;
   int q_units = 0, rm = 0, beg = 0, end = 0, extra = 0;
-  bool whole_segments = false;
+  int own = 0;  // 0, or tiles of a CTA that has tiles of one segment only
   bool longs = false;  // long segments
   auto range_start = [&](int c) { return c * q_units + min(c, rm); };
   // Where segment j of sequence b begins in units, and the first tile at unit x or behind it.
-  auto units_of = [&](int nt) { return whole_segments ? 1 : nt + extra; };
-  auto segment_unit = [&](int b, int j, int nt, int seg0) { return extra == 0 ? seg0 : p.h_kv * pre_units[b] + j * units_of(nt); };
+  auto units_of = [&](int b, int nt) { return own > 0 ? pre_units[b + 1] - pre_units[b] : nt + extra; };
+  auto segment_unit = [&](int b, int j, int nt, int seg0) {
+    return own == 0 && extra == 0 ? seg0 : p.h_kv * pre_units[b] + j * units_of(b, nt);
+  };
   auto tile_at = [&](int x) {
-    if (extra == 0) return x;
+    if (own == 0 && extra == 0) return x;
     if (x >= p.h_kv * pre_units[p.B]) return p.h_kv * pre[p.B];
     int lo = 0, hi = p.B - 1;
     while (lo < hi) {
@@ -585,18 +589,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
       if (p.h_kv * pre_units[mid] <= x) lo = mid; else hi = mid - 1;
     }
     const int nt = pre[lo + 1] - pre[lo], off = x - p.h_kv * pre_units[lo];
-    const int j = off / units_of(nt);
-    return p.h_kv * pre[lo] + j * nt + max(0, off - j * units_of(nt) - extra);
+    const int of = units_of(lo, nt), j = off / of, r = off - j * of;
+    return p.h_kv * pre[lo] + j * nt + (own > 0 ? min(nt, r * own) : max(0, r - extra));
   };
   auto find_range = [&]() {
     const int total = p.h_kv * pre[p.B];
-    longs = S::kLongUnit != S::kUnit && pre[p.B] >= S::kLong * p.B;
+    own = misc[17];
+    longs = own == 0 && S::kLongUnit != S::kUnit && pre[p.B] >= S::kLong * p.B;
     const int together = S::tiles_at_once(longs);
-    whole_segments = misc[17] != 0;
-    const int NC = whole_segments ? p.h_kv * pre_units[p.B] : min((total + together - 1) / together, grid);
+    const int NC = own > 0 ? p.h_kv * pre_units[p.B] : min((total + together - 1) / together, grid);
     if (NC == 0) return;
-    extra = whole_segments ? 1 : total >= S::kSegmentFrom * grid ? S::kSegment : 0;
-    const int units = extra > 0 ? p.h_kv * pre_units[p.B] : total;
+    extra = own == 0 && total >= S::kSegmentFrom * grid ? S::kSegment : 0;
+    const int units = own > 0 || extra > 0 ? p.h_kv * pre_units[p.B] : total;
     q_units = units / NC;
     rm = units - q_units * NC;
     if (cta >= NC) return;
@@ -679,12 +683,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
     named_bar_sync(3, 128);
     int64_t run = incl - sum;
     for (int w = 0; w < warp; ++w) run += sums[w];
-    const bool whole = max(max(misc[8], misc[9]), max(misc[10], misc[11])) <= S::kWhole &&
-                       p.h_kv * static_cast<int>((sums[0] + sums[1] + sums[2] + sums[3]) >> 32) <= grid;
-    if (tid == 0) misc[17] = whole;
+    const int64_t all = sums[0] + sums[1] + sums[2] + sums[3];
+    const int segments = p.h_kv * static_cast<int>(all >> 32);
+    int own_tiles = 0;
+    if (segments <= grid && max(max(misc[8], misc[9]), max(misc[10], misc[11])) <= S::kWhole) {
+      own_tiles = S::kWholeTiles;
+    } else if (segments < grid) {  // ceil(nt / t) CTAs for each, nt / t + 1 at most
+      const int t = max(S::tiles_at_once(false), (p.h_kv * static_cast<int>(all) + grid - segments - 1) / (grid - segments));
+      if (t <= S::kOwn) own_tiles = t;
+    }
+    if (tid == 0) misc[17] = own_tiles;
     auto note = [&](int i) {
-      pre[i] = static_cast<int>(run);
-      pre_units[i] = whole ? static_cast<int>(run >> 32) : static_cast<int>(run) + S::kSegment * static_cast<int>(run >> 32);
+      // (own: at least ceil(nt / t) units further for each sequence)
+      const int tiles = static_cast<int>(run), before = static_cast<int>(run >> 32);
+      pre[i] = tiles;
+      pre_units[i] = own_tiles > 0 ? tiles / own_tiles + before : tiles + S::kSegment * before;
     };
     for (int i = i0; i < i1; ++i) {
       note(i);
@@ -826,7 +839,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
             return i < big ? i / (q_units + 1) : rm + (i - big) / q_units;
           };
           const int unit0 = segment_unit(pc.b, pc.j, pc.nt, pc.seg0);
-          const int c_first = cta_of(unit0 + extra), c_last = cta_of(unit0 + extra + pc.nt - 1);
+          const int c_first = own > 0 ? unit0 : cta_of(unit0 + extra);
+          const int c_last = own > 0 ? unit0 + (pc.nt - 1) / own : cta_of(unit0 + extra + pc.nt - 1);
           named_bar_sync(1, 64);
           if (tid == 64) {
             // publishes what the barrier gathered (cumulativity), and sees what those before published

@@ -79,23 +79,31 @@ def test_the_model_finds_what_is_early(stages, groups):
     assert search(stages, groups, 28)[0] in ("filled", "worked on")
 
 
-def _split(nts, h_kv, grid, segment, per_cta, together, whole):
-    """The kernel's shares: (pieces of each CTA, range_start, unit0 of a segment, cta_of), every division as there."""
-    whole = max(nts) <= whole and h_kv * sum(nt > 0 for nt in nts) <= grid
-    pre, units = [0], [0]
+def _split(nts, h_kv, grid, segment, per_cta, together, whole, most_own):
+    """The kernel's shares: (pieces of each CTA, a function that gives the first and last CTA of a segment and where the parts of
+    a CTA of them are), every division as there."""
+    segments, tiles = h_kv * sum(nt > 0 for nt in nts), h_kv * sum(nts)
+    own = 0
+    if segments <= grid and max(nts) <= whole:
+        own = 1 << 20
+    elif segments < grid:
+        t = max(2, (tiles + grid - segments - 1) // (grid - segments))
+        own = t if t <= most_own else 0
+    pre, before, units = [0], 0, [0]
     for nt in nts:
+        before += nt > 0
         pre.append(pre[-1] + nt)
-        units.append(units[-1] + (nt > 0 if whole else nt + (segment if nt else 0)))
-    total = h_kv * pre[-1]
-    ctas = h_kv * units[-1] if whole else min(-(-total // together), grid)
+        units.append(pre[-1] // own + before if own else pre[-1] + segment * before)
+    ctas = h_kv * units[-1] if own else min(-(-tiles // together), grid)
+    assert ctas <= grid
     if ctas == 0:
-        return [], None, None, 0
-    extra = 1 if whole else segment if total >= per_cta * grid else 0
-
-    def units_of(nt):
-        return 1 if whole else nt + extra
-    n_units = h_kv * units[-1] if extra else total
+        return [], None
+    extra = segment if not own and tiles >= per_cta * grid else 0
+    n_units = h_kv * units[-1] if own or extra else tiles
     share, more = divmod(n_units, ctas)
+
+    def units_of(b):
+        return units[b + 1] - units[b] if own else nts[b] + extra
 
     def range_start(c):
         return c * share + min(c, more)
@@ -104,20 +112,24 @@ def _split(nts, h_kv, grid, segment, per_cta, together, whole):
         return max(b for b in range(len(nts)) if h_kv * prefix[b] <= x)
 
     def tile_at(x):
-        if not extra:
+        if not own and not extra:
             return x
         if x >= h_kv * units[-1]:
-            return total
+            return tiles
         b = sequence_at(units, x)
-        j, off = divmod(x - h_kv * units[b], units_of(nts[b]))
-        return h_kv * pre[b] + j * nts[b] + max(0, off - extra)
+        j, r = divmod(x - h_kv * units[b], units_of(b))
+        return h_kv * pre[b] + j * nts[b] + (min(nts[b], r * own) if own else max(0, r - extra))
 
-    def unit0(b, j, seg0):
-        return h_kv * units[b] + j * units_of(nts[b]) if extra else seg0
+    def parts(b, j, seg0):
+        unit0 = h_kv * units[b] + j * units_of(b) if own or extra else seg0
 
-    def cta_of(i):
-        big = more * (share + 1)
-        return i // (share + 1) if i < big else more + (i - big) // share
+        def cta_of(i):
+            big = more * (share + 1)
+            return i // (share + 1) if i < big else more + (i - big) // share
+
+        first = unit0 if own else cta_of(unit0 + extra)
+        last = unit0 + (nts[b] - 1) // own if own else cta_of(unit0 + extra + nts[b] - 1)
+        return [(c, 0 if range_start(c) >= unit0 else 1) for c in range(first, last + 1)]
 
     pieces = []
     for c in range(ctas):
@@ -130,19 +142,19 @@ def _split(nts, h_kv, grid, segment, per_cta, together, whole):
             mine.append((b, j, tl, n, x - tl))
             x += n
         pieces.append(mine)
-    return pieces, range_start, lambda b, j, seg0: (unit0(b, j, seg0), extra), cta_of
+    return pieces, parts
 
 
 @pytest.mark.parametrize("segment", [0, 3])
 def test_shares_cover_all_tiles_and_cut_segments_find_their_parts(segment):
     rng = random.Random(segment)
     for _ in range(1500):
-        h_kv, grid = rng.randint(1, 5), rng.randint(1, 12)
+        h_kv, grid = rng.randint(1, 5), rng.choice([rng.randint(1, 12), rng.randint(10, 150)])
         nts = [rng.choice([0, 1, 2, rng.randint(1, 40)]) for _ in range(rng.randint(1, 9))]
         if rng.random() < 0.2:
             nts = [nt % 9 for nt in nts]
-        pieces, range_start, unit0, cta_of = _split(nts, h_kv, grid, segment, rng.randint(0, 4), rng.choice([2, 4]),
-                                                    rng.choice([0, 8, 40]))
+        pieces, parts_of = _split(nts, h_kv, grid, segment, rng.randint(0, 4), rng.choice([2, 4]), rng.choice([0, 8, 40]),
+                                  rng.choice([0, 6, 40]))
         seen, cut = {}, {}
         for c, mine in enumerate(pieces):
             for i, (b, j, tl, n, seg0) in enumerate(mine):
@@ -152,9 +164,7 @@ def test_shares_cover_all_tiles_and_cut_segments_find_their_parts(segment):
                     cut.setdefault((b, j, seg0), []).append((c, 0 if i == 0 else 1))
         assert len(seen) == h_kv * sum(nts)
         firsts = set()
-        for (b, j, seg0), parts in cut.items():
-            at, extra = unit0(b, j, seg0)
-            first, last = cta_of(at + extra), cta_of(at + extra + nts[b] - 1)
-            assert parts == [(c, 0 if range_start(c) >= at else 1) for c in range(first, last + 1)]
-            assert first not in firsts  # a counter of its own
-            firsts.add(first)
+        for segment_at, parts in cut.items():
+            assert parts == parts_of(*segment_at)
+            assert parts[0][0] not in firsts  # a counter of its own
+            firsts.add(parts[0][0])
