@@ -467,8 +467,9 @@ struct Joined {
   // n <= kMost parts: references of the four heads at `refs` (`step` floats from one part to the next; they are overwritten),
   // sums at `sums`, this lane's dimensions of the outputs at `outs` (o_step to the next part's, head_step to the next head's).
   // Every head's factors are found at once, the lanes sharing the parts: one head after the other, with all parts to a lane,
-  // joining 8 warps' 16 heads took 10000 cycles.
-  template <int kMost>
+  // joining 8 warps' 16 heads took 10000 cycles. (kUnrolled: the working warps' parts 4 at a time; cut segments' one, as a longer
+  // kernel is a slower one: 16 sequences of up to 32K keys 60.2 us, with 2 or 4 at a time there 61.2.)
+  template <int kMost, int kUnrolled>
   __device__ __forceinline__ void add(float* refs, const float* sums, int step, int n, const float* outs, int o_step, int head_step,
                                       int lane) {
     constexpr int kPer = (kMost + 7) / 8;
@@ -502,7 +503,7 @@ struct Joined {
       const float f = __shfl_sync(0xffffffffu, old, k);
       o[k] = make_float4(o[k].x * f, o[k].y * f, o[k].z * f, o[k].w * f);
     }
-#pragma unroll 4
+#pragma unroll kUnrolled
     for (int u = 0; u < n; ++u) {
       const float4 a4 = *reinterpret_cast<const float4*>(refs + u * step);
       const float a[4] = {a4.x, a4.y, a4.z, a4.w};
@@ -812,28 +813,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
         uint16_t* out = p.out + (static_cast<int64_t>(pc.b) * p.h_q + static_cast<int64_t>(pc.j) * p.G) * kD + d4;
         float* mine = p.partials + (static_cast<int64_t>(cta) * 2 + (pi == 0 ? 0 : 1)) * kGqaSlotFloats;
         Joined all;
+        auto put = [&](float* to, int h) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (h + k < p.G) *reinterpret_cast<float4*>(to + 32 + (h + k) * kD + d4) = all.o[k];
+          if (lane < 4) {
+            to[h + lane] = all.ref;
+            to[16 + h + lane] = all.sum;
+          }
+        };
         // the warps' parts
         for (int h = 4 * half; h < p.G; h += 8) {
           float* r = refs + h;
           all.clear();
-          all.add<kWarps>(r, r + kWarps * 16, 16, kWarps, join + h * kRow + d4, 8 * kNT * kRow, kRow, lane);
+          all.add<kWarps, 4>(r, r + kWarps * 16, 16, kWarps, join + h * kRow + d4, 8 * kNT * kRow, kRow, lane);
           if (whole) {
             all.store(out, h, p.G);
           } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (h + k < p.G) *reinterpret_cast<float4*>(mine + 32 + (h + k) * kD + d4) = all.o[k];
-            if (lane < 4) {
-              mine[h + lane] = all.ref;
-              mine[16 + h + lane] = all.sum;
-            }
+            put(mine, h);
           }
         }
         if (!whole) {
-          // A segment cut between CTAs: the last to publish its piece joins them all, in CTA order. Their partials (references
-          // and sums of 16 heads, then the heads' outputs) come with bulk copies into the hand-over buffer, as many as fit it
-          // at once: with loads into registers a warp had a few of them under way, and 20 pieces took 8 us.
-          fence_proxy_async_all();  // (they are read with copies)
+          // A segment cut between CTAs: the last to publish its piece joins them all, in CTA order; of more than two batches, the
+          // last of each kMost joins those and publishes the result in the first one's place, and the last of these joins those.
+          // (All by one CTA: a sequence of 128K keys and one key/value head 41 us instead of 19, one of 10000 with 16 heads 26
+          // instead of 16.) Partials (references and sums of 16 heads, then the heads' outputs) come with bulk copies into the
+          // hand-over buffer, as many as fit it at once: with loads into registers a warp had a few of them under way, and 20
+          // pieces took 8 us.
           auto cta_of = [&](int i) {
             const int big = rm * (q_units + 1);
             return i < big ? i / (q_units + 1) : rm + (i - big) / q_units;
@@ -841,45 +847,66 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
           const int unit0 = segment_unit(pc.b, pc.j, pc.nt, pc.seg0);
           const int c_first = own > 0 ? unit0 : cta_of(unit0 + extra);
           const int c_last = own > 0 ? unit0 + (pc.nt - 1) / own : cta_of(unit0 + extra + pc.nt - 1);
-          named_bar_sync(1, 64);
-          if (tid == 64) {
-            // publishes what the barrier gathered (cumulativity), and sees what those before published
-            const bool last = atom_add_acq_rel(&p.counters[c_first], 1) == c_last - c_first;
-            if (last) p.counters[c_first] = 0;
-            misc[16] = last;
-          }
-          __syncwarp();
-          named_bar_sync(1, 64);
-          if (misc[16]) {
-            const int part = 32 + kD * p.G;  // floats
+          const int part = 32 + kD * p.G;  // floats
+          auto place_of = [&](int c) {
+            return p.partials + (static_cast<int64_t>(c) * 2 + (range_start(c) >= unit0 ? 0 : 1)) * kGqaSlotFloats;
+          };
+          // Whether this CTA is the last of n that count there (both warps ask).
+          auto last_of = [&](int counter, int n) {
+            fence_proxy_async_all();  // (what was written is read with copies)
+            named_bar_sync(1, 64);
+            if (tid == 64) {
+              // publishes what the barrier gathered (cumulativity), and sees what those before published
+              const bool last = n == 1 || atom_add_acq_rel(&p.counters[counter], 1) == n - 1;
+              if (last && n > 1) p.counters[counter] = 0;
+              misc[16] = last;
+            }
+            __syncwarp();
+            named_bar_sync(1, 64);
+            return misc[16] != 0;
+          };
+          // The partials of n CTAs, `step` apart, to the output or (to) joined into a partial.
+          auto join_parts = [&](int first, int step, int parts, float* to) {
             for (int h0 = 0; h0 < p.G; h0 += 8) {  // (both warps take every turn: they meet in it)
               const int h = h0 + 4 * half;
               all.clear();
-              for (int c0 = c_first; c0 <= c_last; c0 += S::kMost) {
-                const int n = min(S::kMost, c_last + 1 - c0);
-                if (h0 == 0 || c_last - c_first >= S::kMost) {  // (else they are there already)
+              for (int i0 = 0; i0 < parts; i0 += S::kMost) {
+                const int n = min(S::kMost, parts - i0);
+                if (h0 == 0 || parts > S::kMost) {  // (else they are there already)
                   // what was read and written there plainly comes before the copies
                   fence_proxy_async_all();
                   named_bar_sync(1, 64);
                   if (half == 0 && ok) {
                     if (lane == 0) mbar_arrive_expect_tx(m_full, static_cast<uint32_t>(n * part) * 4u);
                     __syncwarp();
-                    if (lane < n) {
-                      const int c = c0 + lane;
-                      bulk_load(join + lane * part,
-                                p.partials + (static_cast<int64_t>(c) * 2 + (range_start(c) >= unit0 ? 0 : 1)) * kGqaSlotFloats,
-                                static_cast<uint32_t>(part) * 4u, m_full, l2_policy_evict_first());
-                    }
+                    if (lane < n)
+                      bulk_load(join + lane * part, place_of(first + (i0 + lane) * step), static_cast<uint32_t>(part) * 4u, m_full,
+                                l2_policy_evict_first());
                     copied = merges;
                   }
                   wait(m_full, merges & 1, kStatusWaitFullTimeout);
                   ++merges;
                 }
-                if (h < p.G) all.add<S::kMost>(join + h, join + 16 + h, part, n, join + 32 + h * kD + d4, part, kD, lane);
+                if (h < p.G) all.add<S::kMost, 1>(join + h, join + 16 + h, part, n, join + 32 + h * kD + d4, part, kD, lane);
               }
-              if (h < p.G) all.store(out, h, p.G);
+              if (h >= p.G) continue;
+              if (to) put(to, h);
+              else all.store(out, h, p.G);
             }
+          };
+          // Counters: a segment's is its first CTA's, a group's too, and that of the second CTA counts groups. CTAs between the first
+          // and the last have no other segment; a group of the last CTA alone needs no counter.
+          const int parts = c_last - c_first + 1;
+          const bool deep = parts > 2 * S::kMost;
+          const int lead = deep ? c_first + (cta - c_first) / S::kMost * S::kMost : c_first;
+          const int members = deep ? min(S::kMost, c_last + 1 - lead) : parts;
+          const int groups = deep ? (parts + S::kMost - 1) / S::kMost : parts;
+          bool joins = last_of(lead, members);
+          if (deep && joins) {
+            if (members > 1) join_parts(lead, 1, members, place_of(lead));
+            joins = last_of(c_first + 1, groups);
           }
+          if (joins) join_parts(c_first, deep ? S::kMost : 1, groups, nullptr);
           named_bar_sync(1, 64);  // misc[16] is written again by the next cut piece, the buffer by the next piece
         }
         __syncwarp();

@@ -414,6 +414,24 @@ def test_decode_one_sequence_over_all_ctas():
         check_decode(c, [n], *decode(c, [n], h_q, hide=False))
 
 
+@pytest.mark.parametrize("h_q,h_kv", [(8, 1), (32, 2)])
+def test_decode_joins_in_groups_repeat_exactly(h_q, h_kv):
+    """Segments cut into more pieces than are joined at once, between shorter ones, on one workspace: the same bits every time."""
+    lens = [40000, 0, 2500, 1, 30001, 17]
+    c = step.Kv4(lens, h_kv, 64, DEV, seed=h_q)
+    q, out, sees = decode(c, lens, h_q, hide=False)
+    check_decode(c, lens, q, out, sees)
+    ws = moe.alloc_paged_workspace(len(lens), len(lens), h_q, h_kv, D, device=DEV)
+    full, first, again = i32(lens), [40000, 0, 0, 0, 0, 0], torch.empty_like(out)
+    alone = decode(c, first, h_q, hide=False, q=q)[1]
+    for _ in range(20):
+        for n, want in ((full, out), (i32(first), alone)):
+            again.fill_(float("nan"))
+            moe.moe_gqa_kv4_decode(q, c.raw, c.table, n, SCALE, again, ws)
+            assert torch.equal(again, want)
+    assert moe.workspace_status(ws) == 0 and not ws[4:4096].any()
+
+
 def test_calls_without_work():
     """No tokens, no sequences, sequences without keys."""
     raw = moe.alloc_kv4_cache(2, 2, 16, DEV)

@@ -163,8 +163,13 @@ def test_shares_cover_all_tiles_and_cut_segments_find_their_parts(segment):
                 if n < nts[b]:
                     cut.setdefault((b, j, seg0), []).append((c, 0 if i == 0 else 1))
         assert len(seen) == h_kv * sum(nts)
-        firsts = set()
+        most, used = rng.choice([2, 3, 8]), []
         for segment_at, parts in cut.items():
             assert parts == parts_of(*segment_at)
-            assert parts[0][0] not in firsts  # a counter of its own
-            firsts.add(parts[0][0])
+            # the counters: the first CTA's, or those of groups of more than one CTA and the second CTA's for the groups
+            first, last = parts[0][0], parts[-1][0]
+            if len(parts) > 2 * most:
+                used += [lead for lead in range(first, last + 1, most) if lead < last] + [first + 1]
+            else:
+                used.append(first)
+        assert len(used) == len(set(used))
