@@ -36,7 +36,7 @@
 // (One warp that loads, 8 or 11 that work and join through barriers: 255 sequences of up to 4K keys took 125 us, then 85.)
 //
 // GB300: 16 sequences of up to 32K keys, 4 heads a group, in 60 us (4.9 TB/s, 72% of a copy; 155 us in bf16); 24 with 16 heads
-// a group in 74 (3.2 TB/s, 180 TFLOP/s); 64 behind a window of 1024 in 25; 255 of up to 4K in 74 (3.9 TB/s); one sequence of 512
+// a group in 74 (3.2 TB/s, 180 TFLOP/s); 64 behind a window of 1024 in 26; 255 of up to 4K in 74 (3.9 TB/s); one sequence of 512
 // visible keys in 7.5. With two chunks a warp the working warps were at it 76% of the time in the first of these, the integer pipe
 // then 68% busy; the rest is the start (lengths, table, first tile: 3 us), the last pieces' joins, and a hand-over per piece.
 #include <cuda_fp16.h>

@@ -1,7 +1,8 @@
 """A model of the ring of tiles in attention over the 4-bit cache (no GPU needed): two loading warps take four tiles in turn,
 groups of working warps take every n-th tile, and a stage's barriers tell apart only neighbouring phases. Every reachable
 state of their progress is visited: no stage is filled again before its tile has been worked on, and no tile worked on before
-it is there, for the numbers of stages and groups the kernel uses; with others that its static_assert refuses, some are."""
+it is there, for the numbers of stages and groups the kernel uses; with others that its static_assert refuses, some are. And a
+model of how the list of tiles is shared out: every tile once, a cut segment's parts where they are looked for, counters apart."""
 import os
 import random
 import re
