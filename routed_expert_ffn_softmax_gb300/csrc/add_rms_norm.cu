@@ -84,11 +84,13 @@ __global__ void __launch_bounds__(kMaxThreads, kVecs <= 2 ? 2 : 1) add_rms_norm_
     if (p.weight && mine[i]) w[i] = *reinterpret_cast<const uint4*>(p.weight + at[i]);
   }
   uint4 a[kVecs], b[kVecs];
-  auto load = [&](int n) {
+  // (N may be up to 2^31 - 1, and a grid more still fits 32 bits without a sign)
+  const uint32_t rows = static_cast<uint32_t>(p.N);
+  auto load = [&](uint32_t n) {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (mine[i] && n < p.N) {
+      if (mine[i] && n < rows) {
         b[i] = load16(p.residual + static_cast<int64_t>(n) * p.H + at[i]);
         if (kAdd) a[i] = load16(p.x + static_cast<int64_t>(n) * p.x_stride + at[i]);
       }
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(kMaxThreads, kVecs <= 2 ? 2 : 1) add_rms_norm_
   };
   load(blockIdx.x);
   int turn = 0;
-  for (int n = blockIdx.x; n < p.N; n += gridDim.x, turn ^= 1) {
+  for (uint32_t n = blockIdx.x; n < rows; n += gridDim.x, turn ^= 1) {
     uint32_t r[kVecs][4];
     float ss = 0.0f;
 #pragma unroll
