@@ -77,8 +77,10 @@ __global__ void __launch_bounds__(kLoadThreads) kv4_load_kernel(const Kv4LoadArg
 
   const int q = lane & 3;  // of a row's codes: words 8 q .. 8 q + 7 are dimensions 32 w + 8 q .. + 7 for each w
   const int page_blocks = 1 << (p.page_shift - 4);
-  const int total = pre[p.B] * p.h_kv;
-  for (int it = blockIdx.x * kLoadWarps + warp; it < total; it += gridDim.x * kLoadWarps) {
+  // (up to 2^31 - 1; a turn more still fits 32 bits without a sign)
+  const uint32_t total = static_cast<uint32_t>(pre[p.B] * p.h_kv);
+  for (uint32_t item = blockIdx.x * kLoadWarps + warp; item < total; item += gridDim.x * kLoadWarps) {
+    const int it = static_cast<int>(item);
     int lo = 0, hi = p.B - 1;
     while (lo < hi) {  // the last sequence whose first item is <= it (skips empty ones)
       const int mid = (lo + hi + 1) >> 1;

@@ -75,3 +75,33 @@ int main() {{
   }}
 }}
 """)
+
+
+@pytest.mark.parametrize("grid", [1, 152, 912])
+def test_blocks_read_back(tmp_path, grid):
+    loop, item = found(r"(for \(\w+ (\w+) = blockIdx\.x \* kLoadWarps[^{]*\)) \{", "kv4_load.cu")
+    total = found(r"const (\w+) total = ", "kv4_load.cu")
+    warps = int(found(r"constexpr int kLoadThreads = (\d+);", "kv4_load.cu")) // 32
+    run(tmp_path, f"""
+constexpr int kLoadWarps = {warps};
+int main() {{
+  gridDim.x = {grid};
+  for (int64_t count : {{2147483647, 2147483640, 2147483647 - {grid}}}) {{
+    const {total} total = count;
+    for (unsigned back = 0; back < 2 * gridDim.x * kLoadWarps; ++back) {{
+      const int64_t at = count - 1 - back;
+      blockIdx.x = static_cast<unsigned>(at / kLoadWarps);
+      const int warp = static_cast<int>(at % kLoadWarps);
+      turns = 0;
+      {loop} {{
+        seen[turns] = {item};
+        if (bad(seen[turns], count) || ++turns > 3) {{ turns = 100; break; }}
+      }}
+      if (turns != 1 + static_cast<int>(back / (gridDim.x * kLoadWarps))) {{
+        std::printf("%lld blocks, block %lld: %d turns\\n", (long long)count, (long long)at, turns);
+        return 1;
+      }}
+    }}
+  }}
+}}
+""")
