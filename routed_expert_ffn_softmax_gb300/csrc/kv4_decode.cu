@@ -68,7 +68,9 @@ constexpr int kRow = kD + 4;               // floats of a head's outputs handed 
 constexpr float kMost = 32768.0f;          // what p s may reach
 constexpr float kRaise = 14.5f;            // log2 of the p s from which a head's reference is raised when one is too large
 constexpr float kStart = 6.0f;             // log2 of the largest p s right after a reference is set
-constexpr float kLeastScale = 8.6736174e-19f;  // 2^-60: smaller value scales count as this where references are concerned
+// 2^-80: smaller value scales, 0 among them, count as this where references are concerned. A weight is then below 2^95 (2^kRaise
+// over the least), and a sum of 2^31 of them below 2^126, which the last division needs.
+constexpr float kLeastScale = 8.2718061e-25f;
 static_assert(kFold == kChunk, "sink keys are folded in whole chunks");
 
 // Warps 0..3: two that load, two that prepare queries and finish pieces; the others work.
@@ -199,7 +201,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// log2 of the largest of a key's value scales.
+// log2 of the largest of a key's value scales that is not NaN.
 __device__ __forceinline__ float log_scale(const uint2& v) {
   const uint32_t m = __vmaxu2(v.x, v.y);
   return lg2_approx(max3_f32(bf_lo(m), bf_hi(m), kLeastScale));
@@ -376,7 +378,8 @@ struct State {
           for (int i = 0; i < 4; ++i) p[c][nt][i] = ex2_approx(x[c][nt][i] - ref[nt][i & 1]);
     };
     weigh();
-    // Whether the lane's largest weight times its largest value scale (scales are not negative) is small enough. NaN is not.
+    // Whether the lane's largest weight times its largest value scale (scales are not negative) is small enough. NaN is not: one
+    // among the scales stands above all others here and would hide them.
     auto larger = [](uint32_t a, uint32_t b) { return __vmaxu2(a, b); };
     uint32_t m = larger(larger(vs[0][0].x, vs[0][0].y), larger(vs[0][1].x, vs[0][1].y));
 #pragma unroll
