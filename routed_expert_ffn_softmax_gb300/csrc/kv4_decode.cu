@@ -203,8 +203,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 // log2 of the largest of a key's value scales that is not NaN.
 __device__ __forceinline__ float log_scale(const uint2& v) {
-  const uint32_t m = __vmaxu2(v.x, v.y);
-  return lg2_approx(max3_f32(bf_lo(m), bf_hi(m), kLeastScale));
+  return lg2_approx(max3_f32(max3_f32(bf_lo(v.x), bf_hi(v.x), kLeastScale), bf_lo(v.y), bf_hi(v.y)));
 }
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float d;
@@ -389,7 +388,7 @@ struct State {
     for (int c = 0; c < kCount; ++c)
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) top_p = max3_nan(max3_nan(top_p, p[c][nt][0], p[c][nt][1]), p[c][nt][2], p[c][nt][3]);
-    const bool fits = top_p * max3_f32(bf_lo(m), bf_hi(m), kLeastScale) <= kMost;
+    const bool fits = top_p * max3_nan(bf_lo(m), bf_hi(m), kLeastScale) <= kMost;
     if (!__all_sync(0xffffffffu, fits)) {
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt)

@@ -1,4 +1,4 @@
-"""Attention over a paged cache held in 4 bits at the edges its header names: the least value scales (needs a GPU)."""
+"""Attention over a paged cache held in 4 bits at the edges its header names: the least value scales, NaN scales (needs a GPU)."""
 import math
 
 import pytest
@@ -57,3 +57,27 @@ def test_values_that_are_all_zero(h_q):
     c.put(0, slice(0, n), *c.rows[0])
     _, out, _ = decode(c, [n], h_q, scale=scale, hide=False, q=q)
     assert not out.any()
+
+
+@pytest.mark.parametrize("h_q", [4, 16])
+@pytest.mark.parametrize("at", [37, 293])
+@pytest.mark.parametrize("near", [0, 8, 16, 24, 100, None])
+def test_a_nan_scale_of_values_leaves_the_other_dimensions_right(near, at, h_q):
+    """Of key `at`, in a warp's first unit or behind others, the first group's value scale is 2^20 times the others', and of a key
+    `near` it (in the same or another lane, unit or tile; None: of that key itself) the third group's is NaN. Dimensions 64 .. 95
+    are NaN, all others as without it."""
+    n = 400
+    c = step.Kv4([n], 1, 16, DEV, seed=3)
+    k, (vc, vs) = c.rows[0]
+    vs = torch.ones_like(vs)
+    vs[at, :, 0] = 2.0 ** 20
+    c.rows[0] = [k, (vc, vs)]
+    bad = vs.clone()
+    bad[at if near is None else (at + near + (near == 0)) % n, :, 2] = float("nan")
+    c.put(0, slice(0, n), k, (vc, bad))
+    q, out, sees = decode(c, [n], h_q, hide=False)
+    assert out[0, :, 64:96].isnan().all()
+    kv = c.values(0)
+    want = step.attend(q[0], *kv, sees[0], D ** -0.5, c.rows[0][0][1])
+    live = [w.unflatten(-1, (4, 32))[:, [0, 1, 3]].flatten(1) for w in (out[0].float(), *want)]
+    step.check(*live, n, f"NaN near {near}")
