@@ -147,6 +147,7 @@ struct Params {
   int B, h_q, h_kv, G, L_cap;
   float scale_log2;
   PagedKv kv;
+  int piece_waits;   // limits of a wait that may last as long as a piece
   int give_up_tile;
 };
 
@@ -810,6 +811,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Params p)
       Piece pc{};
       for (int x = beg; x < end; x += pc.n, ++pi) {
         pc = x == beg ? locate(x) : after(pc, x);
+        // (a piece may take several limits)
+        for (int i = 1; ok && i < p.piece_waits && !mbar_wait(h_full, pi & 1);) ++i;
         wait(h_full, pi & 1, kStatusWaitFullTimeout);
         const bool whole = pc.tl == 0 && pc.n == pc.nt;
         uint16_t* out = p.out + (static_cast<int64_t>(pc.b) * p.h_q + static_cast<int64_t>(pc.j) * p.G) * kD + d4;
@@ -1062,6 +1065,8 @@ cudaError_t launch_kv4_decode(const Kv4DecodePlan& plan, cudaStream_t stream) {
   p.L_cap = plan.L_cap;
   p.scale_log2 = plan.scale_log2;
   p.kv = plan.paged;
+  // a tile takes at most some 0.9 us (16 heads a group), so 2^20 of them less than half a wait's limit
+  p.piece_waits = 1 + (p.L_cap / kv4::kKeys >> 20);
   p.give_up_tile = plan.give_up_tile;
   return p.G <= 8 ? kv4::launch<1>(p, plan.num_ctas, stream) : kv4::launch<2>(p, plan.num_ctas, stream);
 }
