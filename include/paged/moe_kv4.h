@@ -70,6 +70,9 @@ moe_status_t moe_gqa_kv4_decode(const uint16_t* q, const uint8_t* kv4_cache, con
  * first[b] .. seq_lens[b] - 1 (from 0 with first null), each value code * scale rounded once.
  *   block_table [B, max_pages], dst_table [B, dst_max_pages] int32: the pages of the 4-bit cache and of k_cache and
  *               v_cache [dst_pages, h_kv, page_size, d] bf16. Entries before first[b] / page_size are not looked at.
+ * For moe_gqa_paged_prefill over those pages every row that a query sees has to stand there, the context's too, not only the
+ * rows that the step adds: first is null, or at most the earliest position that a query of the sequence sees, unless the
+ * earlier rows have been read back into these pages before (moe_qk_norm_rope_kv4 does not write them).
  * Other rows of k_cache and v_cache are left as they were. Pages in dst_table are distinct. A length that is negative or
  * past either table, or a negative first, makes that sequence empty (status 4); a source page outside [0, num_pages)
  * reads as zeros, rows for a destination outside [0, dst_pages) are not written (status 6). B as in moe_gqa_paged_decode;

@@ -439,7 +439,8 @@ def moe_gqa_kv4_decode(q, kv4_cache, block_table, seq_lens, scale: float, out, w
 
 def moe_kv4_load(kv4_cache, block_table, first, seq_lens, k_cache, v_cache, dst_table, workspace, stream=None) -> None:
     """Rows first[b] .. seq_lens[b] - 1 (first None: from 0) of the 4-bit cache's pages block_table [B, max_pages] as bf16
-    rows of k_cache and v_cache [pages, h_kv, page_size, d] at the pages dst_table [B, dst_max_pages]. All lists int32."""
+    rows of k_cache and v_cache [pages, h_kv, page_size, d] at the pages dst_table [B, dst_max_pages]. All lists int32. Every row
+    that moe_gqa_paged_prefill is to see has to stand there: first None, or at most the earliest position that is seen."""
     st = (_native or _load_native()).moe_kv4_load(kv4_cache, block_table, first, seq_lens, k_cache, v_cache, dst_table,
                                                   workspace, _raw(stream))
     if st:
