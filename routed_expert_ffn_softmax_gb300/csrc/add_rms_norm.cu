@@ -6,12 +6,14 @@
 // 4 bytes are read and 3 or 4 written per value, so HBM bounds it. A block holds a row in registers: each thread takes
 // vectors of 8 values, one or more, and the sum of squares is a block reduction with one barrier. A block keeps its
 // part of the weight from row to row and has the next row's loads under way while it works on one. GB300: 8191 rows of 7168 to
-// bf16 in 72.6 us (6.47 TB/s, 96% of a copy), 2048 rows of 6144 to 8 bits in 17.6 (5.0 TB/s), 64 rows of 4096 in 2.8.
+// bf16 in 72.6 us (6.47 TB/s, 96% of a copy), 2048 rows of 6144 to 8 bits in 18.7 (4.7 TB/s), 64 rows of 4096 in 2.8.
+// What does not fit the registers: 8 vectors a thread (H above 16384) spill 84 to 428 bytes, the 8-bit form with 2 vectors 36.
 //
 // The codes: the norm's factor is the same for all of a group, so q does not depend on it, and 127 t is exact in fp32
 // (8 + 8 + 7 bits). A multiplication with the rounded 127 / T is off by 127 2^-23 < 2^-16 and decides every code but those
-// next to a half; a thread that holds one within 2^-14 (one warp in 30) divides all of its eight, which is exact: a quotient
-// of a number of 23 bits and one of 16 that is not a half is 2^-17 or more away from one.
+// next to a half; a thread that holds one within 2^-14 (one warp in 30) divides all of its eight, correctly rounded, which makes
+// a half of no other quotient: with T = B and t = n 2^-j, whole numbers of 16 bits and t <= T, a quotient Q = 127 t / T that is not
+// the half h has |Q - h| >= Q / (254 n) (of Q / (254 n 2^-j) for j < 0), more than 2^-24 Q, and so than half a step of Q in fp32.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -84,15 +86,16 @@ __global__ void __launch_bounds__(kMaxThreads, kVecs <= 2 ? 2 : 1) add_rms_norm_
     if (p.weight && mine[i]) w[i] = *reinterpret_cast<const uint4*>(p.weight + at[i]);
   }
   uint4 a[kVecs], b[kVecs];
-  // (N may be up to 2^31 - 1, and a grid more still fits 32 bits without a sign)
+  // (N may be up to 2^31 - 1, and a grid more still fits 32 bits without a sign. Addresses take the sign again: without it the form
+  // for H above 16384 is 3 to 5% slower in 8 bits.)
   const uint32_t rows = static_cast<uint32_t>(p.N);
   auto load = [&](uint32_t n) {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
       if (mine[i] && n < rows) {
-        b[i] = load16(p.residual + static_cast<int64_t>(n) * p.H + at[i]);
-        if (kAdd) a[i] = load16(p.x + static_cast<int64_t>(n) * p.x_stride + at[i]);
+        b[i] = load16(p.residual + static_cast<int64_t>(static_cast<int>(n)) * p.H + at[i]);
+        if (kAdd) a[i] = load16(p.x + static_cast<int64_t>(static_cast<int>(n)) * p.x_stride + at[i]);
       }
     }
   };
@@ -111,7 +114,7 @@ __global__ void __launch_bounds__(kMaxThreads, kVecs <= 2 ? 2 : 1) add_rms_norm_
         ss = fmaf(hi(r[i][k]), hi(r[i][k]), ss);
       }
       if (p.residual_out && mine[i])
-        *reinterpret_cast<uint4*>(p.residual_out + static_cast<int64_t>(n) * p.H + at[i]) =
+        *reinterpret_cast<uint4*>(p.residual_out + static_cast<int64_t>(static_cast<int>(n)) * p.H + at[i]) =
             make_uint4(r[i][0], r[i][1], r[i][2], r[i][3]);
     }
     load(n + gridDim.x);
@@ -136,7 +139,7 @@ __global__ void __launch_bounds__(kMaxThreads, kVecs <= 2 ? 2 : 1) add_rms_norm_
         t[2 * k] = lo(r[i][k]) * lo(wv[k]);
         t[2 * k + 1] = hi(r[i][k]) * hi(wv[k]);
       }
-      const int64_t to = static_cast<int64_t>(n) * p.H + at[i];
+      const int64_t to = static_cast<int64_t>(static_cast<int>(n)) * p.H + at[i];
       if (p.y && mine[i])
         *reinterpret_cast<uint4*>(p.y + to) = make_uint4(pack(t[0] * factor, t[1] * factor), pack(t[2] * factor, t[3] * factor),
                                                           pack(t[4] * factor, t[5] * factor), pack(t[6] * factor, t[7] * factor));
