@@ -52,13 +52,15 @@ moe_status_t moe_qk_norm_rope_kv4(const uint16_t* qkv, int64_t row_stride, int N
  * moe_gqa_paged_decode over the 4-bit cache: one query token per sequence, at position seq_lens[b] - 1.
  *   q [B, h_q, d] bf16, seq_lens [B] int32 (the new token included), out [B, h_q, d] bf16
  * Numerics: a query's products with the codes are exact, their sums, the scales and the softmax in fp32 (the codes enter as
- * c + 8, the offset is taken off within each group's sum: a score is off by at most 15 * 2^-20 * |scale| * sum |q| s over the
- * dimensions), 2^x to 2^-22. Each probability times a value scale is rounded once, to fp16 (2^-11 of it), and multiplied with
- * the exact codes into fp32 sums; the last division to 2^-22, one rounding to bf16. Products of probability and value scale are
- * held relative to the largest of the sequence: below 2^-20 of it they are off by up to 2^-31 of it instead. Queries are held
- * relative to the largest of their head, exactly down to 2^-20 of it; they may be up to 2^100 in magnitude. Scales are not
- * negative, and those of the values at least 2^-80 or 0. A query that holds a NaN or an infinity gives NaN, a value scale of
- * NaN gives NaN in its dimensions. Everything else as in moe_gqa_paged_decode.
+ * c + 8, the offset is taken off within each group's sum: a score is off by at most 15 * 2^-20 * |scale| * sum |q| s over
+ * the dimensions), 2^x to 2^-22 (its argument to 2^-18 where value scales are near the least, 2^-20 for ordinary ones). Each
+ * probability times a value scale is rounded once, to fp16 (2^-11 of it), and multiplied with the exact codes into fp32
+ * sums; the last division to 2^-22, one rounding to bf16. Products of probability and value scale are held relative to the
+ * largest of the sequence: below 2^-20 of it they are off by up to 2^-31 of it instead. Queries are held relative to the
+ * largest of their head (2^-100 where that is smaller), exactly down to 2^-20 of it; they may be up to 2^100 in magnitude.
+ * Scales are not negative, and those of the values at least 2^-80 or 0. A query that holds a NaN or an infinity gives NaN. A
+ * value scale of NaN gives NaN in its dimensions and changes no others, one of the keys' NaN in all of its key/value head's;
+ * no scale is infinite (moe_qk_norm_rope_kv4 stores none). Everything else as in moe_gqa_paged_decode.
  */
 moe_status_t moe_gqa_kv4_decode(const uint16_t* q, const uint8_t* kv4_cache, const int32_t* block_table,
                                 const int32_t* seq_lens, int B, int h_q, int h_kv, int d, int num_pages,

@@ -33,8 +33,9 @@ extern "C" {
  *                scale = 1 where T = 0. At least one of y and q is given.
  * Squares are summed in fp32, and y rounded once. The codes are those of the exact quotient: r has 8 bits and t 16, so
  * nothing before the division is rounded, and a quotient that is not a half is far enough from one. That holds while |t|
- * is 0 or within 2^-110 .. 2^120. A row whose squares sum past 2^128 comes out as 0; NaN gives NaN (in 8 bits: a NaN
- * scale, for the groups that hold one and, through the mean, for the whole row).
+ * is 0 or within 2^-110 .. 2^120. y is r * weight in fp32 times the factor, so it needs r * weight within fp32's range too. A
+ * row whose squares sum past 2^128 comes out as 0 (an infinity, or an r * weight past fp32's range, as NaN); NaN gives NaN (in
+ * 8 bits: a NaN scale, for the groups that hold one and, through the mean, for the whole row).
  * H is a multiple of 8 (of 128 with q) up to 32768. N = 0 is a no-op. All pointers 16-byte aligned, scales 4-byte.
  */
 moe_status_t moe_add_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* residual, const uint16_t* weight,

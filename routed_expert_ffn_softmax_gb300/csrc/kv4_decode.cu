@@ -1,23 +1,26 @@
 // Decode attention over a paged cache held in 4 bits (include/paged/moe_kv4.h): one query token per sequence, the G query
 // heads of a group against each key/value head, under a sliding window with sink tokens.
 //
-// What bounds it. A key costs 144 bytes of HBM a key/value head (72 for K, 72 for V), 3.6 times less than in bf16, so an
-// SM has 6.2 cycles of memory time per key. Tensor-core operands would have to pass through shared memory as 16-bit tiles:
-// 512 bytes written and 512 read per key, 8 cycles of the shared memory's 128 bytes a cycle, more than the memory time. So
-// the codes go from shared memory straight into registers as mma.sync operands: the key axis is the M side of both
-// products, so a group of up to 8 heads (the N side) wastes nothing.
+// What bounds it. A key costs 144 bytes of HBM a key/value head (72 for K, 72 for V), 3.6 times less than in bf16, so an SM has
+// 6.2 cycles of memory time per key. 16-bit operands of tcgen05 would have to pass through shared memory: 512 bytes written and
+// 512 read per key, 8 cycles of the shared memory's 128 bytes a cycle, more than the memory time. (In 8 bits the keys would
+// pass: the bytes 0 .. 15 are exactly n 2^-9 in e4m3, 128 bytes written and read, 2 cycles. Scores and probabilities would then
+// go through TMEM and back; that was not tried.) Here the codes go from shared memory straight into registers as mma.sync
+// operands: the key axis is the M side of both products, so a group of up to 8 heads (the N side) wastes nothing.
 //     S [16 keys x 8 heads]  = codes(K) [16 x 32] . q [32 x 8]           for each of the 4 groups of 32 dimensions
 //     O [16 dims x 8 heads] += codes(V)^T [16 x 16 keys] . (p s) [16 x 8]  s the value scale of the group the dims are in
 // K's scales multiply the four group sums in fp32; V's scales go into the probabilities, once per group.
 //
-// Unpacking is what the kernel spends its time on (the integer pipe takes 2 cycles an instruction). 16 bits of a row hold four
-// codes of a group; two such of the same row (K) or of two keys (V) in one register give all four fp16 pairs with four masks
-// and a shift. K's are left as fp16 subnormals n 2^-24 (n 2^-20 for the odd codes,
-// whose queries are a 16th): exact products, n = c + 8, and -8 sum(q) is where the accumulator starts. V's are turned into
-// exact c by an exponent and a subtraction, as a sum over many keys must not carry an offset (as subnormals too, corrected by a
-// product with -8, a key of large weight and code 0 left 2^-20 of its weight; it was no faster). K's codes as e4m3 bytes, two
-// masks for eight, with the queries in two e4m3 parts: the instruction is made of conversions and fp16 products, 16 sequences
-// of up to 32K keys took 78 us instead of the 65 of that time.
+// Unpacking is most of the instructions (the integer pipe takes 2 cycles each), but no unit is full over the whole kernel (16
+// long sequences: integer pipe 44%, tensor 21%, fma 21%, issue 48%): each of the two working warps of a scheduler goes through
+// one chain a unit (score products, 2^x, the vote, fp16, value products) with nothing of the next unit under way, and
+// instruction fetch is the largest stall after the waits of idle roles. 16 bits of a row hold four codes of a group; two such
+// of the same row (K) or of two keys (V) in one register give all four fp16 pairs with four masks and a shift. K's are left as
+// fp16 subnormals n 2^-24 (n 2^-20 for the odd codes, whose queries are a 16th): exact products, n = c + 8, and -8 sum(q) is
+// where the accumulator starts. V's are turned into exact c by an exponent and a subtraction, as a sum over many keys must not
+// carry an offset (as subnormals too, corrected by a product with -8, a key of large weight and code 0 left 2^-20 of its
+// weight; it was no faster). K's codes as e4m3 bytes, two masks for eight, with the queries in two e4m3 parts: the instruction
+// is made of conversions and fp16 products, 16 sequences of up to 32K keys took 78 us instead of the 65 of that time.
 //
 // Range. p s must fit fp16, whatever the scales are: the softmax reference R of a head bounds score + log2(largest scale of
 // the key) instead of the score alone, p = 2^(score - R) is held in fp32, and R is raised (outputs and sums rescaled) only
@@ -35,7 +38,7 @@
 //          soon as its part is handed over.
 // (One warp that loads, 8 or 11 that work and join through barriers: 255 sequences of up to 4K keys took 125 us, then 85.)
 //
-// GB300: 16 sequences of up to 32K keys, 4 heads a group, in 60 us (4.9 TB/s, 72% of a copy; 155 us in bf16); 24 with 16 heads
+// GB300: 16 sequences of up to 32K keys, 4 heads a group, in 60 us (4.8 TB/s, 71% of a copy; 155 us in bf16); 24 with 16 heads
 // a group in 74 (3.2 TB/s, 180 TFLOP/s); 64 behind a window of 1024 in 26; 255 of up to 4K in 74 (3.9 TB/s); one sequence of 512
 // visible keys in 7.5. With two chunks a warp the working warps were at it 76% of the time in the first of these, the integer pipe
 // then 68% busy; the rest is the start (lengths, table, first tile: 3 us), the last pieces' joins, and a hand-over per piece.

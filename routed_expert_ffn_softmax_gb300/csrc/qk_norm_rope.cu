@@ -18,6 +18,7 @@
 //
 // Four heads' sums of squares are reduced together (9 shuffles instead of 16, one root instead of four): halves of 32 65 -> 60 us.
 // The next heads are loaded after that in the kernel for full rotations, which has no registers for both.
+// (With 80 a thread that kernel spills 4 bytes, for several axes or a 4-bit cache 24, for both 40; the first one, with 128, up to 48.)
 //
 // Positions with several axes (kAxes; include/paged/moe_norm.h): the lanes that compute a pair's sine and cosine look up the
 // pair's axis once and load that axis's position per token; nothing else differs (8191 tokens of 64 + 8 heads: 54 us).
@@ -26,7 +27,7 @@
 // 4) lanes that hold a group of 32 dimensions share its largest magnitude, taken of the bits as whole numbers (two groups
 // in one shuffle; NaN stands above infinity), and lanes that hold parts of the same stored bytes exchange them, so that a
 // head's 64 bytes of codes leave in 8- or 16-byte stores. Every code is that of the exact quotient: see codes2. 9603 tokens of
-// 32 + 2 8 heads in 47 us (4.4 TB/s, issue-bound; their bf16 store takes 42).
+// 32 + 2 8 heads in 48 us (4.3 TB/s; issue slots 60% used; their bf16 store takes 42 for more bytes: the rest is instructions).
 //
 // The angle: inv_freq / (2 pi) is kept as a 64-bit fraction of a turn (computed in fp64, rounded once), so
 // pos * fraction modulo 2^64 is the angle modulo one turn without any loss for large pos, and sin and cos are taken of a

@@ -81,3 +81,18 @@ def test_a_nan_scale_of_values_leaves_the_other_dimensions_right(near, at, h_q):
     want = step.attend(q[0], *kv, sees[0], D ** -0.5, c.rows[0][0][1])
     live = [w.unflatten(-1, (4, 32))[:, [0, 1, 3]].flatten(1) for w in (out[0].float(), *want)]
     step.check(*live, n, f"NaN near {near}")
+
+
+def test_a_nan_scale_of_keys_is_its_heads_alone():
+    """A NaN scale of a visible key makes the outputs of that key/value head's queries NaN and leaves the others' right."""
+    lens = [200, 700]
+    c = step.Kv4(lens, 2, 16, DEV, seed=4)
+    (kc, ks), v = c.rows[1]
+    bad = ks.clone()
+    bad[333, 0, 1] = float("nan")
+    c.put(1, slice(0, 700), (kc, bad), v)
+    q, out, sees = decode(c, lens, 8, hide=False)
+    assert out[1, :4].isnan().all()
+    for b, heads in ((0, slice(0, 8)), (1, slice(4, 8))):
+        want = step.attend(q[b], *c.values(b), sees[b], D ** -0.5, c.rows[b][0][1])
+        step.check(out[b, heads], *(w[heads] for w in want), lens[b], f"sequence {b}")
